@@ -306,6 +306,75 @@ bi_status bi_kv_write(const void* k_new, const void* v_new, const int32_t* seq,
                       int64_t num_pages, int max_blocks_per_seq, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Quantised paged KV cache (about half the bytes of the bf16 one)          */
+/* ------------------------------------------------------------------------ */
+/* The pages define no quantised cache; this is the library's addition.
+ * cache [num_pages][Hkv][BI_KV_Q8_RECORD_BYTES(D)] bytes: the record of one
+ * page and kv head holds
+ *   K [16][D] e4m3, V [16][D] e4m3, K scales [16], V scales [16].
+ * Page tables and lengths are those of the bf16 cache.  A row (one token's K
+ * or V of one head) has one scale byte c that stands for 2^(c - 127):
+ *   amax = the row's largest magnitude,
+ *   e = the least integer in -124 .. 7 with amax * 2^-e <= 448 (7 if none),
+ *   c = e + 127, element = e4m3(x * 2^-e), rounded to nearest even, magnitudes
+ *   above 448 (only where amax > 448 * 2^7 = 57344) stored as 448.
+ * A row with an infinity or a NaN is stored as zeros with c = 135 and reads
+ * back as NaN throughout.  Every other stored value e4m3 * 2^e is a bf16
+ * number, so reading back is exact, and an element is off by at most 2^-4 of
+ * its magnitude or 2^(e - 10), whichever is larger.
+ * Records written by other means: scale bytes outside 3 .. 135 and the bytes
+ * 0x7f and 0xff (read as 480 and -480, not NaN) give unspecified values, but
+ * no access outside the buffers.
+ * Requirements of all three calls: D in {64, 128}; page_size == 16;
+ * num_pages * Hkv * 16 < 2^31; cache 16-byte aligned. */
+#define BI_KV_Q8_RECORD_BYTES(D) (32 * (D) + 32)
+
+/* Quantise the K/V rows of new tokens and write them into the cache: as
+ * bi_kv_write, with the same arguments but one cache.  A (sequence, position)
+ * given twice in one call, or two sequences' positions in one shared slot,
+ * leaves that slot's rows unspecified (its scale may be one row's and its
+ * elements the other's); no other slot is touched.  num_seqs: the rows of
+ * block_table.  A token whose sequence (outside 0 .. num_seqs-1), position
+ * or page is out of range is recorded as BI_ERR_DEVICE_BOUNDS and skipped.
+ * Further requirement: n_tokens * Hkv < 2^31. */
+bi_status bi_kv_write_q8(const void* k_new, const void* v_new, const int32_t* seq,
+                         const int32_t* pos, int64_t n_tokens, void* cache,
+                         const int32_t* block_table, int num_seqs, int Hkv, int D,
+                         int page_size, int64_t num_pages, int max_blocks_per_seq,
+                         void* stream);
+
+/* Read the tokens 0 .. kv_lens[b]-1 of each sequence back as bf16 pages
+ * k_out, v_out [num_out_pages][Hkv][16][D], the layout of the bf16 cache:
+ * block j of sequence b goes to page out_table[b][j] (out_table int32
+ * [B][max_out_blocks], device), so that bi_attn_prefill_chunk can run on the
+ * result.  out_table may be block_table itself (the same page ids in a pool
+ * of the same size).  Slots behind a sequence's last token and other pages
+ * are left as they were.  Two sequences may share a page (and an out page)
+ * whose tokens they agree on.
+ * max_kv_len: host bound on kv_lens (sizes the grid).  A length outside
+ * 0 .. max_kv_len or past either table is recorded as BI_ERR_DEVICE_BOUNDS
+ * and its sequence skipped; a page id outside its pool likewise skips that
+ * page.  B <= 65535. */
+bi_status bi_kv_read_q8(const void* cache, const int32_t* block_table, const int32_t* kv_lens,
+                        int B, int Hkv, int D, int page_size, int64_t num_pages,
+                        int max_blocks_per_seq, int max_kv_len, void* k_out, void* v_out,
+                        const int32_t* out_table, int64_t num_out_pages, int max_out_blocks,
+                        void* stream);
+
+/* Decode over the quantised cache: bi_attn_decode with one cache in place of
+ * two (same modes, split plan, workspace size, checks and errors).  The
+ * result in BI_MODE_INVARIANT has exactly the bytes of bi_attn_decode on the
+ * pages that bi_kv_read_q8 gives, and so those of bi_attn_prefill_chunk on
+ * them at every position.  BI_MODE_VARIANT sizes its chunks from this
+ * kernel's resident blocks, so its plan may differ from bi_attn_decode's. */
+bi_status bi_attn_decode_q8(const void* q, const void* cache, const int32_t* block_table,
+                            const int32_t* kv_lens, void* out, float* out_f32, int B, int Hq,
+                            int Hkv, int D, int page_size, int64_t num_pages,
+                            int max_blocks_per_seq, int max_kv_len, int split_size,
+                            float sm_scale, bi_mode mode, int variant_splits, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Element-wise decoder-layer steps (P1 §5.4: batch-invariant by nature)    */
 /* ------------------------------------------------------------------------ */
 /* Row gather: dst[i, :] = src[idx[i], :] for i < n (token embedding lookup,
@@ -331,6 +400,54 @@ bi_status bi_gather_rows(const void* src, int64_t rows, int64_t H, const int32_t
  * Requirements: D % 16 == 0, D <= 1024, theta > 1.  Errors: as bi_rmsnorm. */
 bi_status bi_rope_qkv(const void* qkv, const int32_t* pos, int64_t T, int Hq, int Hkv, int D,
                       double theta, void* q, void* k, void* v, void* stream);
+
+/* Rotation frequencies of rotary positions stretched for long contexts, on
+ * the host: freqs [rot_dim / 2] (a HOST array; copy it to the device for
+ * bi_rope_qkv_scaled) and the factor on cosine and sine.  With
+ * f_i = theta^(-2i/rot_dim):
+ *   BI_ROPE_NONE     f_i
+ *   BI_ROPE_LINEAR   f_i / factor (position interpolation)
+ *   BI_ROPE_NTK      f_i with theta * factor^(rot_dim / (rot_dim - 2))
+ *   BI_ROPE_LLAMA3   (1 - w) f_i / factor + w f_i, w = clamp((n_i - low_turns)
+ *                    / (high_turns - low_turns), 0, 1), n_i = trained_len f_i
+ *                    / (2 pi) the turns of pair i over the trained length
+ *   BI_ROPE_YARN     the same mix with w = 1 - clamp((i - a) / (b - a), 0, 1),
+ *                    a = max(floor(p(high_turns)), 0), b = min(ceil(
+ *                    p(low_turns)), rot_dim - 1) (b - a at least 0.001),
+ *                    p(n) = rot_dim ln(trained_len / (2 pi n)) / (2 ln theta);
+ *                    *attn_scale = 0.1 ln(factor) + 1 (1 in the other cases)
+ * theta > 1; factor >= 1 (not read for NONE); trained_len >= 1 and
+ * 0 < low_turns < high_turns (read for LLAMA3 and YARN only); rot_dim even,
+ * at most 1024 (NTK: above 2).  Touches no device. */
+typedef enum bi_rope_scaling {
+  BI_ROPE_NONE = 0,
+  BI_ROPE_LINEAR = 1,
+  BI_ROPE_NTK = 2,
+  BI_ROPE_LLAMA3 = 3,
+  BI_ROPE_YARN = 4
+} bi_rope_scaling;
+bi_status bi_rope_frequencies(int rot_dim, double theta, bi_rope_scaling scaling, double factor,
+                              double trained_len, double low_turns, double high_turns,
+                              double* freqs, float* attn_scale);
+
+/* bi_rope_qkv with a table of frequencies, either pair arrangement and a
+ * rotation of part of the head.  qkv, pos, q, k, v as bi_rope_qkv; freqs
+ * [rot_dim / 2] double (device, 16-byte aligned; finite values, a NaN or
+ * infinity makes its pairs NaN).  For pair i < rot_dim / 2 of a query or key
+ * head, with a = pos * freqs[i], c = attn_scale cos a, s = attn_scale sin a:
+ *   interleaved = 0: x0 = x[i], x1 = x[i + rot_dim / 2];
+ *   interleaved = 1: x0 = x[2i], x1 = x[2i + 1];
+ *   y0 = x0 c - x1 s, y1 = x1 c + x0 s in their places.
+ * Elements rot_dim .. D-1 and the value heads are copied.  The angle is kept
+ * in turns as a 64-bit fraction (an error below 2^-33 turns beside that of
+ * freqs at any int32 position, negative ones included); cosine, sine and the
+ * rotation are fp32, rounded once to bf16.
+ * q, k and v must not overlap qkv or one another.
+ * Requirements: D % 16 == 0, D <= 1024, rot_dim even and at most D,
+ *   attn_scale positive and finite, T < 2^31.  Errors: as bi_rmsnorm. */
+bi_status bi_rope_qkv_scaled(const void* qkv, const int32_t* pos, int64_t T, int Hq, int Hkv,
+                             int D, int rot_dim, int interleaved, const double* freqs,
+                             float attn_scale, void* q, void* k, void* v, void* stream);
 
 /* SwiGLU product: out[t, j] = bf16(silu(g) * u), silu(g) = g / (1 + exp(-g))
  * in fp32, out [T][F] bf16, from the gate and up projections stacked in one

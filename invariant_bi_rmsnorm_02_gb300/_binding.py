@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libbi.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_BOUNDS, ERR_TIMEOUT = range(7)
 INVARIANT, VARIANT = 0, 1
+ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_LLAMA3, ROPE_YARN = range(5)   # bi_rope_scaling
 NOALLOC_SCRATCH_BYTES = 32 << 20   # BI_NOALLOC_SCRATCH_BYTES in include/bi.h
 
 __all__ = [
@@ -33,6 +34,10 @@ __all__ = [
     "bi_attn_prefill_chunk", "bi_kv_write", "bi_check_device_errors", "bi_status_string",
     "bi_version", "bi_attn_decode_noalloc", "bi_selftest_wait_timeout", "bi_add_rmsnorm",
     "bi_sample", "bi_gather_rows", "bi_rope_qkv", "bi_silu_mul", "bi_gemm_swiglu",
+    "bi_kv_write_q8", "bi_kv_read_q8", "bi_attn_decode_q8", "bi_rope_frequencies",
+    "bi_rope_qkv_scaled", "ROPE_NONE", "ROPE_LINEAR", "ROPE_NTK", "ROPE_LLAMA3", "ROPE_YARN",
+    "kv_q8_record_bytes", "kv_cache_q8", "kv_write_q8", "kv_read_q8", "attn_decode_q8",
+    "rope_frequencies", "rope_qkv_scaled",
     "NOALLOC_SCRATCH_BYTES", "rmsnorm", "add_rmsnorm", "gemm", "gemm_swiglu",
     "swiglu_interleave", "attn_decode", "attn_prefill_chunk", "kv_write", "sample",
     "gather_rows", "rope_qkv", "silu_mul", "EXPORTED_SYMBOLS",
@@ -45,6 +50,8 @@ EXPORTED_SYMBOLS = (
     "bi_attn_prefill_chunk", "bi_kv_write", "bi_check_device_errors", "bi_status_string",
     "bi_version", "bi_attn_decode_noalloc", "bi_selftest_wait_timeout", "bi_add_rmsnorm",
     "bi_sample", "bi_gather_rows", "bi_rope_qkv", "bi_silu_mul", "bi_gemm_swiglu",
+    "bi_kv_write_q8", "bi_kv_read_q8", "bi_attn_decode_q8", "bi_rope_frequencies",
+    "bi_rope_qkv_scaled",
 )
 
 
@@ -59,6 +66,7 @@ _lib = None
 
 _vp, _i64, _i32, _f32, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
                              ctypes.c_size_t)
+_f64 = ctypes.c_double
 
 
 def library_path() -> str:
@@ -106,6 +114,17 @@ def load(build_if_missing: bool = True):
             "bi_rope_qkv": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, ctypes.c_double, _vp, _vp,
                                    _vp, _vp]),
             "bi_silu_mul": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp]),
+            "bi_kv_write_q8": (_i32, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32,
+                                      _i64, _i32, _vp]),
+            "bi_kv_read_q8": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i64, _i32, _i32, _vp,
+                                     _vp, _vp, _i64, _i32, _vp]),
+            "bi_attn_decode_q8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                                         _i32, _i64, _i32, _i32, _i32, _f32, _i32, _i32, _vp, _sz,
+                                         _vp]),
+            "bi_rope_frequencies": (_i32, [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp,
+                                           ctypes.POINTER(ctypes.c_float)]),
+            "bi_rope_qkv_scaled": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _f32,
+                                          _vp, _vp, _vp, _vp]),
             "bi_check_device_errors": (_i32, [_vp]),
             "bi_selftest_wait_timeout": (_i32, [ctypes.c_uint32, _vp]),
             "bi_status_string": (ctypes.c_char_p, [_i32]),
@@ -315,6 +334,109 @@ def bi_rope_qkv(qkv, pos, Hq, Hkv, D, theta, q, k, v, stream=None):
                               _stream(stream)), "bi_rope_qkv")
 
 
+def _same_device(*tensors):
+    """The library works on the current device; a tensor of another one is
+    refused here rather than read through a foreign pointer."""
+    d = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != d:
+            raise ValueError("a tensor is on cuda:%d, the current device is cuda:%d"
+                             % (t.device.index, d))
+
+
+def _cache_q8(cache, Hkv, D):
+    if cache.dim() != 3 or tuple(cache.shape[1:]) != (Hkv, kv_q8_record_bytes(D)):
+        raise ValueError("cache must be [num_pages, %d, %d]" % (Hkv, kv_q8_record_bytes(D)))
+
+
+def bi_kv_write_q8(k_new, v_new, seq, pos, cache, block_table, stream=None):
+    """Quantise K/V rows of new tokens into the paged cache (include/bi.h)."""
+    n, Hkv, D = k_new.shape
+    if v_new.shape != k_new.shape or seq.shape != (n,) or pos.shape != (n,):
+        raise ValueError("k_new, v_new must be [n, Hkv, D] and seq, pos [n]")
+    _cache_q8(cache, Hkv, D)
+    num_seqs, max_blocks = block_table.shape
+    _same_device(k_new, v_new, seq, pos, cache, block_table)
+    _check(load().bi_kv_write_q8(
+        _ptr(k_new, torch.bfloat16, "k_new"), _ptr(v_new, torch.bfloat16, "v_new"),
+        _ptr(seq, torch.int32, "seq"), _ptr(pos, torch.int32, "pos"), n,
+        _ptr(cache, torch.uint8, "cache"), _ptr(block_table, torch.int32, "block_table"),
+        num_seqs, Hkv, D, 16, cache.shape[0], max_blocks, _stream(stream)), "bi_kv_write_q8")
+
+
+def bi_kv_read_q8(cache, block_table, kv_lens, k_out, v_out, out_table, *, max_kv_len,
+                  stream=None):
+    """Read the sequences' cached tokens back into bf16 pages (include/bi.h)."""
+    num_out, Hkv, page, D = k_out.shape
+    B = kv_lens.shape[0]
+    if v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out must have the same shape")
+    if block_table.dim() != 2 or block_table.shape[0] != B or out_table.dim() != 2 \
+            or out_table.shape[0] != B:
+        raise ValueError("block_table and out_table must be [B, blocks], kv_lens [B]")
+    _cache_q8(cache, Hkv, D)
+    _same_device(cache, block_table, kv_lens, k_out, v_out, out_table)
+    _check(load().bi_kv_read_q8(
+        _ptr(cache, torch.uint8, "cache"), _ptr(block_table, torch.int32, "block_table"),
+        _ptr(kv_lens, torch.int32, "kv_lens"), B, Hkv, D, page, cache.shape[0],
+        block_table.shape[1], int(max_kv_len), _ptr(k_out, torch.bfloat16, "k_out"),
+        _ptr(v_out, torch.bfloat16, "v_out"), _ptr(out_table, torch.int32, "out_table"), num_out,
+        out_table.shape[1], _stream(stream)), "bi_kv_read_q8")
+
+
+def bi_attn_decode_q8(q, cache, block_table, kv_lens, out, out_f32=None, *, max_kv_len,
+                      split_size, sm_scale, mode=INVARIANT, variant_splits=0, workspace=None,
+                      stream=None):
+    """Decode attention over the quantised cache (include/bi.h)."""
+    B, Hq, D = q.shape
+    Hkv = cache.shape[1]
+    _cache_q8(cache, Hkv, D)
+    if out.shape != q.shape or (out_f32 is not None and out_f32.shape != q.shape):
+        raise ValueError("out must have q's shape")
+    if block_table.dim() != 2 or block_table.shape[0] != B or kv_lens.shape != (B,):
+        raise ValueError("block_table must be [B, max_blocks] and kv_lens [B]")
+    _same_device(q, cache, block_table, kv_lens, out, out_f32, workspace)
+    wp, wb = _ws(workspace)
+    _check(load().bi_attn_decode_q8(
+        _ptr(q, torch.bfloat16, "q"), _ptr(cache, torch.uint8, "cache"),
+        _ptr(block_table, torch.int32, "block_table"), _ptr(kv_lens, torch.int32, "kv_lens"),
+        _ptr(out, torch.bfloat16, "out"), _ptr(out_f32, torch.float32, "out_f32"), B, Hq, Hkv, D,
+        16, cache.shape[0], block_table.shape[1], int(max_kv_len), int(split_size),
+        float(sm_scale), int(mode), int(variant_splits), wp, wb, _stream(stream)),
+        "bi_attn_decode_q8")
+
+
+def bi_rope_frequencies(rot_dim, theta, scaling, factor, trained_len, low_turns, high_turns,
+                        freqs):
+    """freqs (numpy float64 [rot_dim / 2], host) <- the rotation frequencies;
+    returns the factor on cosine and sine (include/bi.h)."""
+    if not isinstance(freqs, np.ndarray) or freqs.dtype != np.float64 \
+            or not freqs.flags.c_contiguous or freqs.shape != (int(rot_dim) // 2,):
+        raise TypeError("freqs must be a contiguous float64 array of rot_dim / 2 values")
+    m = ctypes.c_float()
+    _check(load().bi_rope_frequencies(int(rot_dim), float(theta), int(scaling), float(factor),
+                                      float(trained_len), float(low_turns), float(high_turns),
+                                      freqs.ctypes.data, ctypes.byref(m)), "bi_rope_frequencies")
+    return m.value
+
+
+def bi_rope_qkv_scaled(qkv, pos, Hq, Hkv, D, freqs, q, k, v, interleaved=False, attn_scale=1.0,
+                       stream=None):
+    """Rotary positions from a table of frequencies (device float64
+    [rot_dim / 2]); include/bi.h."""
+    T = qkv.shape[0]
+    if qkv.shape != (T, (Hq + 2 * Hkv) * D) or pos.shape != (T,) or freqs.dim() != 1:
+        raise ValueError("qkv must be [T, (Hq + 2 Hkv) D], pos [T] and freqs [rot_dim / 2]")
+    if q.shape != (T, Hq, D) or k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
+        raise ValueError("q, k, v must be [T, H, D]")
+    _same_device(qkv, pos, freqs, q, k, v)
+    _check(load().bi_rope_qkv_scaled(
+        _ptr(qkv, torch.bfloat16, "qkv"), _ptr(pos, torch.int32, "pos"), T, Hq, Hkv, D,
+        2 * freqs.shape[0], 1 if interleaved else 0, _ptr(freqs, torch.float64, "freqs"),
+        float(attn_scale), _ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"),
+        _ptr(v, torch.bfloat16, "v"), _stream(stream)), "bi_rope_qkv_scaled")
+
+
 def bi_silu_mul(gate_up, out, block=None, stream=None):
     """block: features per gate/up block (None: F, i.e. the gate half then
     the up half; 128: the layout bi_gemm writes with bi_gemm_swiglu's
@@ -428,6 +550,83 @@ def rope_qkv(qkv, pos, Hq, Hkv, D, theta=500000.0, stream=None):
     k = torch.empty(T, Hkv, D, dtype=qkv.dtype, device=qkv.device)
     v = torch.empty(T, Hkv, D, dtype=qkv.dtype, device=qkv.device)
     bi_rope_qkv(qkv, pos, Hq, Hkv, D, theta, q, k, v, stream)
+    return q, k, v
+
+
+def kv_q8_record_bytes(D: int) -> int:
+    """Bytes of one (page, kv head) of the quantised cache: K and V of 16
+    tokens, one byte per element, and 32 scale bytes."""
+    return 32 * D + 32
+
+
+def kv_cache_q8(num_pages, Hkv, D, device) -> torch.Tensor:
+    """A zeroed quantised cache [num_pages, Hkv, kv_q8_record_bytes(D)]."""
+    return torch.zeros(num_pages, Hkv, kv_q8_record_bytes(D), dtype=torch.uint8, device=device)
+
+
+def kv_write_q8(k_new, v_new, seq, pos, cache, block_table, stream=None):
+    bi_kv_write_q8(k_new, v_new, seq, pos, cache, block_table, stream)
+
+
+def _alloc(stream, make):
+    """make() -> tensors for a call on ``stream``: allocated in that stream's
+    order (memory freed on the current stream may still be in use there) and
+    held until the current stream, where the caller reads them, is past its
+    uses too."""
+    if stream is None:
+        return make()
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(s):
+        ts = make()
+    for t in ts:
+        if t is not None:
+            t.record_stream(here)
+    return ts
+
+
+def kv_read_q8(cache, D, block_table, kv_lens, *, max_kv_len, stream=None):
+    """The cached tokens of each sequence as bf16 pages (k, v), under the
+    cache's own page ids; every other slot is zero."""
+    k, v = _alloc(stream, lambda: [torch.zeros(cache.shape[0], cache.shape[1], 16, D,
+                                               dtype=torch.bfloat16, device=cache.device)
+                                   for _ in range(2)])
+    bi_kv_read_q8(cache, block_table, kv_lens, k, v, block_table, max_kv_len=max_kv_len,
+                  stream=stream)
+    return k, v
+
+
+def attn_decode_q8(q, cache, block_table, kv_lens, *, max_kv_len, split_size, sm_scale=None,
+                   mode=INVARIANT, variant_splits=0, want_f32=False, stream=None):
+    B, Hq, D = q.shape
+    sm_scale = D ** -0.5 if sm_scale is None else sm_scale
+    nws = bi_attn_decode_workspace_size(B, Hq, cache.shape[1], D, max_kv_len, split_size, mode,
+                                        variant_splits)
+    out, out32, ws = _alloc(stream, lambda: (
+        torch.empty_like(q),
+        torch.empty(q.shape, dtype=torch.float32, device=q.device) if want_f32 else None,
+        _workspace(nws, q.device)))
+    bi_attn_decode_q8(q, cache, block_table, kv_lens, out, out32, max_kv_len=max_kv_len,
+                      split_size=split_size, sm_scale=sm_scale, mode=mode,
+                      variant_splits=variant_splits, workspace=ws, stream=stream)
+    return (out, out32) if want_f32 else out
+
+
+def rope_frequencies(rot_dim, theta=500000.0, scaling=ROPE_NONE, factor=1.0, trained_len=8192,
+                     low_turns=1.0, high_turns=4.0, device=None):
+    """(freqs, attn_scale) of rotary positions: a float64 tensor of
+    rot_dim / 2 rotation frequencies on ``device`` (the current CUDA device
+    if None) and the factor on cosine and sine, both for rope_qkv_scaled."""
+    f = np.empty(int(rot_dim) // 2, np.float64)
+    m = bi_rope_frequencies(rot_dim, theta, scaling, factor, trained_len, low_turns, high_turns, f)
+    return torch.from_numpy(f).to("cuda" if device is None else device), m
+
+
+def rope_qkv_scaled(qkv, pos, Hq, Hkv, D, freqs, interleaved=False, attn_scale=1.0, stream=None):
+    T = qkv.shape[0]
+    q, k, v = _alloc(stream, lambda: [torch.empty(T, h, D, dtype=qkv.dtype, device=qkv.device)
+                                      for h in (Hq, Hkv, Hkv)])
+    bi_rope_qkv_scaled(qkv, pos, Hq, Hkv, D, freqs, q, k, v, interleaved, attn_scale, stream)
     return q, k, v
 
 

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <math.h>
+
 #include <mutex>
 
 #include "bi.h"
@@ -100,6 +102,21 @@ bool make_tmap_groups_bf16(CUtensorMap* map, const void* base, uint64_t rows, ui
   const cuuint32_t estr[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
                 box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+bool make_tmap_records(CUtensorMap* map, const void* base, uint64_t records, int D) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (!encode) return false;
+  const uint64_t rec = kv_q8_record_bytes(D);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), 32, records};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), rec};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
@@ -351,19 +368,19 @@ size_t bi_attn_decode_workspace_size(int B, int Hq, int Hkv, int D, int max_kv_l
   return attn_decode_workspace_bytes(B, Hq, D, ms);
 }
 
-bi_status bi_attn_decode(const void* q, const void* k_cache, const void* v_cache,
-                         const int32_t* block_table, const int32_t* kv_lens, void* out,
-                         float* out_f32, int B, int Hq, int Hkv, int D, int page_size,
-                         int64_t num_pages, int max_blocks_per_seq, int max_kv_len,
-                         int split_size, float sm_scale, bi_mode mode, int variant_splits,
-                         void* workspace, size_t workspace_bytes, void* stream) {
+static bi_status attn_decode(const void* q, const void* k_cache, const void* v_cache, bool q8,
+                             const int32_t* block_table, const int32_t* kv_lens, void* out,
+                             float* out_f32, int B, int Hq, int Hkv, int D, int page_size,
+                             int64_t num_pages, int max_blocks_per_seq, int max_kv_len,
+                             int split_size, float sm_scale, bi_mode mode, int variant_splits,
+                             void* workspace, size_t workspace_bytes, void* stream) {
   bi_status st = attn_common_checks(q, k_cache, v_cache, block_table, kv_lens, out, out_f32, B,
                                     Hq, Hkv, D, page_size, num_pages, max_blocks_per_seq,
                                     max_kv_len, split_size, mode);
   if (st != BI_OK || B == 0) return st;
   if (!scale_ok(sm_scale)) return BI_ERR_INVALID_ARG;
   AttnArgs a{};
-  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.block_table = block_table;
+  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.q8 = q8; a.block_table = block_table;
   a.kv_lens = kv_lens; a.out = out; a.out_f32 = out_f32;
   a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.page_size = page_size; a.num_pages = num_pages;
   a.max_blocks = max_blocks_per_seq; a.max_kv_len = max_kv_len; a.split_size = split_size;
@@ -385,6 +402,28 @@ bi_status bi_attn_decode(const void* q, const void* k_cache, const void* v_cache
   }
   a.ws = static_cast<float*>(workspace);
   return launch_attn_decode(a, static_cast<cudaStream_t>(stream));
+}
+
+bi_status bi_attn_decode(const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* block_table, const int32_t* kv_lens, void* out,
+                         float* out_f32, int B, int Hq, int Hkv, int D, int page_size,
+                         int64_t num_pages, int max_blocks_per_seq, int max_kv_len,
+                         int split_size, float sm_scale, bi_mode mode, int variant_splits,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  return attn_decode(q, k_cache, v_cache, false, block_table, kv_lens, out, out_f32, B, Hq, Hkv, D,
+                     page_size, num_pages, max_blocks_per_seq, max_kv_len, split_size, sm_scale,
+                     mode, variant_splits, workspace, workspace_bytes, stream);
+}
+
+bi_status bi_attn_decode_q8(const void* q, const void* cache, const int32_t* block_table,
+                            const int32_t* kv_lens, void* out, float* out_f32, int B, int Hq,
+                            int Hkv, int D, int page_size, int64_t num_pages,
+                            int max_blocks_per_seq, int max_kv_len, int split_size,
+                            float sm_scale, bi_mode mode, int variant_splits, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  return attn_decode(q, cache, cache, true, block_table, kv_lens, out, out_f32, B, Hq, Hkv, D,
+                     page_size, num_pages, max_blocks_per_seq, max_kv_len, split_size, sm_scale,
+                     mode, variant_splits, workspace, workspace_bytes, stream);
 }
 
 bi_status bi_attn_prefill_chunk(const void* q, const int32_t* cu_q, const int32_t* q_start_pos,
@@ -448,6 +487,54 @@ bi_status bi_kv_write(const void* k_new, const void* v_new, const int32_t* seq,
                          static_cast<cudaStream_t>(stream));
 }
 
+// ------------------------------------------------------- quantised KV cache
+static bi_status kv_q8_checks(int Hkv, int D, int page_size, int64_t num_pages, int max_blocks) {
+  if (Hkv <= 0 || D <= 0 || page_size <= 0 || num_pages <= 0 || max_blocks <= 0)
+    return BI_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || page_size != 16 || Hkv > 65535) return BI_ERR_UNSUPPORTED;
+  if (num_pages >= (int64_t(1) << 31) || num_pages * Hkv * page_size >= (int64_t(1) << 31))
+    return BI_ERR_UNSUPPORTED;
+  return BI_OK;
+}
+
+bi_status bi_kv_write_q8(const void* k_new, const void* v_new, const int32_t* seq,
+                         const int32_t* pos, int64_t n_tokens, void* cache,
+                         const int32_t* block_table, int num_seqs, int Hkv, int D,
+                         int page_size, int64_t num_pages, int max_blocks_per_seq,
+                         void* stream) {
+  if (n_tokens < 0 || num_seqs < 0) return BI_ERR_INVALID_ARG;
+  const bi_status st = kv_q8_checks(Hkv, D, page_size, num_pages, max_blocks_per_seq);
+  if (st != BI_OK || n_tokens == 0) return st;
+  if (n_tokens >= (int64_t(1) << 31) || n_tokens * Hkv >= (int64_t(1) << 31))
+    return BI_ERR_UNSUPPORTED;
+  if (!k_new || !v_new || !seq || !pos || !cache || !block_table) return BI_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(cache)) return BI_ERR_INVALID_ARG;
+  return launch_kv_write_q8(k_new, v_new, seq, pos, n_tokens, cache, block_table, num_seqs,
+                            Hkv, D, num_pages, max_blocks_per_seq, device_error_word(),
+                            static_cast<cudaStream_t>(stream));
+}
+
+bi_status bi_kv_read_q8(const void* cache, const int32_t* block_table, const int32_t* kv_lens,
+                        int B, int Hkv, int D, int page_size, int64_t num_pages,
+                        int max_blocks_per_seq, int max_kv_len, void* k_out, void* v_out,
+                        const int32_t* out_table, int64_t num_out_pages, int max_out_blocks,
+                        void* stream) {
+  if (B < 0 || max_kv_len < 0 || num_out_pages <= 0 || max_out_blocks <= 0)
+    return BI_ERR_INVALID_ARG;
+  const bi_status st = kv_q8_checks(Hkv, D, page_size, num_pages, max_blocks_per_seq);
+  if (st != BI_OK) return st;
+  if (B > 65535 || num_out_pages >= (int64_t(1) << 31) ||
+      num_out_pages * Hkv * page_size >= (int64_t(1) << 31))
+    return BI_ERR_UNSUPPORTED;
+  if (B == 0 || max_kv_len == 0) return BI_OK;
+  if (!cache || !block_table || !kv_lens || !k_out || !v_out || !out_table)
+    return BI_ERR_INVALID_ARG;
+  if (!aligned16(cache) || !aligned16(k_out) || !aligned16(v_out)) return BI_ERR_INVALID_ARG;
+  return launch_kv_read_q8(cache, block_table, kv_lens, B, Hkv, D, num_pages, max_blocks_per_seq,
+                           k_out, v_out, out_table, num_out_pages, max_out_blocks, max_kv_len,
+                           device_error_word(), static_cast<cudaStream_t>(stream));
+}
+
 // ------------------------------------------------------- element-wise layer ops
 bi_status bi_gather_rows(const void* src, int64_t rows, int64_t H, const int32_t* idx, int64_t n,
                          void* dst, void* stream) {
@@ -470,6 +557,72 @@ bi_status bi_rope_qkv(const void* qkv, const int32_t* pos, int64_t T, int Hq, in
     return BI_ERR_INVALID_ARG;
   return launch_rope_qkv(qkv, pos, T, Hq, Hkv, D, theta, q, k, v,
                          static_cast<cudaStream_t>(stream));
+}
+
+bi_status bi_rope_frequencies(int rot_dim, double theta, bi_rope_scaling scaling, double factor,
+                              double trained_len, double low_turns, double high_turns,
+                              double* freqs, float* attn_scale) {
+  if (rot_dim <= 0 || !freqs || !attn_scale) return BI_ERR_INVALID_ARG;
+  if (!(theta > 1.0) || !(theta < 1e300)) return BI_ERR_INVALID_ARG;
+  if (scaling < BI_ROPE_NONE || scaling > BI_ROPE_YARN) return BI_ERR_INVALID_ARG;
+  if (rot_dim % 2 != 0 || rot_dim > 1024) return BI_ERR_UNSUPPORTED;
+  if (scaling != BI_ROPE_NONE && (!(factor >= 1.0) || !(factor < 1e9))) return BI_ERR_INVALID_ARG;
+  const bool by_turns = scaling == BI_ROPE_LLAMA3 || scaling == BI_ROPE_YARN;
+  if (by_turns && (!(trained_len >= 1.0) || !(trained_len < 1e12) || !(low_turns > 0.0) ||
+                   !(high_turns > low_turns) || !(high_turns < 1e9)))
+    return BI_ERR_INVALID_ARG;
+  if (scaling == BI_ROPE_NTK && rot_dim <= 2) return BI_ERR_UNSUPPORTED;
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  const double r = rot_dim;
+  double base = theta;
+  if (scaling == BI_ROPE_NTK) base = theta * pow(factor, r / (r - 2.0));
+  // YaRN's ramp runs over the pair index between the pairs that make
+  // high_turns and low_turns turns over the trained length
+  double first = 0.0, width = 1.0;
+  if (scaling == BI_ROPE_YARN) {
+    auto pair_of = [&](double turns) {
+      return r * log(trained_len / (turns * kTwoPi)) / (2.0 * log(theta));
+    };
+    first = floor(pair_of(high_turns));
+    double last = ceil(pair_of(low_turns));
+    if (!(first > 0.0)) first = 0.0;
+    if (last > r - 1.0) last = r - 1.0;
+    width = last - first > 0.001 ? last - first : 0.001;
+  }
+  auto clamp01 = [](double x) { return x < 0.0 ? 0.0 : x > 1.0 ? 1.0 : x; };
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f = pow(base, -2.0 * i / r);
+    double keep = 1.0;  // the share of the unscaled frequency
+    if (scaling == BI_ROPE_LINEAR) keep = 0.0;
+    if (scaling == BI_ROPE_LLAMA3)
+      keep = clamp01((trained_len * f / kTwoPi - low_turns) / (high_turns - low_turns));
+    if (scaling == BI_ROPE_YARN) keep = 1.0 - clamp01((i - first) / width);
+    freqs[i] = scaling == BI_ROPE_NONE || scaling == BI_ROPE_NTK
+                   ? f
+                   : (1.0 - keep) * f / factor + keep * f;
+  }
+  *attn_scale =
+      scaling == BI_ROPE_YARN ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.0f;
+  return BI_OK;
+}
+
+bi_status bi_rope_qkv_scaled(const void* qkv, const int32_t* pos, int64_t T, int Hq, int Hkv,
+                             int D, int rot_dim, int interleaved, const double* freqs,
+                             float attn_scale, void* q, void* k, void* v, void* stream) {
+  if (T < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || rot_dim <= 0 || rot_dim > D)
+    return BI_ERR_INVALID_ARG;
+  if (!(attn_scale > 0.0f) || !(attn_scale <= 3.4e38f)) return BI_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return BI_ERR_INVALID_ARG;
+  if (D % 16 != 0 || D > 1024 || rot_dim % 2 != 0 || Hq > 65535 || Hkv > 65535 ||
+      Hq + 2 * Hkv > 65535)
+    return BI_ERR_UNSUPPORTED;
+  if (T >= (int64_t(1) << 31)) return BI_ERR_UNSUPPORTED;
+  if (T == 0) return BI_OK;
+  if (!qkv || !pos || !freqs || !q || !k || !v) return BI_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(freqs) || !aligned16(q) || !aligned16(k) || !aligned16(v))
+    return BI_ERR_INVALID_ARG;
+  return launch_rope_qkv_scaled(qkv, pos, T, Hq, Hkv, D, rot_dim, interleaved != 0, freqs,
+                                attn_scale, q, k, v, static_cast<cudaStream_t>(stream));
 }
 
 bi_status bi_silu_mul(const void* gate_up, int64_t T, int64_t F, int64_t block, void* out,

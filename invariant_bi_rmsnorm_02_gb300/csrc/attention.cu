@@ -54,6 +54,7 @@
 
 #include "bi_internal.h"
 #include "device_common.cuh"
+#include "e4m3.cuh"
 #include "tcgen05.cuh"
 
 namespace bi {
@@ -78,6 +79,27 @@ template <int D>
 __device__ __forceinline__ uint32_t tile_off(int n, int d) {
   const int p = n >> 4, r = n & 15, hf = d >> 6, chunk = (d & 63) >> 3;
   return (uint32_t)((p * TileGeom<D>::kHalves + hf) * 2048 + r * 128 + ((chunk ^ (r & 7)) << 4));
+}
+
+// A tile of 64 keys of the quantised cache in shared memory: four pages of
+// K[16][D] then V[16][D] e4m3 bytes (one TMA box each, 16-byte chunks
+// swizzled within the rows), then the pages' 32 scale bytes (16 of K, 16 of
+// V).  Half a bf16 tile, so about twice the blocks fit on an SM.
+template <int D>
+struct Q8Geom {
+  static constexpr int kRecord = kv_q8_record_bytes(D);
+  static constexpr int kPageBytes = 32 * D;
+  static constexpr int kScales = kPagesPerTile * kPageBytes;  // offset of the scale bytes
+  static constexpr int kBufBytes = kScales + 1024;  // the next buffer stays 1024-byte aligned
+};
+
+// byte offset of 16-byte chunk c of key n's K row (V: 16 D further on): the
+// 128-byte swizzle for rows of 128 bytes, the 64-byte one for rows of 64
+template <int D>
+__device__ __forceinline__ uint32_t q8_off(int n, int c) {
+  const int r = n & 15;
+  const int x = D == 128 ? (r & 7) : ((r >> 1) & 3);
+  return (uint32_t)((n >> 4) * Q8Geom<D>::kPageBytes + r * D + ((c ^ x) << 4));
 }
 
 // 2^x on the special function unit (ex2.approx.ftz: relative error about
@@ -154,6 +176,27 @@ __device__ __forceinline__ void load_q_frags(uint32_t (&qf)[NQ][D / 16][2],
     }
 }
 
+// The same for keys read from the quantised cache: a k-step's 16 elements of
+// a key come as 4 bytes per thread (d = 4t .. 4t+3 for t = lane % 4), whose
+// even bytes take the k positions 2t, 2t+1 of the MMA and whose odd bytes
+// 2t+8, 2t+9.  Q is put in the same order; the sum over a k-step does not
+// depend on the order inside it (checked byte for byte against the bf16
+// kernel by the tests).
+template <int D, int NQ>
+__device__ __forceinline__ void load_q_frags_q8(uint32_t (&qf)[NQ][D / 16][2],
+                                                const __nv_bfloat16* qs) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const uint2 x =
+          *reinterpret_cast<const uint2*>(qs + (8 * nq + g) * D + 16 * ks + 4 * t);
+      qf[nq][ks][0] = __byte_perm(x.x, x.y, 0x5410);
+      qf[nq][ks][1] = __byte_perm(x.x, x.y, 0x7632);
+    }
+}
+
 // P = hi + lo: the probabilities of keys k, k+1 as two bf16 pairs (key k in
 // the low half).  hi is p with its low 16 bits cleared (bf16 by truncation),
 // lo the exact remainder p - hi truncated the same way, so hi + lo keeps 16
@@ -204,10 +247,16 @@ constexpr float kRescaleLog2 = 8.0f;
 // One tile of 64 keys (absolute indices key0 .. key0+63).  Query column
 // (nq, cc) sees key k iff lo <= k < hi[nq][cc].  A column that sees no key
 // of the tile is left exactly as it was.
-template <int D, int NQ>
+// kQ8: the tile is one of the quantised cache; every element becomes the
+// bf16 value that reading the cache back gives, so the arithmetic is that of
+// the bf16 kernel on the cache read back.  `scales` is then the tile's scale
+// bytes and vbase is not used; rows d of o come in the order 2g, 2g+1
+// (d_of_row below) because an e4m3 pair shares a 16-bit element of the
+// transposing load.
+template <int D, int NQ, bool kQ8>
 __device__ __forceinline__ void tile_step(SplitState<D, NQ>& st,
                                           const uint32_t (&qf)[NQ][D / 16][2], uint32_t kbase,
-                                          uint32_t vbase, int key0, int lo,
+                                          uint32_t vbase, const uint8_t* scales, int key0, int lo,
                                           const int (&hi)[NQ][2], float scale_log2) {
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, mi = lane >> 3, r8 = lane & 7;
@@ -217,15 +266,38 @@ __device__ __forceinline__ void tile_step(SplitState<D, NQ>& st,
   for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) s[mt][nq][0] = s[mt][nq][1] = s[mt][nq][2] = s[mt][nq][3] = 0.0f;
+  if constexpr (kQ8) {
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt)
+    for (int mt = 0; mt < 4; ++mt) {
+      // factors of keys 16 mt + g and 16 mt + g + 8
+      const uint32_t f0 = q8_factor2(scales[32 * mt + g]);
+      const uint32_t f1 = q8_factor2(scales[32 * mt + 8 + g]);
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t a[4];
-      ldsm_x4(kbase + tile_off<D>(16 * mt + r8 + 8 * (mi & 1), 16 * ks + 8 * (mi >> 1)), a);
+      for (int kp = 0; kp < D / 32; ++kp) {
+        uint32_t r[4];  // keys g and g + 8 of k-steps 2 kp and 2 kp + 1
+        ldsm_x4(kbase + q8_off<D>(16 * mt + r8 + 8 * (mi & 1), 2 * kp + (mi >> 1)), r);
 #pragma unroll
-      for (int nq = 0; nq < NQ; ++nq) mma_bf16(s[mt][nq], a, qf[nq][ks][0], qf[nq][ks][1]);
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t a[4] = {
+              mul_bf16x2(e4m3_even(r[2 * u]), f0), mul_bf16x2(e4m3_even(r[2 * u + 1]), f1),
+              mul_bf16x2(e4m3_odd(r[2 * u]), f0), mul_bf16x2(e4m3_odd(r[2 * u + 1]), f1)};
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq)
+            mma_bf16(s[mt][nq], a, qf[nq][2 * kp + u][0], qf[nq][2 * kp + u][1]);
+        }
+      }
     }
+  } else {
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t a[4];
+        ldsm_x4(kbase + tile_off<D>(16 * mt + r8 + 8 * (mi & 1), 16 * ks + 8 * (mi >> 1)), a);
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) mma_bf16(s[mt][nq], a, qf[nq][ks][0], qf[nq][ks][1]);
+      }
+  }
   // ---- mask, column max of the raw scores, scaled once: rounding is
   // monotone, so RN(max s * c) = max RN(s * c) for the positive scale c
   float mx[NQ][2];
@@ -310,17 +382,47 @@ __device__ __forceinline__ void tile_step(SplitState<D, NQ>& st,
         bh[nq][half] = transpose8x8(hp);
         bl[nq][half] = transpose8x8(lp);
       }
+    if constexpr (kQ8) {
+      // factors of keys 16 kk + 2t, + 1 and of 16 kk + 8 + 2t, + 1
+      const int t = lane & 3;
+      const uint8_t* sv = scales + 32 * kk + 16 + 2 * t;
+      const uint32_t f0 = q8_factors(*reinterpret_cast<const uint16_t*>(sv));
+      const uint32_t f1 = q8_factors(*reinterpret_cast<const uint16_t*>(sv + 8));
 #pragma unroll
-    for (int md = 0; md < D / 16; ++md) {
-      uint32_t a[4];
-      ldsm_x4_t(vbase + tile_off<D>(16 * kk + r8 + 8 * (mi >> 1), 16 * md + 8 * (mi & 1)), a);
+      for (int mp = 0; mp < D / 32; ++mp) {
+        uint32_t r[4];  // key pairs 2t and 8 + 2t of columns 2g, 2g+1 of chunks 2 mp, 2 mp + 1
+        ldsm_x4_t(kbase + 16 * D + q8_off<D>(16 * kk + r8 + 8 * (mi & 1), 2 * mp + (mi >> 1)), r);
 #pragma unroll
-      for (int nq = 0; nq < NQ; ++nq) {
-        mma_bf16(st.o[md][nq], a, bh[nq][0], bh[nq][1]);
-        mma_bf16(st.o[md][nq], a, bl[nq][0], bl[nq][1]);
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t a[4] = {
+              mul_bf16x2(e4m3_even(r[2 * u]), f0), mul_bf16x2(e4m3_odd(r[2 * u]), f0),
+              mul_bf16x2(e4m3_even(r[2 * u + 1]), f1), mul_bf16x2(e4m3_odd(r[2 * u + 1]), f1)};
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq) {
+            mma_bf16(st.o[2 * mp + u][nq], a, bh[nq][0], bh[nq][1]);
+            mma_bf16(st.o[2 * mp + u][nq], a, bl[nq][0], bl[nq][1]);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int md = 0; md < D / 16; ++md) {
+        uint32_t a[4];
+        ldsm_x4_t(vbase + tile_off<D>(16 * kk + r8 + 8 * (mi >> 1), 16 * md + 8 * (mi & 1)), a);
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+          mma_bf16(st.o[md][nq], a, bh[nq][0], bh[nq][1]);
+          mma_bf16(st.o[md][nq], a, bl[nq][0], bl[nq][1]);
+        }
       }
     }
   }
+}
+
+// The column d of o[md][.][2 hh + cc] of a thread with lane / 4 = g.
+template <bool kQ8>
+__device__ __forceinline__ int d_of_row(int md, int g, int hh) {
+  return kQ8 ? 16 * md + 2 * g + hh : 16 * md + g + 8 * hh;
 }
 
 // Log-sum-exp merge of partial (mb, lb, ob) into (m, l, o), in that order.
@@ -356,6 +458,29 @@ __device__ __forceinline__ void issue_pages(uint8_t* buf, uint64_t* bar, const C
     tma_load_3d_hint(buf + off, km, 0, y, 0, bar, pol);
     tma_load_3d_hint(buf + TileGeom<D>::kKBytes + off, vm, 0, y, 0, bar, pol);
   }
+}
+
+// Issue the copies of a quantised tile's first np pages, one page per lane:
+// its K and V rows in one box, its scale bytes behind them.
+template <int D>
+__device__ __forceinline__ void issue_records(uint8_t* buf, uint64_t* bar, const CUtensorMap* map,
+                                              const uint8_t* cache, int pid, int p, int np,
+                                              int Hkv, int h) {
+  if (p >= np) return;
+  const uint64_t pol = l2_policy_evict_first();
+  const int64_t rec = (int64_t)pid * Hkv + h;
+  tma_load_3d_hint(buf + p * Q8Geom<D>::kPageBytes, map, 0, 0, (int)rec, bar, pol);
+  bulk_load(buf + Q8Geom<D>::kScales + 32 * p,
+            cache + rec * Q8Geom<D>::kRecord + Q8Geom<D>::kPageBytes, 32, bar);
+}
+
+// The V scale bytes of keys >= limit in a landed quantised tile become 0:
+// unwritten slots may hold any bits, and an element's magnitude is finite
+// whatever its bits, so a finite factor is enough for 0 * v to be 0.
+template <int D>
+__device__ __forceinline__ void clear_v_scales(uint8_t* buf, int key0, int limit, int lane) {
+  for (int n = max(limit - key0, 0) + lane; n < kTile; n += 32)
+    buf[Q8Geom<D>::kScales + 32 * (n >> 4) + 16 + (n & 15)] = 0;
 }
 
 __device__ __forceinline__ int pages_below(int key0, int limit) {
@@ -414,6 +539,7 @@ struct KernelParams {
   int64_t num_pages;
   float scale_log2;
   bool variant;
+  const uint8_t* cache_q8;  // decode over the quantised cache: its records
 };
 
 __device__ __forceinline__ bool len_ok(int L, const KernelParams& p) {
@@ -558,15 +684,17 @@ __device__ __forceinline__ int unit_tiles(int4 d) {  // {b, j, lo, hi}
 // limits residency: the bound lets ptxas keep the whole tile step in
 // registers instead of its default for this block size, which measurably
 // starved the G <= 8 instantiation.
-template <int D, int NQ>
+template <int D, int NQ, bool kQ8>
 __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
     const KernelParams p) {
+  constexpr int kBufBytes = kQ8 ? Q8Geom<D>::kBufBytes : TileGeom<D>::kBufBytes;
+  constexpr int kPageTx = kQ8 ? Q8Geom<D>::kRecord : 2 * TileGeom<D>::kPageBytes;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* bufs = smem;  // 2 tile buffers
-  __nv_bfloat16* qbuf = reinterpret_cast<__nv_bfloat16*>(smem + 2 * TileGeom<D>::kBufBytes);
+  __nv_bfloat16* qbuf = reinterpret_cast<__nv_bfloat16*>(smem + 2 * kBufBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(qbuf + 2 * 8 * NQ * D);  // [2]
   uint64_t* empty = full + 2;                                            // [2]
   uint64_t* ready = empty + 2;                                           // [kQueue]
@@ -798,13 +926,19 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
                                                         (first >> 4) + idx];
         }
         if (lane == 0) {
-          uint8_t* buf = bufs + rs * TileGeom<D>::kBufBytes;
+          uint8_t* buf = bufs + rs * kBufBytes;
           const uint32_t qbytes = lt == 0 ? (uint32_t)(G * D * 2) : 0u;
-          mbar_arrive_expect_tx(&full[rs], np * 2 * TileGeom<D>::kPageBytes + qbytes);
+          mbar_arrive_expect_tx(&full[rs], np * kPageTx + qbytes);
           if (lt == 0)
             bulk_load(qbuf + (q_issued & 1) * 8 * NQ * D,
                       p.q + ((int64_t)d.x * p.Hq + (int64_t)h * G) * D, qbytes, &full[rs]);
-          issue_pages<D>(buf, &full[rs], &kmap, &vmap, pid, np, Hkv, h);
+          if constexpr (!kQ8) issue_pages<D>(buf, &full[rs], &kmap, &vmap, pid, np, Hkv, h);
+        }
+        if constexpr (kQ8) {
+          __syncwarp();  // the expected bytes are set before any copy completes
+          const int mine = lane == 0 ? pid[0] : lane == 1 ? pid[1] : lane == 2 ? pid[2] : pid[3];
+          issue_records<D>(bufs + rs * kBufBytes, &full[rs], &kmap, p.cache_q8, mine, lane, np,
+                           Hkv, h);
         }
         if (lt == 0) ++q_issued;
         ++n_issued;
@@ -867,20 +1001,27 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
         alive = false;
         break;
       }
-      uint8_t* buf = bufs + rs * TileGeom<D>::kBufBytes;
+      uint8_t* buf = bufs + rs * kBufBytes;
       if (ti == 0) {
-        load_q_frags<D, NQ>(qf, qbuf + (q_used & 1) * 8 * NQ * D, D);
+        const __nv_bfloat16* qs = qbuf + (q_used & 1) * 8 * NQ * D;
+        if constexpr (kQ8)
+          load_q_frags_q8<D, NQ>(qf, qs);
+        else
+          load_q_frags<D, NQ>(qf, qs, D);
         ++q_used;
         st.reset();
       }
       const int key0 = first + ti * kTile;
       const bool tail = key0 + kTile > hi;
       if (tail) {
-        clear_v_tail<D>(buf, key0, hi, lane, 32);
+        if constexpr (kQ8)
+          clear_v_scales<D>(buf, key0, hi, lane);
+        else
+          clear_v_tail<D>(buf, key0, hi, lane, 32);
         __syncwarp();
       }
-      tile_step<D, NQ>(st, qf, smem_u32(buf), smem_u32(buf + TileGeom<D>::kKBytes), key0, lo,
-                       hcol, p.scale_log2);
+      tile_step<D, NQ, kQ8>(st, qf, smem_u32(buf), smem_u32(buf + TileGeom<D>::kKBytes),
+                            buf + Q8Geom<D>::kScales, key0, lo, hcol, p.scale_log2);
       ++n_done;
       // the buffer goes back to the producer; the rows this warp zeroed are
       // ordered before the copy that will overwrite them
@@ -907,7 +1048,7 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
             const float ov = helper ? o_odd : st.o[md][0][2 * hh];
             if (col < G) {
               const float v = lv > 0.0f ? normalize(ov, inv_l(lv)) : 0.0f;
-              const int64_t idx = orow + 16 * md + g + 8 * hh;
+              const int64_t idx = orow + d_of_row<kQ8>(md, g, hh);
               static_cast<__nv_bfloat16*>(p.out)[idx] = __float2bfloat16_rn(v);
               if (p.out_f32) p.out_f32[idx] = v;
             }
@@ -927,7 +1068,7 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               const float v = lv > 0.0f ? normalize(st.o[md][nq][2 * hh + cc], inv_l(lv)) : 0.0f;
-              const int64_t idx = orow + 16 * md + g + 8 * hh;
+              const int64_t idx = orow + d_of_row<kQ8>(md, g, hh);
               static_cast<__nv_bfloat16*>(p.out)[idx] = __float2bfloat16_rn(v);
               if (p.out_f32) p.out_f32[idx] = v;
             }
@@ -949,8 +1090,8 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
         float* orow = p.o + ((row0 + col) * p.max_splits + j) * D;
 #pragma unroll
         for (int md = 0; md < D / 16; ++md) {
-          orow[16 * md + g] = st.o[md][nq][cc];
-          orow[16 * md + g + 8] = st.o[md][nq][2 + cc];
+          orow[d_of_row<kQ8>(md, g, 0)] = st.o[md][nq][cc];
+          orow[d_of_row<kQ8>(md, g, 1)] = st.o[md][nq][2 + cc];
         }
       }
   }
@@ -1742,9 +1883,9 @@ __global__ void kv_write_kernel(const uint4* __restrict__ k_new, const uint4* __
   }
 }
 
-template <int D, int NQ>
+template <int D, int NQ, bool kQ8>
 size_t decode_smem() {  // ring, q buffers, barriers (full, empty: 2 each; ready, free)
-  return 1024 + 2 * TileGeom<D>::kBufBytes + 2 * 8 * NQ * D * 2 + (4 + 2 * kQueue) * 8;
+  return 1024 + 2 * (kQ8 ? Q8Geom<D>::kBufBytes : TileGeom<D>::kBufBytes) + 2 * 8 * NQ * D * 2 + (4 + 2 * kQueue) * 8;
 }
 KernelParams make_params(const AttnArgs& a) {
   KernelParams p{};
@@ -1826,12 +1967,19 @@ DecodeWs decode_ws_layout(int B, int Hq, int D, int max_splits) {
   return w;
 }
 
-template <int D, int NQ>
+template <int D, int NQ, bool kQ8>
 bi_status decode_impl(const AttnArgs& a, cudaStream_t s) {
   KernelParams p = make_params(a);
   if (a.max_splits > 0) {
     CUtensorMap km, vm;
-    if (!make_kv_page_maps(a, &km, &vm)) return BI_ERR_CUDA;
+    if constexpr (kQ8) {
+      if (!make_tmap_records(&km, a.k_cache, static_cast<uint64_t>(a.num_pages) * a.Hkv, D))
+        return BI_ERR_CUDA;
+      vm = km;
+      p.cache_q8 = static_cast<const uint8_t*>(a.k_cache);
+    } else {
+      if (!make_kv_page_maps(a, &km, &vm)) return BI_ERR_CUDA;
+    }
     const DecodeWs w = decode_ws_layout(a.B, a.Hq, a.D, a.max_splits);
     char* base = reinterpret_cast<char*>(a.ws);
     p.unit_count = reinterpret_cast<int*>(base);
@@ -1841,12 +1989,12 @@ bi_status decode_impl(const AttnArgs& a, cudaStream_t s) {
     p.ml_stride = w.ml_stride;
     p.local_plan = a.B <= kLocalPlanMax;
     if (p.local_plan) p.order = reinterpret_cast<int2*>(base + w.units_off);  // units unused
-    const size_t sm = decode_smem<D, NQ>();
-    if (set_smem(attn_decode_split_kernel<D, NQ>, sm) != cudaSuccess) return BI_ERR_CUDA;
+    const size_t sm = decode_smem<D, NQ, kQ8>();
+    if (set_smem(attn_decode_split_kernel<D, NQ, kQ8>, sm) != cudaSuccess) return BI_ERR_CUDA;
     static int per_sm[2][3] = {};
     int& occ = per_sm[D == 128][NQ];
     if (occ == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                        &occ, attn_decode_split_kernel<D, NQ>, kSplitThreads, sm) !=
+                        &occ, attn_decode_split_kernel<D, NQ, kQ8>, kSplitThreads, sm) !=
                         cudaSuccess)
       return BI_ERR_CUDA;
     const int sms = device_sm_count();
@@ -1859,7 +2007,7 @@ bi_status decode_impl(const AttnArgs& a, cudaStream_t s) {
     p.target_units = static_cast<int>(4 * cap);
     if (!p.local_plan) attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
     const int grid = static_cast<int>(max_units < cap ? max_units : cap);
-    if (launch_pdl(attn_decode_split_kernel<D, NQ>, dim3(grid), dim3(kSplitThreads), sm, s, km,
+    if (launch_pdl(attn_decode_split_kernel<D, NQ, kQ8>, dim3(grid), dim3(kSplitThreads), sm, s, km,
                    vm, p) !=
         cudaSuccess)
       return BI_ERR_CUDA;
@@ -2001,8 +2149,15 @@ size_t attn_decode_workspace_bytes(int B, int Hq, int D, int max_splits) {
 
 bi_status launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
   const int G = a.Hq / a.Hkv;
-  if (a.D == 64) return G <= 8 ? decode_impl<64, 1>(a, s) : decode_impl<64, 2>(a, s);
-  if (a.D == 128) return G <= 8 ? decode_impl<128, 1>(a, s) : decode_impl<128, 2>(a, s);
+  if (a.q8) {
+    if (a.D == 64) return G <= 8 ? decode_impl<64, 1, true>(a, s) : decode_impl<64, 2, true>(a, s);
+    if (a.D == 128)
+      return G <= 8 ? decode_impl<128, 1, true>(a, s) : decode_impl<128, 2, true>(a, s);
+    return BI_ERR_UNSUPPORTED;
+  }
+  if (a.D == 64) return G <= 8 ? decode_impl<64, 1, false>(a, s) : decode_impl<64, 2, false>(a, s);
+  if (a.D == 128)
+    return G <= 8 ? decode_impl<128, 1, false>(a, s) : decode_impl<128, 2, false>(a, s);
   return BI_ERR_UNSUPPORTED;
 }
 

@@ -31,6 +31,15 @@ bool make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64
 bool make_tmap_groups_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                            uint32_t box_rows, uint32_t box_groups);
 
+// Encode a tensor map over the quantised cache's page records: per record 32
+// rows (16 of K, 16 of V) of D bytes, records kv_q8_record_bytes(D) apart, a
+// box of one record's rows, swizzled over the row's width (128 or 64 bytes).
+bool make_tmap_records(CUtensorMap* map, const void* base, uint64_t records, int D);
+
+// Bytes of one (page, kv head) of the quantised cache: K[16][D], V[16][D],
+// then 16 scale bytes of K and 16 of V.
+constexpr int kv_q8_record_bytes(int D) { return 32 * D + 32; }
+
 inline bi_status cuda_status(cudaError_t e) { return e == cudaSuccess ? BI_OK : BI_ERR_CUDA; }
 
 // ---- RMSNorm (rmsnorm.cu) ---------------------------------------------------
@@ -44,6 +53,9 @@ bi_status launch_gather_rows(const void* src, int64_t rows, int64_t H, const int
                              int64_t n, void* dst, int* err, cudaStream_t s);
 bi_status launch_rope_qkv(const void* qkv, const int32_t* pos, int64_t T, int Hq, int Hkv, int D,
                           double theta, void* q, void* k, void* v, cudaStream_t s);
+bi_status launch_rope_qkv_scaled(const void* qkv, const int32_t* pos, int64_t T, int Hq, int Hkv,
+                                 int D, int rot_dim, bool interleaved, const double* freqs,
+                                 float attn_scale, void* q, void* k, void* v, cudaStream_t s);
 bi_status launch_silu_mul(const void* gu, int64_t T, int64_t F, int64_t block, void* out,
                           cudaStream_t s);
 bi_status launch_sample(const void* logits, int64_t B, int64_t V, const float* temperature,
@@ -119,6 +131,7 @@ struct AttnArgs {
   int split_count;            // variant: fixed split count (decode)
   bool variant;
   float sm_scale;
+  bool q8;                    // decode: k_cache holds the quantised records
   float* ws;                  // decode partials
   int max_splits;             // decode: partial slots per (b, q-head)
   int* err;
@@ -128,6 +141,14 @@ int attn_variant_split_count(int B, int Hkv, int max_kv_len, int num_sms);
 size_t attn_decode_workspace_bytes(int B, int Hq, int D, int max_splits);
 bi_status launch_attn_decode(const AttnArgs& a, cudaStream_t s);
 bi_status launch_attn_prefill(const AttnArgs& a, cudaStream_t s);
+bi_status launch_kv_write_q8(const void* k_new, const void* v_new, const int32_t* seq,
+                             const int32_t* pos, int64_t n_tokens, void* cache,
+                             const int32_t* block_table, int num_seqs, int Hkv, int D,
+                             int64_t num_pages, int max_blocks, int* err, cudaStream_t s);
+bi_status launch_kv_read_q8(const void* cache, const int32_t* block_table, const int32_t* kv_lens,
+                            int B, int Hkv, int D, int64_t num_pages, int max_blocks, void* k_out,
+                            void* v_out, const int32_t* out_table, int64_t num_out_pages,
+                            int max_out_blocks, int max_kv_len, int* err, cudaStream_t s);
 bi_status launch_kv_write(const void* k_new, const void* v_new, const int32_t* seq,
                           const int32_t* pos, int64_t n_tokens, void* k_cache, void* v_cache,
                           const int32_t* block_table, int Hkv, int D, int page_size,

@@ -1,0 +1,213 @@
+// cache_q8.cu -- the quantised paged KV cache: K/V rows of new tokens
+// quantised as they are written, and cached pages read back as bf16.
+//
+// One scale per row (token, kv head, K or V): the least power of two, within
+// 2^-124 .. 2^7, that brings the row's largest magnitude to 448 or less (the
+// largest e4m3 number).  A power of two costs nothing against a general scale
+// (e4m3's relative step is the same in every binade) and makes every stored
+// value exact in bf16, so the attention on this cache is the bf16 attention
+// on the pages read back, bit for bit.  Each row is a function of its own
+// elements only, whatever the batch around it.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "bi_internal.h"
+#include "device_common.cuh"
+#include "e4m3.cuh"
+
+namespace bi {
+namespace {
+
+constexpr int kPage = 16;
+constexpr int kThreads = 256;
+constexpr unsigned kFull = 0xffffffffu;
+
+// ------------------------------------------------------------------ write
+// D/8 lanes per row, 16 bytes of bf16 each; rows in the order (token, head,
+// K then V).
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_write_q8_kernel(
+    const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+    const int32_t* __restrict__ seq, const int32_t* __restrict__ pos, int64_t rows, int Hkv,
+    uint8_t* __restrict__ cache, const int32_t* __restrict__ bt, int num_seqs, int64_t num_pages,
+    int max_blocks, int* err) {
+  constexpr int kLanes = D / 8;
+  const int64_t row = (blockIdx.x * (int64_t)kThreads + threadIdx.x) / kLanes;
+  const int c = threadIdx.x % kLanes;
+  const int64_t rr = row < rows ? row : rows - 1;
+  const bool is_v = rr & 1;
+  const int64_t th = rr >> 1;  // token * Hkv + head
+  const int64_t tok = th / Hkv;
+  const int h = (int)(th - tok * Hkv);
+  const uint4 x = (is_v ? v_new : k_new)[th * kLanes + c];
+  const int s = seq[tok], ps = pos[tok];
+  int64_t page = -1;
+  if (s >= 0 && s < num_seqs && ps >= 0 && ps < max_blocks * (int64_t)kPage)
+    page = bt[(int64_t)s * max_blocks + ps / kPage];
+  const bool ok = page >= 0 && page < num_pages;
+  // the largest magnitude bits of the row: bf16 magnitudes order as integers
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+#pragma unroll
+  for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+  if (row >= rows) return;
+  if (!ok) {
+    if (c == 0) record_error(err, BI_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  // least e with amax 2^-e <= 448 = 1.75 * 2^8
+  int e = kQ8MinExp;
+  if (top >= 0x80) {  // a normal number: 1.f * 2^(exponent - 127)
+    e = (int)(top >> 7) - 127 - 8 + ((top & 0x7f) > 0x60 ? 1 : 0);
+    e = max(kQ8MinExp, min(kQ8MaxExp, e));
+  }
+  const bool fine = top < 0x7f80;
+  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+  uint32_t q[2] = {0, 0};
+  if (fine) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = make_float2(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+      const uint32_t p = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+      q[i >> 1] |= p << (16 * (i & 1));
+    }
+  }
+  uint8_t* rec = cache + (page * Hkv + h) * kv_q8_record_bytes(D);
+  const int slot = ps % kPage;
+  *reinterpret_cast<uint2*>(rec + (is_v ? kPage * D : 0) + slot * D + 8 * c) =
+      make_uint2(q[0], q[1]);
+  if (c == 0)
+    rec[2 * kPage * D + (is_v ? kPage : 0) + slot] = (uint8_t)(fine ? e + kQ8ScaleBias : kQ8NonFinite);
+}
+
+// ------------------------------------------------------------------- read
+// One warp per (page, kv head) of the batch's pages: the warp finds its pages
+// from a running sum of the sequences' page counts.
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_read_q8_kernel(
+    const uint8_t* __restrict__ cache, const int32_t* __restrict__ bt,
+    const int32_t* __restrict__ kv_lens, int B, int Hkv, int64_t num_pages, int max_blocks,
+    __nv_bfloat16* __restrict__ k_out, __nv_bfloat16* __restrict__ v_out,
+    const int32_t* __restrict__ out_bt, int64_t num_out, int max_out_blocks, int max_kv_len,
+    int* err) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  int64_t u = (blockIdx.x * (int64_t)kThreads + threadIdx.x) / 32;  // this warp's next unit
+  int64_t base = 0;                                                 // units before the slab
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int bl = b0 + lane;
+    int L = bl < B ? kv_lens[bl] : 0;
+    if (L < 0 || L > max_kv_len || L > max_blocks * (int64_t)kPage ||
+        L > max_out_blocks * (int64_t)kPage) {
+      record_error(err, BI_ERR_DEVICE_BOUNDS);
+      L = 0;
+    }
+    const int64_t mine = (int64_t)((L + kPage - 1) / kPage) * Hkv;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const int64_t total = __shfl_sync(kFull, incl, 31);
+    for (; u < base + total; u += warps) {
+      const int64_t r = u - base;
+      const int w = __popc(__ballot_sync(kFull, incl <= r));
+      const int64_t in_seq = r - __shfl_sync(kFull, incl - mine, w);
+      const int len = __shfl_sync(kFull, L, w);
+      const int j = (int)(in_seq / Hkv), h = (int)(in_seq - (int64_t)j * Hkv);
+      const int64_t b = b0 + w;
+      const int64_t page = bt[b * max_blocks + j], outp = out_bt[b * max_out_blocks + j];
+      if (page < 0 || page >= num_pages || outp < 0 || outp >= num_out) {
+        if (lane == 0) record_error(err, BI_ERR_DEVICE_BOUNDS);
+        continue;
+      }
+      const uint8_t* rec = cache + (page * Hkv + h) * kv_q8_record_bytes(D);
+      const uint32_t scale = rec[2 * kPage * D + lane];
+      const int64_t out = (outp * Hkv + h) * kPage * D;
+      const int valid = min(kPage, len - j * kPage);
+      constexpr int kChunks = 2 * kPage * D / 16 / 32;  // 16-byte chunks per lane
+      uint4 x[kChunks];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i)
+        x[i] = reinterpret_cast<const uint4*>(rec)[32 * i + lane];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = 32 * i + lane;
+        const int row = c / (D / 16);  // 0..15 of K, then of V
+        const uint32_t f = q8_factor2(__shfl_sync(kFull, scale, row));
+        if ((row & 15) >= valid) continue;
+        const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t ev = mul_bf16x2(e4m3_even(in[k]), f), od = mul_bf16x2(e4m3_odd(in[k]), f);
+          o[2 * k] = __byte_perm(ev, od, 0x5410);
+          o[2 * k + 1] = __byte_perm(ev, od, 0x7632);
+        }
+        uint4* dst = reinterpret_cast<uint4*>((row < 16 ? k_out : v_out) + out + (row & 15) * D +
+                                              (c % (D / 16)) * 16);
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    }
+    base += total;
+  }
+}
+
+template <int D>
+bi_status write_impl(const void* k_new, const void* v_new, const int32_t* seq, const int32_t* pos,
+                     int64_t n_tokens, void* cache, const int32_t* bt, int num_seqs, int Hkv,
+                     int64_t num_pages, int max_blocks, int* err, cudaStream_t s) {
+  const int64_t rows = n_tokens * Hkv * 2;
+  const int64_t blocks = (rows * (D / 8) + kThreads - 1) / kThreads;
+  kv_write_q8_kernel<D><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
+      static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), seq, pos, rows, Hkv,
+      static_cast<uint8_t*>(cache), bt, num_seqs, num_pages, max_blocks, err);
+  return cuda_status(cudaGetLastError());
+}
+
+template <int D>
+bi_status read_impl(const void* cache, const int32_t* bt, const int32_t* kv_lens, int B, int Hkv,
+                    int64_t num_pages, int max_blocks, void* k_out, void* v_out,
+                    const int32_t* out_bt, int64_t num_out, int max_out_blocks, int max_kv_len,
+                    int* err, cudaStream_t s) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return BI_ERR_CUDA;
+  const int64_t most = static_cast<int64_t>(B) * ((max_kv_len + kPage - 1) / kPage) * Hkv;
+  const int64_t want = (most + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t cap = static_cast<int64_t>(sms) * 4;
+  kv_read_q8_kernel<D><<<static_cast<unsigned>(want < cap ? want : cap), kThreads, 0, s>>>(
+      static_cast<const uint8_t*>(cache), bt, kv_lens, B, Hkv, num_pages, max_blocks,
+      static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), out_bt, num_out,
+      max_out_blocks, max_kv_len, err);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+bi_status launch_kv_write_q8(const void* k_new, const void* v_new, const int32_t* seq,
+                             const int32_t* pos, int64_t n_tokens, void* cache,
+                             const int32_t* block_table, int num_seqs, int Hkv, int D,
+                             int64_t num_pages, int max_blocks, int* err, cudaStream_t s) {
+  return D == 64 ? write_impl<64>(k_new, v_new, seq, pos, n_tokens, cache, block_table, num_seqs,
+                                  Hkv, num_pages, max_blocks, err, s)
+                 : write_impl<128>(k_new, v_new, seq, pos, n_tokens, cache, block_table, num_seqs,
+                                   Hkv, num_pages, max_blocks, err, s);
+}
+
+bi_status launch_kv_read_q8(const void* cache, const int32_t* block_table, const int32_t* kv_lens,
+                            int B, int Hkv, int D, int64_t num_pages, int max_blocks, void* k_out,
+                            void* v_out, const int32_t* out_table, int64_t num_out_pages,
+                            int max_out_blocks, int max_kv_len, int* err, cudaStream_t s) {
+  return D == 64 ? read_impl<64>(cache, block_table, kv_lens, B, Hkv, num_pages, max_blocks, k_out,
+                                 v_out, out_table, num_out_pages, max_out_blocks, max_kv_len, err, s)
+                 : read_impl<128>(cache, block_table, kv_lens, B, Hkv, num_pages, max_blocks,
+                                  k_out, v_out, out_table, num_out_pages, max_out_blocks,
+                                  max_kv_len, err, s);
+}
+
+}  // namespace bi
