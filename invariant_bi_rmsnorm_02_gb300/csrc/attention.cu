@@ -81,27 +81,6 @@ __device__ __forceinline__ uint32_t tile_off(int n, int d) {
   return (uint32_t)((p * TileGeom<D>::kHalves + hf) * 2048 + r * 128 + ((chunk ^ (r & 7)) << 4));
 }
 
-// A tile of 64 keys of the quantised cache in shared memory: four pages of
-// K[16][D] then V[16][D] e4m3 bytes (one TMA box each, 16-byte chunks
-// swizzled within the rows), then the pages' 32 scale bytes (16 of K, 16 of
-// V).  Half a bf16 tile, so about twice the blocks fit on an SM.
-template <int D>
-struct Q8Geom {
-  static constexpr int kRecord = kv_q8_record_bytes(D);
-  static constexpr int kPageBytes = 32 * D;
-  static constexpr int kScales = kPagesPerTile * kPageBytes;  // offset of the scale bytes
-  static constexpr int kBufBytes = kScales + 1024;  // the next buffer stays 1024-byte aligned
-};
-
-// byte offset of 16-byte chunk c of key n's K row (V: 16 D further on): the
-// 128-byte swizzle for rows of 128 bytes, the 64-byte one for rows of 64
-template <int D>
-__device__ __forceinline__ uint32_t q8_off(int n, int c) {
-  const int r = n & 15;
-  const int x = D == 128 ? (r & 7) : ((r >> 1) & 3);
-  return (uint32_t)((n >> 4) * Q8Geom<D>::kPageBytes + r * D + ((c ^ x) << 4));
-}
-
 // 2^x on the special function unit (ex2.approx.ftz: relative error about
 // 2^-22, results below 2^-126 flushed to zero).  Decode and prefill use it
 // for the probabilities and the rescale factors.
@@ -176,27 +155,6 @@ __device__ __forceinline__ void load_q_frags(uint32_t (&qf)[NQ][D / 16][2],
     }
 }
 
-// The same for keys read from the quantised cache: a k-step's 16 elements of
-// a key come as 4 bytes per thread (d = 4t .. 4t+3 for t = lane % 4), whose
-// even bytes take the k positions 2t, 2t+1 of the MMA and whose odd bytes
-// 2t+8, 2t+9.  Q is put in the same order; the sum over a k-step does not
-// depend on the order inside it (checked byte for byte against the bf16
-// kernel by the tests).
-template <int D, int NQ>
-__device__ __forceinline__ void load_q_frags_q8(uint32_t (&qf)[NQ][D / 16][2],
-                                                const __nv_bfloat16* qs) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      const uint2 x =
-          *reinterpret_cast<const uint2*>(qs + (8 * nq + g) * D + 16 * ks + 4 * t);
-      qf[nq][ks][0] = __byte_perm(x.x, x.y, 0x5410);
-      qf[nq][ks][1] = __byte_perm(x.x, x.y, 0x7632);
-    }
-}
-
 // P = hi + lo: the probabilities of keys k, k+1 as two bf16 pairs (key k in
 // the low half).  hi is p with its low 16 bits cleared (bf16 by truncation),
 // lo the exact remainder p - hi truncated the same way, so hi + lo keeps 16
@@ -247,16 +205,10 @@ constexpr float kRescaleLog2 = 8.0f;
 // One tile of 64 keys (absolute indices key0 .. key0+63).  Query column
 // (nq, cc) sees key k iff lo <= k < hi[nq][cc].  A column that sees no key
 // of the tile is left exactly as it was.
-// kQ8: the tile is one of the quantised cache; every element becomes the
-// bf16 value that reading the cache back gives, so the arithmetic is that of
-// the bf16 kernel on the cache read back.  `scales` is then the tile's scale
-// bytes and vbase is not used; rows d of o come in the order 2g, 2g+1
-// (d_of_row below) because an e4m3 pair shares a 16-bit element of the
-// transposing load.
-template <int D, int NQ, bool kQ8>
+template <int D, int NQ>
 __device__ __forceinline__ void tile_step(SplitState<D, NQ>& st,
                                           const uint32_t (&qf)[NQ][D / 16][2], uint32_t kbase,
-                                          uint32_t vbase, const uint8_t* scales, int key0, int lo,
+                                          uint32_t vbase, int key0, int lo,
                                           const int (&hi)[NQ][2], float scale_log2) {
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, mi = lane >> 3, r8 = lane & 7;
@@ -266,38 +218,15 @@ __device__ __forceinline__ void tile_step(SplitState<D, NQ>& st,
   for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) s[mt][nq][0] = s[mt][nq][1] = s[mt][nq][2] = s[mt][nq][3] = 0.0f;
-  if constexpr (kQ8) {
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      // factors of keys 16 mt + g and 16 mt + g + 8
-      const uint32_t f0 = q8_factor2(scales[32 * mt + g]);
-      const uint32_t f1 = q8_factor2(scales[32 * mt + 8 + g]);
+  for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-      for (int kp = 0; kp < D / 32; ++kp) {
-        uint32_t r[4];  // keys g and g + 8 of k-steps 2 kp and 2 kp + 1
-        ldsm_x4(kbase + q8_off<D>(16 * mt + r8 + 8 * (mi & 1), 2 * kp + (mi >> 1)), r);
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t a[4];
+      ldsm_x4(kbase + tile_off<D>(16 * mt + r8 + 8 * (mi & 1), 16 * ks + 8 * (mi >> 1)), a);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t a[4] = {
-              mul_bf16x2(e4m3_even(r[2 * u]), f0), mul_bf16x2(e4m3_even(r[2 * u + 1]), f1),
-              mul_bf16x2(e4m3_odd(r[2 * u]), f0), mul_bf16x2(e4m3_odd(r[2 * u + 1]), f1)};
-#pragma unroll
-          for (int nq = 0; nq < NQ; ++nq)
-            mma_bf16(s[mt][nq], a, qf[nq][2 * kp + u][0], qf[nq][2 * kp + u][1]);
-        }
-      }
+      for (int nq = 0; nq < NQ; ++nq) mma_bf16(s[mt][nq], a, qf[nq][ks][0], qf[nq][ks][1]);
     }
-  } else {
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t a[4];
-        ldsm_x4(kbase + tile_off<D>(16 * mt + r8 + 8 * (mi & 1), 16 * ks + 8 * (mi >> 1)), a);
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) mma_bf16(s[mt][nq], a, qf[nq][ks][0], qf[nq][ks][1]);
-      }
-  }
   // ---- mask, column max of the raw scores, scaled once: rounding is
   // monotone, so RN(max s * c) = max RN(s * c) for the positive scale c
   float mx[NQ][2];
@@ -382,47 +311,17 @@ __device__ __forceinline__ void tile_step(SplitState<D, NQ>& st,
         bh[nq][half] = transpose8x8(hp);
         bl[nq][half] = transpose8x8(lp);
       }
-    if constexpr (kQ8) {
-      // factors of keys 16 kk + 2t, + 1 and of 16 kk + 8 + 2t, + 1
-      const int t = lane & 3;
-      const uint8_t* sv = scales + 32 * kk + 16 + 2 * t;
-      const uint32_t f0 = q8_factors(*reinterpret_cast<const uint16_t*>(sv));
-      const uint32_t f1 = q8_factors(*reinterpret_cast<const uint16_t*>(sv + 8));
 #pragma unroll
-      for (int mp = 0; mp < D / 32; ++mp) {
-        uint32_t r[4];  // key pairs 2t and 8 + 2t of columns 2g, 2g+1 of chunks 2 mp, 2 mp + 1
-        ldsm_x4_t(kbase + 16 * D + q8_off<D>(16 * kk + r8 + 8 * (mi & 1), 2 * mp + (mi >> 1)), r);
+    for (int md = 0; md < D / 16; ++md) {
+      uint32_t a[4];
+      ldsm_x4_t(vbase + tile_off<D>(16 * kk + r8 + 8 * (mi >> 1), 16 * md + 8 * (mi & 1)), a);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t a[4] = {
-              mul_bf16x2(e4m3_even(r[2 * u]), f0), mul_bf16x2(e4m3_odd(r[2 * u]), f0),
-              mul_bf16x2(e4m3_even(r[2 * u + 1]), f1), mul_bf16x2(e4m3_odd(r[2 * u + 1]), f1)};
-#pragma unroll
-          for (int nq = 0; nq < NQ; ++nq) {
-            mma_bf16(st.o[2 * mp + u][nq], a, bh[nq][0], bh[nq][1]);
-            mma_bf16(st.o[2 * mp + u][nq], a, bl[nq][0], bl[nq][1]);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int md = 0; md < D / 16; ++md) {
-        uint32_t a[4];
-        ldsm_x4_t(vbase + tile_off<D>(16 * kk + r8 + 8 * (mi >> 1), 16 * md + 8 * (mi & 1)), a);
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) {
-          mma_bf16(st.o[md][nq], a, bh[nq][0], bh[nq][1]);
-          mma_bf16(st.o[md][nq], a, bl[nq][0], bl[nq][1]);
-        }
+      for (int nq = 0; nq < NQ; ++nq) {
+        mma_bf16(st.o[md][nq], a, bh[nq][0], bh[nq][1]);
+        mma_bf16(st.o[md][nq], a, bl[nq][0], bl[nq][1]);
       }
     }
   }
-}
-
-// The column d of o[md][.][2 hh + cc] of a thread with lane / 4 = g.
-template <bool kQ8>
-__device__ __forceinline__ int d_of_row(int md, int g, int hh) {
-  return kQ8 ? 16 * md + 2 * g + hh : 16 * md + g + 8 * hh;
 }
 
 // Log-sum-exp merge of partial (mb, lb, ob) into (m, l, o), in that order.
@@ -458,29 +357,6 @@ __device__ __forceinline__ void issue_pages(uint8_t* buf, uint64_t* bar, const C
     tma_load_3d_hint(buf + off, km, 0, y, 0, bar, pol);
     tma_load_3d_hint(buf + TileGeom<D>::kKBytes + off, vm, 0, y, 0, bar, pol);
   }
-}
-
-// Issue the copies of a quantised tile's first np pages, one page per lane:
-// its K and V rows in one box, its scale bytes behind them.
-template <int D>
-__device__ __forceinline__ void issue_records(uint8_t* buf, uint64_t* bar, const CUtensorMap* map,
-                                              const uint8_t* cache, int pid, int p, int np,
-                                              int Hkv, int h) {
-  if (p >= np) return;
-  const uint64_t pol = l2_policy_evict_first();
-  const int64_t rec = (int64_t)pid * Hkv + h;
-  tma_load_3d_hint(buf + p * Q8Geom<D>::kPageBytes, map, 0, 0, (int)rec, bar, pol);
-  bulk_load(buf + Q8Geom<D>::kScales + 32 * p,
-            cache + rec * Q8Geom<D>::kRecord + Q8Geom<D>::kPageBytes, 32, bar);
-}
-
-// The V scale bytes of keys >= limit in a landed quantised tile become 0:
-// unwritten slots may hold any bits, and an element's magnitude is finite
-// whatever its bits, so a finite factor is enough for 0 * v to be 0.
-template <int D>
-__device__ __forceinline__ void clear_v_scales(uint8_t* buf, int key0, int limit, int lane) {
-  for (int n = max(limit - key0, 0) + lane; n < kTile; n += 32)
-    buf[Q8Geom<D>::kScales + 32 * (n >> 4) + 16 + (n & 15)] = 0;
 }
 
 __device__ __forceinline__ int pages_below(int key0, int limit) {
@@ -539,7 +415,6 @@ struct KernelParams {
   int64_t num_pages;
   float scale_log2;
   bool variant;
-  const uint8_t* cache_q8;  // decode over the quantised cache: its records
 };
 
 __device__ __forceinline__ bool len_ok(int L, const KernelParams& p) {
@@ -684,17 +559,15 @@ __device__ __forceinline__ int unit_tiles(int4 d) {  // {b, j, lo, hi}
 // limits residency: the bound lets ptxas keep the whole tile step in
 // registers instead of its default for this block size, which measurably
 // starved the G <= 8 instantiation.
-template <int D, int NQ, bool kQ8>
+template <int D, int NQ>
 __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
     const KernelParams p) {
-  constexpr int kBufBytes = kQ8 ? Q8Geom<D>::kBufBytes : TileGeom<D>::kBufBytes;
-  constexpr int kPageTx = kQ8 ? Q8Geom<D>::kRecord : 2 * TileGeom<D>::kPageBytes;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* bufs = smem;  // 2 tile buffers
-  __nv_bfloat16* qbuf = reinterpret_cast<__nv_bfloat16*>(smem + 2 * kBufBytes);
+  __nv_bfloat16* qbuf = reinterpret_cast<__nv_bfloat16*>(smem + 2 * TileGeom<D>::kBufBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(qbuf + 2 * 8 * NQ * D);  // [2]
   uint64_t* empty = full + 2;                                            // [2]
   uint64_t* ready = empty + 2;                                           // [kQueue]
@@ -926,19 +799,13 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
                                                         (first >> 4) + idx];
         }
         if (lane == 0) {
-          uint8_t* buf = bufs + rs * kBufBytes;
+          uint8_t* buf = bufs + rs * TileGeom<D>::kBufBytes;
           const uint32_t qbytes = lt == 0 ? (uint32_t)(G * D * 2) : 0u;
-          mbar_arrive_expect_tx(&full[rs], np * kPageTx + qbytes);
+          mbar_arrive_expect_tx(&full[rs], np * 2 * TileGeom<D>::kPageBytes + qbytes);
           if (lt == 0)
             bulk_load(qbuf + (q_issued & 1) * 8 * NQ * D,
                       p.q + ((int64_t)d.x * p.Hq + (int64_t)h * G) * D, qbytes, &full[rs]);
-          if constexpr (!kQ8) issue_pages<D>(buf, &full[rs], &kmap, &vmap, pid, np, Hkv, h);
-        }
-        if constexpr (kQ8) {
-          __syncwarp();  // the expected bytes are set before any copy completes
-          const int mine = lane == 0 ? pid[0] : lane == 1 ? pid[1] : lane == 2 ? pid[2] : pid[3];
-          issue_records<D>(bufs + rs * kBufBytes, &full[rs], &kmap, p.cache_q8, mine, lane, np,
-                           Hkv, h);
+          issue_pages<D>(buf, &full[rs], &kmap, &vmap, pid, np, Hkv, h);
         }
         if (lt == 0) ++q_issued;
         ++n_issued;
@@ -1001,27 +868,20 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
         alive = false;
         break;
       }
-      uint8_t* buf = bufs + rs * kBufBytes;
+      uint8_t* buf = bufs + rs * TileGeom<D>::kBufBytes;
       if (ti == 0) {
-        const __nv_bfloat16* qs = qbuf + (q_used & 1) * 8 * NQ * D;
-        if constexpr (kQ8)
-          load_q_frags_q8<D, NQ>(qf, qs);
-        else
-          load_q_frags<D, NQ>(qf, qs, D);
+        load_q_frags<D, NQ>(qf, qbuf + (q_used & 1) * 8 * NQ * D, D);
         ++q_used;
         st.reset();
       }
       const int key0 = first + ti * kTile;
       const bool tail = key0 + kTile > hi;
       if (tail) {
-        if constexpr (kQ8)
-          clear_v_scales<D>(buf, key0, hi, lane);
-        else
-          clear_v_tail<D>(buf, key0, hi, lane, 32);
+        clear_v_tail<D>(buf, key0, hi, lane, 32);
         __syncwarp();
       }
-      tile_step<D, NQ, kQ8>(st, qf, smem_u32(buf), smem_u32(buf + TileGeom<D>::kKBytes),
-                            buf + Q8Geom<D>::kScales, key0, lo, hcol, p.scale_log2);
+      tile_step<D, NQ>(st, qf, smem_u32(buf), smem_u32(buf + TileGeom<D>::kKBytes), key0, lo,
+                       hcol, p.scale_log2);
       ++n_done;
       // the buffer goes back to the producer; the rows this warp zeroed are
       // ordered before the copy that will overwrite them
@@ -1048,7 +908,7 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
             const float ov = helper ? o_odd : st.o[md][0][2 * hh];
             if (col < G) {
               const float v = lv > 0.0f ? normalize(ov, inv_l(lv)) : 0.0f;
-              const int64_t idx = orow + d_of_row<kQ8>(md, g, hh);
+              const int64_t idx = orow + 16 * md + g + 8 * hh;
               static_cast<__nv_bfloat16*>(p.out)[idx] = __float2bfloat16_rn(v);
               if (p.out_f32) p.out_f32[idx] = v;
             }
@@ -1068,7 +928,7 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               const float v = lv > 0.0f ? normalize(st.o[md][nq][2 * hh + cc], inv_l(lv)) : 0.0f;
-              const int64_t idx = orow + d_of_row<kQ8>(md, g, hh);
+              const int64_t idx = orow + 16 * md + g + 8 * hh;
               static_cast<__nv_bfloat16*>(p.out)[idx] = __float2bfloat16_rn(v);
               if (p.out_f32) p.out_f32[idx] = v;
             }
@@ -1090,9 +950,593 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
         float* orow = p.o + ((row0 + col) * p.max_splits + j) * D;
 #pragma unroll
         for (int md = 0; md < D / 16; ++md) {
-          orow[d_of_row<kQ8>(md, g, 0)] = st.o[md][nq][cc];
-          orow[d_of_row<kQ8>(md, g, 1)] = st.o[md][nq][2 + cc];
+          orow[16 * md + g] = st.o[md][nq][cc];
+          orow[16 * md + g + 8] = st.o[md][nq][2 + cc];
         }
+      }
+  }
+  if (!alive) s_abort = 1;
+}
+
+// ------------------------------------------- decode split, quantised cache
+// The same units, arithmetic and outputs over the records of the quantised
+// cache: every e4m3 element becomes the bf16 value that reading the cache
+// back gives (an exact product), so the sums are those of the bf16 kernel on
+// the pages read back, bit for bit.
+//
+// What bounds it: half the bytes per tile, but an element costs about 1.7
+// more instructions (unpacking, V's factor), ~1,600 per 64-key tile of
+// D = 128, while at the measured HBM rate an SM receives a tile every ~700
+// cycles.  So the work has to be spread over all four of an SM's schedulers
+// with two compute warps each: one block per SM holds kQ8Pairs pairs of a
+// compute warp (warps 0..7) and the producer warp that feeds it (8..15),
+// with the register file split between them.  (With the bf16 kernel's blocks
+// of one compute and one producer warp, all compute warps sat on two of the
+// four schedulers: 59% of their issue slots used against 9% of the others',
+// and the 64-request case took 149 us.)
+//
+// A pair's ring holds kStages half tiles, K and V in turn: K's half goes back
+// to the producer as soon as the scores are done.  The tile's scale bytes
+// ride with its K half in a ring of their own (kScaleSlots tiles): a slot is
+// written again only after a wait that follows the release of the V half
+// that reads it.
+constexpr int kQ8Pairs = 8;
+constexpr int kQ8Threads = 2 * kQ8Pairs * 32;
+constexpr int kQ8ComputeRegs = 200, kQ8ProducerRegs = 56;
+static_assert((kQ8ComputeRegs + kQ8ProducerRegs) * kQ8Pairs * 32 <= 65536,
+              "the two shares are the launch's 128 registers a thread");
+
+template <int D>
+struct Q8Geom {
+  static constexpr int kRecord = kv_q8_record_bytes(D);
+  static constexpr int kPageHalf = kPage * D;               // one page's K (or V) bytes
+  static constexpr int kHalf = kPagesPerTile * kPageHalf;   // one ring stage
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kScaleSlots = D == 128 ? 2 : 4;
+  static constexpr int kScaleBytes = 2 * kTile;             // per tile: page p at 32 p, K then V
+  static constexpr int kPairBytes = kStages * kHalf;
+  static constexpr int kSmem = 1024 + kQ8Pairs * (kPairBytes + kScaleSlots * kScaleBytes);
+};
+
+// byte offset of 16-byte chunk c of key n's row in a half tile: the TMA
+// swizzle of the row's width (128 or 64 bytes)
+template <int D>
+__device__ __forceinline__ uint32_t q8_off(int n, int c) {
+  const int r = n & 15;
+  const int x = D == 128 ? (r & 7) : ((r >> 1) & 3);
+  return (uint32_t)((n >> 4) * Q8Geom<D>::kPageHalf + r * D + ((c ^ x) << 4));
+}
+
+// K's elements enter the score MMA without their scale, as their value times
+// 2^-120 (e4m3_even / e4m3_odd); Q times 2^32 keeps the fp32 sums far from
+// fp32's smallest numbers, and the key's factor 2^(e + 120) afterwards makes
+// each score its true value times 2^32, which the softmax's scale takes off.
+// All of these are powers of two, so no bit of a score changes.
+constexpr uint32_t kQ8QScale = 0x4f804f80u;   // 2^32 as a bf16 pair
+constexpr float kQ8ScoreScale = 0x1p-32f;
+
+// Q^T fragments straight from global memory.  A k-step's 16 elements of a key
+// reach a thread as bytes d = 4t .. 4t+3 (t = lane % 4): the even ones take
+// the MMA's k positions 2t, 2t+1 and the odd ones 2t+8, 2t+9, and Q's
+// elements go to the same places (the MMA's sum over a k-step does not depend
+// on the order inside it; the tests compare the bytes with the bf16 kernel).
+// Rows G .. 8 NQ - 1 are zero.
+template <int D, int NQ>
+__device__ __forceinline__ void q8_load_q(uint32_t (&qf)[NQ][D / 16][2], const __nv_bfloat16* q,
+                                          int G) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint2 x = make_uint2(0, 0);
+      if (8 * nq + g < G)
+        x = *reinterpret_cast<const uint2*>(q + (8 * nq + g) * D + 16 * ks + 4 * t);
+      qf[nq][ks][0] = mul_bf16x2(__byte_perm(x.x, x.y, 0x5410), kQ8QScale);
+      qf[nq][ks][1] = mul_bf16x2(__byte_perm(x.x, x.y, 0x7632), kQ8QScale);
+    }
+}
+
+// S^T = K Q^T of a half tile, times 2^32: 4 m-tiles of 16 keys.
+template <int D, int NQ>
+__device__ __forceinline__ void q8_scores(float (&s)[4][NQ][4],
+                                          const uint32_t (&qf)[NQ][D / 16][2], uint32_t kbase,
+                                          const uint8_t* scales) {
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> 2, mi = lane >> 3, r8 = lane & 7;
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq) s[mt][nq][0] = s[mt][nq][1] = s[mt][nq][2] = s[mt][nq][3] = 0.0f;
+#pragma unroll
+    for (int kp = 0; kp < D / 32; ++kp) {
+      uint32_t r[4];  // keys g and g + 8 of k-steps 2 kp and 2 kp + 1
+      ldsm_x4(kbase + q8_off<D>(16 * mt + r8 + 8 * (mi & 1), 2 * kp + (mi >> 1)), r);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t a[4] = {e4m3_even(r[2 * u]), e4m3_even(r[2 * u + 1]), e4m3_odd(r[2 * u]),
+                               e4m3_odd(r[2 * u + 1])};
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+          mma_bf16(s[mt][nq], a, qf[nq][2 * kp + u][0], qf[nq][2 * kp + u][1]);
+      }
+    }
+    const float f0 = q8_factor_f32(scales[32 * mt + g]);
+    const float f1 = q8_factor_f32(scales[32 * mt + 8 + g]);
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq) {
+      s[mt][nq][0] = __fmul_rn(s[mt][nq][0], f0);
+      s[mt][nq][1] = __fmul_rn(s[mt][nq][1], f0);
+      s[mt][nq][2] = __fmul_rn(s[mt][nq][2], f1);
+      s[mt][nq][3] = __fmul_rn(s[mt][nq][3], f1);
+    }
+  }
+}
+
+// The softmax of tile_step on those scores: probabilities into s, the
+// running maximum, sum and o brought to the tile's reference.  Only the last
+// tile of a sequence has keys to mask (limit: its length in the tile);
+// padding columns are never read, so they need none.
+template <int D, int NQ>
+__device__ __forceinline__ void q8_softmax(SplitState<D, NQ>& st, float (&s)[4][NQ][4], int limit,
+                                           float scale) {
+  const int g = (threadIdx.x & 31) >> 2;
+  if (limit < kTile) {
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (16 * mt + g + 8 * (c >> 1) >= limit) s[mt][nq][c] = -CUDART_INF_F;
+  }
+  float alpha[NQ][2];
+  bool moved = false;
+#pragma unroll
+  for (int nq = 0; nq < NQ; ++nq) {
+    float mb[2], cs[2];
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc) {
+      float mx = fmaxf(s[0][nq][cc], s[0][nq][2 + cc]);
+#pragma unroll
+      for (int mt = 1; mt < 4; ++mt) mx = max3(mx, s[mt][nq][cc], s[mt][nq][2 + cc]);
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+      const float t = __fmul_rn(mx, scale), m_in = st.m[nq][cc];
+      float mnew = m_in;
+      alpha[nq][cc] = 1.0f;
+      if (t == -CUDART_INF_F) {
+        // no visible key: exact no-op for this column
+      } else if (m_in == -CUDART_INF_F) {
+        mnew = t;
+        alpha[nq][cc] = 0.0f;
+      } else if (__fsub_rn(t, m_in) > kRescaleLog2) {
+        mnew = t;
+        alpha[nq][cc] = exp2_sfu(__fsub_rn(m_in, t));
+      }
+      moved = moved || alpha[nq][cc] != 1.0f;
+      st.m[nq][cc] = mnew;
+      mb[cc] = mnew == -CUDART_INF_F ? 0.0f : mnew;
+      cs[cc] = 0.0f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int cc = c & 1;
+        const float pv = exp2_sfu(__fmaf_rn(s[mt][nq][c], scale, -mb[cc]));
+        s[mt][nq][c] = pv;
+        cs[cc] = __fadd_rn(cs[cc], pv);
+      }
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc) {
+      cs[cc] = __fadd_rn(cs[cc], __shfl_xor_sync(kFull, cs[cc], 4));
+      cs[cc] = __fadd_rn(cs[cc], __shfl_xor_sync(kFull, cs[cc], 8));
+      cs[cc] = __fadd_rn(cs[cc], __shfl_xor_sync(kFull, cs[cc], 16));
+      st.l[nq][cc] = __fadd_rn(__fmul_rn(st.l[nq][cc], alpha[nq][cc]), cs[cc]);
+    }
+  }
+  // a product with 1 changes nothing, so it is left out where no column moved
+  if (__any_sync(kFull, moved)) {
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+      for (int md = 0; md < D / 16; ++md)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          st.o[md][nq][c] = __fmul_rn(st.o[md][nq][c], alpha[nq][c & 1]);
+  }
+}
+
+// O^T += V^T P^T.  The transposing load moves 16-bit elements, so a thread
+// gets columns 2g and 2g + 1 of a 16-column chunk for keys 2t, 2t + 1: the
+// even bytes are the A operand's row g, the odd ones its row g + 8, and o's
+// rows stand for d = 16 md + 2g (c = 0, 1) and 16 md + 2g + 1 (c = 2, 3).
+template <int D, int NQ>
+__device__ __forceinline__ void q8_values(SplitState<D, NQ>& st, const float (&s)[4][NQ][4],
+                                          uint32_t vbase, const uint8_t* scales) {
+  const int lane = threadIdx.x & 31;
+  const int t = lane & 3, mi = lane >> 3, r8 = lane & 7;
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    uint32_t bh[NQ][2], bl[NQ][2];
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t hp, lp;
+        split_p_bf16(s[kk][nq][2 * half], s[kk][nq][2 * half + 1], hp, lp);
+        bh[nq][half] = transpose8x8(hp);
+        bl[nq][half] = transpose8x8(lp);
+      }
+    // factors of keys 16 kk + 2t, + 1 and of 16 kk + 8 + 2t, + 1
+    const uint8_t* sv = scales + 32 * kk + 16 + 2 * t;
+    const uint32_t f0 = q8_factors(*reinterpret_cast<const uint16_t*>(sv));
+    const uint32_t f1 = q8_factors(*reinterpret_cast<const uint16_t*>(sv + 8));
+#pragma unroll
+    for (int mp = 0; mp < D / 32; ++mp) {
+      uint32_t r[4];  // keys 0-7 and 8-15 of column chunks 2 mp and 2 mp + 1
+      ldsm_x4_t(vbase + q8_off<D>(16 * kk + r8 + 8 * (mi & 1), 2 * mp + (mi >> 1)), r);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t a[4] = {
+            mul_bf16x2(e4m3_even(r[2 * u]), f0), mul_bf16x2(e4m3_odd(r[2 * u]), f0),
+            mul_bf16x2(e4m3_even(r[2 * u + 1]), f1), mul_bf16x2(e4m3_odd(r[2 * u + 1]), f1)};
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+          mma_bf16(st.o[2 * mp + u][nq], a, bh[nq][0], bh[nq][1]);
+          mma_bf16(st.o[2 * mp + u][nq], a, bl[nq][0], bl[nq][1]);
+        }
+      }
+    }
+  }
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(kQ8Threads, 1) attn_decode_q8_split_kernel(
+    const __grid_constant__ CUtensorMap map, const uint8_t* __restrict__ cache,
+    const KernelParams p) {
+  using Geom = Q8Geom<D>;
+  constexpr int kStages = Geom::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  __shared__ uint64_t b_full[kQ8Pairs][kStages], b_empty[kQ8Pairs][kStages];
+  __shared__ uint64_t b_ready[kQ8Pairs][kQueue], b_freed[kQ8Pairs][kQueue];
+  __shared__ int4 q_unit[kQ8Pairs][kQueue];   // b, j, lo, hi of opened units (b < 0: no more)
+  __shared__ int q_head[kQ8Pairs][kQueue];    // kv head h, or -(h+1) if its pages are bad
+  __shared__ int q_single[kQ8Pairs][kQueue];  // the sequence has this one split
+  __shared__ int s_incl[kLocalPlanMax], s_len[kLocalPlanMax];
+  __shared__ int s_plan[2];                   // the splits of all sequences, the variant's chunk
+  __shared__ int s_abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pair = warp % kQ8Pairs;
+  uint8_t* ring = smem + pair * Geom::kPairBytes;
+  uint8_t* scale_ring =
+      smem + kQ8Pairs * Geom::kPairBytes + pair * Geom::kScaleSlots * Geom::kScaleBytes;
+  uint64_t* full = b_full[pair];
+  uint64_t* empty = b_empty[pair];
+  uint64_t* ready = b_ready[pair];
+  uint64_t* freed = b_freed[pair];
+  const int G = p.G, Hkv = p.Hkv;
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&map);
+    for (int w = 0; w < kQ8Pairs; ++w) {
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&b_full[w][i], 1);
+        mbar_init(&b_empty[w][i], 1);
+      }
+      for (int i = 0; i < kQueue; ++i) {
+        mbar_init(&b_ready[w][i], 1);
+        mbar_init(&b_freed[w][i], 1);
+      }
+    }
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  grid_dependency_wait();  // inputs and the plan kernel's unit list are complete from here
+
+  // ---- the plan, as in attn_decode_split_kernel: for small batches the
+  // running split count and the length of every sequence in shared memory
+  if (warp == 0 && p.local_plan) {
+    int csize = 0;
+    if (p.variant) {
+      long long tiles = 0;
+      int tmax = 0;
+#pragma unroll
+      for (int k = 0; k < kLocalSlabs; ++k) {
+        const int b = lane + 32 * k;
+        const int L = b < p.B ? p.kv_lens[b] : 0;
+        if (b < p.B && len_ok(L, p)) {
+          tiles += (L + kTile - 1) / kTile;
+          tmax = max(tmax, (L + kTile - 1) / kTile);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        tiles += __shfl_xor_sync(kFull, tiles, o);
+        tmax = max(tmax, __shfl_xor_sync(kFull, tmax, o));
+      }
+      csize = kTile * variant_chunk_tiles(tiles, tmax, p);
+      if (blockIdx.x == 0 && lane == 0) p.unit_count[1] = csize;  // for the merge
+    }
+    int total = 0;
+#pragma unroll
+    for (int k = 0; k < kLocalSlabs; ++k) {
+      const int b = lane + 32 * k;
+      int L = 0, n = 0;
+      if (b < p.B) {
+        L = p.kv_lens[b];
+        if (!len_ok(L, p)) {
+          record_error(p.err, BI_ERR_DEVICE_BOUNDS);
+          L = 0;
+        }
+        if (L > 0) n = plan_splits(L, csize, p);
+      }
+      int v = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += t;
+      }
+      s_incl[b] = total + v;
+      s_len[b] = L;
+      total += __shfl_sync(kFull, v, 31);
+    }
+    if (lane == 0) {
+      s_plan[0] = total;
+      s_plan[1] = csize;
+    }
+    __syncwarp();
+    // the merge takes sequences longest first: rank of sequence x among all
+    for (int x = blockIdx.x; x < p.B; x += gridDim.x) {
+      auto splits = [&](int b) { return s_incl[b] - (b > 0 ? s_incl[b - 1] : 0); };
+      const int nx = splits(x);
+      int ahead = 0;
+#pragma unroll
+      for (int k = 0; k < kLocalSlabs; ++k) {
+        const int b = lane + 32 * k;
+        if (b < p.B) {
+          const int nb = splits(b);
+          ahead += (nb > nx || (nb == nx && b < x)) ? 1 : 0;
+        }
+      }
+      ahead = __reduce_add_sync(kFull, ahead);
+      if (lane == 0) p.order[ahead] = make_int2(x, nx);
+    }
+  }
+  if (threadIdx.x == 0 && !p.local_plan) {
+    s_plan[0] = *p.unit_count;
+    s_plan[1] = p.variant ? p.unit_count[1] : 0;
+  }
+  __syncthreads();
+
+  if (warp >= kQ8Pairs) {
+    // ============================================================ producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQ8ProducerRegs));
+    const int U = s_plan[0] * Hkv, csize = s_plan[1];
+    const int stride = gridDim.x * kQ8Pairs;
+    auto unit_at = [&](int s) -> int4 {  // {b, j, lo, hi} of split s; warp-uniform s
+      if (!p.local_plan) return p.units[s];
+      int b = 0;
+#pragma unroll
+      for (int k = 0; k < kLocalSlabs; ++k)
+        b += __popc(__ballot_sync(kFull, s_incl[lane + 32 * k] <= s));
+      const int L = s_len[b];
+      const int j = s - (b > 0 ? s_incl[b - 1] : 0);
+      const int c = p.variant ? csize : p.split_size;
+      return make_int4(b, j, j * c, min((j + 1) * c, L));
+    };
+    // the pending unit: its descriptor and first page ids (in flight in
+    // registers: lane i holds pages i and 32 + i)
+    int lu = pair * gridDim.x + blockIdx.x;  // next unit to fetch: neighbours on other SMs
+    bool pend = false;
+    int4 pd = make_int4(0, 0, 0, 0);
+    int ph = 0, pg0 = 0, pg1 = 0;
+    auto fetch = [&]() {
+      pend = lu < U;
+      if (!pend) return;
+      ph = lu % Hkv;
+      pd = unit_at(lu / Hkv);
+      lu += stride;
+      const int npg = (pd.w - pd.z + kPage - 1) / kPage;
+      const int32_t* bt = p.block_table + (int64_t)pd.x * p.max_blocks + (pd.z >> 4);
+      pg0 = lane < npg ? bt[lane] : 0;
+      pg1 = lane + 32 < npg ? bt[lane + 32] : 0;
+    };
+    const uint64_t pol = l2_policy_evict_first();
+    int n_units = 0, n = 0, tiles = 0;  // units opened, stages filled, tiles issued
+    int stage = 0;
+    uint32_t phase = 1;                 // parity of the wait for a free stage (first round: free)
+    bool ok = true;
+    fetch();
+    while (ok) {
+      const int slot = n_units % kQueue;
+      if (n_units >= kQueue)
+        ok = __all_sync(kFull, mbar_wait(&freed[slot], ((n_units / kQueue) - 1) & 1, p.err,
+                                         &s_abort));
+      if (!ok) break;
+      if (!pend) {  // no more units: the end marker
+        if (lane == 0) {
+          q_unit[pair][slot] = make_int4(-1, 0, 0, 0);
+          mbar_arrive(&ready[slot]);
+        }
+        break;
+      }
+      // check the pending unit's pages and queue its descriptor
+      const int4 d = pd;
+      const int h = ph, c0 = pg0, c1 = pg1;
+      const int npg = (d.w - d.z + kPage - 1) / kPage;
+      const int32_t* bt = p.block_table + (int64_t)d.x * p.max_blocks;
+      bool good = c0 >= 0 && c0 < p.num_pages && c1 >= 0 && c1 < p.num_pages;
+      if (npg > 64 && !pages_ok(bt, d.z + 64 * kPage, d.w, p.num_pages, lane, 32)) good = false;
+      good = __all_sync(kFull, good);
+      if (lane == 0) {
+        // split 0 is the only one iff it ends below the chunk size or the
+        // sequence is exactly one chunk long
+        const int c = p.variant ? csize : p.split_size;
+        q_unit[pair][slot] = d;
+        q_head[pair][slot] = good ? h : -(h + 1);
+        q_single[pair][slot] =
+            d.y == 0 && (d.w < c || (p.local_plan ? s_len[d.x] : p.kv_lens[d.x]) == c);
+        if (!good) record_error(p.err, BI_ERR_DEVICE_BOUNDS);
+        mbar_arrive(&ready[slot]);
+      }
+      __syncwarp();
+      ++n_units;
+      fetch();  // the next unit's page ids load while this unit's tiles are issued
+      if (!good) continue;
+      const int ntiles = (d.w - d.z + kTile - 1) / kTile;
+      for (int lt = 0; lt < ntiles && ok; ++lt) {
+        const int np = min(kPagesPerTile, npg - 4 * lt);
+        const int idx = 4 * lt + (lane & 3);  // this lane's page of the unit
+        const int in0 = __shfl_sync(kFull, c0, idx & 31), in1 = __shfl_sync(kFull, c1, idx & 31);
+        const int pid = lane >= np ? 0 : idx < 32 ? in0 : idx < 64 ? in1 : bt[(d.z >> 4) + idx];
+        const int64_t rec = (int64_t)pid * Hkv + h;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // K, then V
+          if (n >= kStages)
+            ok = __all_sync(kFull, mbar_wait(&empty[stage], phase, p.err, &s_abort));
+          if (!ok) break;
+          uint64_t* bar = &full[stage];
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar, np * (Geom::kPageHalf + (half == 0 ? 32 : 0)));
+          __syncwarp();
+          if (lane < np) {
+            tma_load_3d_hint(ring + stage * Geom::kHalf + lane * Geom::kPageHalf, &map, 0,
+                             half * kPage, (int)rec, bar, pol);
+            if (half == 0)
+              bulk_load(scale_ring + (tiles % Geom::kScaleSlots) * Geom::kScaleBytes + 32 * lane,
+                        cache + rec * Geom::kRecord + 2 * Geom::kPageHalf, 32, bar);
+          }
+          ++n;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        ++tiles;
+      }
+    }
+    if (!ok) s_abort = 1;
+    // the copies in flight land before the block exits
+    if (lane == 0)
+      for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
+        mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr);
+    return;
+  }
+  // ============================================================== compute
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQ8ComputeRegs));
+  const float scale = p.scale_log2 * kQ8ScoreScale;
+  SplitState<D, NQ> st;
+  uint32_t qf[NQ][D / 16][2];
+  const int g = lane >> 2, t = lane & 3;
+  int n = 0, tiles = 0, stage = 0;
+  uint32_t phase = 0;
+  bool alive = true;
+  auto next_stage = [&]() {  // back to the producer, on to the next
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[stage]);
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  };
+  for (;;) {
+    const int slot = n % kQueue;
+    if (!__all_sync(kFull, mbar_wait(&ready[slot], (n / kQueue) & 1, p.err, &s_abort))) {
+      alive = false;
+      break;
+    }
+    const int4 d = q_unit[pair][slot];
+    const int hv = q_head[pair][slot];
+    const bool single = q_single[pair][slot] != 0;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&freed[slot]);
+    ++n;
+    if (d.x < 0) break;  // no more units
+    const bool pages_good = hv >= 0;
+    const int h = pages_good ? hv : -hv - 1;
+    const int b = d.x, j = d.y, lo = d.z, hi = d.w;
+    const int64_t row0 = (int64_t)b * p.Hq + (int64_t)h * G;  // first q-head row
+    if (!pages_good) {  // l = -1 makes the merge emit zeros
+      if (single) {
+        for (int i = lane; i < G * D; i += 32) {
+          static_cast<__nv_bfloat16*>(p.out)[row0 * D + i] = __float2bfloat16_rn(0.0f);
+          if (p.out_f32) p.out_f32[row0 * D + i] = 0.0f;
+        }
+      } else if (lane < G) {
+        const int64_t s = (row0 + lane) * p.ml_stride + j;
+        p.ml[2 * s] = -CUDART_INF_F;
+        p.ml[2 * s + 1] = -1.0f;
+      }
+      continue;
+    }
+    q8_load_q<D, NQ>(qf, p.q + row0 * D, G);
+    st.reset();
+    for (int key0 = lo; key0 < hi; key0 += kTile, ++tiles) {
+      uint8_t* scales = scale_ring + (tiles % Geom::kScaleSlots) * Geom::kScaleBytes;
+      const int limit = hi - key0;  // keys of the tile that exist (or more)
+      float s[4][NQ][4];
+      if (!__all_sync(kFull, mbar_wait(&full[stage], phase, p.err, &s_abort))) {
+        alive = false;
+        break;
+      }
+      q8_scores<D, NQ>(s, qf, smem_u32(ring + stage * Geom::kHalf), scales);
+      next_stage();
+      q8_softmax<D, NQ>(st, s, limit, scale);
+      if (!__all_sync(kFull, mbar_wait(&full[stage], phase, p.err, &s_abort))) {
+        alive = false;
+        break;
+      }
+      if (limit < kTile) {
+        // The V scale bytes of slots behind the last token become 0: those
+        // slots may hold any bits, and an element is finite whatever its
+        // bits, so a finite factor is enough for 0 * v to be 0.
+        for (int i = limit + lane; i < kTile; i += 32) scales[32 * (i >> 4) + 16 + (i & 15)] = 0;
+        __syncwarp();
+      }
+      q8_values<D, NQ>(st, s, smem_u32(ring + stage * Geom::kHalf), scales);
+      // this warp's bytes before the copy that will overwrite them
+      if (limit < kTile) fence_proxy_async_smem();
+      next_stage();
+    }
+    if (!alive) break;
+    // ---- the output of a single split, or the partial state; columns d and
+    // d + 1 are neighbours in a thread
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        const int col = 8 * nq + 2 * t + cc;
+        if (col >= G) continue;
+        const float lv = st.l[nq][cc];
+        if (single) {
+          const float rl = inv_l(lv);
+          const int64_t orow = (row0 + col) * D + 2 * g;
+#pragma unroll
+          for (int md = 0; md < D / 16; ++md) {
+            const float v0 = lv > 0.0f ? normalize(st.o[md][nq][cc], rl) : 0.0f;
+            const float v1 = lv > 0.0f ? normalize(st.o[md][nq][2 + cc], rl) : 0.0f;
+            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow + 16 * md) =
+                pack_bf16x2(v0, v1);
+            if (p.out_f32)
+              *reinterpret_cast<float2*>(p.out_f32 + orow + 16 * md) = make_float2(v0, v1);
+          }
+          continue;
+        }
+        const int64_t sm = (row0 + col) * p.ml_stride + j;
+        if (g == 0) {
+          p.ml[2 * sm] = st.m[nq][cc];
+          p.ml[2 * sm + 1] = lv;
+        }
+        float* orow = p.o + ((row0 + col) * p.max_splits + j) * D + 2 * g;
+#pragma unroll
+        for (int md = 0; md < D / 16; ++md)
+          *reinterpret_cast<float2*>(orow + 16 * md) =
+              make_float2(st.o[md][nq][cc], st.o[md][nq][2 + cc]);
       }
   }
   if (!alive) s_abort = 1;
@@ -1883,9 +2327,9 @@ __global__ void kv_write_kernel(const uint4* __restrict__ k_new, const uint4* __
   }
 }
 
-template <int D, int NQ, bool kQ8>
+template <int D, int NQ>
 size_t decode_smem() {  // ring, q buffers, barriers (full, empty: 2 each; ready, free)
-  return 1024 + 2 * (kQ8 ? Q8Geom<D>::kBufBytes : TileGeom<D>::kBufBytes) + 2 * 8 * NQ * D * 2 + (4 + 2 * kQueue) * 8;
+  return 1024 + 2 * TileGeom<D>::kBufBytes + 2 * 8 * NQ * D * 2 + (4 + 2 * kQueue) * 8;
 }
 KernelParams make_params(const AttnArgs& a) {
   KernelParams p{};
@@ -1967,19 +2411,12 @@ DecodeWs decode_ws_layout(int B, int Hq, int D, int max_splits) {
   return w;
 }
 
-template <int D, int NQ, bool kQ8>
+template <int D, int NQ>
 bi_status decode_impl(const AttnArgs& a, cudaStream_t s) {
   KernelParams p = make_params(a);
   if (a.max_splits > 0) {
     CUtensorMap km, vm;
-    if constexpr (kQ8) {
-      if (!make_tmap_records(&km, a.k_cache, static_cast<uint64_t>(a.num_pages) * a.Hkv, D))
-        return BI_ERR_CUDA;
-      vm = km;
-      p.cache_q8 = static_cast<const uint8_t*>(a.k_cache);
-    } else {
-      if (!make_kv_page_maps(a, &km, &vm)) return BI_ERR_CUDA;
-    }
+    if (!make_kv_page_maps(a, &km, &vm)) return BI_ERR_CUDA;
     const DecodeWs w = decode_ws_layout(a.B, a.Hq, a.D, a.max_splits);
     char* base = reinterpret_cast<char*>(a.ws);
     p.unit_count = reinterpret_cast<int*>(base);
@@ -1989,12 +2426,12 @@ bi_status decode_impl(const AttnArgs& a, cudaStream_t s) {
     p.ml_stride = w.ml_stride;
     p.local_plan = a.B <= kLocalPlanMax;
     if (p.local_plan) p.order = reinterpret_cast<int2*>(base + w.units_off);  // units unused
-    const size_t sm = decode_smem<D, NQ, kQ8>();
-    if (set_smem(attn_decode_split_kernel<D, NQ, kQ8>, sm) != cudaSuccess) return BI_ERR_CUDA;
+    const size_t sm = decode_smem<D, NQ>();
+    if (set_smem(attn_decode_split_kernel<D, NQ>, sm) != cudaSuccess) return BI_ERR_CUDA;
     static int per_sm[2][3] = {};
     int& occ = per_sm[D == 128][NQ];
     if (occ == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                        &occ, attn_decode_split_kernel<D, NQ, kQ8>, kSplitThreads, sm) !=
+                        &occ, attn_decode_split_kernel<D, NQ>, kSplitThreads, sm) !=
                         cudaSuccess)
       return BI_ERR_CUDA;
     const int sms = device_sm_count();
@@ -2007,13 +2444,46 @@ bi_status decode_impl(const AttnArgs& a, cudaStream_t s) {
     p.target_units = static_cast<int>(4 * cap);
     if (!p.local_plan) attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
     const int grid = static_cast<int>(max_units < cap ? max_units : cap);
-    if (launch_pdl(attn_decode_split_kernel<D, NQ, kQ8>, dim3(grid), dim3(kSplitThreads), sm, s, km,
+    if (launch_pdl(attn_decode_split_kernel<D, NQ>, dim3(grid), dim3(kSplitThreads), sm, s, km,
                    vm, p) !=
         cudaSuccess)
       return BI_ERR_CUDA;
   }
   if (launch_pdl(attn_decode_merge_kernel<D>, dim3(a.Hq, a.B), dim3(D), 0, s, p) !=
       cudaSuccess)
+    return BI_ERR_CUDA;
+  return BI_OK;
+}
+
+template <int D, int NQ>
+bi_status decode_q8_impl(const AttnArgs& a, cudaStream_t s) {
+  KernelParams p = make_params(a);
+  if (a.max_splits > 0) {
+    CUtensorMap map;
+    if (!make_tmap_records(&map, a.k_cache, static_cast<uint64_t>(a.num_pages) * a.Hkv, D))
+      return BI_ERR_CUDA;
+    const DecodeWs w = decode_ws_layout(a.B, a.Hq, a.D, a.max_splits);
+    char* base = reinterpret_cast<char*>(a.ws);
+    p.unit_count = reinterpret_cast<int*>(base);
+    p.units = reinterpret_cast<int4*>(base + w.units_off);
+    p.ml = reinterpret_cast<float*>(base + w.ml_off);
+    p.o = reinterpret_cast<float*>(base + w.o_off);
+    p.ml_stride = w.ml_stride;
+    p.local_plan = a.B <= kLocalPlanMax;
+    if (p.local_plan) p.order = reinterpret_cast<int2*>(base + w.units_off);  // units unused
+    const size_t sm = Q8Geom<D>::kSmem;
+    if (set_smem(attn_decode_q8_split_kernel<D, NQ>, sm) != cudaSuccess) return BI_ERR_CUDA;
+    const int sms = device_sm_count();
+    if (sms <= 0) return BI_ERR_CUDA;
+    const int64_t max_units = static_cast<int64_t>(a.B) * a.Hkv * a.max_splits;
+    p.target_units = 4 * kQ8Pairs * sms;  // variant: units per pair, as the bf16 kernel's
+    if (!p.local_plan) attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+    const int grid = static_cast<int>(max_units < sms ? max_units : sms);
+    if (launch_pdl(attn_decode_q8_split_kernel<D, NQ>, dim3(grid), dim3(kQ8Threads), sm, s, map,
+                   static_cast<const uint8_t*>(a.k_cache), p) != cudaSuccess)
+      return BI_ERR_CUDA;
+  }
+  if (launch_pdl(attn_decode_merge_kernel<D>, dim3(a.Hq, a.B), dim3(D), 0, s, p) != cudaSuccess)
     return BI_ERR_CUDA;
   return BI_OK;
 }
@@ -2150,14 +2620,12 @@ size_t attn_decode_workspace_bytes(int B, int Hq, int D, int max_splits) {
 bi_status launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
   const int G = a.Hq / a.Hkv;
   if (a.q8) {
-    if (a.D == 64) return G <= 8 ? decode_impl<64, 1, true>(a, s) : decode_impl<64, 2, true>(a, s);
-    if (a.D == 128)
-      return G <= 8 ? decode_impl<128, 1, true>(a, s) : decode_impl<128, 2, true>(a, s);
+    if (a.D == 64) return G <= 8 ? decode_q8_impl<64, 1>(a, s) : decode_q8_impl<64, 2>(a, s);
+    if (a.D == 128) return G <= 8 ? decode_q8_impl<128, 1>(a, s) : decode_q8_impl<128, 2>(a, s);
     return BI_ERR_UNSUPPORTED;
   }
-  if (a.D == 64) return G <= 8 ? decode_impl<64, 1, false>(a, s) : decode_impl<64, 2, false>(a, s);
-  if (a.D == 128)
-    return G <= 8 ? decode_impl<128, 1, false>(a, s) : decode_impl<128, 2, false>(a, s);
+  if (a.D == 64) return G <= 8 ? decode_impl<64, 1>(a, s) : decode_impl<64, 2>(a, s);
+  if (a.D == 128) return G <= 8 ? decode_impl<128, 1>(a, s) : decode_impl<128, 2>(a, s);
   return BI_ERR_UNSUPPORTED;
 }
 

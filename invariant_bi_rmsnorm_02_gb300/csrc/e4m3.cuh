@@ -33,6 +33,10 @@ __device__ __forceinline__ uint32_t q8_factor2(uint32_t c) { return c * 0x008000
 __device__ __forceinline__ uint32_t q8_factors(uint32_t c0_c1) {
   return __byte_perm(c0_c1, 0, 0x4140) * 128u + kQ8FactorBias;
 }
+// The factor as fp32 (2^(c - 127 + 120), infinity for a non-finite row).
+__device__ __forceinline__ float q8_factor_f32(uint32_t c) {
+  return __uint_as_float((c + 120u) << 23);
+}
 // Product of bf16 pairs; exact here.
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
