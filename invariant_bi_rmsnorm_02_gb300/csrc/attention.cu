@@ -43,6 +43,7 @@
 // (one 16x64 box per 64 columns), completion counted on an mbarrier.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -958,44 +959,119 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
   if (!alive) s_abort = 1;
 }
 
+// mbarrier wait for the roles with slack (the fold and TMA warps): the thread
+// suspends in the wait (a hint of 20 us, then it tries again), leaving the
+// issue slots of its scheduler to the softmax warp beside it; bounded in time
+// like mbar_wait.  The MMA and softmax warps, whose waits are on the
+// critical path, use mbar_wait itself.
+__device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity, int* err,
+                                             volatile int* abort) {
+  if (mbar_try_wait_sleep(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (abort && *abort) return false;
+    if (global_ns() - t0 > kWaitNs) break;
+  }
+  record_error(err, BI_ERR_TIMEOUT);
+  if (abort) *abort = 1;
+  return false;
+}
+
 // ------------------------------------------- decode split, quantised cache
 // The same units, arithmetic and outputs over the records of the quantised
-// cache: every e4m3 element becomes the bf16 value that reading the cache
-// back gives (an exact product), so the sums are those of the bf16 kernel on
-// the pages read back, bit for bit.
+// cache: every e4m3 element stands for the bf16 value that reading the cache
+// back gives, and the sums are those of the bf16 kernel on the pages read
+// back, bit for bit.
 //
-// What bounds it: half the bytes per tile, but an element costs about 1.7
-// more instructions (unpacking, V's factor), ~1,600 per 64-key tile of
-// D = 128, while at the measured HBM rate an SM receives a tile every ~700
-// cycles.  So the work has to be spread over all four of an SM's schedulers
-// with two compute warps each: one block per SM holds kQ8Pairs pairs of a
-// compute warp (warps 0..7) and the producer warp that feeds it (8..15),
-// with the register file split between them.  (With the bf16 kernel's blocks
-// of one compute and one producer warp, all compute warps sat on two of the
-// four schedulers: 59% of their issue slots used against 9% of the others',
-// and the 64-request case took 149 us.)
+// What bounds it: half the bytes per tile, but every element has to be
+// unpacked for the MMA, and at the measured HBM rate an SM receives a 64-key
+// tile of D = 128 every ~700 cycles, in which its four schedulers issue
+// ~1,800 instructions at a good rate.  So the unpacking is kept short, the
+// work is spread over all four schedulers, and a unit is short enough that
+// the last ones do not run alone:
+//   * powers of two are moved where they cost least, changing no bit.  K's
+//     elements become fp16 numbers (one conversion a pair) with Q's rows in
+//     fp16 times a power of two each, and the key's scale multiplies the
+//     score.  (A row of Q whose elements do not all survive as fp16, more
+//     than 2^32 apart or not finite, takes the bf16 form of the same sums.)
+//     V's elements become bf16 bits times 2^-120 (three instructions a pair)
+//     and the key's scale, relative to the largest of the tiles so far,
+//     multiplies P's two parts instead;
+//   * a unit is the work of two compute warps: warp w takes keys 32 w ..
+//     32 w + 31 of a tile for the scores and the probabilities, the two
+//     exchange those through shared memory, and each takes half of the
+//     output's columns.  A block (one per SM) holds kGroups such pairs and a
+//     producer warp for each.
+// 64 requests, 194 MB of records: 78 us with the bf16 kernel's blocks of one
+// compute and one producer warp (all compute warps on two of the four
+// schedulers); 59 us with eight compute warps per SM, a unit each, and an
+// exact product per pair for every scale (1,800 instructions a tile, 5,200
+// cycles a tile and warp, 9.6 tiles a warp on average but 12 at most); 62 us
+// with four warps to a unit (2,750 instructions a tile).
 //
-// A pair's ring holds kStages half tiles, K and V in turn: K's half goes back
+// A group's ring holds kStages half tiles, K and V in turn: K's half goes back
 // to the producer as soon as the scores are done.  The tile's scale bytes
 // ride with its K half in a ring of their own (kScaleSlots tiles): a slot is
 // written again only after a wait that follows the release of the V half
 // that reads it.
-constexpr int kQ8Pairs = 8;
-constexpr int kQ8Threads = 2 * kQ8Pairs * 32;
-constexpr int kQ8ComputeRegs = 200, kQ8ProducerRegs = 56;
-static_assert((kQ8ComputeRegs + kQ8ProducerRegs) * kQ8Pairs * 32 <= 65536,
-              "the two shares are the launch's 128 registers a thread");
+constexpr int kQ8Warps = 2;  // compute warps of a group
 
-template <int D>
+// mma_bf16, and the same with fp16 operands, as functions of their registers
+// alone, which the compiler may move among the loads of other fragments.
+__device__ __forceinline__ void mma_bf16_free(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_free(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// What the warps of a group hand one another for a tile.
+template <int NQ>
+struct Q8Exchange {
+  uint4 frag[4][NQ][32];        // P^T fragments of each 16 keys: high (2), low (2) parts
+  float2 sum[NQ][32];           // warp 0's running sums of the columns, for warp 1 to go on with
+  float top[kQ8Warps][8 * NQ];  // the column maxima of each warp's keys
+  float l[8 * NQ];              // the sums, at the end of a unit
+};
+
+template <int D, int NQ>
 struct Q8Geom {
+  // More groups hide more latency; G > 8 needs the registers of four.
+  static constexpr int kGroups = NQ == 1 ? 6 : 4;
+  static constexpr int kThreads = kGroups * (kQ8Warps + 1) * 32;
   static constexpr int kRecord = kv_q8_record_bytes(D);
   static constexpr int kPageHalf = kPage * D;               // one page's K (or V) bytes
   static constexpr int kHalf = kPagesPerTile * kPageHalf;   // one ring stage
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kScaleSlots = D == 128 ? 2 : 4;
+  static constexpr int kStages = 4 * (128 / D);
+  static constexpr int kScaleSlots = 3 * (128 / D);
   static constexpr int kScaleBytes = 2 * kTile;             // per tile: page p at 32 p, K then V
-  static constexpr int kPairBytes = kStages * kHalf;
-  static constexpr int kSmem = 1024 + kQ8Pairs * (kPairBytes + kScaleSlots * kScaleBytes);
+  static constexpr int kRingBytes = kStages * kHalf;
+  static constexpr int kScaleOff = kGroups * kRingBytes;
+  static constexpr int kExchangeOff = kScaleOff + kGroups * kScaleSlots * kScaleBytes;
+  static constexpr int kSmem =
+      1024 + kExchangeOff + kGroups * static_cast<int>(sizeof(Q8Exchange<NQ>));
+  static_assert(2 * kScaleSlots > kStages, "a scale slot outlives its tile's V half");
+  static_assert(kExchangeOff % 16 == 0 && sizeof(Q8Exchange<NQ>) % 16 == 0, "alignment");
 };
 
 // byte offset of 16-byte chunk c of key n's row in a half tile: the TMA
@@ -1004,65 +1080,121 @@ template <int D>
 __device__ __forceinline__ uint32_t q8_off(int n, int c) {
   const int r = n & 15;
   const int x = D == 128 ? (r & 7) : ((r >> 1) & 3);
-  return (uint32_t)((n >> 4) * Q8Geom<D>::kPageHalf + r * D + ((c ^ x) << 4));
+  return (uint32_t)((n >> 4) * kPage * D + r * D + ((c ^ x) << 4));
 }
 
-// K's elements enter the score MMA without their scale, as their value times
-// 2^-120 (e4m3_even / e4m3_odd); Q times 2^32 keeps the fp32 sums far from
-// fp32's smallest numbers, and the key's factor 2^(e + 120) afterwards makes
-// each score its true value times 2^32, which the softmax's scale takes off.
-// All of these are powers of two, so no bit of a score changes.
-constexpr uint32_t kQ8QScale = 0x4f804f80u;   // 2^32 as a bf16 pair
-constexpr float kQ8ScoreScale = 0x1p-32f;
-
-// Q^T fragments straight from global memory.  A k-step's 16 elements of a key
-// reach a thread as bytes d = 4t .. 4t+3 (t = lane % 4): the even ones take
-// the MMA's k positions 2t, 2t+1 and the odd ones 2t+8, 2t+9, and Q's
-// elements go to the same places (the MMA's sum over a k-step does not depend
-// on the order inside it; the tests compare the bytes with the bf16 kernel).
-// Rows G .. 8 NQ - 1 are zero.
+// Q^T fragments of a unit straight from global memory, and each column's
+// factor from a score sum to its logarithmic score (the softmax scale times
+// the power of two that was taken into Q).  A k-step's 16 elements of a key
+// reach a thread as bytes d = 4t .. 4t+3 (t = lane % 4), and Q's elements go to
+// the same places of the MMA's k (its sum over a k-step does not depend on the
+// order inside it; the tests compare the bytes with the bf16 kernel).  Rows
+// G .. 8 NQ - 1 are zero.  Returns whether the fragments are fp16: each row
+// times 2^k with its largest element in [2^15, 2^16), exact for elements down
+// to 2^-32 of it; otherwise bf16 times 2^32, for K's elements times 2^-120.
 template <int D, int NQ>
-__device__ __forceinline__ void q8_load_q(uint32_t (&qf)[NQ][D / 16][2], const __nv_bfloat16* q,
-                                          int G) {
+__device__ __forceinline__ bool q8_load_q(uint32_t (&qf)[NQ][D / 16][2], float (&sc)[NQ][2],
+                                          const __nv_bfloat16* q, int G, float scale_log2) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  bool exact = true;
+  float grow[NQ], shrink[NQ];  // 2^(15 - e) for a row's largest exponent e, and its inverse
 #pragma unroll
-  for (int nq = 0; nq < NQ; ++nq)
+  for (int nq = 0; nq < NQ; ++nq) {
+    uint32_t top = 0;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint2 x = make_uint2(0, 0);
       if (8 * nq + g < G)
         x = *reinterpret_cast<const uint2*>(q + (8 * nq + g) * D + 16 * ks + 4 * t);
-      qf[nq][ks][0] = mul_bf16x2(__byte_perm(x.x, x.y, 0x5410), kQ8QScale);
-      qf[nq][ks][1] = mul_bf16x2(__byte_perm(x.x, x.y, 0x7632), kQ8QScale);
+      qf[nq][ks][0] = x.x;
+      qf[nq][ks][1] = x.y;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        top = max(top, max(qf[nq][ks][i] & 0x7fffu, (qf[nq][ks][i] >> 16) & 0x7fffu));
     }
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
+    top = max(top, __shfl_xor_sync(kFull, top, 2));
+    const int up = min(253, 269 - (int)(top >> 7));  // both are normal numbers
+    grow[nq] = __uint_as_float((uint32_t)up << 23);
+    shrink[nq] = __uint_as_float((uint32_t)(254 - up) << 23);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float a = __fmul_rn(bf16_lo(qf[nq][ks][i]), grow[nq]);
+        const float b = __fmul_rn(bf16_hi(qf[nq][ks][i]), grow[nq]);
+        exact = exact && __half2float(__float2half_rn(a)) == a &&
+                __half2float(__float2half_rn(b)) == b;
+      }
+  }
+  exact = __all_sync(kFull, exact);
+#pragma unroll
+  for (int nq = 0; nq < NQ; ++nq) {
+    if (exact) {
+      // column 8 nq + 2t + cc is the row that lanes 4 (2t + cc) .. + 3 hold
+      sc[nq][0] = __fmul_rn(scale_log2, __shfl_sync(kFull, shrink[nq], 8 * t));
+      sc[nq][1] = __fmul_rn(scale_log2, __shfl_sync(kFull, shrink[nq], 8 * t + 4));
+    } else {
+      sc[nq][0] = sc[nq][1] = __fmul_rn(scale_log2, 0x1p88f);
+    }
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const uint32_t x = qf[nq][ks][0], y = qf[nq][ks][1];
+      if (exact) {
+        qf[nq][ks][0] = pack_f16x2(bf16_lo(x) * grow[nq], bf16_hi(x) * grow[nq]);
+        qf[nq][ks][1] = pack_f16x2(bf16_lo(y) * grow[nq], bf16_hi(y) * grow[nq]);
+      } else {  // e4m3_even takes a key's elements 4t and 4t + 2, e4m3_odd the others
+        qf[nq][ks][0] = mul_bf16x2(__byte_perm(x, y, 0x5410), 0x4f804f80u);
+        qf[nq][ks][1] = mul_bf16x2(__byte_perm(x, y, 0x7632), 0x4f804f80u);
+      }
+    }
+  }
+  return exact;
 }
 
-// S^T = K Q^T of a half tile, times 2^32: 4 m-tiles of 16 keys.
-template <int D, int NQ>
-__device__ __forceinline__ void q8_scores(float (&s)[4][NQ][4],
+// S^T = K Q^T of keys 32 w .. 32 w + 31 of a half tile, in two m-tiles: the
+// sums of the products with the stored numbers, times the keys' scales.
+template <int D, int NQ, bool kF16>
+__device__ __forceinline__ void q8_scores(float (&s)[2][NQ][4],
                                           const uint32_t (&qf)[NQ][D / 16][2], uint32_t kbase,
-                                          const uint8_t* scales) {
+                                          const uint8_t* scales, int w) {
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, mi = lane >> 3, r8 = lane & 7;
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt) {
+  for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) s[mt][nq][0] = s[mt][nq][1] = s[mt][nq][2] = s[mt][nq][3] = 0.0f;
 #pragma unroll
-    for (int kp = 0; kp < D / 32; ++kp) {
-      uint32_t r[4];  // keys g and g + 8 of k-steps 2 kp and 2 kp + 1
-      ldsm_x4(kbase + q8_off<D>(16 * mt + r8 + 8 * (mi & 1), 2 * kp + (mi >> 1)), r);
+  for (int kp = 0; kp < D / 32; ++kp) {
+    uint32_t r[2][4];  // keys g and g + 8 of k-steps 2 kp and 2 kp + 1
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t a[4] = {e4m3_even(r[2 * u]), e4m3_even(r[2 * u + 1]), e4m3_odd(r[2 * u]),
-                               e4m3_odd(r[2 * u + 1])};
+    for (int mt = 0; mt < 2; ++mt)
+      ldsm_x4(kbase + q8_off<D>(32 * w + 16 * mt + r8 + 8 * (mi & 1), 2 * kp + (mi >> 1)), r[mt]);
 #pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-          mma_bf16(s[mt][nq], a, qf[nq][2 * kp + u][0], qf[nq][2 * kp + u][1]);
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const uint32_t x0 = r[mt][2 * u], x1 = r[mt][2 * u + 1];
+        if constexpr (kF16) {
+          const uint32_t a[4] = {e4m3_f16_lo(x0), e4m3_f16_lo(x1), e4m3_f16_hi(x0),
+                                 e4m3_f16_hi(x1)};
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq)
+            mma_f16_free(s[mt][nq], a, qf[nq][2 * kp + u][0], qf[nq][2 * kp + u][1]);
+        } else {
+          const uint32_t a[4] = {e4m3_even(x0), e4m3_even(x1), e4m3_odd(x0), e4m3_odd(x1)};
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq)
+            mma_bf16_free(s[mt][nq], a, qf[nq][2 * kp + u][0], qf[nq][2 * kp + u][1]);
+        }
       }
-    }
-    const float f0 = q8_factor_f32(scales[32 * mt + g]);
-    const float f1 = q8_factor_f32(scales[32 * mt + 8 + g]);
+  }
+  // lane i has the scale of key 32 w + i (NaN for a row that is not finite)
+  const uint32_t c = scales[32 * (2 * w + (lane >> 4)) + (lane & 15)];
+  const float f = c == kQ8NonFinite ? CUDART_NAN_F : __uint_as_float(c << 23);
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    const float f0 = __shfl_sync(kFull, f, 16 * mt + g), f1 = __shfl_sync(kFull, f, 16 * mt + 8 + g);
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
       s[mt][nq][0] = __fmul_rn(s[mt][nq][0], f0);
@@ -1073,164 +1205,121 @@ __device__ __forceinline__ void q8_scores(float (&s)[4][NQ][4],
   }
 }
 
-// The softmax of tile_step on those scores: probabilities into s, the
-// running maximum, sum and o brought to the tile's reference.  Only the last
-// tile of a sequence has keys to mask (limit: its length in the tile);
-// padding columns are never read, so they need none.
-template <int D, int NQ>
-__device__ __forceinline__ void q8_softmax(SplitState<D, NQ>& st, float (&s)[4][NQ][4], int limit,
-                                           float scale) {
-  const int g = (threadIdx.x & 31) >> 2;
-  if (limit < kTile) {
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (16 * mt + g + 8 * (c >> 1) >= limit) s[mt][nq][c] = -CUDART_INF_F;
+// The factors of P for V's rows of two scale bytes, relative to the largest
+// scale byte `top` so far: 2^(c - top + 110).  V's elements carry 2^-120, so
+// O is held times 2^-(top - 127) - 10; its true scale comes back at the end
+// (q8_unscale).  A row that is not finite has an infinite factor: its
+// elements are 0, and 0 times infinity is NaN.
+constexpr int kQ8PScale = 110;
+__device__ __forceinline__ uint32_t q8_p_factors(uint32_t c0_c1, int top) {
+  const uint32_t c0 = c0_c1 & 0xffu, c1 = c0_c1 >> 8;
+  uint32_t f = (__byte_perm(c0_c1, 0, 0x4140) << 7) + (uint32_t)(127 + kQ8PScale - top) * 0x00800080u;
+  if (top >= kQ8NonFinite) {
+    if (c0 == kQ8NonFinite) f = (f & 0xffff0000u) | 0x7f80u;
+    if (c1 == kQ8NonFinite) f = (f & 0x0000ffffu) | 0x7f800000u;
   }
-  float alpha[NQ][2];
-  bool moved = false;
-#pragma unroll
-  for (int nq = 0; nq < NQ; ++nq) {
-    float mb[2], cs[2];
-#pragma unroll
-    for (int cc = 0; cc < 2; ++cc) {
-      float mx = fmaxf(s[0][nq][cc], s[0][nq][2 + cc]);
-#pragma unroll
-      for (int mt = 1; mt < 4; ++mt) mx = max3(mx, s[mt][nq][cc], s[mt][nq][2 + cc]);
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-      const float t = __fmul_rn(mx, scale), m_in = st.m[nq][cc];
-      float mnew = m_in;
-      alpha[nq][cc] = 1.0f;
-      if (t == -CUDART_INF_F) {
-        // no visible key: exact no-op for this column
-      } else if (m_in == -CUDART_INF_F) {
-        mnew = t;
-        alpha[nq][cc] = 0.0f;
-      } else if (__fsub_rn(t, m_in) > kRescaleLog2) {
-        mnew = t;
-        alpha[nq][cc] = exp2_sfu(__fsub_rn(m_in, t));
-      }
-      moved = moved || alpha[nq][cc] != 1.0f;
-      st.m[nq][cc] = mnew;
-      mb[cc] = mnew == -CUDART_INF_F ? 0.0f : mnew;
-      cs[cc] = 0.0f;
-    }
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int cc = c & 1;
-        const float pv = exp2_sfu(__fmaf_rn(s[mt][nq][c], scale, -mb[cc]));
-        s[mt][nq][c] = pv;
-        cs[cc] = __fadd_rn(cs[cc], pv);
-      }
-#pragma unroll
-    for (int cc = 0; cc < 2; ++cc) {
-      cs[cc] = __fadd_rn(cs[cc], __shfl_xor_sync(kFull, cs[cc], 4));
-      cs[cc] = __fadd_rn(cs[cc], __shfl_xor_sync(kFull, cs[cc], 8));
-      cs[cc] = __fadd_rn(cs[cc], __shfl_xor_sync(kFull, cs[cc], 16));
-      st.l[nq][cc] = __fadd_rn(__fmul_rn(st.l[nq][cc], alpha[nq][cc]), cs[cc]);
-    }
-  }
-  // a product with 1 changes nothing, so it is left out where no column moved
-  if (__any_sync(kFull, moved)) {
-#pragma unroll
-    for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-      for (int md = 0; md < D / 16; ++md)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          st.o[md][nq][c] = __fmul_rn(st.o[md][nq][c], alpha[nq][c & 1]);
-  }
+  return f;
+}
+__device__ __forceinline__ float q8_unscale(int top) {
+  return __uint_as_float((uint32_t)(top - 127 + 120 - kQ8PScale + 127) << 23);
 }
 
-// O^T += V^T P^T.  The transposing load moves 16-bit elements, so a thread
-// gets columns 2g and 2g + 1 of a 16-column chunk for keys 2t, 2t + 1: the
-// even bytes are the A operand's row g, the odd ones its row g + 8, and o's
-// rows stand for d = 16 md + 2g (c = 0, 1) and 16 md + 2g + 1 (c = 2, 3).
+// O^T += V^T P^T for the D / 2 columns of warp w.  The transposing load moves
+// 16-bit elements, so a thread gets columns 2g and 2g + 1 of a 16-column
+// chunk for keys 2t, 2t + 1: the even bytes are the A operand's row g, the
+// odd ones its row g + 8, and o's rows stand for the chunk's columns 2g
+// (c = 0, 1) and 2g + 1 (c = 2, 3).
 template <int D, int NQ>
-__device__ __forceinline__ void q8_values(SplitState<D, NQ>& st, const float (&s)[4][NQ][4],
-                                          uint32_t vbase, const uint8_t* scales) {
+__device__ __forceinline__ void q8_values(float (&o)[D / 32][NQ][4], const Q8Exchange<NQ>& ex,
+                                          uint32_t vbase, int w) {
+  constexpr int kChunks = D / 32;  // 16-column chunks of a warp
   const int lane = threadIdx.x & 31;
-  const int t = lane & 3, mi = lane >> 3, r8 = lane & 7;
+  const int mi = lane >> 3, r8 = lane & 7;
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
-    uint32_t bh[NQ][2], bl[NQ][2];
+    uint4 f[NQ];  // {high, high, low, low} of keys 16 kk + 0..7 and + 8..15
 #pragma unroll
-    for (int nq = 0; nq < NQ; ++nq)
+    for (int nq = 0; nq < NQ; ++nq) f[nq] = ex.frag[kk][nq][lane];
+    uint32_t a[kChunks][4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t hp, lp;
-        split_p_bf16(s[kk][nq][2 * half], s[kk][nq][2 * half + 1], hp, lp);
-        bh[nq][half] = transpose8x8(hp);
-        bl[nq][half] = transpose8x8(lp);
-      }
-    // factors of keys 16 kk + 2t, + 1 and of 16 kk + 8 + 2t, + 1
-    const uint8_t* sv = scales + 32 * kk + 16 + 2 * t;
-    const uint32_t f0 = q8_factors(*reinterpret_cast<const uint16_t*>(sv));
-    const uint32_t f1 = q8_factors(*reinterpret_cast<const uint16_t*>(sv + 8));
-#pragma unroll
-    for (int mp = 0; mp < D / 32; ++mp) {
-      uint32_t r[4];  // keys 0-7 and 8-15 of column chunks 2 mp and 2 mp + 1
-      ldsm_x4_t(vbase + q8_off<D>(16 * kk + r8 + 8 * (mi & 1), 2 * mp + (mi >> 1)), r);
+    for (int i = 0; i < kChunks / 2; ++i) {
+      uint32_t r[4];  // keys 0-7 and 8-15 of two chunks
+      ldsm_x4_t(vbase + q8_off<D>(16 * kk + r8 + 8 * (mi & 1), kChunks * w + 2 * i + (mi >> 1)), r);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t a[4] = {
-            mul_bf16x2(e4m3_even(r[2 * u]), f0), mul_bf16x2(e4m3_odd(r[2 * u]), f0),
-            mul_bf16x2(e4m3_even(r[2 * u + 1]), f1), mul_bf16x2(e4m3_odd(r[2 * u + 1]), f1)};
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) {
-          mma_bf16(st.o[2 * mp + u][nq], a, bh[nq][0], bh[nq][1]);
-          mma_bf16(st.o[2 * mp + u][nq], a, bl[nq][0], bl[nq][1]);
-        }
+        a[2 * i + u][0] = e4m3_even(r[2 * u]);
+        a[2 * i + u][1] = e4m3_odd(r[2 * u]);
+        a[2 * i + u][2] = e4m3_even(r[2 * u + 1]);
+        a[2 * i + u][3] = e4m3_odd(r[2 * u + 1]);
       }
     }
+    // P's high part before its low one for every sum; the sums of other
+    // chunks and n-tiles are independent
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u)
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) mma_bf16_free(o[u][nq], a[u], f[nq].x, f[nq].y);
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u)
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) mma_bf16_free(o[u][nq], a[u], f[nq].z, f[nq].w);
   }
 }
 
+// Barrier of one group's compute warps.
+__device__ __forceinline__ void q8_group_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kQ8Warps * 32) : "memory");
+}
+// The same, and whether x holds in all of its threads.
+__device__ __forceinline__ bool q8_group_all(int group, bool x) {
+  uint32_t r = x ? 1 : 0;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %0, 0;\n\t"
+      "bar.red.and.pred b, %1, %2, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+      : "+r"(r)
+      : "r"(group + 1), "n"(kQ8Warps * 32)
+      : "memory");
+  return r != 0;
+}
+
 template <int D, int NQ>
-__global__ void __launch_bounds__(kQ8Threads, 1) attn_decode_q8_split_kernel(
+__global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_split_kernel(
     const __grid_constant__ CUtensorMap map, const uint8_t* __restrict__ cache,
     const KernelParams p) {
-  using Geom = Q8Geom<D>;
-  constexpr int kStages = Geom::kStages;
+  using Geom = Q8Geom<D, NQ>;
+  constexpr int kStages = Geom::kStages, kQ8Groups = Geom::kGroups;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  __shared__ uint64_t b_full[kQ8Pairs][kStages], b_empty[kQ8Pairs][kStages];
-  __shared__ uint64_t b_ready[kQ8Pairs][kQueue], b_freed[kQ8Pairs][kQueue];
-  __shared__ int4 q_unit[kQ8Pairs][kQueue];   // b, j, lo, hi of opened units (b < 0: no more)
-  __shared__ int q_head[kQ8Pairs][kQueue];    // kv head h, or -(h+1) if its pages are bad
-  __shared__ int q_single[kQ8Pairs][kQueue];  // the sequence has this one split
+  __shared__ uint64_t b_full[kQ8Groups][kStages], b_empty[kQ8Groups][kStages];
+  __shared__ uint64_t b_ready[kQ8Groups][kQueue], b_freed[kQ8Groups][kQueue];
+  __shared__ int4 q_unit[kQ8Groups][kQueue];   // b, j, lo, hi of opened units (b < 0: no more)
+  __shared__ int q_head[kQ8Groups][kQueue];    // kv head h, or -(h+1) if its pages are bad
+  __shared__ int q_single[kQ8Groups][kQueue];  // the sequence has this one split
   __shared__ int s_incl[kLocalPlanMax], s_len[kLocalPlanMax];
-  __shared__ int s_plan[2];                   // the splits of all sequences, the variant's chunk
+  __shared__ int s_plan[2];                    // the splits of all sequences, the variant's chunk
   __shared__ int s_abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pair = warp % kQ8Pairs;
-  uint8_t* ring = smem + pair * Geom::kPairBytes;
-  uint8_t* scale_ring =
-      smem + kQ8Pairs * Geom::kPairBytes + pair * Geom::kScaleSlots * Geom::kScaleBytes;
-  uint64_t* full = b_full[pair];
-  uint64_t* empty = b_empty[pair];
-  uint64_t* ready = b_ready[pair];
-  uint64_t* freed = b_freed[pair];
+  const bool producer = warp >= kQ8Groups * kQ8Warps;
+  const int group = producer ? warp - kQ8Groups * kQ8Warps : warp / kQ8Warps;
+  uint8_t* ring = smem + group * Geom::kRingBytes;
+  uint8_t* scale_ring = smem + Geom::kScaleOff + group * Geom::kScaleSlots * Geom::kScaleBytes;
+  uint64_t* full = b_full[group];
+  uint64_t* empty = b_empty[group];
+  uint64_t* ready = b_ready[group];
+  uint64_t* freed = b_freed[group];
   const int G = p.G, Hkv = p.Hkv;
   if (threadIdx.x == 0) {
     prefetch_tmap(&map);
-    for (int w = 0; w < kQ8Pairs; ++w) {
+    for (int w = 0; w < kQ8Groups; ++w) {
       for (int i = 0; i < kStages; ++i) {
         mbar_init(&b_full[w][i], 1);
-        mbar_init(&b_empty[w][i], 1);
+        mbar_init(&b_empty[w][i], kQ8Warps);
       }
       for (int i = 0; i < kQueue; ++i) {
         mbar_init(&b_ready[w][i], 1);
-        mbar_init(&b_freed[w][i], 1);
+        mbar_init(&b_freed[w][i], kQ8Warps);
       }
     }
     s_abort = 0;
@@ -1313,11 +1402,10 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attn_decode_q8_split_kernel(
   }
   __syncthreads();
 
-  if (warp >= kQ8Pairs) {
+  if (producer) {
     // ============================================================ producer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQ8ProducerRegs));
     const int U = s_plan[0] * Hkv, csize = s_plan[1];
-    const int stride = gridDim.x * kQ8Pairs;
+    const int stride = gridDim.x * kQ8Groups;
     auto unit_at = [&](int s) -> int4 {  // {b, j, lo, hi} of split s; warp-uniform s
       if (!p.local_plan) return p.units[s];
       int b = 0;
@@ -1331,7 +1419,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attn_decode_q8_split_kernel(
     };
     // the pending unit: its descriptor and first page ids (in flight in
     // registers: lane i holds pages i and 32 + i)
-    int lu = pair * gridDim.x + blockIdx.x;  // next unit to fetch: neighbours on other SMs
+    int lu = group * gridDim.x + blockIdx.x;  // next unit to fetch: neighbours on other SMs
     bool pend = false;
     int4 pd = make_int4(0, 0, 0, 0);
     int ph = 0, pg0 = 0, pg1 = 0;
@@ -1349,18 +1437,18 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attn_decode_q8_split_kernel(
     const uint64_t pol = l2_policy_evict_first();
     int n_units = 0, n = 0, tiles = 0;  // units opened, stages filled, tiles issued
     int stage = 0;
-    uint32_t phase = 1;                 // parity of the wait for a free stage (first round: free)
+    uint32_t phase = 1;                 // parity of the wait for a free stage
     bool ok = true;
     fetch();
     while (ok) {
       const int slot = n_units % kQueue;
       if (n_units >= kQueue)
-        ok = __all_sync(kFull, mbar_wait(&freed[slot], ((n_units / kQueue) - 1) & 1, p.err,
+        ok = __all_sync(kFull, mbar_wait_lazy(&freed[slot], ((n_units / kQueue) - 1) & 1, p.err,
                                          &s_abort));
       if (!ok) break;
       if (!pend) {  // no more units: the end marker
         if (lane == 0) {
-          q_unit[pair][slot] = make_int4(-1, 0, 0, 0);
+          q_unit[group][slot] = make_int4(-1, 0, 0, 0);
           mbar_arrive(&ready[slot]);
         }
         break;
@@ -1377,9 +1465,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attn_decode_q8_split_kernel(
         // split 0 is the only one iff it ends below the chunk size or the
         // sequence is exactly one chunk long
         const int c = p.variant ? csize : p.split_size;
-        q_unit[pair][slot] = d;
-        q_head[pair][slot] = good ? h : -(h + 1);
-        q_single[pair][slot] =
+        q_unit[group][slot] = d;
+        q_head[group][slot] = good ? h : -(h + 1);
+        q_single[group][slot] =
             d.y == 0 && (d.w < c || (p.local_plan ? s_len[d.x] : p.kv_lens[d.x]) == c);
         if (!good) record_error(p.err, BI_ERR_DEVICE_BOUNDS);
         mbar_arrive(&ready[slot]);
@@ -1398,7 +1486,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attn_decode_q8_split_kernel(
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // K, then V
           if (n >= kStages)
-            ok = __all_sync(kFull, mbar_wait(&empty[stage], phase, p.err, &s_abort));
+            ok = __all_sync(kFull, mbar_wait_lazy(&empty[stage], phase, p.err, &s_abort));
           if (!ok) break;
           uint64_t* bar = &full[stage];
           if (lane == 0)
@@ -1428,14 +1516,24 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attn_decode_q8_split_kernel(
     return;
   }
   // ============================================================== compute
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQ8ComputeRegs));
-  const float scale = p.scale_log2 * kQ8ScoreScale;
-  SplitState<D, NQ> st;
+  // A wait that runs out (or is ended by the flag that another's raised)
+  // makes its warp go on without data to the end of the unit, through all of
+  // the group's barriers; the group agrees at the start of each unit to go on
+  // or to leave, so no warp is left at a barrier that another skips.
+  constexpr int kChunks = D / 32;
+  const int w = warp % kQ8Warps;
+  Q8Exchange<NQ>& ex = reinterpret_cast<Q8Exchange<NQ>*>(smem + Geom::kExchangeOff)[group];
   uint32_t qf[NQ][D / 16][2];
+  float sc[NQ][2];
+  float o[kChunks][NQ][4], m[NQ][2], l[NQ][2];  // l: warp 1's
+  int vtop = 0;                                 // the largest V scale byte so far
   const int g = lane >> 2, t = lane & 3;
   int n = 0, tiles = 0, stage = 0;
   uint32_t phase = 0;
   bool alive = true;
+  auto wait_stage = [&]() {
+    alive = __all_sync(kFull, alive && mbar_wait(&full[stage], phase, p.err, &s_abort));
+  };
   auto next_stage = [&]() {  // back to the producer, on to the next
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[stage]);
@@ -1446,13 +1544,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attn_decode_q8_split_kernel(
   };
   for (;;) {
     const int slot = n % kQueue;
-    if (!__all_sync(kFull, mbar_wait(&ready[slot], (n / kQueue) & 1, p.err, &s_abort))) {
-      alive = false;
-      break;
-    }
-    const int4 d = q_unit[pair][slot];
-    const int hv = q_head[pair][slot];
-    const bool single = q_single[pair][slot] != 0;
+    alive = alive && mbar_wait(&ready[slot], (n / kQueue) & 1, p.err, &s_abort);
+    if (!q8_group_all(group, alive)) break;
+    const int4 d = q_unit[group][slot];
+    const int hv = q_head[group][slot];
+    const bool single = q_single[group][slot] != 0;
     __syncwarp();
     if (lane == 0) mbar_arrive(&freed[slot]);
     ++n;
@@ -1462,81 +1558,219 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attn_decode_q8_split_kernel(
     const int b = d.x, j = d.y, lo = d.z, hi = d.w;
     const int64_t row0 = (int64_t)b * p.Hq + (int64_t)h * G;  // first q-head row
     if (!pages_good) {  // l = -1 makes the merge emit zeros
-      if (single) {
+      if (w == 0 && single) {
         for (int i = lane; i < G * D; i += 32) {
           static_cast<__nv_bfloat16*>(p.out)[row0 * D + i] = __float2bfloat16_rn(0.0f);
           if (p.out_f32) p.out_f32[row0 * D + i] = 0.0f;
         }
-      } else if (lane < G) {
+      } else if (w == 0 && lane < G) {
         const int64_t s = (row0 + lane) * p.ml_stride + j;
         p.ml[2 * s] = -CUDART_INF_F;
         p.ml[2 * s + 1] = -1.0f;
       }
       continue;
     }
-    q8_load_q<D, NQ>(qf, p.q + row0 * D, G);
-    st.reset();
+    const bool f16 = q8_load_q<D, NQ>(qf, sc, p.q + row0 * D, G, p.scale_log2);
+    vtop = 0;
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq) {
+      m[nq][0] = m[nq][1] = -CUDART_INF_F;
+      l[nq][0] = l[nq][1] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kChunks; ++u)
+        o[u][nq][0] = o[u][nq][1] = o[u][nq][2] = o[u][nq][3] = 0.0f;
+    }
     for (int key0 = lo; key0 < hi; key0 += kTile, ++tiles) {
       uint8_t* scales = scale_ring + (tiles % Geom::kScaleSlots) * Geom::kScaleBytes;
       const int limit = hi - key0;  // keys of the tile that exist (or more)
-      float s[4][NQ][4];
-      if (!__all_sync(kFull, mbar_wait(&full[stage], phase, p.err, &s_abort))) {
-        alive = false;
-        break;
-      }
-      q8_scores<D, NQ>(s, qf, smem_u32(ring + stage * Geom::kHalf), scales);
-      next_stage();
-      q8_softmax<D, NQ>(st, s, limit, scale);
-      if (!__all_sync(kFull, mbar_wait(&full[stage], phase, p.err, &s_abort))) {
-        alive = false;
-        break;
-      }
+      float s[2][NQ][4];
+      wait_stage();
+      if (f16)
+        q8_scores<D, NQ, true>(s, qf, smem_u32(ring + stage * Geom::kHalf), scales, w);
+      else
+        q8_scores<D, NQ, false>(s, qf, smem_u32(ring + stage * Geom::kHalf), scales, w);
+      // the largest V scale of the tile's keys
+      const uint32_t cv = *reinterpret_cast<const uint16_t*>(scales + 32 * (lane >> 3) + 16 +
+                                                             2 * (lane & 7));
+      uint32_t c0 = cv & 0xffu, c1 = cv >> 8;
       if (limit < kTile) {
-        // The V scale bytes of slots behind the last token become 0: those
-        // slots may hold any bits, and an element is finite whatever its
-        // bits, so a finite factor is enough for 0 * v to be 0.
-        for (int i = limit + lane; i < kTile; i += 32) scales[32 * (i >> 4) + 16 + (i & 15)] = 0;
-        __syncwarp();
+        // Keys behind the last token are masked, and their V scale bytes
+        // become 0: those slots may hold any bits, and an element is finite
+        // whatever its bits, so a finite factor is enough for 0 * v to be 0.
+        // Padding columns are never read and need no mask.
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (32 * w + 16 * mt + g + 8 * (c >> 1) >= limit) s[mt][nq][c] = -CUDART_INF_F;
+        if (2 * lane >= limit) c0 = 0;
+        if (2 * lane + 1 >= limit) c1 = 0;
       }
-      q8_values<D, NQ>(st, s, smem_u32(ring + stage * Geom::kHalf), scales);
-      // this warp's bytes before the copy that will overwrite them
-      if (limit < kTile) fence_proxy_async_smem();
+      const int vnew =
+          max(vtop, (int)min(__reduce_max_sync(kFull, max(c0, c1)), (uint32_t)kQ8NonFinite));
+      next_stage();
+      // ---- the tile's column maxima over both warps' keys
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+        float2 mx = make_float2(fmaxf(max3(s[0][nq][0], s[0][nq][2], s[1][nq][0]), s[1][nq][2]),
+                                fmaxf(max3(s[0][nq][1], s[0][nq][3], s[1][nq][1]), s[1][nq][3]));
+#pragma unroll
+        for (int x = 4; x <= 16; x <<= 1) {
+          mx.x = fmaxf(mx.x, __shfl_xor_sync(kFull, mx.x, x));
+          mx.y = fmaxf(mx.y, __shfl_xor_sync(kFull, mx.y, x));
+        }
+        if (g == 0) *reinterpret_cast<float2*>(&ex.top[w][8 * nq + 2 * t]) = mx;
+      }
+      q8_group_sync(group);
+      // ---- reference, probabilities of this warp's keys: tile_step's rules
+      uint32_t vf[2][2];  // P's factors of keys 16 kk + 2t, + 1 and + 8
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // the bytes of masked keys read as 0
+          const int k = 32 * w + 16 * mt + 8 * half + 2 * t;
+          uint32_t c = *reinterpret_cast<const uint16_t*>(scales + 32 * (2 * w + mt) + 16 +
+                                                          8 * half + 2 * t);
+          if (k >= limit) c = 0;
+          if (k + 1 >= limit) c &= 0xffu;
+          vf[mt][half] = q8_p_factors(c, vnew);
+        }
+      const float vshift = __uint_as_float((uint32_t)max(0, vtop - vnew + 127) << 23);
+      bool moved = vnew != vtop;
+      vtop = vnew;
+      float alpha[NQ][2], cs[NQ][2];
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+        float mb[2];
+        const float2 x0 = *reinterpret_cast<const float2*>(&ex.top[0][8 * nq + 2 * t]);
+        const float2 x1 = *reinterpret_cast<const float2*>(&ex.top[1][8 * nq + 2 * t]);
+        const float mx[2] = {fmaxf(x0.x, x1.x), fmaxf(x0.y, x1.y)};
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          const float top = __fmul_rn(mx[cc], sc[nq][cc]), m_in = m[nq][cc];
+          alpha[nq][cc] = 1.0f;
+          if (top == -CUDART_INF_F) {
+            // no visible key: exact no-op for this column
+          } else if (m_in == -CUDART_INF_F) {
+            m[nq][cc] = top;
+            alpha[nq][cc] = 0.0f;
+          } else if (__fsub_rn(top, m_in) > kRescaleLog2) {
+            m[nq][cc] = top;
+            alpha[nq][cc] = exp2_sfu(__fsub_rn(m_in, top));
+          }
+          moved = moved || alpha[nq][cc] != 1.0f;
+          mb[cc] = m[nq][cc] == -CUDART_INF_F ? 0.0f : m[nq][cc];
+          cs[nq][cc] = 0.0f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            s[mt][nq][c] = exp2_sfu(__fmaf_rn(s[mt][nq][c], sc[nq][c & 1], -mb[c & 1]));
+          uint32_t hp[2], lp[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            split_p_bf16(s[mt][nq][2 * half], s[mt][nq][2 * half + 1], hp[half], lp[half]);
+            hp[half] = mul_bf16x2(transpose8x8(hp[half]), vf[mt][half]);
+            lp[half] = mul_bf16x2(transpose8x8(lp[half]), vf[mt][half]);
+          }
+          ex.frag[2 * w + mt][nq][lane] = make_uint4(hp[0], hp[1], lp[0], lp[1]);
+        }
+        // a thread's keys are summed in order: warp 0's, then warp 1's
+        if (w == 0) {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            cs[nq][0] = __fadd_rn(__fadd_rn(cs[nq][0], s[mt][nq][0]), s[mt][nq][2]);
+            cs[nq][1] = __fadd_rn(__fadd_rn(cs[nq][1], s[mt][nq][1]), s[mt][nq][3]);
+          }
+          ex.sum[nq][lane] = make_float2(cs[nq][0], cs[nq][1]);
+        }
+      }
+      q8_group_sync(group);
+      if (w == 1) {
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+          const float2 before = ex.sum[nq][lane];
+          cs[nq][0] = before.x;
+          cs[nq][1] = before.y;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            cs[nq][0] = __fadd_rn(__fadd_rn(cs[nq][0], s[mt][nq][0]), s[mt][nq][2]);
+            cs[nq][1] = __fadd_rn(__fadd_rn(cs[nq][1], s[mt][nq][1]), s[mt][nq][3]);
+          }
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            cs[nq][cc] = __fadd_rn(cs[nq][cc], __shfl_xor_sync(kFull, cs[nq][cc], 4));
+            cs[nq][cc] = __fadd_rn(cs[nq][cc], __shfl_xor_sync(kFull, cs[nq][cc], 8));
+            cs[nq][cc] = __fadd_rn(cs[nq][cc], __shfl_xor_sync(kFull, cs[nq][cc], 16));
+            l[nq][cc] = __fadd_rn(__fmul_rn(l[nq][cc], alpha[nq][cc]), cs[nq][cc]);
+          }
+        }
+      }
+      // a product with 1 changes nothing, so it is left out where none moved
+      if (__any_sync(kFull, moved)) {
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+          for (int u = 0; u < kChunks; ++u)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              o[u][nq][c] = __fmul_rn(__fmul_rn(o[u][nq][c], alpha[nq][c & 1]), vshift);
+      }
+      wait_stage();
+      q8_values<D, NQ>(o, ex, smem_u32(ring + stage * Geom::kHalf), w);
       next_stage();
     }
-    if (!alive) break;
+    const float back = q8_unscale(vtop);
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+      for (int u = 0; u < kChunks; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[u][nq][c] = __fmul_rn(o[u][nq][c], back);
     // ---- the output of a single split, or the partial state; columns d and
     // d + 1 are neighbours in a thread
+    if (single) {
+      if (w == 1 && g == 0) {
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+          *reinterpret_cast<float2*>(&ex.l[8 * nq + 2 * t]) = make_float2(l[nq][0], l[nq][1]);
+      }
+      q8_group_sync(group);
+    }
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         const int col = 8 * nq + 2 * t + cc;
         if (col >= G) continue;
-        const float lv = st.l[nq][cc];
+        const int dcol = 16 * kChunks * w + 2 * g;
         if (single) {
-          const float rl = inv_l(lv);
-          const int64_t orow = (row0 + col) * D + 2 * g;
+          const float lv = ex.l[col], rl = inv_l(lv);
+          const int64_t orow = (row0 + col) * D + dcol;
 #pragma unroll
-          for (int md = 0; md < D / 16; ++md) {
-            const float v0 = lv > 0.0f ? normalize(st.o[md][nq][cc], rl) : 0.0f;
-            const float v1 = lv > 0.0f ? normalize(st.o[md][nq][2 + cc], rl) : 0.0f;
-            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow + 16 * md) =
+          for (int u = 0; u < kChunks; ++u) {
+            const float v0 = lv > 0.0f ? normalize(o[u][nq][cc], rl) : 0.0f;
+            const float v1 = lv > 0.0f ? normalize(o[u][nq][2 + cc], rl) : 0.0f;
+            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow + 16 * u) =
                 pack_bf16x2(v0, v1);
             if (p.out_f32)
-              *reinterpret_cast<float2*>(p.out_f32 + orow + 16 * md) = make_float2(v0, v1);
+              *reinterpret_cast<float2*>(p.out_f32 + orow + 16 * u) = make_float2(v0, v1);
           }
           continue;
         }
-        const int64_t sm = (row0 + col) * p.ml_stride + j;
-        if (g == 0) {
-          p.ml[2 * sm] = st.m[nq][cc];
-          p.ml[2 * sm + 1] = lv;
+        if (w == 1 && g == 0) {
+          const int64_t sm = (row0 + col) * p.ml_stride + j;
+          p.ml[2 * sm] = m[nq][cc];
+          p.ml[2 * sm + 1] = l[nq][cc];
         }
-        float* orow = p.o + ((row0 + col) * p.max_splits + j) * D + 2 * g;
+        float* orow = p.o + ((row0 + col) * p.max_splits + j) * D + dcol;
 #pragma unroll
-        for (int md = 0; md < D / 16; ++md)
-          *reinterpret_cast<float2*>(orow + 16 * md) =
-              make_float2(st.o[md][nq][cc], st.o[md][nq][2 + cc]);
+        for (int u = 0; u < kChunks; ++u)
+          *reinterpret_cast<float2*>(orow + 16 * u) = make_float2(o[u][nq][cc], o[u][nq][2 + cc]);
       }
   }
   if (!alive) s_abort = 1;
@@ -1718,36 +1952,6 @@ struct PfGeom {
   static constexpr uint32_t kColS = 0, kColO = 2 * kPfPair, kColQ = kColO + 128;
 };
 static_assert(PfGeom<128>::kSmem <= 232448, "prefill shared memory");
-
-// mbarrier wait for the roles with slack (the fold and TMA warps): the thread
-// suspends in the wait (a hint of 20 us, then it tries again), leaving the
-// issue slots of its scheduler to the softmax warp beside it; bounded in time
-// like mbar_wait.  The MMA and softmax warps, whose waits are on the
-// critical path, use mbar_wait itself.
-__device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool pf_wait_lazy(uint64_t* bar, uint32_t parity, int* err,
-                                             volatile int* abort) {
-  if (mbar_try_wait_sleep(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait_sleep(bar, parity)) return true;
-    if (abort && *abort) return false;
-    if (global_ns() - t0 > kWaitNs) break;
-  }
-  record_error(err, BI_ERR_TIMEOUT);
-  if (abort) *abort = 1;
-  return false;
-}
 
 // Wait for up to three barriers: their first tests go out back to back (the
 // common case is that all are complete), then each missing one is waited for.
@@ -1953,7 +2157,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
       if (!is_v) {
         for (int q = 0; q < npairs && ok; ++q) {
           if (q >= kPfKStages)
-            ok = pf_wait_lazy(&kfree[q % kPfKStages], ((q / kPfKStages) - 1) & 1, p.err,
+            ok = mbar_wait_lazy(&kfree[q % kPfKStages], ((q / kPfKStages) - 1) & 1, p.err,
                               &s_abort);
           if (!ok) break;
           issue(kst + (q % kPfKStages) * Gm::kKBytes + hf * (kPfPair * 128),
@@ -1962,12 +2166,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
         }
         // every copy lands before the block exits (bounded waits)
         for (int k = max(0, n - kPfKStages); k < n; ++k)
-          pf_wait_lazy(&kfull[k % kPfKStages], (k / kPfKStages) & 1, ok ? p.err : nullptr,
+          mbar_wait_lazy(&kfull[k % kPfKStages], (k / kPfKStages) & 1, ok ? p.err : nullptr,
                        ok ? &s_abort : nullptr);
       } else {
         for (int i = 0; i < ntiles && ok; ++i) {
           if (i >= kPfVStages)
-            ok = pf_wait_lazy(&vfree[i % kPfVStages], ((i / kPfVStages) - 1) & 1, p.err,
+            ok = mbar_wait_lazy(&vfree[i % kPfVStages], ((i / kPfVStages) - 1) & 1, p.err,
                               &s_abort);
           if (!ok) break;
           issue(vst + (i % kPfVStages) * Gm::kVBytes + hf * (kTile * 128),
@@ -1975,7 +2179,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
           ++n;
         }
         for (int k = max(0, n - kPfVStages); k < n; ++k)
-          pf_wait_lazy(&vfull[k % kPfVStages], (k / kPfVStages) & 1, ok ? p.err : nullptr,
+          mbar_wait_lazy(&vfull[k % kPfVStages], (k / kPfVStages) & 1, ok ? p.err : nullptr,
                        ok ? &s_abort : nullptr);
       }
     }
@@ -2220,8 +2424,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
     bool have = false;
     bool live = true;
     for (int j = 0; j < nsplits && live; ++j) {
-      live = __all_sync(kFull, pf_wait_lazy(&sdone[j & 1], (j >> 1) & 1, p.err, &s_abort) &&
-                                   pf_wait_lazy(odone, j & 1, p.err, &s_abort));
+      live = __all_sync(kFull, mbar_wait_lazy(&sdone[j & 1], (j >> 1) & 1, p.err, &s_abort) &&
+                                   mbar_wait_lazy(odone, j & 1, p.err, &s_abort));
       if (!live) break;
       tc_fence_after();
       const float m_s = xsplit[(j & 1) * 2 * kPfRows + r];
@@ -2471,15 +2675,16 @@ bi_status decode_q8_impl(const AttnArgs& a, cudaStream_t s) {
     p.ml_stride = w.ml_stride;
     p.local_plan = a.B <= kLocalPlanMax;
     if (p.local_plan) p.order = reinterpret_cast<int2*>(base + w.units_off);  // units unused
-    const size_t sm = Q8Geom<D>::kSmem;
+    const size_t sm = Q8Geom<D, NQ>::kSmem;
     if (set_smem(attn_decode_q8_split_kernel<D, NQ>, sm) != cudaSuccess) return BI_ERR_CUDA;
     const int sms = device_sm_count();
     if (sms <= 0) return BI_ERR_CUDA;
     const int64_t max_units = static_cast<int64_t>(a.B) * a.Hkv * a.max_splits;
-    p.target_units = 4 * kQ8Pairs * sms;  // variant: units per pair, as the bf16 kernel's
+    p.target_units = 4 * Q8Geom<D, NQ>::kGroups * sms;  // variant: units per group, as the bf16 kernel's
     if (!p.local_plan) attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
     const int grid = static_cast<int>(max_units < sms ? max_units : sms);
-    if (launch_pdl(attn_decode_q8_split_kernel<D, NQ>, dim3(grid), dim3(kQ8Threads), sm, s, map,
+    if (launch_pdl(attn_decode_q8_split_kernel<D, NQ>, dim3(grid), dim3(Q8Geom<D, NQ>::kThreads), sm, s,
+                   map,
                    static_cast<const uint8_t*>(a.k_cache), p) != cudaSuccess)
       return BI_ERR_CUDA;
   }

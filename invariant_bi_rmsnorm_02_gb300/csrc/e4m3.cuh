@@ -26,17 +26,33 @@ __device__ __forceinline__ uint32_t e4m3_even(uint32_t x) {
   return (y << 4) & 0x87f087f0u;
 }
 __device__ __forceinline__ uint32_t e4m3_odd(uint32_t x) {
-  return ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+  uint32_t y;
+  asm("prmt.b32 %0, %1, 0, 0xB391;" : "=r"(y) : "r"(x));
+  return (y << 4) & 0x87f087f0u;
 }
-// The factor of one scale byte in both halves; the factors of two.
+// Bytes 0 and 1 (2 and 3) of x as the fp16 pair (low, high), exact.
+__device__ __forceinline__ uint32_t e4m3_f16_lo(uint32_t x) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
+      : "=r"(y)
+      : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t e4m3_f16_hi(uint32_t x) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
+      : "=r"(y)
+      : "r"(x));
+  return y;
+}
+// The fp16 pair (low, high) of two floats.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The factor of one scale byte in both halves.
 __device__ __forceinline__ uint32_t q8_factor2(uint32_t c) { return c * 0x00800080u + kQ8FactorBias; }
-__device__ __forceinline__ uint32_t q8_factors(uint32_t c0_c1) {
-  return __byte_perm(c0_c1, 0, 0x4140) * 128u + kQ8FactorBias;
-}
-// The factor as fp32 (2^(c - 127 + 120), infinity for a non-finite row).
-__device__ __forceinline__ float q8_factor_f32(uint32_t c) {
-  return __uint_as_float((c + 120u) << 23);
-}
 // Product of bf16 pairs; exact here.
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
