@@ -7,7 +7,7 @@
 // Every output element is a function of its own head and position only, so
 // the result does not depend on the batch.
 #include <cuda_runtime.h>
-#include <math.h>
+#include <math_constants.h>
 
 #include "bi_internal.h"
 #include "device_common.cuh"
@@ -26,48 +26,163 @@ __device__ __forceinline__ uint64_t turn_fraction(double freq) {
   t -= floor(t);
   return __double2ull_rn(t * 18446744073709551616.0);  // 2^64
 }
-// Cosine and sine of phase 2^-64 turns.  The signed phase is converted with
-// its own relative precision, so small angles keep theirs.
-__device__ __forceinline__ void cos_sin(uint64_t phase, float& c, float& s) {
+// attn_scale times cosine and sine of pos * frac turns.  The signed phase is
+// converted with its own relative precision, so small angles keep theirs.
+__device__ __forceinline__ float2 cos_sin(int32_t pos, uint64_t frac, float attn_scale) {
+  const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * frac;
   const float half_turns = __ll2float_rn(static_cast<int64_t>(phase)) * 0x1p-63f;
+  float s, c;
   sincospif(half_turns, &s, &c);
+  return make_float2(__fmul_rn(c, attn_scale), __fmul_rn(s, attn_scale));
+}
+// (x0, x1) turned: both elements of a pair, rounded once to bf16 (low, high).
+__device__ __forceinline__ uint32_t rotate(float x0, float x1, float2 cs) {
+  return pack_bf16x2(__fsub_rn(__fmul_rn(x0, cs.x), __fmul_rn(x1, cs.y)),
+                     __fadd_rn(__fmul_rn(x1, cs.x), __fmul_rn(x0, cs.y)));
 }
 
-// One thread per pair of elements of a head: pair p < rot / 2 is rotated, the
-// others are the head's remaining elements, copied.
-__global__ void __launch_bounds__(kThreads) rope_pairs_kernel(
-    const uint16_t* __restrict__ qkv, const int32_t* __restrict__ pos, int64_t T, int Hq, int Hkv,
-    int D, int rot, bool interleaved, const double* __restrict__ freqs, float attn_scale,
-    uint16_t* __restrict__ q, uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
-  const int heads = Hq + 2 * Hkv, half = D / 2;
-  const int64_t total = T * heads * half;
+struct RopeArgs {
+  const void* qkv;
+  const int32_t* pos;
+  const double* freqs;
+  void *q, *k, *v;
+  int64_t T;
+  int Hq, Hkv, D, rot;
+  float attn_scale;
+  int tokens;                 // per step of a block
+  uint32_t inv_heads, inv_D, inv_half;  // reciprocals for div_by
+};
+
+// n / d for n * d < 2^32 through m = ceil(2^32 / d), exact there (m = 0: d = 1).
+__device__ __forceinline__ int div_by(int n, uint32_t m) {
+  return m ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), m)) : n;
+}
+
+// A block takes `tokens` tokens a step.  Its threads first make the step's
+// cosines and sines, each (token, pair) once for all heads, in shared memory
+// (the frequencies' turn fractions, the only fp64 work, once per block); then
+// every item of 16 elements, two 16-byte vectors, is read, turned or passed
+// through, and written by one thread.  The loads of an item do not depend on
+// the table, so they are issued before it is made.
+// Bound by memory: 8192 tokens of 32 + 2 * 8 heads of 128 move 201 MB.
+constexpr int kItems = 3;  // items in flight per thread
+
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+  const int heads = a.Hq + 2 * a.Hkv, half = a.rot / 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float2* table = reinterpret_cast<float2*>(smem);                       // [tokens][rot / 2]
+  uint64_t* frac = reinterpret_cast<uint64_t*>(table + a.tokens * half);  // [rot / 2]
+  float* amp = reinterpret_cast<float*>(frac + half);                    // [rot / 2]
+  for (int p = threadIdx.x; p < half; p += kThreads) {
+    const double f = a.freqs[p];
+    frac[p] = turn_fraction(f);
+    amp[p] = isfinite(f) ? a.attn_scale : CUDART_NAN_F;
+  }
+  const int per_head = a.D / 16, per_token = heads * per_head;
+  const int rot_items = a.rot / 16;
+  const uint4* src = static_cast<const uint4*>(a.qkv);
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
+       t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
+    const int nt = static_cast<int>(a.T - t0 < a.tokens ? a.T - t0 : a.tokens);
+    const int items = nt * per_token;
+    for (int i0 = 0; i0 < items; i0 += kItems * kThreads) {
+      uint4 x[kItems][2];
+      int tok[kItems], head[kItems], sub[kItems];
+#pragma unroll
+      for (int u = 0; u < kItems; ++u) {
+        const int i = i0 + u * kThreads + threadIdx.x;
+        if (i >= items) continue;
+        const int th = div_by(i, a.inv_D);   // (token, head) of the step
+        sub[u] = i - th * per_head;
+        tok[u] = div_by(th, a.inv_heads);
+        head[u] = th - tok[u] * heads;
+        const bool turn = head[u] < a.Hq + a.Hkv && sub[u] < rot_items;
+        const uint4* row = src + (t0 * heads + th) * (a.D / 8);
+        // rotate-half: a vector of the first half and its partner
+        const bool apart = !kInterleaved && turn;
+        x[u][0] = __ldcs(row + (apart ? sub[u] : 2 * sub[u]));
+        x[u][1] = __ldcs(row + (apart ? sub[u] + rot_items : 2 * sub[u] + 1));
+      }
+      if (i0 == 0) {
+        __syncthreads();  // the fractions are there, the last step's table has been read
+        for (int e = threadIdx.x; e < nt * half; e += kThreads) {
+          const int t = div_by(e, a.inv_half), p = e - t * half;
+          table[e] = cos_sin(a.pos[t0 + t], frac[p], amp[p]);
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int u = 0; u < kItems; ++u) {
+        const int i = i0 + u * kThreads + threadIdx.x;
+        if (i >= items) continue;
+        const bool turn = head[u] < a.Hq + a.Hkv && sub[u] < rot_items;
+        if (turn) {
+          const float4* cs4 =
+              reinterpret_cast<const float4*>(table + tok[u] * half + 8 * sub[u]);
+          uint32_t r0[4] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w};
+          uint32_t r1[4] = {x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float4 c = cs4[w];  // pairs 2w and 2w + 1 of the item's eight
+            const float2 ca = make_float2(c.x, c.y), cb = make_float2(c.z, c.w);
+            if (kInterleaved) {
+              uint32_t& lo = w < 2 ? r0[2 * w] : r1[2 * w - 4];
+              uint32_t& hi = w < 2 ? r0[2 * w + 1] : r1[2 * w - 3];
+              lo = rotate(bf16_lo(lo), bf16_hi(lo), ca);
+              hi = rotate(bf16_lo(hi), bf16_hi(hi), cb);
+            } else {
+              const uint32_t ya = rotate(bf16_lo(r0[w]), bf16_lo(r1[w]), ca);
+              const uint32_t yb = rotate(bf16_hi(r0[w]), bf16_hi(r1[w]), cb);
+              r0[w] = __byte_perm(ya, yb, 0x5410);
+              r1[w] = __byte_perm(ya, yb, 0x7632);
+            }
+          }
+          x[u][0] = make_uint4(r0[0], r0[1], r0[2], r0[3]);
+          x[u][1] = make_uint4(r1[0], r1[1], r1[2], r1[3]);
+        }
+        const int64_t t = t0 + tok[u];
+        const int h = head[u];
+        uint4* dst = (h < a.Hq ? static_cast<uint4*>(a.q) + (t * a.Hq + h) * (a.D / 8)
+                      : h < a.Hq + a.Hkv
+                          ? static_cast<uint4*>(a.k) + (t * a.Hkv + h - a.Hq) * (a.D / 8)
+                          : static_cast<uint4*>(a.v) + (t * a.Hkv + h - a.Hq - a.Hkv) * (a.D / 8));
+        const bool apart = !kInterleaved && turn;
+        dst[apart ? sub[u] : 2 * sub[u]] = x[u][0];
+        dst[apart ? sub[u] + rot_items : 2 * sub[u] + 1] = x[u][1];
+      }
+    }
+  }
+}
+
+// rot_dim not a multiple of 16: one thread per pair of elements of a head;
+// pair p < rot / 2 is rotated, the others are the head's remaining elements,
+// copied.
+__global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const RopeArgs a, bool interleaved) {
+  const int heads = a.Hq + 2 * a.Hkv, half = a.D / 2;
+  const int64_t total = a.T * heads * half;
+  const uint16_t* qkv = static_cast<const uint16_t*>(a.qkv);
   for (int64_t e = blockIdx.x * (int64_t)kThreads + threadIdx.x; e < total;
        e += (int64_t)gridDim.x * kThreads) {
     const int64_t th = e / half;
     const int p = (int)(e - th * half);
     const int64_t t = th / heads;
     const int h = (int)(th - t * heads);
-    const uint16_t* src = qkv + th * D;
-    uint16_t* dst = h < Hq         ? q + (t * Hq + h) * D
-                    : h < Hq + Hkv ? k + (t * Hkv + (h - Hq)) * D
-                                   : v + (t * Hkv + (h - Hq - Hkv)) * D;
-    if (h >= Hq + Hkv || p >= rot / 2) {
-      dst[2 * p] = src[2 * p];
-      dst[2 * p + 1] = src[2 * p + 1];
+    const uint16_t* src = qkv + th * a.D;
+    uint16_t* dst =
+        h < a.Hq           ? static_cast<uint16_t*>(a.q) + (t * a.Hq + h) * a.D
+        : h < a.Hq + a.Hkv ? static_cast<uint16_t*>(a.k) + (t * a.Hkv + (h - a.Hq)) * a.D
+                           : static_cast<uint16_t*>(a.v) + (t * a.Hkv + (h - a.Hq - a.Hkv)) * a.D;
+    if (h >= a.Hq + a.Hkv || p >= a.rot / 2) {
+      *reinterpret_cast<uint32_t*>(dst + 2 * p) = *reinterpret_cast<const uint32_t*>(src + 2 * p);
       continue;
     }
-    const double f = freqs[p];
-    float c, s;
-    cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos[t])) * turn_fraction(f), c, s);
-    if (!isfinite(f)) c = s = __int_as_float(0x7fffffff);
-    c *= attn_scale;
-    s *= attn_scale;
-    const int i0 = interleaved ? 2 * p : p, i1 = interleaved ? 2 * p + 1 : p + rot / 2;
-    const float x0 = __uint_as_float((uint32_t)src[i0] << 16);
-    const float x1 = __uint_as_float((uint32_t)src[i1] << 16);
-    const uint32_t y =
-        pack_bf16x2(__fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s)),
-                    __fadd_rn(__fmul_rn(x1, c), __fmul_rn(x0, s)));
+    const double f = a.freqs[p];
+    float2 cs = cos_sin(a.pos[t], turn_fraction(f), a.attn_scale);
+    if (!isfinite(f)) cs = make_float2(CUDART_NAN_F, CUDART_NAN_F);
+    const int i0 = interleaved ? 2 * p : p, i1 = interleaved ? 2 * p + 1 : p + a.rot / 2;
+    const uint32_t y = rotate(__uint_as_float((uint32_t)src[i0] << 16),
+                              __uint_as_float((uint32_t)src[i1] << 16), cs);
     dst[i0] = (uint16_t)y;
     dst[i1] = (uint16_t)(y >> 16);
   }
@@ -78,12 +193,40 @@ __global__ void __launch_bounds__(kThreads) rope_pairs_kernel(
 bi_status launch_rope_qkv_scaled(const void* qkv, const int32_t* pos, int64_t T, int Hq, int Hkv,
                                  int D, int rot_dim, bool interleaved, const double* freqs,
                                  float attn_scale, void* q, void* k, void* v, cudaStream_t s) {
-  const int64_t pairs = T * (Hq + 2 * Hkv) * (D / 2);
+  RopeArgs a{qkv, pos, freqs, q, k, v, T, Hq, Hkv, D, rot_dim, attn_scale, 0, 0, 0, 0};
+  const int sms = device_sm_count();
+  if (sms <= 0) return BI_ERR_CUDA;
+  const int heads = Hq + 2 * Hkv;
+  // 16-byte vectors need the rotated part in whole vectors of each half
+  // (rotate-half) or of pairs, and the table in shared memory's default 48 KB
+  if (rot_dim % 16 == 0) {
+    const int per_token = heads * (D / 16);
+    // enough tokens to give every thread its kItems items, no more than the
+    // table's room, and no fewer blocks than would fill the GPU
+    int tokens = kItems * kThreads / per_token;
+    const int half = rot_dim / 2;
+    const int room = (49152 - half * 12) / (half * 8);
+    if (tokens > room) tokens = room;
+    while (tokens > 1 && T / tokens < 2 * sms) --tokens;
+    if (tokens < 1) tokens = 1;
+    a.tokens = tokens;
+    auto inv = [](uint32_t d) {
+      return static_cast<uint32_t>(((uint64_t(1) << 32) + d - 1) / d);
+    };
+    a.inv_D = inv(D / 16);
+    a.inv_heads = inv(heads);
+    a.inv_half = inv(half);
+    int64_t blocks = (T + tokens - 1) / tokens;
+    if (blocks > 8 * sms) blocks = 8 * sms;
+    const size_t sm = static_cast<size_t>(half) * (8 * tokens + 12);
+    auto kernel = interleaved ? rope_kernel<true> : rope_kernel<false>;
+    kernel<<<static_cast<unsigned>(blocks), kThreads, sm, s>>>(a);
+    return cuda_status(cudaGetLastError());
+  }
+  const int64_t pairs = T * heads * (D / 2);
   int64_t blocks = (pairs + kThreads - 1) / kThreads;
-  if (blocks > 152 * 32) blocks = 152 * 32;
-  rope_pairs_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-      static_cast<const uint16_t*>(qkv), pos, T, Hq, Hkv, D, rot_dim, interleaved, freqs,
-      attn_scale, static_cast<uint16_t*>(q), static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
+  if (blocks > 32 * sms) blocks = 32 * sms;
+  rope_pairs_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a, interleaved);
   return cuda_status(cudaGetLastError());
 }
 
