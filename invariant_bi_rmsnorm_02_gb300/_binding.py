@@ -76,6 +76,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load libbi.so (building it with nvcc first if it is absent)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -150,8 +152,15 @@ def _check(status: int, what: str) -> None:
         raise BiError(status, what)
 
 
+# the current stream's handle without building a Stream object (a few
+# microseconds per call, as long as a small kernel runs)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -334,14 +343,25 @@ def bi_rope_qkv(qkv, pos, Hq, Hkv, D, theta, q, k, v, stream=None):
                               _stream(stream)), "bi_rope_qkv")
 
 
-def _same_device(*tensors):
-    """The library works on the current device; a tensor of another one is
-    refused here rather than read through a foreign pointer."""
-    d = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != d:
-            raise ValueError("a tensor is on cuda:%d, the current device is cuda:%d"
-                             % (t.device.index, d))
+def _dptr(t, dtype, dev, name):
+    """_ptr for a tensor that has to be on the current device ``dev``: the
+    library works there only, and a tensor of another device is refused here
+    rather than read through a foreign pointer."""
+    if t is None:
+        return None
+    try:
+        on = t.get_device()
+    except AttributeError:
+        raise TypeError("%s must be a CUDA tensor" % name) from None
+    if on != dev:
+        if on < 0:
+            raise TypeError("%s must be a CUDA tensor" % name)
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, on, dev))
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
 def _cache_q8(cache, Hkv, D):
@@ -356,12 +376,13 @@ def bi_kv_write_q8(k_new, v_new, seq, pos, cache, block_table, stream=None):
         raise ValueError("k_new, v_new must be [n, Hkv, D] and seq, pos [n]")
     _cache_q8(cache, Hkv, D)
     num_seqs, max_blocks = block_table.shape
-    _same_device(k_new, v_new, seq, pos, cache, block_table)
+    dev = torch.cuda.current_device()
     _check(load().bi_kv_write_q8(
-        _ptr(k_new, torch.bfloat16, "k_new"), _ptr(v_new, torch.bfloat16, "v_new"),
-        _ptr(seq, torch.int32, "seq"), _ptr(pos, torch.int32, "pos"), n,
-        _ptr(cache, torch.uint8, "cache"), _ptr(block_table, torch.int32, "block_table"),
-        num_seqs, Hkv, D, 16, cache.shape[0], max_blocks, _stream(stream)), "bi_kv_write_q8")
+        _dptr(k_new, torch.bfloat16, dev, "k_new"), _dptr(v_new, torch.bfloat16, dev, "v_new"),
+        _dptr(seq, torch.int32, dev, "seq"), _dptr(pos, torch.int32, dev, "pos"), n,
+        _dptr(cache, torch.uint8, dev, "cache"),
+        _dptr(block_table, torch.int32, dev, "block_table"), num_seqs, Hkv, D, 16,
+        cache.shape[0], max_blocks, _stream(stream)), "bi_kv_write_q8")
 
 
 def bi_kv_read_q8(cache, block_table, kv_lens, k_out, v_out, out_table, *, max_kv_len,
@@ -375,13 +396,15 @@ def bi_kv_read_q8(cache, block_table, kv_lens, k_out, v_out, out_table, *, max_k
             or out_table.shape[0] != B:
         raise ValueError("block_table and out_table must be [B, blocks], kv_lens [B]")
     _cache_q8(cache, Hkv, D)
-    _same_device(cache, block_table, kv_lens, k_out, v_out, out_table)
+    dev = torch.cuda.current_device()
     _check(load().bi_kv_read_q8(
-        _ptr(cache, torch.uint8, "cache"), _ptr(block_table, torch.int32, "block_table"),
-        _ptr(kv_lens, torch.int32, "kv_lens"), B, Hkv, D, page, cache.shape[0],
-        block_table.shape[1], int(max_kv_len), _ptr(k_out, torch.bfloat16, "k_out"),
-        _ptr(v_out, torch.bfloat16, "v_out"), _ptr(out_table, torch.int32, "out_table"), num_out,
-        out_table.shape[1], _stream(stream)), "bi_kv_read_q8")
+        _dptr(cache, torch.uint8, dev, "cache"),
+        _dptr(block_table, torch.int32, dev, "block_table"),
+        _dptr(kv_lens, torch.int32, dev, "kv_lens"), B, Hkv, D, page, cache.shape[0],
+        block_table.shape[1], int(max_kv_len), _dptr(k_out, torch.bfloat16, dev, "k_out"),
+        _dptr(v_out, torch.bfloat16, dev, "v_out"),
+        _dptr(out_table, torch.int32, dev, "out_table"), num_out, out_table.shape[1],
+        _stream(stream)), "bi_kv_read_q8")
 
 
 def bi_attn_decode_q8(q, cache, block_table, kv_lens, out, out_f32=None, *, max_kv_len,
@@ -395,13 +418,16 @@ def bi_attn_decode_q8(q, cache, block_table, kv_lens, out, out_f32=None, *, max_
         raise ValueError("out must have q's shape")
     if block_table.dim() != 2 or block_table.shape[0] != B or kv_lens.shape != (B,):
         raise ValueError("block_table must be [B, max_blocks] and kv_lens [B]")
-    _same_device(q, cache, block_table, kv_lens, out, out_f32, workspace)
+    dev = torch.cuda.current_device()
+    if workspace is not None and workspace.get_device() != dev:
+        raise ValueError("workspace must be on the current device")
     wp, wb = _ws(workspace)
     _check(load().bi_attn_decode_q8(
-        _ptr(q, torch.bfloat16, "q"), _ptr(cache, torch.uint8, "cache"),
-        _ptr(block_table, torch.int32, "block_table"), _ptr(kv_lens, torch.int32, "kv_lens"),
-        _ptr(out, torch.bfloat16, "out"), _ptr(out_f32, torch.float32, "out_f32"), B, Hq, Hkv, D,
-        16, cache.shape[0], block_table.shape[1], int(max_kv_len), int(split_size),
+        _dptr(q, torch.bfloat16, dev, "q"), _dptr(cache, torch.uint8, dev, "cache"),
+        _dptr(block_table, torch.int32, dev, "block_table"),
+        _dptr(kv_lens, torch.int32, dev, "kv_lens"), _dptr(out, torch.bfloat16, dev, "out"),
+        _dptr(out_f32, torch.float32, dev, "out_f32"), B, Hq, Hkv, D, 16, cache.shape[0],
+        block_table.shape[1], int(max_kv_len), int(split_size),
         float(sm_scale), int(mode), int(variant_splits), wp, wb, _stream(stream)),
         "bi_attn_decode_q8")
 
@@ -429,12 +455,13 @@ def bi_rope_qkv_scaled(qkv, pos, Hq, Hkv, D, freqs, q, k, v, interleaved=False, 
         raise ValueError("qkv must be [T, (Hq + 2 Hkv) D], pos [T] and freqs [rot_dim / 2]")
     if q.shape != (T, Hq, D) or k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
         raise ValueError("q, k, v must be [T, H, D]")
-    _same_device(qkv, pos, freqs, q, k, v)
+    dev = torch.cuda.current_device()
     _check(load().bi_rope_qkv_scaled(
-        _ptr(qkv, torch.bfloat16, "qkv"), _ptr(pos, torch.int32, "pos"), T, Hq, Hkv, D,
-        2 * freqs.shape[0], 1 if interleaved else 0, _ptr(freqs, torch.float64, "freqs"),
-        float(attn_scale), _ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"),
-        _ptr(v, torch.bfloat16, "v"), _stream(stream)), "bi_rope_qkv_scaled")
+        _dptr(qkv, torch.bfloat16, dev, "qkv"), _dptr(pos, torch.int32, dev, "pos"), T, Hq, Hkv,
+        D, 2 * freqs.shape[0], 1 if interleaved else 0, _dptr(freqs, torch.float64, dev, "freqs"),
+        float(attn_scale), _dptr(q, torch.bfloat16, dev, "q"),
+        _dptr(k, torch.bfloat16, dev, "k"), _dptr(v, torch.bfloat16, dev, "v"),
+        _stream(stream)), "bi_rope_qkv_scaled")
 
 
 def bi_silu_mul(gate_up, out, block=None, stream=None):

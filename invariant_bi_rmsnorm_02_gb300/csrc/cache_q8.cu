@@ -12,6 +12,8 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "bi_internal.h"
 #include "device_common.cuh"
 #include "e4m3.cuh"
@@ -24,63 +26,92 @@ constexpr int kThreads = 256;
 constexpr unsigned kFull = 0xffffffffu;
 
 // ------------------------------------------------------------------ write
-// D/8 lanes per row, 16 bytes of bf16 each; rows in the order (token, head,
-// K then V).
+// D/8 lanes per row, 16 bytes of bf16 each: the K row of a (token, head) and
+// its V row on neighbouring lanes, kRows such pairs in flight per thread (a
+// step of `stride` apart), since a pair is only loads behind one another
+// (sequence and position, page id, then the stores).
+constexpr int kRows = 4;
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv_write_q8_kernel(
     const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
-    const int32_t* __restrict__ seq, const int32_t* __restrict__ pos, int64_t rows, int Hkv,
+    const int32_t* __restrict__ seq, const int32_t* __restrict__ pos, uint32_t pairs, uint32_t Hkv,
     uint8_t* __restrict__ cache, const int32_t* __restrict__ bt, int num_seqs, int64_t num_pages,
     int max_blocks, int* err) {
-  constexpr int kLanes = D / 8;
-  const int64_t row = (blockIdx.x * (int64_t)kThreads + threadIdx.x) / kLanes;
-  const int c = threadIdx.x % kLanes;
-  const int64_t rr = row < rows ? row : rows - 1;
-  const bool is_v = rr & 1;
-  const int64_t th = rr >> 1;  // token * Hkv + head
-  const int64_t tok = th / Hkv;
-  const int h = (int)(th - tok * Hkv);
-  const uint4 x = (is_v ? v_new : k_new)[th * kLanes + c];
-  const int s = seq[tok], ps = pos[tok];
-  int64_t page = -1;
-  if (s >= 0 && s < num_seqs && ps >= 0 && ps < max_blocks * (int64_t)kPage)
-    page = bt[(int64_t)s * max_blocks + ps / kPage];
-  const bool ok = page >= 0 && page < num_pages;
-  // the largest magnitude bits of the row: bf16 magnitudes order as integers
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t top = 0;
+  constexpr uint32_t kLanes = D / 8;
+  constexpr uint32_t kPerWarp = 32 / (2 * kLanes);  // pairs of a warp
+  const uint32_t warp = (blockIdx.x * kThreads + threadIdx.x) / 32;
+  const uint32_t stride = gridDim.x * (kThreads / 32) * kPerWarp;
+  const uint32_t mine = (threadIdx.x % 32) / (2 * kLanes);
+  const uint32_t c = threadIdx.x % kLanes;
+  const bool is_v = (threadIdx.x / kLanes) & 1;
+  const uint4* src = is_v ? v_new : k_new;
+  // a warp's lanes stay together: it goes on while its first pair exists
+  for (uint64_t base = (uint64_t)warp * kPerWarp; base < pairs; base += (uint64_t)kRows * stride) {
+    const uint64_t first = base + mine;
+    uint4 x[kRows];
+    uint32_t head[kRows];
+    int s[kRows], ps[kRows];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    for (int u = 0; u < kRows; ++u) {
+      const uint64_t th = first + (uint64_t)u * stride;  // token * Hkv + head
+      x[u] = make_uint4(0, 0, 0, 0);
+      s[u] = -1;
+      if (th >= pairs) continue;
+      const uint32_t tok = (uint32_t)th / Hkv;
+      head[u] = (uint32_t)th - tok * Hkv;
+      x[u] = src[th * kLanes + c];
+      s[u] = seq[tok];
+      ps[u] = pos[tok];
+    }
+    int64_t page[kRows];
 #pragma unroll
-  for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-  if (row >= rows) return;
-  if (!ok) {
-    if (c == 0) record_error(err, BI_ERR_DEVICE_BOUNDS);
-    return;
-  }
-  // least e with amax 2^-e <= 448 = 1.75 * 2^8
-  int e = kQ8MinExp;
-  if (top >= 0x80) {  // a normal number: 1.f * 2^(exponent - 127)
-    e = (int)(top >> 7) - 127 - 8 + ((top & 0x7f) > 0x60 ? 1 : 0);
-    e = max(kQ8MinExp, min(kQ8MaxExp, e));
-  }
-  const bool fine = top < 0x7f80;
-  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-  uint32_t q[2] = {0, 0};
-  if (fine) {
+    for (int u = 0; u < kRows; ++u) {
+      page[u] = -1;
+      if (first + (uint64_t)u * stride < pairs && s[u] >= 0 && s[u] < num_seqs && ps[u] >= 0 &&
+          ps[u] < max_blocks * (int64_t)kPage)
+        page[u] = bt[(int64_t)s[u] * max_blocks + ps[u] / kPage];
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = make_float2(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
-      const uint32_t p = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-      q[i >> 1] |= p << (16 * (i & 1));
+    for (int u = 0; u < kRows; ++u) {
+      // the largest magnitude bits of the row: bf16 magnitudes order as integers
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+#pragma unroll
+      for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+      if (first + (uint64_t)u * stride >= pairs) continue;
+      if (page[u] < 0 || page[u] >= num_pages) {
+        if (c == 0) record_error(err, BI_ERR_DEVICE_BOUNDS);
+        continue;
+      }
+      // least e with amax 2^-e <= 448 = 1.75 * 2^8
+      int e = kQ8MinExp;
+      if (top >= 0x80) {  // a normal number: 1.f * 2^(exponent - 127)
+        e = (int)(top >> 7) - 127 - 8 + ((top & 0x7f) > 0x60 ? 1 : 0);
+        e = max(kQ8MinExp, min(kQ8MaxExp, e));
+      }
+      const bool fine = top < 0x7f80;
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+      uint32_t q[2] = {0, 0};
+      if (fine) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = make_float2(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+          const uint32_t p = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+          q[i >> 1] |= p << (16 * (i & 1));
+        }
+      }
+      uint8_t* rec = cache + (page[u] * Hkv + head[u]) * kv_q8_record_bytes(D);
+      const int slot = ps[u] % kPage;
+      *reinterpret_cast<uint2*>(rec + (is_v ? kPage * D : 0) + slot * D + 8 * c) =
+          make_uint2(q[0], q[1]);
+      if (c == 0)
+        rec[2 * kPage * D + (is_v ? kPage : 0) + slot] =
+            (uint8_t)(fine ? e + kQ8ScaleBias : kQ8NonFinite);
     }
   }
-  uint8_t* rec = cache + (page * Hkv + h) * kv_q8_record_bytes(D);
-  const int slot = ps % kPage;
-  *reinterpret_cast<uint2*>(rec + (is_v ? kPage * D : 0) + slot * D + 8 * c) =
-      make_uint2(q[0], q[1]);
-  if (c == 0)
-    rec[2 * kPage * D + (is_v ? kPage : 0) + slot] = (uint8_t)(fine ? e + kQ8ScaleBias : kQ8NonFinite);
 }
 
 // ------------------------------------------------------------------- read
@@ -162,11 +193,17 @@ template <int D>
 bi_status write_impl(const void* k_new, const void* v_new, const int32_t* seq, const int32_t* pos,
                      int64_t n_tokens, void* cache, const int32_t* bt, int num_seqs, int Hkv,
                      int64_t num_pages, int max_blocks, int* err, cudaStream_t s) {
-  const int64_t rows = n_tokens * Hkv * 2;
-  const int64_t blocks = (rows * (D / 8) + kThreads - 1) / kThreads;
+  const int sms = device_sm_count();
+  if (sms <= 0) return BI_ERR_CUDA;
+  const int64_t pairs = n_tokens * Hkv, per_block = kThreads / (2 * D / 8);
+  // a pair per thread while that leaves SMs idle, kRows behind each other after
+  int64_t blocks = (pairs + per_block - 1) / per_block;
+  if (blocks > 4 * sms) blocks = std::max<int64_t>(4 * sms, (blocks + kRows - 1) / kRows);
+  if (blocks > 32 * sms) blocks = 32 * sms;
   kv_write_q8_kernel<D><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-      static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), seq, pos, rows, Hkv,
-      static_cast<uint8_t*>(cache), bt, num_seqs, num_pages, max_blocks, err);
+      static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), seq, pos,
+      static_cast<uint32_t>(pairs), static_cast<uint32_t>(Hkv), static_cast<uint8_t*>(cache), bt,
+      num_seqs, num_pages, max_blocks, err);
   return cuda_status(cudaGetLastError());
 }
 

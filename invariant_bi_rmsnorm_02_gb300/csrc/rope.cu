@@ -67,7 +67,11 @@ __device__ __forceinline__ int div_by(int n, uint32_t m) {
 // Bound by memory: 8192 tokens of 32 + 2 * 8 heads of 128 move 201 MB.
 constexpr int kItems = 3;  // items in flight per thread
 
-template <bool kInterleaved>
+// kAligned: rot_dim % 16 == 0, so that rotated items are whole vectors of
+// either half of the rotated part (rotate-half) or of pairs.  Otherwise the
+// items that hold rotated elements gather their pairs one by one; those are
+// read again from L1, the head's other items stay vectors.
+template <bool kInterleaved, bool kAligned>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   const int heads = a.Hq + 2 * a.Hkv, half = a.rot / 2;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -80,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
     amp[p] = isfinite(f) ? a.attn_scale : CUDART_NAN_F;
   }
   const int per_head = a.D / 16, per_token = heads * per_head;
-  const int rot_items = a.rot / 16;
+  const int rot_items = (a.rot + 15) / 16;
   const uint4* src = static_cast<const uint4*>(a.qkv);
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
        t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
@@ -99,8 +103,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
         head[u] = th - tok[u] * heads;
         const bool turn = head[u] < a.Hq + a.Hkv && sub[u] < rot_items;
         const uint4* row = src + (t0 * heads + th) * (a.D / 8);
+        if (!kAligned && turn) continue;
         // rotate-half: a vector of the first half and its partner
-        const bool apart = !kInterleaved && turn;
+        const bool apart = kAligned && !kInterleaved && turn;
         x[u][0] = __ldcs(row + (apart ? sub[u] : 2 * sub[u]));
         x[u][1] = __ldcs(row + (apart ? sub[u] + rot_items : 2 * sub[u] + 1));
       }
@@ -117,7 +122,25 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
         const int i = i0 + u * kThreads + threadIdx.x;
         if (i >= items) continue;
         const bool turn = head[u] < a.Hq + a.Hkv && sub[u] < rot_items;
-        if (turn) {
+        if (!kAligned && turn) {
+          const uint16_t* row =
+              static_cast<const uint16_t*>(a.qkv) + ((t0 + tok[u]) * heads + head[u]) * a.D;
+          auto element = [&](int i) { return __uint_as_float((uint32_t)row[i] << 16); };
+          auto turned = [&](int e) -> uint32_t {  // element e of the head's output
+            if (e >= a.rot) return row[e];
+            const int p = kInterleaved ? e >> 1 : e < half ? e : e - half;
+            const uint32_t y = rotate(element(kInterleaved ? 2 * p : p),
+                                      element(kInterleaved ? 2 * p + 1 : p + half),
+                                      table[tok[u] * half + p]);
+            return (kInterleaved ? (e & 1) : e >= half) ? y >> 16 : y & 0xffffu;
+          };
+          uint32_t r[8];
+#pragma unroll
+          for (int w = 0; w < 8; ++w)
+            r[w] = turned(16 * sub[u] + 2 * w) | turned(16 * sub[u] + 2 * w + 1) << 16;
+          x[u][0] = make_uint4(r[0], r[1], r[2], r[3]);
+          x[u][1] = make_uint4(r[4], r[5], r[6], r[7]);
+        } else if (turn) {
           const float4* cs4 =
               reinterpret_cast<const float4*>(table + tok[u] * half + 8 * sub[u]);
           uint32_t r0[4] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w};
@@ -147,44 +170,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
                       : h < a.Hq + a.Hkv
                           ? static_cast<uint4*>(a.k) + (t * a.Hkv + h - a.Hq) * (a.D / 8)
                           : static_cast<uint4*>(a.v) + (t * a.Hkv + h - a.Hq - a.Hkv) * (a.D / 8));
-        const bool apart = !kInterleaved && turn;
+        const bool apart = kAligned && !kInterleaved && turn;
         dst[apart ? sub[u] : 2 * sub[u]] = x[u][0];
         dst[apart ? sub[u] + rot_items : 2 * sub[u] + 1] = x[u][1];
       }
     }
-  }
-}
-
-// rot_dim not a multiple of 16: one thread per pair of elements of a head;
-// pair p < rot / 2 is rotated, the others are the head's remaining elements,
-// copied.
-__global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const RopeArgs a, bool interleaved) {
-  const int heads = a.Hq + 2 * a.Hkv, half = a.D / 2;
-  const int64_t total = a.T * heads * half;
-  const uint16_t* qkv = static_cast<const uint16_t*>(a.qkv);
-  for (int64_t e = blockIdx.x * (int64_t)kThreads + threadIdx.x; e < total;
-       e += (int64_t)gridDim.x * kThreads) {
-    const int64_t th = e / half;
-    const int p = (int)(e - th * half);
-    const int64_t t = th / heads;
-    const int h = (int)(th - t * heads);
-    const uint16_t* src = qkv + th * a.D;
-    uint16_t* dst =
-        h < a.Hq           ? static_cast<uint16_t*>(a.q) + (t * a.Hq + h) * a.D
-        : h < a.Hq + a.Hkv ? static_cast<uint16_t*>(a.k) + (t * a.Hkv + (h - a.Hq)) * a.D
-                           : static_cast<uint16_t*>(a.v) + (t * a.Hkv + (h - a.Hq - a.Hkv)) * a.D;
-    if (h >= a.Hq + a.Hkv || p >= a.rot / 2) {
-      *reinterpret_cast<uint32_t*>(dst + 2 * p) = *reinterpret_cast<const uint32_t*>(src + 2 * p);
-      continue;
-    }
-    const double f = a.freqs[p];
-    float2 cs = cos_sin(a.pos[t], turn_fraction(f), a.attn_scale);
-    if (!isfinite(f)) cs = make_float2(CUDART_NAN_F, CUDART_NAN_F);
-    const int i0 = interleaved ? 2 * p : p, i1 = interleaved ? 2 * p + 1 : p + a.rot / 2;
-    const uint32_t y = rotate(__uint_as_float((uint32_t)src[i0] << 16),
-                              __uint_as_float((uint32_t)src[i1] << 16), cs);
-    dst[i0] = (uint16_t)y;
-    dst[i1] = (uint16_t)(y >> 16);
   }
 }
 
@@ -197,36 +187,26 @@ bi_status launch_rope_qkv_scaled(const void* qkv, const int32_t* pos, int64_t T,
   const int sms = device_sm_count();
   if (sms <= 0) return BI_ERR_CUDA;
   const int heads = Hq + 2 * Hkv;
-  // 16-byte vectors need the rotated part in whole vectors of each half
-  // (rotate-half) or of pairs, and the table in shared memory's default 48 KB
-  if (rot_dim % 16 == 0) {
-    const int per_token = heads * (D / 16);
-    // enough tokens to give every thread its kItems items, no more than the
-    // table's room, and no fewer blocks than would fill the GPU
-    int tokens = kItems * kThreads / per_token;
-    const int half = rot_dim / 2;
-    const int room = (49152 - half * 12) / (half * 8);
-    if (tokens > room) tokens = room;
-    while (tokens > 1 && T / tokens < 2 * sms) --tokens;
-    if (tokens < 1) tokens = 1;
-    a.tokens = tokens;
-    auto inv = [](uint32_t d) {
-      return static_cast<uint32_t>(((uint64_t(1) << 32) + d - 1) / d);
-    };
-    a.inv_D = inv(D / 16);
-    a.inv_heads = inv(heads);
-    a.inv_half = inv(half);
-    int64_t blocks = (T + tokens - 1) / tokens;
-    if (blocks > 8 * sms) blocks = 8 * sms;
-    const size_t sm = static_cast<size_t>(half) * (8 * tokens + 12);
-    auto kernel = interleaved ? rope_kernel<true> : rope_kernel<false>;
-    kernel<<<static_cast<unsigned>(blocks), kThreads, sm, s>>>(a);
-    return cuda_status(cudaGetLastError());
-  }
-  const int64_t pairs = T * heads * (D / 2);
-  int64_t blocks = (pairs + kThreads - 1) / kThreads;
-  if (blocks > 32 * sms) blocks = 32 * sms;
-  rope_pairs_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a, interleaved);
+  const int per_token = heads * (D / 16), half = rot_dim / 2;
+  // enough tokens to give every thread its kItems items, no more than the
+  // default 48 KB of shared memory hold, and no fewer blocks than two an SM
+  int tokens = kItems * kThreads / per_token;
+  const int room = (49152 - half * 12) / (half * 8);
+  if (tokens > room) tokens = room;
+  while (tokens > 1 && T / tokens < 2 * sms) --tokens;
+  if (tokens < 1) tokens = 1;
+  a.tokens = tokens;
+  auto inv = [](uint32_t d) { return static_cast<uint32_t>(((uint64_t(1) << 32) + d - 1) / d); };
+  a.inv_D = inv(D / 16);
+  a.inv_heads = inv(heads);
+  a.inv_half = inv(half);
+  int64_t blocks = (T + tokens - 1) / tokens;
+  if (blocks > 8 * sms) blocks = 8 * sms;
+  const size_t sm = static_cast<size_t>(half) * (8 * tokens + 12);
+  const bool aligned = rot_dim % 16 == 0;
+  auto kernel = interleaved ? (aligned ? rope_kernel<true, true> : rope_kernel<true, false>)
+                            : (aligned ? rope_kernel<false, true> : rope_kernel<false, false>);
+  kernel<<<static_cast<unsigned>(blocks), kThreads, sm, s>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
