@@ -959,36 +959,6 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
   if (!alive) s_abort = 1;
 }
 
-// mbarrier wait for the roles with slack (the fold and TMA warps): the thread
-// suspends in the wait (a hint of 20 us, then it tries again), leaving the
-// issue slots of its scheduler to the softmax warp beside it; bounded in time
-// like mbar_wait.  The MMA and softmax warps, whose waits are on the
-// critical path, use mbar_wait itself.
-__device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity, int* err,
-                                             volatile int* abort) {
-  if (mbar_try_wait_sleep(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait_sleep(bar, parity)) return true;
-    if (abort && *abort) return false;
-    if (global_ns() - t0 > kWaitNs) break;
-  }
-  record_error(err, BI_ERR_TIMEOUT);
-  if (abort) *abort = 1;
-  return false;
-}
-
 // ------------------------------------------- decode split, quantised cache
 // The same units, arithmetic and outputs over the records of the quantised
 // cache: every e4m3 element stands for the bf16 value that reading the cache
@@ -998,9 +968,7 @@ __device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity, i
 // What bounds it: half the bytes per tile, but every element has to be
 // unpacked for the MMA, and at the measured HBM rate an SM receives a 64-key
 // tile of D = 128 every ~700 cycles, in which its four schedulers issue
-// ~1,800 instructions at a good rate.  So the unpacking is kept short, the
-// work is spread over all four schedulers, and a unit is short enough that
-// the last ones do not run alone:
+// ~1,600 instructions at a good rate.  So instructions are what is saved:
 //   * powers of two are moved where they cost least, changing no bit.  K's
 //     elements become fp16 numbers (one conversion a pair) with Q's rows in
 //     fp16 times a power of two each, and the key's scale multiplies the
@@ -1009,24 +977,25 @@ __device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity, i
 //     V's elements become bf16 bits times 2^-120 (three instructions a pair)
 //     and the key's scale, relative to the largest of the tiles so far,
 //     multiplies P's two parts instead;
-//   * a unit is the work of two compute warps: warp w takes keys 32 w ..
-//     32 w + 31 of a tile for the scores and the probabilities, the two
-//     exchange those through shared memory, and each takes half of the
-//     output's columns.  A block (one per SM) holds kGroups such pairs and a
-//     producer warp for each.
-// 64 requests, 194 MB of records: 78 us with the bf16 kernel's blocks of one
-// compute and one producer warp (all compute warps on two of the four
-// schedulers); 59 us with eight compute warps per SM, a unit each, and an
-// exact product per pair for every scale (1,800 instructions a tile, 5,200
-// cycles a tile and warp, 9.6 tiles a warp on average but 12 at most); 62 us
-// with four warps to a unit (2,750 instructions a tile).
-//
-// A group's ring holds kStages half tiles, K and V in turn: K's half goes back
-// to the producer as soon as the scores are done.  The tile's scale bytes
-// ride with its K half in a ring of their own (kScaleSlots tiles): a slot is
-// written again only after a wait that follows the release of the V half
-// that reads it.
-constexpr int kQ8Warps = 2;  // compute warps of a group
+//   * every warp is on its own: it works units out, copies a unit's tiles into
+//     its own shared memory with cp.async and computes them, with no barrier
+//     and no other warp to wait for.  Its one tile is two buffers: K's is
+//     filled again as soon as the scores are done and V's after the output
+//     step, so either copy has the other half of the tile's arithmetic to
+//     land in, and the warps of a scheduler fill each other's gaps.
+template <int D, int NQ>
+struct Q8Geom {
+  // As many warps as the registers allow, a multiple of the four schedulers.
+  static constexpr int kWarps = NQ == 1 ? (D == 64 ? 16 : 12) : (D == 64 ? 12 : 8);
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRecord = kv_q8_record_bytes(D);
+  static constexpr int kPageHalf = kPage * D;              // one page's K (or V) bytes
+  static constexpr int kHalf = kPagesPerTile * kPageHalf;  // a tile's
+  static constexpr int kScaleBytes = 2 * kTile;            // per tile: page p at 32 p, K then V
+  // K, V, and the scale bytes of two tiles (the next tile's come with its K)
+  static constexpr int kWarpBytes = 2 * kHalf + 2 * kScaleBytes;
+  static constexpr int kSmem = 1024 + kWarps * kWarpBytes;
+};
 
 // mma_bf16, and the same with fp16 operands, as functions of their registers
 // alone, which the compiler may move among the loads of other fragments.
@@ -1045,37 +1014,9 @@ __device__ __forceinline__ void mma_f16_free(float (&c)[4], const uint32_t (&a)[
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// What the warps of a group hand one another for a tile.
-template <int NQ>
-struct Q8Exchange {
-  uint4 frag[4][NQ][32];        // P^T fragments of each 16 keys: high (2), low (2) parts
-  float2 sum[NQ][32];           // warp 0's running sums of the columns, for warp 1 to go on with
-  float top[kQ8Warps][8 * NQ];  // the column maxima of each warp's keys
-  float l[8 * NQ];              // the sums, at the end of a unit
-};
-
-template <int D, int NQ>
-struct Q8Geom {
-  // More groups hide more latency; G > 8 needs the registers of four.
-  static constexpr int kGroups = NQ == 1 ? 6 : 4;
-  static constexpr int kThreads = kGroups * (kQ8Warps + 1) * 32;
-  static constexpr int kRecord = kv_q8_record_bytes(D);
-  static constexpr int kPageHalf = kPage * D;               // one page's K (or V) bytes
-  static constexpr int kHalf = kPagesPerTile * kPageHalf;   // one ring stage
-  static constexpr int kStages = 4 * (128 / D);
-  static constexpr int kScaleSlots = 3 * (128 / D);
-  static constexpr int kScaleBytes = 2 * kTile;             // per tile: page p at 32 p, K then V
-  static constexpr int kRingBytes = kStages * kHalf;
-  static constexpr int kScaleOff = kGroups * kRingBytes;
-  static constexpr int kExchangeOff = kScaleOff + kGroups * kScaleSlots * kScaleBytes;
-  static constexpr int kSmem =
-      1024 + kExchangeOff + kGroups * static_cast<int>(sizeof(Q8Exchange<NQ>));
-  static_assert(2 * kScaleSlots > kStages, "a scale slot outlives its tile's V half");
-  static_assert(kExchangeOff % 16 == 0 && sizeof(Q8Exchange<NQ>) % 16 == 0, "alignment");
-};
-
-// byte offset of 16-byte chunk c of key n's row in a half tile: the TMA
-// swizzle of the row's width (128 or 64 bytes)
+// byte offset of 16-byte chunk c of key n's row in a half tile: the chunks of
+// a row are permuted so that eight rows' chunks of one column are in
+// different banks
 template <int D>
 __device__ __forceinline__ uint32_t q8_off(int n, int c) {
   const int r = n & 15;
@@ -1100,7 +1041,9 @@ __device__ __forceinline__ bool q8_load_q(uint32_t (&qf)[NQ][D / 16][2], float (
   float grow[NQ], shrink[NQ];  // 2^(15 - e) for a row's largest exponent e, and its inverse
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) {
-    uint32_t top = 0;
+    // the largest magnitude bits, and the smallest ones that are not zero
+    // (less 1, so that zeros come last), two elements at a time
+    uint32_t top2 = 0, low2 = 0xffffffffu;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint2 x = make_uint2(0, 0);
@@ -1109,23 +1052,25 @@ __device__ __forceinline__ bool q8_load_q(uint32_t (&qf)[NQ][D / 16][2], float (
       qf[nq][ks][0] = x.x;
       qf[nq][ks][1] = x.y;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        top = max(top, max(qf[nq][ks][i] & 0x7fffu, (qf[nq][ks][i] >> 16) & 0x7fffu));
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t m = qf[nq][ks][i] & 0x7fff7fffu;
+        uint32_t less;
+        asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(m));
+        asm("add.u16x2 %0, %1, %2;" : "=r"(less) : "r"(m), "r"(0xffffffffu));
+        asm("min.u16x2 %0, %0, %1;" : "+r"(low2) : "r"(less));
+      }
     }
+    uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+    const uint32_t low = min(low2 & 0xffffu, low2 >> 16);
     top = max(top, __shfl_xor_sync(kFull, top, 1));
     top = max(top, __shfl_xor_sync(kFull, top, 2));
-    const int up = min(253, 269 - (int)(top >> 7));  // both are normal numbers
+    const int et = (int)(top >> 7);
+    const int up = min(253, 269 - et);  // both are normal numbers
     grow[nq] = __uint_as_float((uint32_t)up << 23);
     shrink[nq] = __uint_as_float((uint32_t)(254 - up) << 23);
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float a = __fmul_rn(bf16_lo(qf[nq][ks][i]), grow[nq]);
-        const float b = __fmul_rn(bf16_hi(qf[nq][ks][i]), grow[nq]);
-        exact = exact && __half2float(__float2half_rn(a)) == a &&
-                __half2float(__float2half_rn(b)) == b;
-      }
+    // every element a finite one at most 2^32 below the largest (its 8 bits
+    // then end at 2^-24 or above)
+    exact = exact && et < 255 && (int)low + 1 >= (et - 32) * 128;
   }
   exact = __all_sync(kFull, exact);
 #pragma unroll
@@ -1152,28 +1097,29 @@ __device__ __forceinline__ bool q8_load_q(uint32_t (&qf)[NQ][D / 16][2], float (
   return exact;
 }
 
-// S^T = K Q^T of keys 32 w .. 32 w + 31 of a half tile, in two m-tiles: the
-// sums of the products with the stored numbers, times the keys' scales.
+// S^T = K Q^T of a tile, in four m-tiles of 16 keys: the sums of the products
+// with the stored numbers, times the keys' scales.
 template <int D, int NQ, bool kF16>
-__device__ __forceinline__ void q8_scores(float (&s)[2][NQ][4],
+__device__ __forceinline__ void q8_scores(float (&s)[4][NQ][4],
                                           const uint32_t (&qf)[NQ][D / 16][2], uint32_t kbase,
-                                          const uint8_t* scales, int w) {
+                                          const uint8_t* scales) {
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, mi = lane >> 3, r8 = lane & 7;
 #pragma unroll
-  for (int mt = 0; mt < 2; ++mt)
+  for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) s[mt][nq][0] = s[mt][nq][1] = s[mt][nq][2] = s[mt][nq][3] = 0.0f;
+  // k-steps outermost: the four m-tiles' sums are independent chains
 #pragma unroll
   for (int kp = 0; kp < D / 32; ++kp) {
-    uint32_t r[2][4];  // keys g and g + 8 of k-steps 2 kp and 2 kp + 1
+    uint32_t r[4][4];  // keys g and g + 8 of k-steps 2 kp and 2 kp + 1
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-      ldsm_x4(kbase + q8_off<D>(32 * w + 16 * mt + r8 + 8 * (mi & 1), 2 * kp + (mi >> 1)), r[mt]);
+    for (int mt = 0; mt < 4; ++mt)
+      ldsm_x4(kbase + q8_off<D>(16 * mt + r8 + 8 * (mi & 1), 2 * kp + (mi >> 1)), r[mt]);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < 4; ++mt) {
         const uint32_t x0 = r[mt][2 * u], x1 = r[mt][2 * u + 1];
         if constexpr (kF16) {
           const uint32_t a[4] = {e4m3_f16_lo(x0), e4m3_f16_lo(x1), e4m3_f16_hi(x0),
@@ -1189,18 +1135,23 @@ __device__ __forceinline__ void q8_scores(float (&s)[2][NQ][4],
         }
       }
   }
-  // lane i has the scale of key 32 w + i (NaN for a row that is not finite)
-  const uint32_t c = scales[32 * (2 * w + (lane >> 4)) + (lane & 15)];
-  const float f = c == kQ8NonFinite ? CUDART_NAN_F : __uint_as_float(c << 23);
 #pragma unroll
-  for (int mt = 0; mt < 2; ++mt) {
-    const float f0 = __shfl_sync(kFull, f, 16 * mt + g), f1 = __shfl_sync(kFull, f, 16 * mt + 8 + g);
+  for (int mp = 0; mp < 2; ++mp) {
+    // lane i has the scale of key 32 mp + i (NaN for a row that is not finite)
+    const uint32_t c = scales[32 * (2 * mp + (lane >> 4)) + (lane & 15)];
+    const float f = c == kQ8NonFinite ? CUDART_NAN_F : __uint_as_float(c << 23);
 #pragma unroll
-    for (int nq = 0; nq < NQ; ++nq) {
-      s[mt][nq][0] = __fmul_rn(s[mt][nq][0], f0);
-      s[mt][nq][1] = __fmul_rn(s[mt][nq][1], f0);
-      s[mt][nq][2] = __fmul_rn(s[mt][nq][2], f1);
-      s[mt][nq][3] = __fmul_rn(s[mt][nq][3], f1);
+    for (int m2 = 0; m2 < 2; ++m2) {
+      const int mt = 2 * mp + m2;
+      const float f0 = __shfl_sync(kFull, f, 16 * m2 + g);
+      const float f1 = __shfl_sync(kFull, f, 16 * m2 + 8 + g);
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+        s[mt][nq][0] = __fmul_rn(s[mt][nq][0], f0);
+        s[mt][nq][1] = __fmul_rn(s[mt][nq][1], f0);
+        s[mt][nq][2] = __fmul_rn(s[mt][nq][2], f1);
+        s[mt][nq][3] = __fmul_rn(s[mt][nq][3], f1);
+      }
     }
   }
 }
@@ -1224,107 +1175,157 @@ __device__ __forceinline__ float q8_unscale(int top) {
   return __uint_as_float((uint32_t)(top - 127 + 120 - kQ8PScale + 127) << 23);
 }
 
-// O^T += V^T P^T for the D / 2 columns of warp w.  The transposing load moves
-// 16-bit elements, so a thread gets columns 2g and 2g + 1 of a 16-column
-// chunk for keys 2t, 2t + 1: the even bytes are the A operand's row g, the
-// odd ones its row g + 8, and o's rows stand for the chunk's columns 2g
-// (c = 0, 1) and 2g + 1 (c = 2, 3).
+// The softmax of tile_step on those scores: probabilities into s, the running
+// maximum and sum, and o, held relative to V's largest scale byte `vtop`,
+// brought to the tile's references (vnew: its V scale byte).  Padding columns
+// are never read.
 template <int D, int NQ>
-__device__ __forceinline__ void q8_values(float (&o)[D / 32][NQ][4], const Q8Exchange<NQ>& ex,
-                                          uint32_t vbase, int w) {
-  constexpr int kChunks = D / 32;  // 16-column chunks of a warp
-  const int lane = threadIdx.x & 31;
-  const int mi = lane >> 3, r8 = lane & 7;
+__device__ __forceinline__ void q8_softmax(SplitState<D, NQ>& st, float (&s)[4][NQ][4],
+                                           const float (&sc)[NQ][2], int vtop, int vnew) {
+  float alpha[NQ][2];
+  bool moved = vnew != vtop;
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
-    uint4 f[NQ];  // {high, high, low, low} of keys 16 kk + 0..7 and + 8..15
+  for (int nq = 0; nq < NQ; ++nq) {
+    float mb[2], cs[2];
 #pragma unroll
-    for (int nq = 0; nq < NQ; ++nq) f[nq] = ex.frag[kk][nq][lane];
-    uint32_t a[kChunks][4];
+    for (int cc = 0; cc < 2; ++cc) {
+      float mx = fmaxf(s[0][nq][cc], s[0][nq][2 + cc]);
 #pragma unroll
-    for (int i = 0; i < kChunks / 2; ++i) {
-      uint32_t r[4];  // keys 0-7 and 8-15 of two chunks
-      ldsm_x4_t(vbase + q8_off<D>(16 * kk + r8 + 8 * (mi & 1), kChunks * w + 2 * i + (mi >> 1)), r);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        a[2 * i + u][0] = e4m3_even(r[2 * u]);
-        a[2 * i + u][1] = e4m3_odd(r[2 * u]);
-        a[2 * i + u][2] = e4m3_even(r[2 * u + 1]);
-        a[2 * i + u][3] = e4m3_odd(r[2 * u + 1]);
+      for (int mt = 1; mt < 4; ++mt) mx = max3(mx, s[mt][nq][cc], s[mt][nq][2 + cc]);
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+      const float t = __fmul_rn(mx, sc[nq][cc]), m_in = st.m[nq][cc];
+      float mnew = m_in;
+      alpha[nq][cc] = 1.0f;
+      if (t == -CUDART_INF_F) {
+        // no visible key: exact no-op for this column
+      } else if (m_in == -CUDART_INF_F) {
+        mnew = t;
+        alpha[nq][cc] = 0.0f;
+      } else if (__fsub_rn(t, m_in) > kRescaleLog2) {
+        mnew = t;
+        alpha[nq][cc] = exp2_sfu(__fsub_rn(m_in, t));
       }
+      moved = moved || alpha[nq][cc] != 1.0f;
+      st.m[nq][cc] = mnew;
+      mb[cc] = mnew == -CUDART_INF_F ? 0.0f : mnew;
+      cs[cc] = 0.0f;
     }
-    // P's high part before its low one for every sum; the sums of other
-    // chunks and n-tiles are independent
 #pragma unroll
-    for (int u = 0; u < kChunks; ++u)
+    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-      for (int nq = 0; nq < NQ; ++nq) mma_bf16_free(o[u][nq], a[u], f[nq].x, f[nq].y);
+      for (int c = 0; c < 4; ++c) {
+        const int cc = c & 1;
+        const float pv = exp2_sfu(__fmaf_rn(s[mt][nq][c], sc[nq][cc], -mb[cc]));
+        s[mt][nq][c] = pv;
+        cs[cc] = __fadd_rn(cs[cc], pv);
+      }
 #pragma unroll
-    for (int u = 0; u < kChunks; ++u)
+    for (int cc = 0; cc < 2; ++cc) {
+      cs[cc] = __fadd_rn(cs[cc], __shfl_xor_sync(kFull, cs[cc], 4));
+      cs[cc] = __fadd_rn(cs[cc], __shfl_xor_sync(kFull, cs[cc], 8));
+      cs[cc] = __fadd_rn(cs[cc], __shfl_xor_sync(kFull, cs[cc], 16));
+      st.l[nq][cc] = __fadd_rn(__fmul_rn(st.l[nq][cc], alpha[nq][cc]), cs[cc]);
+    }
+  }
+  // a product with 1 changes nothing, so it is left out where none moved
+  if (__any_sync(kFull, moved)) {
+    const float vshift = __uint_as_float((uint32_t)max(0, vtop - vnew + 127) << 23);
 #pragma unroll
-      for (int nq = 0; nq < NQ; ++nq) mma_bf16_free(o[u][nq], a[u], f[nq].z, f[nq].w);
+    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+      for (int md = 0; md < D / 16; ++md)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          st.o[md][nq][c] = __fmul_rn(__fmul_rn(st.o[md][nq][c], alpha[nq][c & 1]), vshift);
   }
 }
 
-// Barrier of one group's compute warps.
-__device__ __forceinline__ void q8_group_sync(int group) {
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kQ8Warps * 32) : "memory");
+// O^T += V^T P^T.  The transposing load moves 16-bit elements, so a thread
+// gets columns 2g and 2g + 1 of a 16-column chunk for keys 2t, 2t + 1: the
+// even bytes are the A operand's row g, the odd ones its row g + 8, and o's
+// rows stand for d = 16 md + 2g (c = 0, 1) and 16 md + 2g + 1 (c = 2, 3).
+// Only the first `limit` keys exist: the scale bytes of the others read as 0,
+// since their slots may hold any bits; an element is finite whatever its
+// bits, so that a finite factor is enough for 0 * v to be 0.
+template <int D, int NQ>
+__device__ __forceinline__ void q8_values(SplitState<D, NQ>& st, const float (&s)[4][NQ][4],
+                                          uint32_t vbase, const uint8_t* scales, int limit,
+                                          int vtop) {
+  const int lane = threadIdx.x & 31;
+  const int t = lane & 3, mi = lane >> 3, r8 = lane & 7;
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    uint32_t vf[2];  // factors of keys 16 kk + 2t, + 1 and of 16 kk + 8 + 2t, + 1
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t c = *reinterpret_cast<const uint16_t*>(scales + 32 * kk + 16 + 8 * half + 2 * t);
+      if (limit < kTile) {
+        const int k = 16 * kk + 8 * half + 2 * t;
+        if (k >= limit) c = 0;
+        if (k + 1 >= limit) c &= 0xffu;
+      }
+      vf[half] = q8_p_factors(c, vtop);
+    }
+    uint32_t bh[NQ][2], bl[NQ][2];
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t hp, lp;
+        split_p_bf16(s[kk][nq][2 * half], s[kk][nq][2 * half + 1], hp, lp);
+        bh[nq][half] = mul_bf16x2(transpose8x8(hp), vf[half]);
+        bl[nq][half] = mul_bf16x2(transpose8x8(lp), vf[half]);
+      }
+#pragma unroll
+    for (int mp = 0; mp < D / 32; ++mp) {
+      uint32_t r[4];  // keys 0-7 and 8-15 of column chunks 2 mp and 2 mp + 1
+      ldsm_x4_t(vbase + q8_off<D>(16 * kk + r8 + 8 * (mi & 1), 2 * mp + (mi >> 1)), r);
+      uint32_t a[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        a[u][0] = e4m3_even(r[2 * u]);
+        a[u][1] = e4m3_odd(r[2 * u]);
+        a[u][2] = e4m3_even(r[2 * u + 1]);
+        a[u][3] = e4m3_odd(r[2 * u + 1]);
+      }
+      // P's high part before its low one for every sum; the sums of other
+      // chunks and n-tiles are independent
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+          mma_bf16_free(st.o[2 * mp + u][nq], a[u], bh[nq][0], bh[nq][1]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+          mma_bf16_free(st.o[2 * mp + u][nq], a[u], bl[nq][0], bl[nq][1]);
+    }
+  }
 }
-// The same, and whether x holds in all of its threads.
-__device__ __forceinline__ bool q8_group_all(int group, bool x) {
-  uint32_t r = x ? 1 : 0;
-  asm volatile(
-      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %0, 0;\n\t"
-      "bar.red.and.pred b, %1, %2, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
-      : "+r"(r)
-      : "r"(group + 1), "n"(kQ8Warps * 32)
-      : "memory");
-  return r != 0;
+
+// Asynchronous copy of 16 bytes, evicted from L2 first (the cache is read
+// once a call; the partials written meanwhile stay for the merge).
+__device__ __forceinline__ void q8_copy16(uint32_t dst, const uint8_t* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "l"(policy)
+               : "memory");
 }
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_split_kernel(
-    const __grid_constant__ CUtensorMap map, const uint8_t* __restrict__ cache,
-    const KernelParams p) {
+    const uint8_t* __restrict__ cache, const KernelParams p) {
   using Geom = Q8Geom<D, NQ>;
-  constexpr int kStages = Geom::kStages, kQ8Groups = Geom::kGroups;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  __shared__ uint64_t b_full[kQ8Groups][kStages], b_empty[kQ8Groups][kStages];
-  __shared__ uint64_t b_ready[kQ8Groups][kQueue], b_freed[kQ8Groups][kQueue];
-  __shared__ int4 q_unit[kQ8Groups][kQueue];   // b, j, lo, hi of opened units (b < 0: no more)
-  __shared__ int q_head[kQ8Groups][kQueue];    // kv head h, or -(h+1) if its pages are bad
-  __shared__ int q_single[kQ8Groups][kQueue];  // the sequence has this one split
   __shared__ int s_incl[kLocalPlanMax], s_len[kLocalPlanMax];
-  __shared__ int s_plan[2];                    // the splits of all sequences, the variant's chunk
-  __shared__ int s_abort;
+  __shared__ int s_plan[2];  // the splits of all sequences, the variant's chunk
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool producer = warp >= kQ8Groups * kQ8Warps;
-  const int group = producer ? warp - kQ8Groups * kQ8Warps : warp / kQ8Warps;
-  uint8_t* ring = smem + group * Geom::kRingBytes;
-  uint8_t* scale_ring = smem + Geom::kScaleOff + group * Geom::kScaleSlots * Geom::kScaleBytes;
-  uint64_t* full = b_full[group];
-  uint64_t* empty = b_empty[group];
-  uint64_t* ready = b_ready[group];
-  uint64_t* freed = b_freed[group];
   const int G = p.G, Hkv = p.Hkv;
-  if (threadIdx.x == 0) {
-    prefetch_tmap(&map);
-    for (int w = 0; w < kQ8Groups; ++w) {
-      for (int i = 0; i < kStages; ++i) {
-        mbar_init(&b_full[w][i], 1);
-        mbar_init(&b_empty[w][i], kQ8Warps);
-      }
-      for (int i = 0; i < kQueue; ++i) {
-        mbar_init(&b_ready[w][i], 1);
-        mbar_init(&b_freed[w][i], kQ8Warps);
-      }
-    }
-    s_abort = 0;
-    fence_mbar_init();
-  }
   grid_dependency_wait();  // inputs and the plan kernel's unit list are complete from here
 
   // ---- the plan, as in attn_decode_split_kernel: for small batches the
@@ -1402,378 +1403,230 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
   }
   __syncthreads();
 
-  if (producer) {
-    // ============================================================ producer
-    const int U = s_plan[0] * Hkv, csize = s_plan[1];
-    const int stride = gridDim.x * kQ8Groups;
-    auto unit_at = [&](int s) -> int4 {  // {b, j, lo, hi} of split s; warp-uniform s
-      if (!p.local_plan) return p.units[s];
+
+  // ------------------------------------------------- units and their copies
+  struct Unit {
+    int b, j, lo, hi, h;  // h < 0: none
+    int pg0, pg1;         // page ids: lane i has the unit's pages i and 32 + i
+  };
+  const int U = s_plan[0] * Hkv, csize = s_plan[1];
+  const int stride = gridDim.x * Geom::kWarps;
+  int lu = warp * gridDim.x + blockIdx.x;  // next unit to fetch: neighbours on other SMs
+  auto fetch = [&]() -> Unit {             // the next unit, its page ids in flight
+    Unit u;
+    u.h = -1;
+    if (lu >= U) return u;
+    const int s = lu / Hkv;
+    u.h = lu - s * Hkv;
+    lu += stride;
+    if (p.local_plan) {
       int b = 0;
 #pragma unroll
       for (int k = 0; k < kLocalSlabs; ++k)
         b += __popc(__ballot_sync(kFull, s_incl[lane + 32 * k] <= s));
-      const int L = s_len[b];
-      const int j = s - (b > 0 ? s_incl[b - 1] : 0);
       const int c = p.variant ? csize : p.split_size;
-      return make_int4(b, j, j * c, min((j + 1) * c, L));
-    };
-    // the pending unit: its descriptor and first page ids (in flight in
-    // registers: lane i holds pages i and 32 + i)
-    int lu = group * gridDim.x + blockIdx.x;  // next unit to fetch: neighbours on other SMs
-    bool pend = false;
-    int4 pd = make_int4(0, 0, 0, 0);
-    int ph = 0, pg0 = 0, pg1 = 0;
-    auto fetch = [&]() {
-      pend = lu < U;
-      if (!pend) return;
-      ph = lu % Hkv;
-      pd = unit_at(lu / Hkv);
-      lu += stride;
-      const int npg = (pd.w - pd.z + kPage - 1) / kPage;
-      const int32_t* bt = p.block_table + (int64_t)pd.x * p.max_blocks + (pd.z >> 4);
-      pg0 = lane < npg ? bt[lane] : 0;
-      pg1 = lane + 32 < npg ? bt[lane + 32] : 0;
-    };
-    const uint64_t pol = l2_policy_evict_first();
-    int n_units = 0, n = 0, tiles = 0;  // units opened, stages filled, tiles issued
-    int stage = 0;
-    uint32_t phase = 1;                 // parity of the wait for a free stage
-    bool ok = true;
-    fetch();
-    while (ok) {
-      const int slot = n_units % kQueue;
-      if (n_units >= kQueue)
-        ok = __all_sync(kFull, mbar_wait_lazy(&freed[slot], ((n_units / kQueue) - 1) & 1, p.err,
-                                         &s_abort));
-      if (!ok) break;
-      if (!pend) {  // no more units: the end marker
-        if (lane == 0) {
-          q_unit[group][slot] = make_int4(-1, 0, 0, 0);
-          mbar_arrive(&ready[slot]);
-        }
-        break;
-      }
-      // check the pending unit's pages and queue its descriptor
-      const int4 d = pd;
-      const int h = ph, c0 = pg0, c1 = pg1;
-      const int npg = (d.w - d.z + kPage - 1) / kPage;
-      const int32_t* bt = p.block_table + (int64_t)d.x * p.max_blocks;
-      bool good = c0 >= 0 && c0 < p.num_pages && c1 >= 0 && c1 < p.num_pages;
-      if (npg > 64 && !pages_ok(bt, d.z + 64 * kPage, d.w, p.num_pages, lane, 32)) good = false;
+      u.b = b;
+      u.j = s - (b > 0 ? s_incl[b - 1] : 0);
+      u.lo = u.j * c;
+      u.hi = min(u.lo + c, s_len[b]);
+    } else {
+      const int4 d = p.units[s];
+      u.b = d.x;
+      u.j = d.y;
+      u.lo = d.z;
+      u.hi = d.w;
+    }
+    const int npg = (u.hi - u.lo + kPage - 1) / kPage;
+    const int32_t* bt = p.block_table + (int64_t)u.b * p.max_blocks + (u.lo >> 4);
+    u.pg0 = lane < npg ? bt[lane] : 0;
+    u.pg1 = lane + 32 < npg ? bt[lane + 32] : 0;
+    return u;
+  };
+  // Split 0 is a sequence's only one iff it ends below the chunk size or the
+  // sequence is exactly one chunk long; it writes the output itself.
+  auto single_split = [&](const Unit& u) {
+    const int c = p.variant ? csize : p.split_size;
+    return u.j == 0 && (u.hi < c || (p.local_plan ? s_len[u.b] : p.kv_lens[u.b]) == c);
+  };
+  Unit pend = fetch();
+  // The next unit whose pages are all in the pool (h < 0: no more); a unit with
+  // a bad page is recorded and its rows become zeros (l = -1 makes the merge
+  // write them).
+  auto open = [&]() -> Unit {
+    for (;;) {
+      const Unit u = pend;
+      if (u.h < 0) return u;
+      const int32_t* bt = p.block_table + (int64_t)u.b * p.max_blocks;
+      bool good = u.pg0 >= 0 && u.pg0 < p.num_pages && u.pg1 >= 0 && u.pg1 < p.num_pages;
+      if (u.hi - u.lo > 64 * kPage &&
+          !pages_ok(bt, u.lo + 64 * kPage, u.hi, p.num_pages, lane, 32))
+        good = false;
       good = __all_sync(kFull, good);
-      if (lane == 0) {
-        // split 0 is the only one iff it ends below the chunk size or the
-        // sequence is exactly one chunk long
-        const int c = p.variant ? csize : p.split_size;
-        q_unit[group][slot] = d;
-        q_head[group][slot] = good ? h : -(h + 1);
-        q_single[group][slot] =
-            d.y == 0 && (d.w < c || (p.local_plan ? s_len[d.x] : p.kv_lens[d.x]) == c);
-        if (!good) record_error(p.err, BI_ERR_DEVICE_BOUNDS);
-        mbar_arrive(&ready[slot]);
-      }
-      __syncwarp();
-      ++n_units;
-      fetch();  // the next unit's page ids load while this unit's tiles are issued
-      if (!good) continue;
-      const int ntiles = (d.w - d.z + kTile - 1) / kTile;
-      for (int lt = 0; lt < ntiles && ok; ++lt) {
-        const int np = min(kPagesPerTile, npg - 4 * lt);
-        const int idx = 4 * lt + (lane & 3);  // this lane's page of the unit
-        const int in0 = __shfl_sync(kFull, c0, idx & 31), in1 = __shfl_sync(kFull, c1, idx & 31);
-        const int pid = lane >= np ? 0 : idx < 32 ? in0 : idx < 64 ? in1 : bt[(d.z >> 4) + idx];
-        const int64_t rec = (int64_t)pid * Hkv + h;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {  // K, then V
-          if (n >= kStages)
-            ok = __all_sync(kFull, mbar_wait_lazy(&empty[stage], phase, p.err, &s_abort));
-          if (!ok) break;
-          uint64_t* bar = &full[stage];
-          if (lane == 0)
-            mbar_arrive_expect_tx(bar, np * (Geom::kPageHalf + (half == 0 ? 32 : 0)));
-          __syncwarp();
-          if (lane < np) {
-            tma_load_3d_hint(ring + stage * Geom::kHalf + lane * Geom::kPageHalf, &map, 0,
-                             half * kPage, (int)rec, bar, pol);
-            if (half == 0)
-              bulk_load(scale_ring + (tiles % Geom::kScaleSlots) * Geom::kScaleBytes + 32 * lane,
-                        cache + rec * Geom::kRecord + 2 * Geom::kPageHalf, 32, bar);
-          }
-          ++n;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-        ++tiles;
-      }
-    }
-    if (!ok) s_abort = 1;
-    // the copies in flight land before the block exits
-    if (lane == 0)
-      for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
-        mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr);
-    return;
-  }
-  // ============================================================== compute
-  // A wait that runs out (or is ended by the flag that another's raised)
-  // makes its warp go on without data to the end of the unit, through all of
-  // the group's barriers; the group agrees at the start of each unit to go on
-  // or to leave, so no warp is left at a barrier that another skips.
-  constexpr int kChunks = D / 32;
-  const int w = warp % kQ8Warps;
-  Q8Exchange<NQ>& ex = reinterpret_cast<Q8Exchange<NQ>*>(smem + Geom::kExchangeOff)[group];
-  uint32_t qf[NQ][D / 16][2];
-  float sc[NQ][2];
-  float o[kChunks][NQ][4], m[NQ][2], l[NQ][2];  // l: warp 1's
-  int vtop = 0;                                 // the largest V scale byte so far
-  const int g = lane >> 2, t = lane & 3;
-  int n = 0, tiles = 0, stage = 0;
-  uint32_t phase = 0;
-  bool alive = true;
-  auto wait_stage = [&]() {
-    alive = __all_sync(kFull, alive && mbar_wait(&full[stage], phase, p.err, &s_abort));
-  };
-  auto next_stage = [&]() {  // back to the producer, on to the next
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[stage]);
-    if (++stage == kStages) {
-      stage = 0;
-      phase ^= 1;
-    }
-  };
-  for (;;) {
-    const int slot = n % kQueue;
-    alive = alive && mbar_wait(&ready[slot], (n / kQueue) & 1, p.err, &s_abort);
-    if (!q8_group_all(group, alive)) break;
-    const int4 d = q_unit[group][slot];
-    const int hv = q_head[group][slot];
-    const bool single = q_single[group][slot] != 0;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&freed[slot]);
-    ++n;
-    if (d.x < 0) break;  // no more units
-    const bool pages_good = hv >= 0;
-    const int h = pages_good ? hv : -hv - 1;
-    const int b = d.x, j = d.y, lo = d.z, hi = d.w;
-    const int64_t row0 = (int64_t)b * p.Hq + (int64_t)h * G;  // first q-head row
-    if (!pages_good) {  // l = -1 makes the merge emit zeros
-      if (w == 0 && single) {
+      pend = fetch();  // its page ids load while this unit is computed
+      if (good) return u;
+      if (lane == 0) record_error(p.err, BI_ERR_DEVICE_BOUNDS);
+      const int64_t row0 = (int64_t)u.b * p.Hq + (int64_t)u.h * G;
+      if (single_split(u)) {
         for (int i = lane; i < G * D; i += 32) {
           static_cast<__nv_bfloat16*>(p.out)[row0 * D + i] = __float2bfloat16_rn(0.0f);
           if (p.out_f32) p.out_f32[row0 * D + i] = 0.0f;
         }
-      } else if (w == 0 && lane < G) {
-        const int64_t s = (row0 + lane) * p.ml_stride + j;
+      } else if (lane < G) {
+        const int64_t s = (row0 + lane) * p.ml_stride + u.j;
         p.ml[2 * s] = -CUDART_INF_F;
         p.ml[2 * s + 1] = -1.0f;
       }
-      continue;
     }
+  };
+  uint8_t* kv = smem + warp * 2 * Geom::kHalf;  // K, then V
+  uint8_t* scale_buf =
+      smem + Geom::kWarps * 2 * Geom::kHalf + warp * 2 * Geom::kScaleBytes;
+  const uint64_t pol = l2_policy_evict_first();
+  // where a lane's 16 bytes of a 512-byte piece of a page go (even and odd
+  // pieces): rows of D bytes, the chunk swizzled as q8_off says
+  const uint32_t off0 = q8_off<D>(16 * lane / D, lane % (D / 16));
+  const uint32_t off1 = q8_off<D>(16 * lane / D + 512 / D, lane % (D / 16)) - 512;
+  // Copy tile lt's K (half 0, with its scale bytes into buffer `parity`) or V;
+  // one group of copies, empty for a unit that is not there.
+  auto copy = [&](const Unit& u, int lt, int half, int parity) {
+    if (u.h >= 0) {
+      const int npg = (u.hi - u.lo + kPage - 1) / kPage;
+      const int np = min(kPagesPerTile, npg - 4 * lt);
+      const int idx = 4 * lt + (lane & 3);  // this lane's page of the unit
+      const int in0 = __shfl_sync(kFull, u.pg0, idx & 31);
+      const int in1 = __shfl_sync(kFull, u.pg1, idx & 31);
+      const int pid = (lane & 3) >= np ? 0
+                      : idx < 32       ? in0
+                      : idx < 64       ? in1
+                                       : p.block_table[(int64_t)u.b * p.max_blocks +
+                                                       (u.lo >> 4) + idx];
+      const uint32_t rec = (uint32_t)pid * (uint32_t)Hkv + (uint32_t)u.h;
+      const uint32_t dst = smem_u32(kv) + half * Geom::kHalf;
+      const uint8_t* src = cache + half * Geom::kPageHalf + 16 * lane;
+#pragma unroll
+      for (int i = 0; i < kPagesPerTile; ++i) {
+        if (i >= np) break;
+        const uint8_t* page =
+            src + (uint64_t)__shfl_sync(kFull, rec, i) * (uint32_t)Geom::kRecord;
+#pragma unroll
+        for (int c = 0; c < Geom::kPageHalf / 512; ++c)
+          q8_copy16(dst + i * Geom::kPageHalf + 512 * c + (c & 1 ? off1 : off0), page + 512 * c,
+                    pol);
+      }
+      if (half == 0) {  // the scale bytes: lane i those of K or V of page i / 2
+        const uint32_t from = __shfl_sync(kFull, rec, (lane >> 1) & 3);
+        if (lane < 2 * np)
+          q8_copy16(smem_u32(scale_buf) + parity * Geom::kScaleBytes + 16 * lane,
+                    cache + (uint64_t)from * (uint32_t)Geom::kRecord + 2 * Geom::kPageHalf +
+                        16 * (lane & 1),
+                    pol);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // all of this warp's copies but the last group have landed
+  auto landed = [&]() {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+  };
+
+  SplitState<D, NQ> st;
+  uint32_t qf[NQ][D / 16][2];
+  float sc[NQ][2];
+  const int g = lane >> 2, t = lane & 3;
+  int parity = 0;
+  Unit next = open();
+  copy(next, 0, 0, 0);
+  copy(next, 0, 1, 0);
+  while (next.h >= 0) {
+    const Unit u = next;
+    next = open();
+    const int64_t row0 = (int64_t)u.b * p.Hq + (int64_t)u.h * G;  // first q-head row
     const bool f16 = q8_load_q<D, NQ>(qf, sc, p.q + row0 * D, G, p.scale_log2);
-    vtop = 0;
-#pragma unroll
-    for (int nq = 0; nq < NQ; ++nq) {
-      m[nq][0] = m[nq][1] = -CUDART_INF_F;
-      l[nq][0] = l[nq][1] = 0.0f;
-#pragma unroll
-      for (int u = 0; u < kChunks; ++u)
-        o[u][nq][0] = o[u][nq][1] = o[u][nq][2] = o[u][nq][3] = 0.0f;
-    }
-    for (int key0 = lo; key0 < hi; key0 += kTile, ++tiles) {
-      uint8_t* scales = scale_ring + (tiles % Geom::kScaleSlots) * Geom::kScaleBytes;
-      const int limit = hi - key0;  // keys of the tile that exist (or more)
-      float s[2][NQ][4];
-      wait_stage();
+    st.reset();
+    int vtop = 0;  // the largest V scale byte so far
+    for (int lt = 0; u.lo + lt * kTile < u.hi; ++lt, parity ^= 1) {
+      const uint8_t* scales = scale_buf + parity * Geom::kScaleBytes;
+      const int limit = u.hi - u.lo - lt * kTile;  // keys of the tile that exist (or more)
+      const bool last = limit <= kTile;
+      float s[4][NQ][4];
+      landed();
       if (f16)
-        q8_scores<D, NQ, true>(s, qf, smem_u32(ring + stage * Geom::kHalf), scales, w);
+        q8_scores<D, NQ, true>(s, qf, smem_u32(kv), scales);
       else
-        q8_scores<D, NQ, false>(s, qf, smem_u32(ring + stage * Geom::kHalf), scales, w);
+        q8_scores<D, NQ, false>(s, qf, smem_u32(kv), scales);
       // the largest V scale of the tile's keys
       const uint32_t cv = *reinterpret_cast<const uint16_t*>(scales + 32 * (lane >> 3) + 16 +
                                                              2 * (lane & 7));
       uint32_t c0 = cv & 0xffu, c1 = cv >> 8;
-      if (limit < kTile) {
-        // Keys behind the last token are masked, and their V scale bytes
-        // become 0: those slots may hold any bits, and an element is finite
-        // whatever its bits, so a finite factor is enough for 0 * v to be 0.
-        // Padding columns are never read and need no mask.
+      if (limit < kTile) {  // keys behind the last token are masked
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (32 * w + 16 * mt + g + 8 * (c >> 1) >= limit) s[mt][nq][c] = -CUDART_INF_F;
+              if (16 * mt + g + 8 * (c >> 1) >= limit) s[mt][nq][c] = -CUDART_INF_F;
         if (2 * lane >= limit) c0 = 0;
         if (2 * lane + 1 >= limit) c1 = 0;
       }
       const int vnew =
           max(vtop, (int)min(__reduce_max_sync(kFull, max(c0, c1)), (uint32_t)kQ8NonFinite));
-      next_stage();
-      // ---- the tile's column maxima over both warps' keys
-#pragma unroll
-      for (int nq = 0; nq < NQ; ++nq) {
-        float2 mx = make_float2(fmaxf(max3(s[0][nq][0], s[0][nq][2], s[1][nq][0]), s[1][nq][2]),
-                                fmaxf(max3(s[0][nq][1], s[0][nq][3], s[1][nq][1]), s[1][nq][3]));
-#pragma unroll
-        for (int x = 4; x <= 16; x <<= 1) {
-          mx.x = fmaxf(mx.x, __shfl_xor_sync(kFull, mx.x, x));
-          mx.y = fmaxf(mx.y, __shfl_xor_sync(kFull, mx.y, x));
-        }
-        if (g == 0) *reinterpret_cast<float2*>(&ex.top[w][8 * nq + 2 * t]) = mx;
-      }
-      q8_group_sync(group);
-      // ---- reference, probabilities of this warp's keys: tile_step's rules
-      uint32_t vf[2][2];  // P's factors of keys 16 kk + 2t, + 1 and + 8
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          // the bytes of masked keys read as 0
-          const int k = 32 * w + 16 * mt + 8 * half + 2 * t;
-          uint32_t c = *reinterpret_cast<const uint16_t*>(scales + 32 * (2 * w + mt) + 16 +
-                                                          8 * half + 2 * t);
-          if (k >= limit) c = 0;
-          if (k + 1 >= limit) c &= 0xffu;
-          vf[mt][half] = q8_p_factors(c, vnew);
-        }
-      const float vshift = __uint_as_float((uint32_t)max(0, vtop - vnew + 127) << 23);
-      bool moved = vnew != vtop;
+      __syncwarp();  // every lane is done with K
+      if (last)
+        copy(next, 0, 0, parity ^ 1);
+      else
+        copy(u, lt + 1, 0, parity ^ 1);
+      q8_softmax<D, NQ>(st, s, sc, vtop, vnew);
       vtop = vnew;
-      float alpha[NQ][2], cs[NQ][2];
-#pragma unroll
-      for (int nq = 0; nq < NQ; ++nq) {
-        float mb[2];
-        const float2 x0 = *reinterpret_cast<const float2*>(&ex.top[0][8 * nq + 2 * t]);
-        const float2 x1 = *reinterpret_cast<const float2*>(&ex.top[1][8 * nq + 2 * t]);
-        const float mx[2] = {fmaxf(x0.x, x1.x), fmaxf(x0.y, x1.y)};
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          const float top = __fmul_rn(mx[cc], sc[nq][cc]), m_in = m[nq][cc];
-          alpha[nq][cc] = 1.0f;
-          if (top == -CUDART_INF_F) {
-            // no visible key: exact no-op for this column
-          } else if (m_in == -CUDART_INF_F) {
-            m[nq][cc] = top;
-            alpha[nq][cc] = 0.0f;
-          } else if (__fsub_rn(top, m_in) > kRescaleLog2) {
-            m[nq][cc] = top;
-            alpha[nq][cc] = exp2_sfu(__fsub_rn(m_in, top));
-          }
-          moved = moved || alpha[nq][cc] != 1.0f;
-          mb[cc] = m[nq][cc] == -CUDART_INF_F ? 0.0f : m[nq][cc];
-          cs[nq][cc] = 0.0f;
-        }
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            s[mt][nq][c] = exp2_sfu(__fmaf_rn(s[mt][nq][c], sc[nq][c & 1], -mb[c & 1]));
-          uint32_t hp[2], lp[2];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            split_p_bf16(s[mt][nq][2 * half], s[mt][nq][2 * half + 1], hp[half], lp[half]);
-            hp[half] = mul_bf16x2(transpose8x8(hp[half]), vf[mt][half]);
-            lp[half] = mul_bf16x2(transpose8x8(lp[half]), vf[mt][half]);
-          }
-          ex.frag[2 * w + mt][nq][lane] = make_uint4(hp[0], hp[1], lp[0], lp[1]);
-        }
-        // a thread's keys are summed in order: warp 0's, then warp 1's
-        if (w == 0) {
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            cs[nq][0] = __fadd_rn(__fadd_rn(cs[nq][0], s[mt][nq][0]), s[mt][nq][2]);
-            cs[nq][1] = __fadd_rn(__fadd_rn(cs[nq][1], s[mt][nq][1]), s[mt][nq][3]);
-          }
-          ex.sum[nq][lane] = make_float2(cs[nq][0], cs[nq][1]);
-        }
-      }
-      q8_group_sync(group);
-      if (w == 1) {
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) {
-          const float2 before = ex.sum[nq][lane];
-          cs[nq][0] = before.x;
-          cs[nq][1] = before.y;
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            cs[nq][0] = __fadd_rn(__fadd_rn(cs[nq][0], s[mt][nq][0]), s[mt][nq][2]);
-            cs[nq][1] = __fadd_rn(__fadd_rn(cs[nq][1], s[mt][nq][1]), s[mt][nq][3]);
-          }
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            cs[nq][cc] = __fadd_rn(cs[nq][cc], __shfl_xor_sync(kFull, cs[nq][cc], 4));
-            cs[nq][cc] = __fadd_rn(cs[nq][cc], __shfl_xor_sync(kFull, cs[nq][cc], 8));
-            cs[nq][cc] = __fadd_rn(cs[nq][cc], __shfl_xor_sync(kFull, cs[nq][cc], 16));
-            l[nq][cc] = __fadd_rn(__fmul_rn(l[nq][cc], alpha[nq][cc]), cs[nq][cc]);
-          }
-        }
-      }
-      // a product with 1 changes nothing, so it is left out where none moved
-      if (__any_sync(kFull, moved)) {
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-          for (int u = 0; u < kChunks; ++u)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              o[u][nq][c] = __fmul_rn(__fmul_rn(o[u][nq][c], alpha[nq][c & 1]), vshift);
-      }
-      wait_stage();
-      q8_values<D, NQ>(o, ex, smem_u32(ring + stage * Geom::kHalf), w);
-      next_stage();
+      landed();
+      q8_values<D, NQ>(st, s, smem_u32(kv + Geom::kHalf), scales, limit, vtop);
+      __syncwarp();  // every lane is done with V
+      if (last)
+        copy(next, 0, 1, 0);
+      else
+        copy(u, lt + 1, 1, 0);
     }
-    const float back = q8_unscale(vtop);
-#pragma unroll
-    for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-      for (int u = 0; u < kChunks; ++u)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[u][nq][c] = __fmul_rn(o[u][nq][c], back);
     // ---- the output of a single split, or the partial state; columns d and
     // d + 1 are neighbours in a thread
-    if (single) {
-      if (w == 1 && g == 0) {
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-          *reinterpret_cast<float2*>(&ex.l[8 * nq + 2 * t]) = make_float2(l[nq][0], l[nq][1]);
-      }
-      q8_group_sync(group);
-    }
+    const bool single = single_split(u);
+    const float back = q8_unscale(vtop);
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         const int col = 8 * nq + 2 * t + cc;
         if (col >= G) continue;
-        const int dcol = 16 * kChunks * w + 2 * g;
+        const float lv = st.l[nq][cc];
         if (single) {
-          const float lv = ex.l[col], rl = inv_l(lv);
-          const int64_t orow = (row0 + col) * D + dcol;
+          const float rl = inv_l(lv);
+          const int64_t orow = (row0 + col) * D + 2 * g;
 #pragma unroll
-          for (int u = 0; u < kChunks; ++u) {
-            const float v0 = lv > 0.0f ? normalize(o[u][nq][cc], rl) : 0.0f;
-            const float v1 = lv > 0.0f ? normalize(o[u][nq][2 + cc], rl) : 0.0f;
-            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow + 16 * u) =
+          for (int md = 0; md < D / 16; ++md) {
+            const float v0 =
+                lv > 0.0f ? normalize(__fmul_rn(st.o[md][nq][cc], back), rl) : 0.0f;
+            const float v1 =
+                lv > 0.0f ? normalize(__fmul_rn(st.o[md][nq][2 + cc], back), rl) : 0.0f;
+            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow + 16 * md) =
                 pack_bf16x2(v0, v1);
             if (p.out_f32)
-              *reinterpret_cast<float2*>(p.out_f32 + orow + 16 * u) = make_float2(v0, v1);
+              *reinterpret_cast<float2*>(p.out_f32 + orow + 16 * md) = make_float2(v0, v1);
           }
           continue;
         }
-        if (w == 1 && g == 0) {
-          const int64_t sm = (row0 + col) * p.ml_stride + j;
-          p.ml[2 * sm] = m[nq][cc];
-          p.ml[2 * sm + 1] = l[nq][cc];
+        const int64_t sm = (row0 + col) * p.ml_stride + u.j;
+        if (g == 0) {
+          p.ml[2 * sm] = st.m[nq][cc];
+          p.ml[2 * sm + 1] = lv;
         }
-        float* orow = p.o + ((row0 + col) * p.max_splits + j) * D + dcol;
+        float* orow = p.o + ((row0 + col) * p.max_splits + u.j) * D + 2 * g;
 #pragma unroll
-        for (int u = 0; u < kChunks; ++u)
-          *reinterpret_cast<float2*>(orow + 16 * u) = make_float2(o[u][nq][cc], o[u][nq][2 + cc]);
+        for (int md = 0; md < D / 16; ++md)
+          *reinterpret_cast<float2*>(orow + 16 * md) = make_float2(
+              __fmul_rn(st.o[md][nq][cc], back), __fmul_rn(st.o[md][nq][2 + cc], back));
       }
   }
-  if (!alive) s_abort = 1;
+  asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the block
 }
 
 // ------------------------------------------------------------ decode merge
@@ -1952,6 +1805,36 @@ struct PfGeom {
   static constexpr uint32_t kColS = 0, kColO = 2 * kPfPair, kColQ = kColO + 128;
 };
 static_assert(PfGeom<128>::kSmem <= 232448, "prefill shared memory");
+
+// mbarrier wait for the roles with slack (the fold and TMA warps): the thread
+// suspends in the wait (a hint of 20 us, then it tries again), leaving the
+// issue slots of its scheduler to the softmax warp beside it; bounded in time
+// like mbar_wait.  The MMA and softmax warps, whose waits are on the
+// critical path, use mbar_wait itself.
+__device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool pf_wait_lazy(uint64_t* bar, uint32_t parity, int* err,
+                                             volatile int* abort) {
+  if (mbar_try_wait_sleep(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (abort && *abort) return false;
+    if (global_ns() - t0 > kWaitNs) break;
+  }
+  record_error(err, BI_ERR_TIMEOUT);
+  if (abort) *abort = 1;
+  return false;
+}
 
 // Wait for up to three barriers: their first tests go out back to back (the
 // common case is that all are complete), then each missing one is waited for.
@@ -2157,7 +2040,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
       if (!is_v) {
         for (int q = 0; q < npairs && ok; ++q) {
           if (q >= kPfKStages)
-            ok = mbar_wait_lazy(&kfree[q % kPfKStages], ((q / kPfKStages) - 1) & 1, p.err,
+            ok = pf_wait_lazy(&kfree[q % kPfKStages], ((q / kPfKStages) - 1) & 1, p.err,
                               &s_abort);
           if (!ok) break;
           issue(kst + (q % kPfKStages) * Gm::kKBytes + hf * (kPfPair * 128),
@@ -2166,12 +2049,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
         }
         // every copy lands before the block exits (bounded waits)
         for (int k = max(0, n - kPfKStages); k < n; ++k)
-          mbar_wait_lazy(&kfull[k % kPfKStages], (k / kPfKStages) & 1, ok ? p.err : nullptr,
+          pf_wait_lazy(&kfull[k % kPfKStages], (k / kPfKStages) & 1, ok ? p.err : nullptr,
                        ok ? &s_abort : nullptr);
       } else {
         for (int i = 0; i < ntiles && ok; ++i) {
           if (i >= kPfVStages)
-            ok = mbar_wait_lazy(&vfree[i % kPfVStages], ((i / kPfVStages) - 1) & 1, p.err,
+            ok = pf_wait_lazy(&vfree[i % kPfVStages], ((i / kPfVStages) - 1) & 1, p.err,
                               &s_abort);
           if (!ok) break;
           issue(vst + (i % kPfVStages) * Gm::kVBytes + hf * (kTile * 128),
@@ -2179,7 +2062,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
           ++n;
         }
         for (int k = max(0, n - kPfVStages); k < n; ++k)
-          mbar_wait_lazy(&vfull[k % kPfVStages], (k / kPfVStages) & 1, ok ? p.err : nullptr,
+          pf_wait_lazy(&vfull[k % kPfVStages], (k / kPfVStages) & 1, ok ? p.err : nullptr,
                        ok ? &s_abort : nullptr);
       }
     }
@@ -2424,8 +2307,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
     bool have = false;
     bool live = true;
     for (int j = 0; j < nsplits && live; ++j) {
-      live = __all_sync(kFull, mbar_wait_lazy(&sdone[j & 1], (j >> 1) & 1, p.err, &s_abort) &&
-                                   mbar_wait_lazy(odone, j & 1, p.err, &s_abort));
+      live = __all_sync(kFull, pf_wait_lazy(&sdone[j & 1], (j >> 1) & 1, p.err, &s_abort) &&
+                                   pf_wait_lazy(odone, j & 1, p.err, &s_abort));
       if (!live) break;
       tc_fence_after();
       const float m_s = xsplit[(j & 1) * 2 * kPfRows + r];
@@ -2663,9 +2546,6 @@ template <int D, int NQ>
 bi_status decode_q8_impl(const AttnArgs& a, cudaStream_t s) {
   KernelParams p = make_params(a);
   if (a.max_splits > 0) {
-    CUtensorMap map;
-    if (!make_tmap_records(&map, a.k_cache, static_cast<uint64_t>(a.num_pages) * a.Hkv, D))
-      return BI_ERR_CUDA;
     const DecodeWs w = decode_ws_layout(a.B, a.Hq, a.D, a.max_splits);
     char* base = reinterpret_cast<char*>(a.ws);
     p.unit_count = reinterpret_cast<int*>(base);
@@ -2680,12 +2560,11 @@ bi_status decode_q8_impl(const AttnArgs& a, cudaStream_t s) {
     const int sms = device_sm_count();
     if (sms <= 0) return BI_ERR_CUDA;
     const int64_t max_units = static_cast<int64_t>(a.B) * a.Hkv * a.max_splits;
-    p.target_units = 4 * Q8Geom<D, NQ>::kGroups * sms;  // variant: units per group, as the bf16 kernel's
+    p.target_units = 4 * Q8Geom<D, NQ>::kWarps * sms;  // variant: units per warp, as the bf16 kernel's
     if (!p.local_plan) attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
     const int grid = static_cast<int>(max_units < sms ? max_units : sms);
-    if (launch_pdl(attn_decode_q8_split_kernel<D, NQ>, dim3(grid), dim3(Q8Geom<D, NQ>::kThreads), sm, s,
-                   map,
-                   static_cast<const uint8_t*>(a.k_cache), p) != cudaSuccess)
+    if (launch_pdl(attn_decode_q8_split_kernel<D, NQ>, dim3(grid), dim3(Q8Geom<D, NQ>::kThreads), sm,
+                   s, static_cast<const uint8_t*>(a.k_cache), p) != cudaSuccess)
       return BI_ERR_CUDA;
   }
   if (launch_pdl(attn_decode_merge_kernel<D>, dim3(a.Hq, a.B), dim3(D), 0, s, p) != cudaSuccess)
