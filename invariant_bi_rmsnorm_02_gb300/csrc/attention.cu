@@ -1630,27 +1630,27 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
 }
 
 // ------------------------------------------------------------ decode merge
-// Block (qh, rank): one q-head row of the rank-th longest sequence (longest
-// first), D threads, one output column each.  Each warp folds its 32
-// columns over the splits in index order, 32 splits per chunk.  Lane j of a
-// warp loads split j's {m, l} and derives that split's coefficients: the
-// running maximum before a split is a prefix maximum, exact in any order,
-// so the whole chunk's coefficients come from one scan; the fold proper is
-// then a chain of products and sums with one select per split and no
-// branch, bit-identical to folding one split at a time.  Empty splits are
-// skipped; a split marked l = -1 (bad pages) makes the whole row zero.  The
-// o values of a chunk are loaded at once (one coalesced 128-byte row per
-// split and warp), and the next chunk's loads are issued before the current
-// chunk is folded.  No shared memory and no waits: the row's latency is a
-// load round trip per chunk plus the fold chain.  A row of a sequence with a
-// single split was written by the split kernel and is skipped here.
-constexpr int kMergeChunk = 32;
-
-template <int D>
-__global__ void __launch_bounds__(D) attn_decode_merge_kernel(const KernelParams p) {
-  // each warp's coefficients of the chunk being folded: {ca, cb, l, kind}
-  __shared__ float4 coef[D / 32][kMergeChunk];
-  const int qh = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Block (qh, rank, part): one warp, kCols columns per lane of one q-head row
+// of the rank-th longest sequence (longest first).  The splits are folded in
+// index order, 32 per chunk.  Lane j loads split j's {m, l} and derives that
+// split's coefficients: the running maximum before a split is a prefix
+// maximum, exact in any order, so the whole chunk's coefficients come from one
+// scan; the fold proper is then a chain of products and sums, bit-identical
+// to folding one split at a time.  Empty splits are skipped; a split marked
+// l = -1 (bad pages) makes the whole row zero.  A lane copies the o values of
+// its columns into shared memory with cp.async, kStages steps of kStep splits
+// ahead, and reads only what it copied itself, so nothing waits but the fold.
+// A row of a sequence with a single split was written by the split kernel and
+// is skipped here.
+// Bound by latency: a row's chain (its length, {m, l}, then the fold).  With
+// many rows a warp takes a whole row, so that the coefficients and l cost one
+// warp's instructions; with few, a row's columns are spread over D / 32 warps
+// and more splits are on their way.
+template <int D, int kCols, int kStep, int kStages>
+__global__ void __launch_bounds__(32) attn_decode_merge_kernel(const KernelParams p) {
+  __shared__ __align__(16) float ring[kStages][kStep][32 * kCols];
+  __shared__ float4 coef[32];  // {ca, cb, l * cb (or l), kind} of a chunk's splits
+  const int qh = blockIdx.x, lane = threadIdx.x;
   grid_dependency_wait();  // every split kernel block has finished
   int b, ns;
   if (p.order) {
@@ -1665,25 +1665,32 @@ __global__ void __launch_bounds__(D) attn_decode_merge_kernel(const KernelParams
   if (ns == 1) return;  // the split kernel wrote this row
   const int64_t row = (int64_t)b * p.Hq + qh;
   const float2* mlrow = reinterpret_cast<const float2*>(p.ml) + row * p.ml_stride;
-  const float* ocol = p.o + row * p.max_splits * D + tid;
-  // chunk starting at split c0: {m, l} of split c0 + lane, o of every split
-  auto load = [&](int c0, float2& ml, float (&ov)[kMergeChunk]) {
-    const int cnt = min(kMergeChunk, ns - c0);
-    ml = lane < cnt ? mlrow[c0 + lane] : make_float2(-CUDART_INF_F, 0.0f);
+  const float* orow = p.o + row * p.max_splits * D + kCols * (32 * blockIdx.z + lane);
+  auto load = [&](int k, int slot) {  // step k's o values, one group of copies
 #pragma unroll
-    for (int j = 0; j < kMergeChunk; ++j)
-      ov[j] = j < cnt ? ocol[static_cast<int64_t>(c0 + j) * D] : 0.0f;
+    for (int i = 0; i < kStep; ++i) {
+      const int j = kStep * k + i;
+      if (j < ns)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                         smem_u32(&ring[slot][i][kCols * lane])),
+                     "l"(orow + (int64_t)j * D), "n"(4 * kCols)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
+#pragma unroll
+  for (int k = 0; k < kStages; ++k) load(k, k);
   float run_m = -CUDART_INF_F;  // max over the splits folded so far
   bool have = false;            // a non-empty split was folded
   bool bad = false;             // a split with bad pages
-  float o = 0.0f, l = 0.0f;
-  // two chunk buffers: the chunk being folded and the next one in flight
-  float2 ml0, ml1;
-  float ov0[kMergeChunk], ov1[kMergeChunk];
-  auto fold = [&](const float2 ml, const float (&ov)[kMergeChunk]) {
-    // coefficients of the chunk's split lane
+  float o[kCols] = {}, l = 0.0f;
+  const float2 none = make_float2(-CUDART_INF_F, 0.0f);
+  float2 ml = lane < ns ? mlrow[lane] : none;
+  int slot = 0, step = 0;
+  for (int c0 = 0; c0 < ns; c0 += 32) {
+    // coefficients of the chunk's split lane; the next chunk's {m, l} on the way
     const float m = ml.x, lj = ml.y;
+    ml = c0 + 32 + lane < ns ? mlrow[c0 + 32 + lane] : none;
     const bool nonempty = m != -CUDART_INF_F;
     float pm = m;  // inclusive prefix max over the chunk
 #pragma unroll
@@ -1704,37 +1711,79 @@ __global__ void __launch_bounds__(D) attn_decode_merge_kernel(const KernelParams
     const int kind = nonempty ? (had ? 2 : 1) : 0;  // 0 empty, 1 first non-empty, 2 fold in
     run_m = fmaxf(run_m, __shfl_sync(kFull, pm, 31));
     have = have || ne != 0;
-    // the fold reads split j's coefficients as one broadcast load, which
-    // can be issued ahead of the chain (shuffles issued in place stalled
-    // every step of it)
-    coef[warp][lane] = make_float4(ca, cb, lj, __int_as_float(kind));
+    const int cnt = min(32, ns - c0);
+    const bool whole = ne == (0xffffffffu >> (32 - cnt));  // every split of the chunk counts
+    __syncwarp();  // every lane is done with the last chunk's coefficients
+    coef[lane] = make_float4(ca, cb, kind == 2 ? __fmul_rn(lj, cb) : lj, __int_as_float(kind));
     __syncwarp();
+    for (int q = 0; kStep * q < cnt; ++q) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      float4 cf[kStep];
+      float ov[kStep][kCols];
 #pragma unroll
-    for (int j = 0; j < kMergeChunk; ++j) {
-      const float4 cf = coef[warp][j];
-      const int kj = __float_as_int(cf.w);
-      const float nl = lse_mix(l, cf.x, cf.z, cf.y);
-      const float no = lse_mix(o, cf.x, ov[j], cf.y);
-      l = kj == 2 ? nl : (kj == 1 ? cf.z : l);
-      o = kj == 2 ? no : (kj == 1 ? ov[j] : o);
+      for (int i = 0; i < kStep; ++i) {
+        cf[i] = coef[kStep * q + i];
+        if constexpr (kCols == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(&ring[slot][i][4 * lane]);
+          ov[i][0] = x.x, ov[i][1] = x.y, ov[i][2] = x.z, ov[i][3] = x.w;
+        } else if constexpr (kCols == 2) {
+          const float2 x = *reinterpret_cast<const float2*>(&ring[slot][i][2 * lane]);
+          ov[i][0] = x.x, ov[i][1] = x.y;
+        } else {
+          ov[i][0] = ring[slot][i][lane];
+        }
+      }
+      // fold split i in by the log-sum-exp rule (lse_mix)
+      auto mix = [&](int i) {
+        l = __fadd_rn(__fmul_rn(l, cf[i].x), cf[i].z);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) o[c] = lse_mix(o[c], cf[i].x, ov[i][c], cf[i].y);
+      };
+      auto first = [&](int i) {
+        l = cf[i].z;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) o[c] = ov[i][c];
+      };
+      if (whole && kStep * (q + 1) <= cnt) {  // a full step: no branch in the chain
+        if (c0 + q == 0)
+          first(0);
+        else
+          mix(0);
+#pragma unroll
+        for (int i = 1; i < kStep; ++i) mix(i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+          const int kj = __float_as_int(cf[i].w);
+          if (kj == 2)
+            mix(i);
+          else if (kj == 1)
+            first(i);
+        }
+      }
+      load(step + kStages, slot);
+      ++step;
+      if (++slot == kStages) slot = 0;
     }
-    __syncwarp();  // every lane is done with the chunk's coefficients
-  };
-  if (ns > 0) load(0, ml0, ov0);
-  for (int c0 = 0; c0 < ns; c0 += 2 * kMergeChunk) {
-    if (c0 + kMergeChunk < ns) load(c0 + kMergeChunk, ml1, ov1);
-    fold(ml0, ov0);
-    if (c0 + kMergeChunk >= ns) break;
-    if (c0 + 2 * kMergeChunk < ns) load(c0 + 2 * kMergeChunk, ml0, ov0);
-    fold(ml1, ov1);
   }
-  const float r = (ns > 0 && !bad && l > 0.0f) ? normalize(o, inv_l(l)) : 0.0f;
-  const int64_t oidx = row * D + tid;
-  const float r_next = __shfl_down_sync(kFull, r, 1);
-  if ((tid & 1) == 0)
-    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + oidx) =
-        pack_bf16x2(r, r_next);
-  if (p.out_f32) p.out_f32[oidx] = r;
+  asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the block
+  const bool some = ns > 0 && !bad && l > 0.0f;
+  const float rl = inv_l(l);
+  float r[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) r[c] = some ? normalize(o[c], rl) : 0.0f;
+  const int64_t oidx = row * D + kCols * (32 * blockIdx.z + lane);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + oidx;
+  if constexpr (kCols == 4) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+    if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + oidx) = make_float4(r[0], r[1], r[2], r[3]);
+  } else if constexpr (kCols == 2) {
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(r[0], r[1]);
+    if (p.out_f32) *reinterpret_cast<float2*>(p.out_f32 + oidx) = make_float2(r[0], r[1]);
+  } else {
+    *out = __float2bfloat16_rn(r[0]);
+    if (p.out_f32) p.out_f32[oidx] = r[0];
+  }
 }
 
 // ---------------------------------------------------- prefill (tcgen05)
@@ -2498,6 +2547,22 @@ DecodeWs decode_ws_layout(int B, int Hq, int D, int max_splits) {
   return w;
 }
 
+// Up to two rows an SM: a warp per 32 columns, 8 steps of 16 splits in flight.
+// More: a warp per row, two steps of 8 (9 KB, so that an SM holds 24 rows).
+template <int D>
+bi_status launch_merge(const KernelParams& p, cudaStream_t s) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return BI_ERR_CUDA;
+  const int64_t rows = static_cast<int64_t>(p.B) * p.Hq;
+  cudaError_t e;
+  if (rows <= 2 * sms)
+    e = launch_pdl(attn_decode_merge_kernel<D, 1, 16, 8>, dim3(p.Hq, p.B, D / 32), dim3(32), 0, s,
+                   p);
+  else
+    e = launch_pdl(attn_decode_merge_kernel<D, D / 32, 8, 2>, dim3(p.Hq, p.B), dim3(32), 0, s, p);
+  return cuda_status(e);
+}
+
 template <int D, int NQ>
 bi_status decode_impl(const AttnArgs& a, cudaStream_t s) {
   KernelParams p = make_params(a);
@@ -2536,10 +2601,7 @@ bi_status decode_impl(const AttnArgs& a, cudaStream_t s) {
         cudaSuccess)
       return BI_ERR_CUDA;
   }
-  if (launch_pdl(attn_decode_merge_kernel<D>, dim3(a.Hq, a.B), dim3(D), 0, s, p) !=
-      cudaSuccess)
-    return BI_ERR_CUDA;
-  return BI_OK;
+  return launch_merge<D>(p, s);
 }
 
 template <int D, int NQ>
@@ -2567,9 +2629,7 @@ bi_status decode_q8_impl(const AttnArgs& a, cudaStream_t s) {
                    s, static_cast<const uint8_t*>(a.k_cache), p) != cudaSuccess)
       return BI_ERR_CUDA;
   }
-  if (launch_pdl(attn_decode_merge_kernel<D>, dim3(a.Hq, a.B), dim3(D), 0, s, p) != cudaSuccess)
-    return BI_ERR_CUDA;
-  return BI_OK;
+  return launch_merge<D>(p, s);
 }
 
 // Launch order of one sequence's prefill blocks.  The hardware gives each
