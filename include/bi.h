@@ -351,6 +351,7 @@ bi_status bi_kv_write_q8(const void* k_new, const void* v_new, const int32_t* se
  * of the same size).  Slots behind a sequence's last token and other pages
  * are left as they were.  Two sequences may share a page (and an out page)
  * whose tokens they agree on.
+ * k_out and v_out must be 32-byte aligned.
  * max_kv_len: host bound on kv_lens (sizes the grid).  A length outside
  * 0 .. max_kv_len or past either table is recorded as BI_ERR_DEVICE_BOUNDS
  * and its sequence skipped; a page id outside its pool likewise skips that

@@ -514,7 +514,9 @@ bi_status bi_kv_read_q8(const void* cache, const int32_t* block_table, const int
   if (B == 0 || max_kv_len == 0) return BI_OK;
   if (!cache || !block_table || !kv_lens || !k_out || !v_out || !out_table)
     return BI_ERR_INVALID_ARG;
-  if (!aligned16(cache) || !aligned16(k_out) || !aligned16(v_out)) return BI_ERR_INVALID_ARG;
+  if (!aligned16(cache) || (reinterpret_cast<uintptr_t>(k_out) & 31u) ||
+      (reinterpret_cast<uintptr_t>(v_out) & 31u))
+    return BI_ERR_INVALID_ARG;
   return launch_kv_read_q8(cache, block_table, kv_lens, B, Hkv, D, num_pages, max_blocks_per_seq,
                            k_out, v_out, out_table, num_out_pages, max_out_blocks, max_kv_len,
                            device_error_word(), static_cast<cudaStream_t>(stream));

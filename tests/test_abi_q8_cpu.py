@@ -56,7 +56,7 @@ def test_read_argument_checks(lib):
     assert _read(lib, nout=1 << 26) == bi.ERR_UNSUPPORTED
     for bad in (dict(B=-1), dict(maxkv=-1), dict(nout=0), dict(outblk=0), dict(cache=None),
                 dict(bt=None), dict(kl=None), dict(ko=None), dict(vo=None), dict(ot=None),
-                dict(ko=P + 2), dict(cache=P + 8)):
+                dict(ko=P + 2), dict(ko=P + 16), dict(vo=P + 16), dict(cache=P + 8)):
         assert _read(lib, **bad) == bi.ERR_INVALID_ARG, bad
     assert _read(lib, B=0, cache=None) == bi.OK
     assert _read(lib, maxkv=0, cache=None) == bi.OK
