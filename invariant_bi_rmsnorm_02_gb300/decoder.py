@@ -8,14 +8,20 @@ which other requests share a step.  Each layer is
 
     y   = RMSNorm(h) * w_attn                       bi_rmsnorm / bi_add_rmsnorm
     qkv = y W_qkv^T                                  bi_gemm
-    q, k, v = RoPE(qkv split), at each token's position   bi_rope_qkv
-    K/V cache <- k, v                                bi_kv_write
-    a   = attention(q, cache)                        bi_attn_decode / bi_attn_prefill_chunk
+    q, k, v = RoPE(qkv split), at each token's position   bi_rope_qkv / bi_rope_qkv_scaled
+    K/V cache <- k, v                                bi_kv_write / bi_kv_write_q8
+    a   = attention(q, cache)                        bi_attn_decode / bi_attn_prefill_chunk,
+          over an e4m3 cache bi_attn_decode_q8 / bi_kv_read_q8 then bi_attn_prefill_chunk
     h  += a W_o^T;  y = RMSNorm(h) * w_mlp            bi_gemm, bi_add_rmsnorm
     h  += (silu(y W_gate^T) * y W_up^T) W_down^T      bi_gemm_swiglu, bi_gemm
 
 followed by a final RMSNorm, the LM-head GEMM on the rows that need a token
-and bi_sample (greedy at temperature 0, seeded Gumbel-max above).  Weights are
+and bi_sample (greedy at temperature 0, seeded Gumbel-max above).  The
+configuration may ask for rotary positions scaled for long contexts
+(``rope_scaling`` and its neighbours) and for a K/V cache of one byte an
+element (``kv_cache="e4m3"``): decode reads that cache as it is, a prompt chunk
+reads its sequences' pages back into one layer's worth of bf16 pages first, and
+the two still give the same bytes for the same position.  Weights are
 random (no trained checkpoint is needed for invariance); the shapes default to
 Llama-3-8B's.  PyTorch only owns memory; every arithmetic step is a libbi call.
 
@@ -45,6 +51,10 @@ from . import _binding as bi
 from . import synth
 
 
+ROPE_SCALINGS = {"none": bi.ROPE_NONE, "linear": bi.ROPE_LINEAR, "ntk": bi.ROPE_NTK,
+                 "llama3": bi.ROPE_LLAMA3, "yarn": bi.ROPE_YARN}
+
+
 @dataclass(frozen=True)
 class DecoderConfig:
     layers: int = 32
@@ -59,6 +69,29 @@ class DecoderConfig:
     page_size: int = 16
     split_size: int = 256
     init_std: float = 0.02
+    # rotary positions: the whole head in the rotate-half arrangement with
+    # frequencies theta^(-2i/D), unless one of these says otherwise
+    rope_dim: int | None = None          # elements of a head that are rotated (None: all)
+    rope_interleaved: bool = False
+    rope_scaling: str = "none"           # a key of ROPE_SCALINGS
+    rope_factor: float = 1.0
+    rope_trained_len: int = 8192
+    rope_low_turns: float = 1.0
+    rope_high_turns: float = 4.0
+    kv_cache: str = "bf16"               # "bf16" or "e4m3" (one byte an element)
+
+    def __post_init__(self):
+        if self.rope_scaling not in ROPE_SCALINGS:
+            raise ValueError("rope_scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+        if self.kv_cache not in ("bf16", "e4m3"):
+            raise ValueError('kv_cache must be "bf16" or "e4m3"')
+        if self.kv_cache == "e4m3" and (self.page_size != 16 or self.head_dim not in (64, 128)):
+            raise ValueError("an e4m3 cache needs pages of 16 tokens and heads of 64 or 128")
+
+    @property
+    def plain_rope(self) -> bool:
+        return (self.rope_dim in (None, self.head_dim) and not self.rope_interleaved
+                and self.rope_scaling == "none")
 
     @property
     def qkv_dim(self) -> int:
@@ -190,8 +223,21 @@ class Decoder:
         self.cfg, self.w, self.mode, self.device = cfg, weights, mode, device
         self.max_tokens, self.max_seqs, self.max_blocks = max_tokens, max_seqs, max_blocks
         c = cfg
-        self.kv = torch.zeros(c.layers, 2, num_pages, c.kv_heads, c.page_size, c.head_dim,
-                              dtype=torch.bfloat16, device=device)
+        pool = (num_pages, c.kv_heads, c.page_size, c.head_dim)
+        if c.kv_cache == "e4m3":
+            self.kv = torch.zeros(c.layers, num_pages, c.kv_heads,
+                                  bi.kv_q8_record_bytes(c.head_dim), dtype=torch.uint8,
+                                  device=device)
+            # one layer's pages read back for the prefill kernel, under the
+            # same page ids
+            self.kv_read = torch.zeros(2, *pool, dtype=torch.bfloat16, device=device)
+        else:
+            self.kv = torch.zeros(c.layers, 2, *pool, dtype=torch.bfloat16, device=device)
+        if not c.plain_rope:
+            self.rope_freqs, self.rope_attn_scale = bi.rope_frequencies(
+                c.rope_dim or c.head_dim, c.rope_theta, ROPE_SCALINGS[c.rope_scaling],
+                c.rope_factor, c.rope_trained_len, c.rope_low_turns, c.rope_high_turns,
+                device=device)
         self.num_pages = num_pages
         T, H, bf = max_tokens, c.hidden, torch.bfloat16
 
@@ -339,21 +385,37 @@ class Decoder:
             qkv = self.qkv[:T]
             self._gemm(y, w.wqkv[layer], qkv)
             q, k, v = self.q[:T], self.k[:T], self.v[:T]
-            bi.bi_rope_qkv(qkv, pos, c.heads, c.kv_heads, c.head_dim, c.rope_theta, q, k, v)
+            if c.plain_rope:
+                bi.bi_rope_qkv(qkv, pos, c.heads, c.kv_heads, c.head_dim, c.rope_theta, q, k, v)
+            else:
+                bi.bi_rope_qkv_scaled(qkv, pos, c.heads, c.kv_heads, c.head_dim, self.rope_freqs,
+                                      q, k, v, interleaved=c.rope_interleaved,
+                                      attn_scale=self.rope_attn_scale)
             cap(layer, "qkv", qkv)
             cap(layer, "q", q)
             cap(layer, "k", k)
             cap(layer, "v", v)
-            kc, vc = self.kv[layer, 0], self.kv[layer, 1]
-            bi.bi_kv_write(k, v, row_seq, pos, kc, vc, table)
+            q8 = c.kv_cache == "e4m3"
+            if q8:
+                rec = self.kv[layer]
+                kc, vc = self.kv_read[0], self.kv_read[1]
+                bi.bi_kv_write_q8(k, v, row_seq, pos, rec, table)
+            else:
+                kc, vc = self.kv[layer, 0], self.kv[layer, 1]
+                bi.bi_kv_write(k, v, row_seq, pos, kc, vc, table)
             att = self.att[:T]
             if n_dec:
                 ws = self._workspace(bi.bi_attn_decode_workspace_size(
                     n_dec, c.heads, c.kv_heads, c.head_dim, kv_max, c.split_size, mode))
-                bi.bi_attn_decode(q[:n_dec], kc, vc, table[:n_dec], kv_lens[:n_dec], att[:n_dec],
-                                  max_kv_len=kv_max, split_size=c.split_size,
-                                  sm_scale=self.sm_scale, mode=mode, workspace=ws)
+                cache = (rec,) if q8 else (kc, vc)
+                decode = bi.bi_attn_decode_q8 if q8 else bi.bi_attn_decode
+                decode(q[:n_dec], *cache, table[:n_dec], kv_lens[:n_dec], att[:n_dec],
+                       max_kv_len=kv_max, split_size=c.split_size, sm_scale=self.sm_scale,
+                       mode=mode, workspace=ws)
             if n_pre:
+                if q8:
+                    bi.bi_kv_read_q8(rec, table[n_dec:], kv_lens[n_dec:], kc, vc, table[n_dec:],
+                                     max_kv_len=kv_max)
                 bi.bi_attn_prefill_chunk(q[n_dec:], cu_q, q_start, kc, vc, table[n_dec:],
                                          kv_lens[n_dec:], att[n_dec:],
                                          max_q_len=max_q,

@@ -8,6 +8,7 @@ request's output does not depend on the batch around it).
 
     python -m invariant_bi_rmsnorm_02_gb300.replay            # 256 requests
     python -m invariant_bi_rmsnorm_02_gb300.replay --requests 32 --new-tokens 64
+    python -m invariant_bi_rmsnorm_02_gb300.replay --kv-cache e4m3 --rope-scaling llama3
 
 Mixes: every request at step 0 with all slots open; Poisson arrivals into
 fewer slots and a smaller token budget; and a few requests served alone.
@@ -26,7 +27,7 @@ import time
 import torch
 
 from . import _binding as bi
-from .decoder import LLAMA3_8B, Decoder, DecoderWeights
+from .decoder import LLAMA3_8B, ROPE_SCALINGS, Decoder, DecoderWeights
 from .serving import Scheduler, first_divergence, synthetic_requests
 
 
@@ -72,10 +73,15 @@ def main(argv=None) -> int:
     ap.add_argument("--token-budget", type=int, default=8192)
     ap.add_argument("--seed", type=int, default=5)
     ap.add_argument("--variant", action="store_true", help="also run the batch-variant kernels")
+    ap.add_argument("--kv-cache", choices=("bf16", "e4m3"), default="bf16")
+    ap.add_argument("--rope-scaling", choices=tuple(ROPE_SCALINGS), default="none")
+    ap.add_argument("--rope-factor", type=float, default=8.0,
+                    help="how far --rope-scaling stretches the positions")
     a = ap.parse_args(argv)
 
     dev = torch.device("cuda", torch.cuda.current_device())
-    cfg = dataclasses.replace(LLAMA3_8B, layers=a.layers)
+    cfg = dataclasses.replace(LLAMA3_8B, layers=a.layers, kv_cache=a.kv_cache,
+                              rope_scaling=a.rope_scaling, rope_factor=a.rope_factor)
     reqs = synthetic_requests(a.requests, a.prompt_lo, a.prompt_hi, a.new_tokens, cfg.vocab,
                               seed=a.seed, mean_gap=2.0)
     burst = [dataclasses.replace(r, arrival=0) for r in reqs]
