@@ -1637,9 +1637,8 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
 // maximum, exact in any order, so the whole chunk's coefficients come from one
 // scan; the fold proper is then a chain of products and sums, bit-identical
 // to folding one split at a time.  Empty splits are skipped; a split marked
-// l = -1 (bad pages) makes the whole row zero.  A lane copies the o values of
-// its columns into shared memory with cp.async, kStages steps of kStep splits
-// ahead, and reads only what it copied itself, so nothing waits but the fold.
+// l = -1 (bad pages) makes the whole row zero.  The o values come through
+// shared memory by cp.async, kStages steps of kStep splits ahead.
 // A row of a sequence with a single split was written by the split kernel and
 // is skipped here.
 // Bound by latency: a row's chain (its length, {m, l}, then the fold).  With
@@ -1665,15 +1664,18 @@ __global__ void __launch_bounds__(32) attn_decode_merge_kernel(const KernelParam
   if (ns == 1) return;  // the split kernel wrote this row
   const int64_t row = (int64_t)b * p.Hq + qh;
   const float2* mlrow = reinterpret_cast<const float2*>(p.ml) + row * p.ml_stride;
-  const float* orow = p.o + row * p.max_splits * D + kCols * (32 * blockIdx.z + lane);
-  auto load = [&](int k, int slot) {  // step k's o values, one group of copies
+  const float* orow = p.o + row * p.max_splits * D + 32 * kCols * blockIdx.z;
+  // Step k's o values, one group of copies of 16 bytes each: piece i of a step
+  // is part i % kParts of its split i / kParts.
+  constexpr int kParts = 8 * kCols;
+  auto load = [&](int k, int slot) {
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) {
-      const int j = kStep * k + i;
+    for (int i = 0; i < kStep * kParts / 32; ++i) {
+      const int piece = 32 * i + lane, part = piece % kParts, j = kStep * k + piece / kParts;
       if (j < ns)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
-                         smem_u32(&ring[slot][i][kCols * lane])),
-                     "l"(orow + (int64_t)j * D), "n"(4 * kCols)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         smem_u32(&ring[slot][piece / kParts][4 * part])),
+                     "l"(orow + (int64_t)j * D + 4 * part)
                      : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -1718,6 +1720,7 @@ __global__ void __launch_bounds__(32) attn_decode_merge_kernel(const KernelParam
     __syncwarp();
     for (int q = 0; kStep * q < cnt; ++q) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
       float4 cf[kStep];
       float ov[kStep][kCols];
 #pragma unroll
@@ -1761,6 +1764,7 @@ __global__ void __launch_bounds__(32) attn_decode_merge_kernel(const KernelParam
             first(i);
         }
       }
+      __syncwarp();  // every lane has read the step
       load(step + kStages, slot);
       ++step;
       if (++slot == kStages) slot = 0;
