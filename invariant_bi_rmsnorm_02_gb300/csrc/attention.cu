@@ -1014,6 +1014,8 @@ __device__ __forceinline__ void mma_f16_free(float (&c)[4], const uint32_t (&a)[
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+constexpr int kQ8PlanMax = 1024;  // largest batch planned in the kernel (32 slabs of 32)
+
 // byte offset of 16-byte chunk c of key n's row in a half tile: the chunks of
 // a row are permuted so that eight rows' chunks of one column are in
 // different banks
@@ -1321,41 +1323,52 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  __shared__ int s_incl[kLocalPlanMax], s_len[kLocalPlanMax];
+  // the in-kernel plan: splits up to and with each sequence of its slab of 32,
+  // lengths, each slab's splits, the splits before it and those up to its end
+  __shared__ int s_incl[kQ8PlanMax], s_len[kQ8PlanMax];
+  __shared__ int s_slab[32], s_base[32], s_end[32];
+  __shared__ long long s_tiles[32];
   __shared__ int s_plan[2];  // the splits of all sequences, the variant's chunk
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.G, Hkv = p.Hkv;
   grid_dependency_wait();  // inputs and the plan kernel's unit list are complete from here
 
-  // ---- the plan, as in attn_decode_split_kernel: for small batches the
-  // running split count and the length of every sequence in shared memory
-  if (warp == 0 && p.local_plan) {
+  // ---- the plan.  For up to kQ8PlanMax sequences every block works it out:
+  // the warps scan slabs of 32 sequences, one warp scans the slabs' totals.
+  const int slabs = (p.B + 31) / 32;
+  if (p.local_plan) {
     int csize = 0;
-    if (p.variant) {
+    if (p.variant) {  // the call's chunk size in keys, from all the lengths
       long long tiles = 0;
       int tmax = 0;
-#pragma unroll
-      for (int k = 0; k < kLocalSlabs; ++k) {
-        const int b = lane + 32 * k;
-        const int L = b < p.B ? p.kv_lens[b] : 0;
-        if (b < p.B && len_ok(L, p)) {
-          tiles += (L + kTile - 1) / kTile;
-          tmax = max(tmax, (L + kTile - 1) / kTile);
-        }
+      for (int b = threadIdx.x; b < p.B; b += Geom::kThreads) {
+        const int L = p.kv_lens[b];
+        if (!len_ok(L, p)) continue;
+        tiles += (L + kTile - 1) / kTile;
+        tmax = max(tmax, (L + kTile - 1) / kTile);
       }
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) {
         tiles += __shfl_xor_sync(kFull, tiles, o);
         tmax = max(tmax, __shfl_xor_sync(kFull, tmax, o));
       }
+      if (lane == 0) {
+        s_tiles[warp] = tiles;
+        s_base[warp] = tmax;
+      }
+      __syncthreads();
+      tiles = 0;
+      for (int w = 0; w < Geom::kWarps; ++w) {
+        tiles += s_tiles[w];
+        tmax = max(tmax, s_base[w]);
+      }
+      __syncthreads();
       csize = kTile * variant_chunk_tiles(tiles, tmax, p);
-      if (blockIdx.x == 0 && lane == 0) p.unit_count[1] = csize;  // for the merge
+      if (blockIdx.x == 0 && threadIdx.x == 0) p.unit_count[1] = csize;  // for the merge
     }
-    int total = 0;
-#pragma unroll
-    for (int k = 0; k < kLocalSlabs; ++k) {
-      const int b = lane + 32 * k;
+    for (int k = warp; k < slabs; k += Geom::kWarps) {
+      const int b = 32 * k + lane;
       int L = 0, n = 0;
       if (b < p.B) {
         L = p.kv_lens[b];
@@ -1365,29 +1378,45 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
         }
         if (L > 0) n = plan_splits(L, csize, p);
       }
-      int v = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(kFull, v, o);
-        if (lane >= o) v += t;
+        const int t = __shfl_up_sync(kFull, n, o);
+        if (lane >= o) n += t;
       }
-      s_incl[b] = total + v;
+      s_incl[b] = n;
       s_len[b] = L;
-      total += __shfl_sync(kFull, v, 31);
+      if (lane == 31) s_slab[k] = n;
     }
-    if (lane == 0) {
-      s_plan[0] = total;
-      s_plan[1] = csize;
+    __syncthreads();
+    if (warp == 0) {
+      const int n = lane < slabs ? s_slab[lane] : 0;
+      int end = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(kFull, end, o);
+        if (lane >= o) end += t;
+      }
+      s_base[lane] = end - n;
+      s_end[lane] = lane < slabs ? end : 0x7fffffff;
+      if (lane == 31) {
+        s_plan[0] = end;
+        s_plan[1] = csize;
+      }
     }
-    __syncwarp();
+  } else if (threadIdx.x == 0) {
+    s_plan[0] = *p.unit_count;
+    s_plan[1] = p.variant ? p.unit_count[1] : 0;
+  }
+  __syncthreads();
+  if (p.local_plan) {
     // the merge takes sequences longest first: rank of sequence x among all
-    for (int x = blockIdx.x; x < p.B; x += gridDim.x) {
-      auto splits = [&](int b) { return s_incl[b] - (b > 0 ? s_incl[b - 1] : 0); };
+    // (more splits first, then lower index)
+    auto splits = [&](int b) { return s_incl[b] - ((b & 31) ? s_incl[b - 1] : 0); };
+    for (int x = blockIdx.x + gridDim.x * warp; x < p.B; x += gridDim.x * Geom::kWarps) {
       const int nx = splits(x);
       int ahead = 0;
-#pragma unroll
-      for (int k = 0; k < kLocalSlabs; ++k) {
-        const int b = lane + 32 * k;
+      for (int k = 0; k < slabs; ++k) {
+        const int b = 32 * k + lane;
         if (b < p.B) {
           const int nb = splits(b);
           ahead += (nb > nx || (nb == nx && b < x)) ? 1 : 0;
@@ -1397,12 +1426,6 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
       if (lane == 0) p.order[ahead] = make_int2(x, nx);
     }
   }
-  if (threadIdx.x == 0 && !p.local_plan) {
-    s_plan[0] = *p.unit_count;
-    s_plan[1] = p.variant ? p.unit_count[1] : 0;
-  }
-  __syncthreads();
-
 
   // ------------------------------------------------- units and their copies
   struct Unit {
@@ -1420,15 +1443,15 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
     u.h = lu - s * Hkv;
     lu += stride;
     if (p.local_plan) {
-      int b = 0;
-#pragma unroll
-      for (int k = 0; k < kLocalSlabs; ++k)
-        b += __popc(__ballot_sync(kFull, s_incl[lane + 32 * k] <= s));
+      // the slab, and in it the sequence, whose running count passes s
+      const int k = __popc(__ballot_sync(kFull, s_end[lane] <= s));
+      const int r = s - s_base[k];
+      const int i = __popc(__ballot_sync(kFull, s_incl[32 * k + lane] <= r));
       const int c = p.variant ? csize : p.split_size;
-      u.b = b;
-      u.j = s - (b > 0 ? s_incl[b - 1] : 0);
+      u.b = 32 * k + i;
+      u.j = r - (i > 0 ? s_incl[32 * k + i - 1] : 0);
       u.lo = u.j * c;
-      u.hi = min(u.lo + c, s_len[b]);
+      u.hi = min(u.lo + c, s_len[u.b]);
     } else {
       const int4 d = p.units[s];
       u.b = d.x;
@@ -2619,7 +2642,7 @@ bi_status decode_q8_impl(const AttnArgs& a, cudaStream_t s) {
     p.ml = reinterpret_cast<float*>(base + w.ml_off);
     p.o = reinterpret_cast<float*>(base + w.o_off);
     p.ml_stride = w.ml_stride;
-    p.local_plan = a.B <= kLocalPlanMax;
+    p.local_plan = a.B <= kQ8PlanMax;
     if (p.local_plan) p.order = reinterpret_cast<int2*>(base + w.units_off);  // units unused
     const size_t sm = Q8Geom<D, NQ>::kSmem;
     if (set_smem(attn_decode_q8_split_kernel<D, NQ>, sm) != cudaSuccess) return BI_ERR_CUDA;

@@ -342,3 +342,37 @@ def test_decode_batch_invariance_and_large_batches(cuda):
     each = bi.attn_decode_q8(qp, kq, kv.block_table[:1].expand(60, -1).contiguous(),
                              i32(range(641, 701), cuda), max_kv_len=704, split_size=S)
     assert same_bytes(pre, each), first_divergence(pre, each)
+
+
+@pytest.mark.parametrize("mode", [bi.INVARIANT, bi.VARIANT])
+@pytest.mark.parametrize("B", [31, 32, 33, 128, 129, 1024, 1025])
+def test_decode_plans_of_every_batch_size(cuda, B, mode):
+    # the plan worked out in the kernel (32 slabs of 32 sequences at most) and
+    # the plan kernel behind it, with idle slots and lengths out of range
+    D, Hq, Hkv = 64, 4, 2
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 200, (B,), generator=g)
+    lens[B // 2:B // 2 + 8] = 0
+    pool = 40
+    kv = synth.paged_kv([pool * PAGE], Hkv, D, PAGE, 23200)
+    rec = quantised(kv, D).to(cuda)
+    bt = torch.randint(0, pool, (B, 13), generator=g, dtype=torch.int32).to(cuda)
+    q = synth.normal_bf16((B, Hq, D), 23201 + B, device=cuda)
+    kl = lens.to(torch.int32).to(cuda)
+    out, out32 = bi.attn_decode_q8(q, rec, bt, kl, max_kv_len=208, split_size=64, mode=mode,
+                                   want_f32=True)
+    assert bi.bi_check_device_errors() == bi.OK
+    k, v = bi.kv_read_q8(rec, D, torch.arange(pool, dtype=torch.int32, device=cuda).view(1, -1),
+                         i32([pool * PAGE], cuda), max_kv_len=pool * PAGE)
+    ref, ref32 = bi.attn_decode(q, k, v, bt, kl, max_kv_len=208, split_size=64, want_f32=True)
+    if mode == bi.INVARIANT:
+        assert same_bytes(out32, ref32) and same_bytes(out, ref)
+    else:
+        check_close(f64(out32), f64(ref32), np.full(out32.shape, 2 * ATOL), "variant")
+    assert (out32[lens == 0] == 0).all()
+    kl[1], kl[B - 1] = -5, 209
+    bad = bi.attn_decode_q8(q, rec, bt, kl, max_kv_len=208, split_size=64, mode=mode)
+    assert bi.bi_check_device_errors() == bi.ERR_DEVICE_BOUNDS
+    assert (bad[1] == 0).all() and (bad[B - 1] == 0).all()
+    if mode == bi.INVARIANT:
+        assert same_bytes(bad[2:B - 1].contiguous(), out[2:B - 1].contiguous())
