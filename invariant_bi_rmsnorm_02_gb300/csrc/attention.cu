@@ -1034,13 +1034,15 @@ __device__ __forceinline__ uint32_t q8_off(int n, int c) {
 // order inside it; the tests compare the bytes with the bf16 kernel).  Rows
 // G .. 8 NQ - 1 are zero.  Returns whether the fragments are fp16: each row
 // times 2^k with its largest element in [2^15, 2^16), exact for elements down
-// to 2^-32 of it; otherwise bf16 times 2^32, for K's elements times 2^-120.
+// to 2^-32 of it; otherwise bf16 times 2^32 (1 from 2^64 on), for K's elements
+// times 2^-120.
 template <int D, int NQ>
 __device__ __forceinline__ bool q8_load_q(uint32_t (&qf)[NQ][D / 16][2], float (&sc)[NQ][2],
                                           const __nv_bfloat16* q, int G, float scale_log2) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   bool exact = true;
   float grow[NQ], shrink[NQ];  // 2^(15 - e) for a row's largest exponent e, and its inverse
+  int raise[NQ];               // the power of two for the bf16 form: 32, 0 for huge rows
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) {
     // the largest magnitude bits, and the smallest ones that are not zero
@@ -1070,6 +1072,7 @@ __device__ __forceinline__ bool q8_load_q(uint32_t (&qf)[NQ][D / 16][2], float (
     const int up = min(253, 269 - et);  // both are normal numbers
     grow[nq] = __uint_as_float((uint32_t)up << 23);
     shrink[nq] = __uint_as_float((uint32_t)(254 - up) << 23);
+    raise[nq] = et < 127 + 64 ? 32 : 0;
     // every element a finite one at most 2^32 below the largest (its 8 bits
     // then end at 2^-24 or above)
     exact = exact && et < 255 && (int)low + 1 >= (et - 32) * 128;
@@ -1077,13 +1080,12 @@ __device__ __forceinline__ bool q8_load_q(uint32_t (&qf)[NQ][D / 16][2], float (
   exact = __all_sync(kFull, exact);
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) {
-    if (exact) {
-      // column 8 nq + 2t + cc is the row that lanes 4 (2t + cc) .. + 3 hold
-      sc[nq][0] = __fmul_rn(scale_log2, __shfl_sync(kFull, shrink[nq], 8 * t));
-      sc[nq][1] = __fmul_rn(scale_log2, __shfl_sync(kFull, shrink[nq], 8 * t + 4));
-    } else {
-      sc[nq][0] = sc[nq][1] = __fmul_rn(scale_log2, 0x1p88f);
-    }
+    // what takes the powers of two off a score; column 8 nq + 2t + cc is the
+    // row that lanes 4 (2t + cc) .. + 3 hold
+    const float off = exact ? shrink[nq] : __uint_as_float((uint32_t)(247 - raise[nq]) << 23);
+    sc[nq][0] = __fmul_rn(scale_log2, __shfl_sync(kFull, off, 8 * t));
+    sc[nq][1] = __fmul_rn(scale_log2, __shfl_sync(kFull, off, 8 * t + 4));
+    const uint32_t up2 = (uint32_t)(127 + raise[nq]) * 0x00800080u;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       const uint32_t x = qf[nq][ks][0], y = qf[nq][ks][1];
@@ -1091,8 +1093,8 @@ __device__ __forceinline__ bool q8_load_q(uint32_t (&qf)[NQ][D / 16][2], float (
         qf[nq][ks][0] = pack_f16x2(bf16_lo(x) * grow[nq], bf16_hi(x) * grow[nq]);
         qf[nq][ks][1] = pack_f16x2(bf16_lo(y) * grow[nq], bf16_hi(y) * grow[nq]);
       } else {  // e4m3_even takes a key's elements 4t and 4t + 2, e4m3_odd the others
-        qf[nq][ks][0] = mul_bf16x2(__byte_perm(x, y, 0x5410), 0x4f804f80u);
-        qf[nq][ks][1] = mul_bf16x2(__byte_perm(x, y, 0x7632), 0x4f804f80u);
+        qf[nq][ks][0] = mul_bf16x2(__byte_perm(x, y, 0x5410), up2);
+        qf[nq][ks][1] = mul_bf16x2(__byte_perm(x, y, 0x7632), up2);
       }
     }
   }

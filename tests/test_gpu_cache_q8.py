@@ -376,3 +376,100 @@ def test_decode_plans_of_every_batch_size(cuda, B, mode):
     assert (bad[1] == 0).all() and (bad[B - 1] == 0).all()
     if mode == bi.INVARIANT:
         assert same_bytes(bad[2:B - 1].contiguous(), out[2:B - 1].contiguous())
+
+
+def test_decode_queries_of_every_range(cuda):
+    # rows of q whose elements do not all fit fp16 beside their largest one
+    # take the bf16 form of the scores: the same bytes again
+    D, Hq, Hkv, L = 128, 16, 4, 300
+    kv = synth.paged_kv([L], Hkv, D, PAGE, 23300)
+    rec = quantised(kv, D).to(cuda)
+    q = synth.normal_bf16((1, Hq, D), 23301)
+    q[0, 0] = 0                                        # all zeros
+    q[0, 1, 1:] = 0                                    # one element
+    q[0, 2, 0], q[0, 2, 1] = 2.0 ** 20, 2.0 ** -12     # 2^32 apart: still exact
+    q[0, 4, 0], q[0, 4, 1] = 2.0 ** 20, 1.5 * 2.0 ** -13   # further apart
+    q[0, 5] *= 2.0 ** -120
+    q[0, 8, 3] = 2.0 ** -133                           # the least bf16 number
+    q[0, 9] *= 2.0 ** 40                               # scores beyond any softmax's range
+    q[0, 12] *= 2.0 ** 70
+    q[0, 13] *= 2.0 ** -20
+    q[0, 13, 5] = 2.0 ** 66
+    q[0, 14, 2] = float("nan")
+    q[0, 15, 2] = float("inf")
+    args = (kv.block_table.to(cuda), kv.kv_lens.to(cuda), D, L, 64)
+    out, out32, ref, ref32, _, _ = both_decodes(q.to(cuda), rec, *args)
+    assert bi.bi_check_device_errors() == bi.OK
+    fine = ~torch.isnan(ref32)
+    assert torch.equal(torch.isnan(out32), ~fine)
+    assert fine[0, :9].all()
+    assert torch.equal(out32[fine], ref32[fine])
+    # groups of four heads share a unit: the same with each head's q alone in
+    # an otherwise ordinary group
+    for h in range(14):
+        q1 = synth.normal_bf16((1, Hq, D), 23302 + h)
+        q1[0, h] = q[0, h]
+        out, out32, ref, ref32, _, _ = both_decodes(q1.to(cuda), rec, *args)
+        nan = torch.isnan(ref32)      # scores past the softmax's range, rows 9 and on
+        assert torch.equal(torch.isnan(out32), nan), h
+        assert torch.equal(out32[~nan], ref32[~nan]), h
+        assert not nan.any() or h >= 9
+
+
+def test_offsets_beyond_32_bits(cuda):
+    # a pool of 4.6 GB of records (and 9 GB of pages read back) whose last
+    # pages hold the sequence
+    D, Hkv, Hq, L = 128, 8, 32, 200
+    P = 140000
+    n = -(-L // PAGE)
+    k = synth.normal_bf16((L, Hkv, D), 23400, device=cuda)
+    v = synth.normal_bf16((L, Hkv, D), 23401, device=cuda)
+    q = synth.normal_bf16((1, Hq, D), 23402, device=cuda)
+    seq, pos = i32([0] * L, cuda), i32(range(L), cuda)
+    outs = []
+    for pages, first in ((n, 0), (P, P - n)):
+        cache = torch.zeros(pages, Hkv, bi.kv_q8_record_bytes(D), dtype=torch.uint8, device=cuda)
+        bt = torch.arange(first, first + n, dtype=torch.int32, device=cuda).view(1, n)
+        bi.kv_write_q8(k, v, seq, pos, cache, bt)
+        ko, vo = bi.kv_read_q8(cache, D, bt, i32([L], cuda), max_kv_len=L)
+        outs.append((cache[first:].clone(), ko[first:].clone(), vo[first:].clone(),
+                     bi.attn_decode_q8(q, cache, bt, i32([L], cuda), max_kv_len=L,
+                                       split_size=64)))
+        del cache, ko, vo
+        torch.cuda.empty_cache()
+    assert bi.bi_check_device_errors() == bi.OK
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_the_binding_refuses_what_the_library_cannot_take(cuda):
+    D, Hkv = 64, 2
+    rec = bi.kv_cache_q8(4, Hkv, D, cuda)
+    k = synth.normal_bf16((3, Hkv, D), 23500, device=cuda)
+    seq, pos = i32([0, 0, 0], cuda), i32([0, 1, 2], cuda)
+    bt = i32([[0, 1]], cuda)
+    bi.kv_write_q8(k, k, seq, pos, rec, bt)
+    with pytest.raises(TypeError):
+        bi.kv_write_q8(k.float(), k, seq, pos, rec, bt)
+    with pytest.raises(TypeError):
+        bi.kv_write_q8(k, k, seq.long(), pos, rec, bt)
+    with pytest.raises(TypeError):
+        bi.kv_write_q8(k, k, seq, pos, rec.view(torch.int8), bt)
+    with pytest.raises(TypeError):
+        bi.kv_write_q8(k.cpu(), k, seq, pos, rec, bt)
+    with pytest.raises(ValueError):
+        bi.kv_write_q8(k.transpose(0, 1).contiguous().transpose(0, 1), k, seq, pos, rec, bt)
+    with pytest.raises(ValueError):
+        bi.kv_write_q8(k, k, seq[:2], pos, rec, bt)
+    with pytest.raises(ValueError):
+        bi.kv_write_q8(k, k, seq, pos, rec[:, :1], bt)
+    odd = torch.zeros(4 * Hkv * PAGE * D + 8, dtype=torch.bfloat16, device=cuda)
+    off = odd[8:].view(4, Hkv, PAGE, D)                # 16- but not 32-byte aligned
+    with pytest.raises(bi.BiError):
+        bi.bi_kv_read_q8(rec, bt, i32([3], cuda), off, off, bt, max_kv_len=3)
+    q = synth.normal_bf16((1, 4, D), 23501, device=cuda)
+    with pytest.raises(bi.BiError) as e:
+        bi.bi_attn_decode_q8(q, rec, bt, i32([3], cuda), torch.empty_like(q), max_kv_len=3,
+                             split_size=64, sm_scale=0.1)
+    assert e.value.status == bi.ERR_WORKSPACE
+    assert bi.bi_check_device_errors() == bi.OK
