@@ -2576,8 +2576,11 @@ DecodeWs decode_ws_layout(int B, int Hq, int D, int max_splits) {
   return w;
 }
 
-// Up to two rows an SM: a warp per 32 columns, 8 steps of 16 splits in flight.
-// More: a warp per row, two steps of 8 (9 KB, so that an SM holds 24 rows).
+// Up to two rows an SM: a warp per 32 columns, 8 steps of 16 splits in flight
+// (one sequence of 131072 keys, 512 splits: 15 us alone, from 30 with a warp
+// per row).  More rows: a warp per row, with four steps of 8 in flight where a
+// row may have more than 16 splits (64 requests of up to 128: 6.6 us from 8.2
+// with two), else two, which leaves room for more rows on an SM.
 template <int D>
 bi_status launch_merge(const KernelParams& p, cudaStream_t s) {
   const int sms = device_sm_count();
@@ -2587,6 +2590,8 @@ bi_status launch_merge(const KernelParams& p, cudaStream_t s) {
   if (rows <= 2 * sms)
     e = launch_pdl(attn_decode_merge_kernel<D, 1, 16, 8>, dim3(p.Hq, p.B, D / 32), dim3(32), 0, s,
                    p);
+  else if (p.max_splits > 16)
+    e = launch_pdl(attn_decode_merge_kernel<D, D / 32, 8, 4>, dim3(p.Hq, p.B), dim3(32), 0, s, p);
   else
     e = launch_pdl(attn_decode_merge_kernel<D, D / 32, 8, 2>, dim3(p.Hq, p.B), dim3(32), 0, s, p);
   return cuda_status(e);

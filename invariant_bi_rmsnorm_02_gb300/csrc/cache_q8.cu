@@ -117,6 +117,15 @@ __global__ void __launch_bounds__(kThreads) kv_write_q8_kernel(
 }
 
 // ------------------------------------------------------------------- read
+// 32 bytes (32-byte aligned) in one store, so that a warp whose lanes write
+// neighbouring 32-byte pieces fills whole sectors with each instruction (two
+// 16-byte stores per lane leave every sector half written twice).
+__device__ __forceinline__ void store32(void* dst, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // One warp per (page, kv head) of the batch's pages: the warp finds its pages
 // from a running sum of the sequences' page counts.  Bound by memory (a third
 // read, two thirds written): 64 sequences, 94,100 tokens of 8 kv heads of 128

@@ -161,15 +161,6 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// 32 bytes (32-byte aligned) in one store, so that a warp whose lanes write
-// neighbouring 32-byte pieces fills whole sectors with each instruction (two
-// 16-byte stores per lane leave every sector half written twice).
-__device__ __forceinline__ void store32(void* dst, const uint4& a, const uint4& b) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x),
-               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
-}
-
 // ------------------------------------------------------------------ PDL
 // Programmatic dependent launch: a kernel launched with the programmatic
 // stream-serialisation attribute may start while the previous kernel on the
