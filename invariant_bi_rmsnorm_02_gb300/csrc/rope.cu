@@ -15,7 +15,7 @@
 namespace bi {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 192;
 
 // The fraction of a turn that one position adds, freq / (2 pi) mod 1, in
 // units of 2^-64.  An angle is then a 64-bit product that wraps at whole
@@ -58,22 +58,24 @@ __device__ __forceinline__ int div_by(int n, uint32_t m) {
   return m ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), m)) : n;
 }
 
-// A block takes `tokens` tokens a step.  Its threads first make the step's
-// cosines and sines, each (token, pair) once for all heads, in shared memory
-// (the frequencies' turn fractions, the only fp64 work, once per block); then
-// every item of 16 elements, two 16-byte vectors, is read, turned or passed
-// through, and written by one thread.  The loads of an item do not depend on
-// the table, so they are issued before it is made.
-// Bound by memory: 8192 tokens of 32 + 2 * 8 heads of 128 move 201 MB in 37 us
-// (5.5 TB/s, 0.80 of the measured copy rate; 39 us with blocks of 256 threads,
-// 42 of 512, 45 with two items in flight per thread, 47 and more with the
-// items staged in shared memory by cp.async).
-constexpr int kItems = 3;  // items in flight per thread
+// A block takes `tokens` tokens a step, in chunks of kItems items per thread.
+// Its threads first make the step's cosines and sines, each (token, pair) once
+// for all heads, in shared memory (the frequencies' turn fractions, the only
+// fp64 work, once per block); then every item of 16 elements, two 16-byte
+// vectors, is turned or passed through and written by one thread, which at
+// once loads its item of the next chunk into the same registers: loads are in
+// flight through the stores and the next step's table.
+// Bound by memory: 8192 tokens of 32 + 2 * 8 heads of 128 move 201 MB in 35 us
+// (5.7 TB/s, 0.85 of the measured copy rate; 37 us with the loads issued at the
+// head of their own step, three items and 128 threads, 39 with 256 threads, 47 and
+// more with the items staged in shared memory by cp.async).
+constexpr int kItems = 2;  // items in flight per thread
+constexpr int kChunk = kItems * kThreads;
 
 // kAligned: rot_dim % 16 == 0, so that rotated items are whole vectors of
 // either half of the rotated part (rotate-half) or of pairs.  Otherwise the
-// items that hold rotated elements gather their pairs one by one; those are
-// read again from L1, the head's other items stay vectors.
+// items that hold rotated elements gather their pairs one by one; the head's
+// other items stay vectors.
 template <bool kInterleaved, bool kAligned>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   const int heads = a.Hq + 2 * a.Hkv, half = a.rot / 2;
@@ -81,73 +83,90 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   float2* table = reinterpret_cast<float2*>(smem);                       // [tokens][rot / 2]
   uint64_t* frac = reinterpret_cast<uint64_t*>(table + a.tokens * half);  // [rot / 2]
   float* amp = reinterpret_cast<float*>(frac + half);                    // [rot / 2]
+  const int per_head = a.D / 16, per_token = heads * per_head;
+  const int rot_items = (a.rot + 15) / 16;
+  const int chunks = (a.tokens * per_token + kChunk - 1) / kChunk;  // of a step
+  const int64_t step = static_cast<int64_t>(gridDim.x) * a.tokens;
+  const uint4* src = static_cast<const uint4*>(a.qkv);
+  struct Item {
+    int tok, head, sub;
+    bool turn, apart;  // rotated; a vector of the first half and its partner
+  };
+  auto item_at = [&](int i) {
+    Item it;
+    const int th = div_by(i, a.inv_D);  // (token, head) of the step
+    it.sub = i - th * per_head;
+    it.tok = div_by(th, a.inv_heads);
+    it.head = th - it.tok * heads;
+    it.turn = it.head < a.Hq + a.Hkv && it.sub < rot_items;
+    it.apart = kAligned && !kInterleaved && it.turn;
+    return it;
+  };
+  auto items_of = [&](int64_t t0) {
+    return static_cast<int>(a.T - t0 < a.tokens ? a.T - t0 : a.tokens) * per_token;
+  };
+  uint4 x[kItems][2];
+  auto load = [&](int u, int64_t t0, int chunk, int items) {
+    const int i = chunk * kChunk + u * kThreads + threadIdx.x;
+    if (i >= items) return;
+    const Item it = item_at(i);
+    if (!kAligned && it.turn) return;
+    const uint4* row = src + ((t0 + it.tok) * heads + it.head) * (a.D / 8);
+    x[u][0] = __ldcs(row + (it.apart ? it.sub : 2 * it.sub));
+    x[u][1] = __ldcs(row + (it.apart ? it.sub + rot_items : 2 * it.sub + 1));
+  };
+  int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
+  int chunk = 0;
+  if (t0 < a.T) {
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) load(u, t0, 0, items_of(t0));
+  }
   for (int p = threadIdx.x; p < half; p += kThreads) {
     const double f = a.freqs[p];
     frac[p] = turn_fraction(f);
     amp[p] = isfinite(f) ? a.attn_scale : CUDART_NAN_F;
   }
-  const int per_head = a.D / 16, per_token = heads * per_head;
-  const int rot_items = (a.rot + 15) / 16;
-  const uint4* src = static_cast<const uint4*>(a.qkv);
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
-       t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
-    const int nt = static_cast<int>(a.T - t0 < a.tokens ? a.T - t0 : a.tokens);
-    const int items = nt * per_token;
-    for (int i0 = 0; i0 < items; i0 += kItems * kThreads) {
-      uint4 x[kItems][2];
-      int tok[kItems], head[kItems], sub[kItems];
-#pragma unroll
-      for (int u = 0; u < kItems; ++u) {
-        const int i = i0 + u * kThreads + threadIdx.x;
-        if (i >= items) continue;
-        const int th = div_by(i, a.inv_D);   // (token, head) of the step
-        sub[u] = i - th * per_head;
-        tok[u] = div_by(th, a.inv_heads);
-        head[u] = th - tok[u] * heads;
-        const bool turn = head[u] < a.Hq + a.Hkv && sub[u] < rot_items;
-        const uint4* row = src + (t0 * heads + th) * (a.D / 8);
-        if (!kAligned && turn) continue;
-        // rotate-half: a vector of the first half and its partner
-        const bool apart = kAligned && !kInterleaved && turn;
-        x[u][0] = __ldcs(row + (apart ? sub[u] : 2 * sub[u]));
-        x[u][1] = __ldcs(row + (apart ? sub[u] + rot_items : 2 * sub[u] + 1));
+  while (t0 < a.T) {
+    const int items = items_of(t0);
+    if (chunk == 0) {
+      __syncthreads();  // the fractions are there, the last step's table has been read
+      for (int e = threadIdx.x; e < (items / per_token) * half; e += kThreads) {
+        const int t = div_by(e, a.inv_half), p = e - t * half;
+        table[e] = cos_sin(a.pos[t0 + t], frac[p], amp[p]);
       }
-      if (i0 == 0) {
-        __syncthreads();  // the fractions are there, the last step's table has been read
-        for (int e = threadIdx.x; e < nt * half; e += kThreads) {
-          const int t = div_by(e, a.inv_half), p = e - t * half;
-          table[e] = cos_sin(a.pos[t0 + t], frac[p], amp[p]);
-        }
-        __syncthreads();
-      }
+      __syncthreads();
+    }
+    const int next_chunk = chunk + 1 == chunks ? 0 : chunk + 1;
+    const int64_t next_t0 = next_chunk ? t0 : t0 + step;
+    const int next_items = next_t0 < a.T ? items_of(next_t0) : 0;
 #pragma unroll
-      for (int u = 0; u < kItems; ++u) {
-        const int i = i0 + u * kThreads + threadIdx.x;
-        if (i >= items) continue;
-        const bool turn = head[u] < a.Hq + a.Hkv && sub[u] < rot_items;
-        if (!kAligned && turn) {
-          const uint16_t* row =
-              static_cast<const uint16_t*>(a.qkv) + ((t0 + tok[u]) * heads + head[u]) * a.D;
-          auto element = [&](int i) { return __uint_as_float((uint32_t)row[i] << 16); };
+    for (int u = 0; u < kItems; ++u) {
+      const int i = chunk * kChunk + u * kThreads + threadIdx.x;
+      if (i < items) {
+        const Item it = item_at(i);
+        uint4 y0 = x[u][0], y1 = x[u][1];
+        if (!kAligned && it.turn) {
+          const uint16_t* row = static_cast<const uint16_t*>(a.qkv) +
+                                ((t0 + it.tok) * heads + it.head) * a.D;
+          auto element = [&](int e) { return __uint_as_float((uint32_t)row[e] << 16); };
           auto turned = [&](int e) -> uint32_t {  // element e of the head's output
             if (e >= a.rot) return row[e];
             const int p = kInterleaved ? e >> 1 : e < half ? e : e - half;
             const uint32_t y = rotate(element(kInterleaved ? 2 * p : p),
                                       element(kInterleaved ? 2 * p + 1 : p + half),
-                                      table[tok[u] * half + p]);
+                                      table[it.tok * half + p]);
             return (kInterleaved ? (e & 1) : e >= half) ? y >> 16 : y & 0xffffu;
           };
           uint32_t r[8];
 #pragma unroll
           for (int w = 0; w < 8; ++w)
-            r[w] = turned(16 * sub[u] + 2 * w) | turned(16 * sub[u] + 2 * w + 1) << 16;
-          x[u][0] = make_uint4(r[0], r[1], r[2], r[3]);
-          x[u][1] = make_uint4(r[4], r[5], r[6], r[7]);
-        } else if (turn) {
+            r[w] = turned(16 * it.sub + 2 * w) | turned(16 * it.sub + 2 * w + 1) << 16;
+          y0 = make_uint4(r[0], r[1], r[2], r[3]);
+          y1 = make_uint4(r[4], r[5], r[6], r[7]);
+        } else if (it.turn) {
           const float4* cs4 =
-              reinterpret_cast<const float4*>(table + tok[u] * half + 8 * sub[u]);
-          uint32_t r0[4] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w};
-          uint32_t r1[4] = {x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+              reinterpret_cast<const float4*>(table + it.tok * half + 8 * it.sub);
+          uint32_t r0[4] = {y0.x, y0.y, y0.z, y0.w}, r1[4] = {y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const float4 c = cs4[w];  // pairs 2w and 2w + 1 of the item's eight
@@ -164,20 +183,23 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
               r1[w] = __byte_perm(ya, yb, 0x7632);
             }
           }
-          x[u][0] = make_uint4(r0[0], r0[1], r0[2], r0[3]);
-          x[u][1] = make_uint4(r1[0], r1[1], r1[2], r1[3]);
+          y0 = make_uint4(r0[0], r0[1], r0[2], r0[3]);
+          y1 = make_uint4(r1[0], r1[1], r1[2], r1[3]);
         }
-        const int64_t t = t0 + tok[u];
-        const int h = head[u];
+        const int64_t t = t0 + it.tok;
+        const int h = it.head;
         uint4* dst = (h < a.Hq ? static_cast<uint4*>(a.q) + (t * a.Hq + h) * (a.D / 8)
                       : h < a.Hq + a.Hkv
                           ? static_cast<uint4*>(a.k) + (t * a.Hkv + h - a.Hq) * (a.D / 8)
                           : static_cast<uint4*>(a.v) + (t * a.Hkv + h - a.Hq - a.Hkv) * (a.D / 8));
-        const bool apart = kAligned && !kInterleaved && turn;
-        dst[apart ? sub[u] : 2 * sub[u]] = x[u][0];
-        dst[apart ? sub[u] + rot_items : 2 * sub[u] + 1] = x[u][1];
+        dst += it.apart ? it.sub : 2 * it.sub;
+        dst[0] = y0;
+        dst[it.apart ? rot_items : 1] = y1;
       }
+      load(u, next_t0, next_chunk, next_items);
     }
+    t0 = next_t0;
+    chunk = next_chunk;
   }
 }
 
@@ -193,7 +215,7 @@ bi_status launch_rope_qkv_scaled(const void* qkv, const int32_t* pos, int64_t T,
   const int per_token = heads * (D / 16), half = rot_dim / 2;
   // enough tokens to give every thread its kItems items, no more than the
   // default 48 KB of shared memory hold, and no fewer blocks than two an SM
-  int tokens = kItems * kThreads / per_token;
+  int tokens = kChunk / per_token;
   const int room = (49152 - half * 12) / (half * 8);
   if (tokens > room) tokens = room;
   while (tokens > 1 && T / tokens < 2 * sms) --tokens;
