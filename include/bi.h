@@ -351,7 +351,8 @@ bi_status bi_kv_write_q8(const void* k_new, const void* v_new, const int32_t* se
  * of the same size).  Slots behind a sequence's last token and other pages
  * are left as they were.  Two sequences may share a page (and an out page)
  * whose tokens they agree on.
- * k_out and v_out must be 32-byte aligned.
+ * k_out and v_out must be 32-byte aligned and overlap neither each other nor
+ * the cache.
  * max_kv_len: host bound on kv_lens (sizes the grid).  A length outside
  * 0 .. max_kv_len or past either table is recorded as BI_ERR_DEVICE_BOUNDS
  * and its sequence skipped; a page id outside its pool likewise skips that
@@ -443,7 +444,7 @@ bi_status bi_rope_frequencies(int rot_dim, double theta, bi_rope_scaling scaling
  * in turns as a 64-bit fraction (an error below 2^-33 turns beside that of
  * freqs at any int32 position, negative ones included); cosine, sine and the
  * rotation are fp32, rounded once to bf16.
- * q, k and v must not overlap qkv or one another.
+ * q, k and v must not overlap qkv or one another (BI_ERR_INVALID_ARG).
  * Requirements: D % 16 == 0, D <= 1024, rot_dim even and at most D,
  *   attn_scale positive and finite, T < 2^31.  Errors: as bi_rmsnorm. */
 bi_status bi_rope_qkv_scaled(const void* qkv, const int32_t* pos, int64_t T, int Hq, int Hkv,

@@ -37,6 +37,11 @@ int current_device() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
+}
+
 }  // namespace
 
 int* device_error_word() {
@@ -517,6 +522,11 @@ bi_status bi_kv_read_q8(const void* cache, const int32_t* block_table, const int
   if (!aligned16(cache) || (reinterpret_cast<uintptr_t>(k_out) & 31u) ||
       (reinterpret_cast<uintptr_t>(v_out) & 31u))
     return BI_ERR_INVALID_ARG;
+  const int64_t pool = num_out_pages * Hkv * page_size * D * 2;
+  const int64_t records = num_pages * Hkv * kv_q8_record_bytes(D);
+  if (overlap(k_out, pool, v_out, pool) || overlap(k_out, pool, cache, records) ||
+      overlap(v_out, pool, cache, records))
+    return BI_ERR_INVALID_ARG;
   return launch_kv_read_q8(cache, block_table, kv_lens, B, Hkv, D, num_pages, max_blocks_per_seq,
                            k_out, v_out, out_table, num_out_pages, max_out_blocks, max_kv_len,
                            device_error_word(), static_cast<cudaStream_t>(stream));
@@ -607,6 +617,12 @@ bi_status bi_rope_qkv_scaled(const void* qkv, const int32_t* pos, int64_t T, int
   if (T == 0) return BI_OK;
   if (!qkv || !pos || !freqs || !q || !k || !v) return BI_ERR_INVALID_ARG;
   if (!aligned16(qkv) || !aligned16(freqs) || !aligned16(q) || !aligned16(k) || !aligned16(v))
+    return BI_ERR_INVALID_ARG;
+  const int64_t head = T * D * 2;  // bytes of one head of all tokens
+  if (overlap(q, Hq * head, qkv, (Hq + 2 * Hkv) * head) ||
+      overlap(k, Hkv * head, qkv, (Hq + 2 * Hkv) * head) ||
+      overlap(v, Hkv * head, qkv, (Hq + 2 * Hkv) * head) || overlap(q, Hq * head, k, Hkv * head) ||
+      overlap(q, Hq * head, v, Hkv * head) || overlap(k, Hkv * head, v, Hkv * head))
     return BI_ERR_INVALID_ARG;
   return launch_rope_qkv_scaled(qkv, pos, T, Hq, Hkv, D, rot_dim, interleaved != 0, freqs,
                                 attn_scale, q, k, v, static_cast<cudaStream_t>(stream));

@@ -41,8 +41,8 @@ def test_write_argument_checks(lib):
 
 
 def _read(lib, **kw):
-    a = dict(cache=P, bt=P, kl=P, B=2, Hkv=2, D=64, page=16, npages=8, maxblk=4, maxkv=64, ko=P,
-             vo=P, ot=P, nout=8, outblk=4)
+    a = dict(cache=P, bt=P, kl=P, B=2, Hkv=2, D=64, page=16, npages=8, maxblk=4, maxkv=64,
+             ko=2 * P, vo=3 * P, ot=P, nout=8, outblk=4)
     a.update(kw)
     return lib.bi_kv_read_q8(a["cache"], a["bt"], a["kl"], a["B"], a["Hkv"], a["D"], a["page"],
                              a["npages"], a["maxblk"], a["maxkv"], a["ko"], a["vo"], a["ot"],
@@ -56,7 +56,8 @@ def test_read_argument_checks(lib):
     assert _read(lib, nout=1 << 26) == bi.ERR_UNSUPPORTED
     for bad in (dict(B=-1), dict(maxkv=-1), dict(nout=0), dict(outblk=0), dict(cache=None),
                 dict(bt=None), dict(kl=None), dict(ko=None), dict(vo=None), dict(ot=None),
-                dict(ko=P + 2), dict(ko=P + 16), dict(vo=P + 16), dict(cache=P + 8)):
+                dict(ko=2 * P + 2), dict(ko=2 * P + 16), dict(vo=3 * P + 16),
+                dict(cache=P + 8), dict(vo=2 * P), dict(ko=P), dict(vo=2 * P + 32)):
         assert _read(lib, **bad) == bi.ERR_INVALID_ARG, bad
     assert _read(lib, B=0, cache=None) == bi.OK
     assert _read(lib, maxkv=0, cache=None) == bi.OK
@@ -87,7 +88,8 @@ def test_decode_argument_checks(lib):
 
 
 def _rope(lib, **kw):
-    a = dict(qkv=P, pos=P, T=4, Hq=4, Hkv=2, D=64, rot=64, inter=0, f=P, m=1.0, q=P, k=P, v=P)
+    a = dict(qkv=P, pos=P, T=4, Hq=4, Hkv=2, D=64, rot=64, inter=0, f=P, m=1.0, q=2 * P, k=3 * P,
+             v=4 * P)
     a.update(kw)
     return lib.bi_rope_qkv_scaled(a["qkv"], a["pos"], a["T"], a["Hq"], a["Hkv"], a["D"], a["rot"],
                                   a["inter"], a["f"], a["m"], a["q"], a["k"], a["v"], None)
@@ -99,8 +101,8 @@ def test_rope_argument_checks(lib):
         assert _rope(lib, **bad) == bi.ERR_UNSUPPORTED, bad
     for bad in (dict(T=-1), dict(rot=0), dict(rot=66), dict(inter=2), dict(m=0.0),
                 dict(m=float("nan")), dict(m=float("inf")), dict(qkv=None), dict(pos=None),
-                dict(f=None), dict(q=None), dict(k=None), dict(v=None), dict(q=P + 2),
-                dict(f=P + 8)):
+                dict(f=None), dict(q=None), dict(k=None), dict(v=None), dict(q=2 * P + 2),
+                dict(f=P + 8), dict(q=P), dict(k=P + 512), dict(v=3 * P), dict(k=2 * P + 1024)):
         assert _rope(lib, **bad) == bi.ERR_INVALID_ARG, bad
     assert _rope(lib, T=0, qkv=None) == bi.OK
 
