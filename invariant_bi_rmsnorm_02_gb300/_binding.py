@@ -364,25 +364,29 @@ def _dptr(t, dtype, dev, name):
     return t.data_ptr()
 
 
-def _cache_q8(cache, Hkv, D):
-    if cache.dim() != 3 or tuple(cache.shape[1:]) != (Hkv, kv_q8_record_bytes(D)):
+def _cache_q8(cache, Hkv, D) -> int:
+    """The cache's page count, once its shape is what Hkv and D ask for."""
+    s = cache.shape
+    if len(s) != 3 or s[1] != Hkv or s[2] != 32 * D + 32:
         raise ValueError("cache must be [num_pages, %d, %d]" % (Hkv, kv_q8_record_bytes(D)))
+    return s[0]
 
 
 def bi_kv_write_q8(k_new, v_new, seq, pos, cache, block_table, stream=None):
     """Quantise K/V rows of new tokens into the paged cache (include/bi.h)."""
-    n, Hkv, D = k_new.shape
-    if v_new.shape != k_new.shape or seq.shape != (n,) or pos.shape != (n,):
+    shape = k_new.shape
+    n, Hkv, D = shape
+    if v_new.shape != shape or seq.shape != (n,) or pos.shape != (n,):
         raise ValueError("k_new, v_new must be [n, Hkv, D] and seq, pos [n]")
-    _cache_q8(cache, Hkv, D)
+    pages = _cache_q8(cache, Hkv, D)
     num_seqs, max_blocks = block_table.shape
     dev = torch.cuda.current_device()
     _check(load().bi_kv_write_q8(
         _dptr(k_new, torch.bfloat16, dev, "k_new"), _dptr(v_new, torch.bfloat16, dev, "v_new"),
         _dptr(seq, torch.int32, dev, "seq"), _dptr(pos, torch.int32, dev, "pos"), n,
         _dptr(cache, torch.uint8, dev, "cache"),
-        _dptr(block_table, torch.int32, dev, "block_table"), num_seqs, Hkv, D, 16,
-        cache.shape[0], max_blocks, _stream(stream)), "bi_kv_write_q8")
+        _dptr(block_table, torch.int32, dev, "block_table"), num_seqs, Hkv, D, 16, pages,
+        max_blocks, _stream(stream)), "bi_kv_write_q8")
 
 
 def bi_kv_read_q8(cache, block_table, kv_lens, k_out, v_out, out_table, *, max_kv_len,
@@ -411,12 +415,14 @@ def bi_attn_decode_q8(q, cache, block_table, kv_lens, out, out_f32=None, *, max_
                       split_size, sm_scale, mode=INVARIANT, variant_splits=0, workspace=None,
                       stream=None):
     """Decode attention over the quantised cache (include/bi.h)."""
-    B, Hq, D = q.shape
+    shape = q.shape
+    B, Hq, D = shape
     Hkv = cache.shape[1]
-    _cache_q8(cache, Hkv, D)
-    if out.shape != q.shape or (out_f32 is not None and out_f32.shape != q.shape):
+    pages = _cache_q8(cache, Hkv, D)
+    if out.shape != shape or (out_f32 is not None and out_f32.shape != shape):
         raise ValueError("out must have q's shape")
-    if block_table.dim() != 2 or block_table.shape[0] != B or kv_lens.shape != (B,):
+    table = block_table.shape
+    if len(table) != 2 or table[0] != B or kv_lens.shape != (B,):
         raise ValueError("block_table must be [B, max_blocks] and kv_lens [B]")
     dev = torch.cuda.current_device()
     if workspace is not None and workspace.get_device() != dev:
@@ -426,10 +432,9 @@ def bi_attn_decode_q8(q, cache, block_table, kv_lens, out, out_f32=None, *, max_
         _dptr(q, torch.bfloat16, dev, "q"), _dptr(cache, torch.uint8, dev, "cache"),
         _dptr(block_table, torch.int32, dev, "block_table"),
         _dptr(kv_lens, torch.int32, dev, "kv_lens"), _dptr(out, torch.bfloat16, dev, "out"),
-        _dptr(out_f32, torch.float32, dev, "out_f32"), B, Hq, Hkv, D, 16, cache.shape[0],
-        block_table.shape[1], int(max_kv_len), int(split_size),
-        float(sm_scale), int(mode), int(variant_splits), wp, wb, _stream(stream)),
-        "bi_attn_decode_q8")
+        _dptr(out_f32, torch.float32, dev, "out_f32"), B, Hq, Hkv, D, 16, pages, table[1],
+        int(max_kv_len), int(split_size), float(sm_scale), int(mode), int(variant_splits), wp, wb,
+        _stream(stream)), "bi_attn_decode_q8")
 
 
 def bi_rope_frequencies(rot_dim, theta, scaling, factor, trained_len, low_turns, high_turns,
