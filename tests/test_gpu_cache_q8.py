@@ -473,3 +473,28 @@ def test_the_binding_refuses_what_the_library_cannot_take(cuda):
                              split_size=64, sm_scale=0.1)
     assert e.value.status == bi.ERR_WORKSPACE
     assert bi.bi_check_device_errors() == bi.OK
+
+
+@pytest.mark.parametrize("mode", [bi.INVARIANT, bi.VARIANT])
+def test_decode_units_of_more_pages_than_a_warp_holds(cuda, mode):
+    # splits of 2048 keys: 128 pages a unit, past the 64 ids kept in registers
+    D, Hq, Hkv, lens = 64, 8, 2, [3001, 1025, 2048, 1040, 7]
+    kv = synth.paged_kv(lens, Hkv, D, PAGE, 23600)
+    rec = quantised(kv, D).to(cuda)
+    q = synth.normal_bf16((len(lens), Hq, D), 23601, device=cuda)
+    bt = kv.block_table.to(cuda)
+    args = (q, rec, bt, kv.kv_lens.to(cuda), D, 3008, 2048, mode, 1)
+    out, out32, ref, ref32, _, _ = both_decodes(*args)
+    assert bi.bi_check_device_errors() == bi.OK
+    if mode == bi.INVARIANT:
+        assert same_bytes(out32, ref32) and same_bytes(out, ref)
+    else:
+        check_close(f64(out32), f64(ref32), np.full(out32.shape, 2 * ATOL), "variant")
+    bad = bt.clone()
+    bad[0, 100] = rec.shape[0]                 # a page of the unit past the first 64
+    got = bi.attn_decode_q8(q, rec, bad, kv.kv_lens.to(cuda), max_kv_len=3008, split_size=2048,
+                            mode=mode, variant_splits=1)
+    assert bi.bi_check_device_errors() == bi.ERR_DEVICE_BOUNDS
+    assert (got[0] == 0).all()
+    if mode == bi.INVARIANT:
+        assert same_bytes(got[1:].contiguous(), out[1:].contiguous())
