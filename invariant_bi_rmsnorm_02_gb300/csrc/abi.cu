@@ -111,6 +111,21 @@ bool make_tmap_groups_bf16(CUtensorMap* map, const void* base, uint64_t rows, ui
          CUDA_SUCCESS;
 }
 
+bool make_tmap_records(CUtensorMap* map, const void* base, uint64_t records, int D) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (!encode) return false;
+  const uint64_t rec = kv_q8_record_bytes(D);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), 32, records};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), rec};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), 16, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
 }  // namespace bi
 
 using namespace bi;

@@ -977,12 +977,12 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
 //     V's elements become bf16 bits times 2^-120 (three instructions a pair)
 //     and the key's scale, relative to the largest of the tiles so far,
 //     multiplies P's two parts instead;
-//   * every warp is on its own: it works units out, copies a unit's tiles into
-//     its own shared memory with cp.async and computes them, with no barrier
-//     and no other warp to wait for.  Its one tile is two buffers: K's is
-//     filled again as soon as the scores are done and V's after the output
-//     step, so either copy has the other half of the tile's arithmetic to
-//     land in, and the warps of a scheduler fill each other's gaps.
+//   * every warp is on its own: it works units out, has a unit's tiles copied
+//     into its own shared memory by TMA and computes them, with no other warp
+//     to wait for.  Its one tile is two buffers: K's is filled again as soon as
+//     the scores are done and V's after the output step, so either copy has
+//     the other half of the tile's arithmetic to land in, and the warps of a
+//     scheduler fill each other's gaps.
 template <int D, int NQ>
 struct Q8Geom {
   // As many warps as the registers allow, a multiple of the four schedulers.
@@ -1016,9 +1016,8 @@ __device__ __forceinline__ void mma_f16_free(float (&c)[4], const uint32_t (&a)[
 
 constexpr int kQ8PlanMax = 1024;  // largest batch planned in the kernel (32 slabs of 32)
 
-// byte offset of 16-byte chunk c of key n's row in a half tile: the chunks of
-// a row are permuted so that eight rows' chunks of one column are in
-// different banks
+// byte offset of 16-byte chunk c of key n's row in a half tile: the TMA
+// swizzle of the row's width (128 or 64 bytes)
 template <int D>
 __device__ __forceinline__ uint32_t q8_off(int n, int c) {
   const int r = n & 15;
@@ -1310,17 +1309,10 @@ __device__ __forceinline__ void q8_values(SplitState<D, NQ>& st, const float (&s
   }
 }
 
-// Asynchronous copy of 16 bytes, evicted from L2 first (the cache is read
-// once a call; the partials written meanwhile stay for the merge).
-__device__ __forceinline__ void q8_copy16(uint32_t dst, const uint8_t* src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "l"(policy)
-               : "memory");
-}
-
 template <int D, int NQ>
 __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_split_kernel(
-    const uint8_t* __restrict__ cache, const KernelParams p) {
+    const __grid_constant__ CUtensorMap map, const uint8_t* __restrict__ cache,
+    const KernelParams p) {
   using Geom = Q8Geom<D, NQ>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -1331,9 +1323,13 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
   __shared__ int s_slab[32], s_base[32], s_end[32];
   __shared__ long long s_tiles[32];
   __shared__ int s_plan[2];  // the splits of all sequences, the variant's chunk
+  __shared__ uint64_t b_full[Geom::kWarps][2];  // a warp's K and V have landed
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.G, Hkv = p.Hkv;
+  if (threadIdx.x < 2 * Geom::kWarps) mbar_init(&b_full[0][0] + threadIdx.x, 1);
+  if (threadIdx.x == 0) prefetch_tmap(&map);
+  fence_mbar_init();
   grid_dependency_wait();  // inputs and the plan kernel's unit list are complete from here
 
   // ---- the plan.  For up to kQ8PlanMax sequences every block works it out:
@@ -1507,52 +1503,44 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
   uint8_t* scale_buf =
       smem + Geom::kWarps * 2 * Geom::kHalf + warp * 2 * Geom::kScaleBytes;
   const uint64_t pol = l2_policy_evict_first();
-  // where a lane's 16 bytes of a 512-byte piece of a page go (even and odd
-  // pieces): rows of D bytes, the chunk swizzled as q8_off says
-  const uint32_t off0 = q8_off<D>(16 * lane / D, lane % (D / 16));
-  const uint32_t off1 = q8_off<D>(16 * lane / D + 512 / D, lane % (D / 16)) - 512;
-  // Copy tile lt's K (half 0, with its scale bytes into buffer `parity`) or V;
-  // one group of copies, empty for a unit that is not there.
-  auto copy = [&](const Unit& u, int lt, int half, int parity) {
-    if (u.h >= 0) {
-      const int npg = (u.hi - u.lo + kPage - 1) / kPage;
-      const int np = min(kPagesPerTile, npg - 4 * lt);
-      const int idx = 4 * lt + (lane & 3);  // this lane's page of the unit
-      const int in0 = __shfl_sync(kFull, u.pg0, idx & 31);
-      const int in1 = __shfl_sync(kFull, u.pg1, idx & 31);
-      const int pid = (lane & 3) >= np ? 0
-                      : idx < 32       ? in0
-                      : idx < 64       ? in1
-                                       : p.block_table[(int64_t)u.b * p.max_blocks +
-                                                       (u.lo >> 4) + idx];
-      const uint32_t rec = (uint32_t)pid * (uint32_t)Hkv + (uint32_t)u.h;
-      const uint32_t dst = smem_u32(kv) + half * Geom::kHalf;
-      const uint8_t* src = cache + half * Geom::kPageHalf + 16 * lane;
-#pragma unroll
-      for (int i = 0; i < kPagesPerTile; ++i) {
-        if (i >= np) break;
-        const uint8_t* page =
-            src + (uint64_t)__shfl_sync(kFull, rec, i) * (uint32_t)Geom::kRecord;
-#pragma unroll
-        for (int c = 0; c < Geom::kPageHalf / 512; ++c)
-          q8_copy16(dst + i * Geom::kPageHalf + 512 * c + (c & 1 ? off1 : off0), page + 512 * c,
-                    pol);
-      }
-      if (half == 0) {  // the scale bytes: lane i those of K or V of page i / 2
-        const uint32_t from = __shfl_sync(kFull, rec, (lane >> 1) & 3);
-        if (lane < 2 * np)
-          q8_copy16(smem_u32(scale_buf) + parity * Geom::kScaleBytes + 16 * lane,
-                    cache + (uint64_t)from * (uint32_t)Geom::kRecord + 2 * Geom::kPageHalf +
-                        16 * (lane & 1),
-                    pol);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  // all of this warp's copies but the last group have landed
-  auto landed = [&]() {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  uint64_t* full = b_full[warp];
+  // Copy tile lt's K (half 0) or V of a unit, if there is one: a box of 16 rows
+  // per page, counted on the half's barrier; with K its scale bytes, by one
+  // 16-byte cp.async per lane, into buffer `slot`.
+  auto copy = [&](const Unit& u, int lt, int half, int slot) {
+    if (u.h < 0) return;
+    const int npg = (u.hi - u.lo + kPage - 1) / kPage;
+    const int np = min(kPagesPerTile, npg - 4 * lt);
+    const int idx = 4 * lt + (lane & 3);  // this lane's page of the unit
+    const int in0 = __shfl_sync(kFull, u.pg0, idx & 31);
+    const int in1 = __shfl_sync(kFull, u.pg1, idx & 31);
+    const int pid = (lane & 3) >= np ? 0
+                    : idx < 32       ? in0
+                    : idx < 64       ? in1
+                                     : p.block_table[(int64_t)u.b * p.max_blocks +
+                                                     (u.lo >> 4) + idx];
+    const int rec = pid * Hkv + u.h;
+    if (lane == 0) mbar_arrive_expect_tx(&full[half], np * Geom::kPageHalf);
     __syncwarp();
+    if (lane < np)
+      tma_load_3d_hint(kv + half * Geom::kHalf + lane * Geom::kPageHalf, &map, 0, half * kPage,
+                       rec, &full[half], pol);
+    if (half == 0) {  // lane i: the scale bytes of K or V of page i / 2
+      const int from = __shfl_sync(kFull, rec, (lane >> 1) & 3);
+      if (lane < 2 * np)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         smem_u32(scale_buf + slot * Geom::kScaleBytes) + 16 * lane),
+                     "l"(cache + (int64_t)from * Geom::kRecord + 2 * Geom::kPageHalf +
+                         16 * (lane & 1))
+                     : "memory");
+    }
+  };
+  // A wait that runs out ends the warp (no other warp depends on it).
+  bool alive = true;
+  auto landed = [&](int half, uint32_t phase) {
+    if (half == 0) asm volatile("cp.async.wait_all;" ::: "memory");  // the scale bytes
+    alive = __all_sync(kFull, mbar_wait(&full[half], phase, p.err));
+    return alive;
   };
 
   SplitState<D, NQ> st;
@@ -1563,7 +1551,7 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
   Unit next = open();
   copy(next, 0, 0, 0);
   copy(next, 0, 1, 0);
-  while (next.h >= 0) {
+  while (alive && next.h >= 0) {
     const Unit u = next;
     next = open();
     const int64_t row0 = (int64_t)u.b * p.Hq + (int64_t)u.h * G;  // first q-head row
@@ -1575,7 +1563,7 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
       const int limit = u.hi - u.lo - lt * kTile;  // keys of the tile that exist (or more)
       const bool last = limit <= kTile;
       float s[4][NQ][4];
-      landed();
+      if (!landed(0, parity)) break;
       if (f16)
         q8_scores<D, NQ, true>(s, qf, smem_u32(kv), scales);
       else
@@ -1604,7 +1592,10 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
         copy(u, lt + 1, 0, parity ^ 1);
       q8_softmax<D, NQ>(st, s, sc, vtop, vnew);
       vtop = vnew;
-      landed();
+      if (!landed(1, parity)) {
+        if (!last || next.h >= 0) mbar_wait(&full[0], parity ^ 1, nullptr);
+        break;
+      }
       q8_values<D, NQ>(st, s, smem_u32(kv + Geom::kHalf), scales, limit, vtop);
       __syncwarp();  // every lane is done with V
       if (last)
@@ -1612,6 +1603,7 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
       else
         copy(u, lt + 1, 1, 0);
     }
+    if (!alive) break;
     // ---- the output of a single split, or the partial state; columns d and
     // d + 1 are neighbours in a thread
     const bool single = single_split(u);
@@ -1651,7 +1643,12 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
               __fmul_rn(st.o[md][nq][cc], back), __fmul_rn(st.o[md][nq][2 + cc], back));
       }
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the block
+  // no copy outlives the block (all have been waited for, unless a wait ran out)
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!alive) {
+    mbar_wait(&full[0], parity, nullptr);
+    mbar_wait(&full[1], parity, nullptr);
+  }
 }
 
 // ------------------------------------------------------------ decode merge
@@ -2642,6 +2639,9 @@ template <int D, int NQ>
 bi_status decode_q8_impl(const AttnArgs& a, cudaStream_t s) {
   KernelParams p = make_params(a);
   if (a.max_splits > 0) {
+    CUtensorMap map;
+    if (!make_tmap_records(&map, a.k_cache, static_cast<uint64_t>(a.num_pages) * a.Hkv, D))
+      return BI_ERR_CUDA;
     const DecodeWs w = decode_ws_layout(a.B, a.Hq, a.D, a.max_splits);
     char* base = reinterpret_cast<char*>(a.ws);
     p.unit_count = reinterpret_cast<int*>(base);
@@ -2660,7 +2660,7 @@ bi_status decode_q8_impl(const AttnArgs& a, cudaStream_t s) {
     if (!p.local_plan) attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
     const int grid = static_cast<int>(max_units < sms ? max_units : sms);
     if (launch_pdl(attn_decode_q8_split_kernel<D, NQ>, dim3(grid), dim3(Q8Geom<D, NQ>::kThreads), sm,
-                   s, static_cast<const uint8_t*>(a.k_cache), p) != cudaSuccess)
+                   s, map, static_cast<const uint8_t*>(a.k_cache), p) != cudaSuccess)
       return BI_ERR_CUDA;
   }
   return launch_merge<D>(p, s);

@@ -31,6 +31,11 @@ bool make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64
 bool make_tmap_groups_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                            uint32_t box_rows, uint32_t box_groups);
 
+// Encode a tensor map over the quantised cache's page records: per record 32
+// rows (16 of K, 16 of V) of D bytes, records kv_q8_record_bytes(D) apart, a
+// box of 16 rows, swizzled over the row's width (128 or 64 bytes).
+bool make_tmap_records(CUtensorMap* map, const void* base, uint64_t records, int D);
+
 // Bytes of one (page, kv head) of the quantised cache: K[16][D], V[16][D],
 // then 16 scale bytes of K and 16 of V.
 constexpr int kv_q8_record_bytes(int D) { return 32 * D + 32; }
