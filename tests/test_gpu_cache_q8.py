@@ -498,3 +498,43 @@ def test_decode_units_of_more_pages_than_a_warp_holds(cuda, mode):
     assert (got[0] == 0).all()
     if mode == bi.INVARIANT:
         assert same_bytes(got[1:].contiguous(), out[1:].contiguous())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_of_a_cache_on_a_16_byte_boundary_with_shared_pages(cuda, D):
+    # the least alignment the cache may have; two sequences that share pages
+    Hq, Hkv, lens = 8, 2, [77, 64, 1, 16]
+    kv = synth.paged_kv(lens, Hkv, D, PAGE, 23700)
+    rec = quantised(kv, D).to(cuda)
+    q = synth.normal_bf16((len(lens) + 1, Hq, D), 23701, device=cuda)
+    bt = torch.cat([kv.block_table, kv.block_table[:1]]).to(cuda)
+    L = i32(lens + [70], cuda)
+    raw = torch.zeros(rec.numel() + 16, dtype=torch.uint8, device=cuda)
+    off = raw[16:].view(rec.shape)
+    off.copy_(rec)
+    assert off.data_ptr() % 32 == 16
+    want = both_decodes(q, rec, bt, L, D, 77, 64)
+    got = bi.attn_decode_q8(q, off, bt, L, max_kv_len=77, split_size=64)
+    assert bi.bi_check_device_errors() == bi.OK
+    assert same_bytes(got, want[0]) and same_bytes(got, want[2])
+
+
+def test_empty_calls(cuda):
+    D, Hq, Hkv = 64, 4, 2
+    cache = torch.full((3, Hkv, bi.kv_q8_record_bytes(D)), 0x55, dtype=torch.uint8, device=cuda)
+    before = cache.clone()
+    bt = torch.zeros(2, 1, dtype=torch.int32, device=cuda)
+    zero = i32([0, 0], cuda)
+    q = synth.normal_bf16((2, Hq, D), 23702, device=cuda)
+    for most in (0, 16):                       # every length zero: rows of zeros
+        out, out32 = bi.attn_decode_q8(q, cache, bt, zero, max_kv_len=most, split_size=64,
+                                       want_f32=True)
+        assert (out == 0).all() and (out32 == 0).all()
+        k, v = bi.kv_read_q8(cache, D, bt, zero, max_kv_len=most)
+        assert (k == 0).all() and (v == 0).all()
+    none = bi.attn_decode_q8(q[:0], cache, bt[:0], zero[:0], max_kv_len=16, split_size=64)
+    assert none.shape == (0, Hq, D)
+    rows = q[:0, :Hkv].contiguous()
+    bi.kv_write_q8(rows, rows, zero[:0], zero[:0], cache, bt)
+    assert bi.bi_check_device_errors() == bi.OK
+    assert torch.equal(cache, before)
