@@ -1538,7 +1538,12 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
   // A wait that runs out ends the warp (no other warp depends on it).
   bool alive = true;
   auto landed = [&](int half, uint32_t phase) {
-    if (half == 0) asm volatile("cp.async.wait_all;" ::: "memory");  // the scale bytes
+    if (half == 0) {
+      // each lane's scale bytes are there for itself, and after the warp's
+      // barrier for the others (a vote orders no memory)
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+    }
     alive = __all_sync(kFull, mbar_wait(&full[half], phase, p.err));
     return alive;
   };
