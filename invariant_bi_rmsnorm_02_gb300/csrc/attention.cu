@@ -1739,6 +1739,7 @@ __global__ void __launch_bounds__(32) attn_decode_merge_kernel(const KernelParam
     }
     const int kind = nonempty ? (had ? 2 : 1) : 0;  // 0 empty, 1 first non-empty, 2 fold in
     run_m = fmaxf(run_m, __shfl_sync(kFull, pm, 31));
+    const bool fresh = !have;  // the chunk's first non-empty split is the row's first
     have = have || ne != 0;
     const int cnt = min(32, ns - c0);
     const bool whole = ne == (0xffffffffu >> (32 - cnt));  // every split of the chunk counts
@@ -1775,7 +1776,7 @@ __global__ void __launch_bounds__(32) attn_decode_merge_kernel(const KernelParam
         for (int c = 0; c < kCols; ++c) o[c] = ov[i][c];
       };
       if (whole && kStep * (q + 1) <= cnt) {  // a full step: no branch in the chain
-        if (c0 + q == 0)
+        if (fresh && q == 0)
           first(0);
         else
           mix(0);

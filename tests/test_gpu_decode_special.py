@@ -56,3 +56,103 @@ def test_every_tile_takes_its_own_scales(cuda):
                                        want_f32=True)
             assert same_bytes(out, ref), (D, Hq, Hkv, first_divergence(out, ref))
     assert bi.bi_check_device_errors() == bi.OK
+
+
+def masked_case(lens, empty, Hq, Hkv, D, split, seed, lowest=-57344.0):
+    """A cache whose keys in the splits that ``empty`` names (per sequence)
+    score below every finite number for every query: the queries' first
+    channel holds 2^125 and those keys' first channel ``lowest``, the other
+    keys' first channel 0.  Returns the cache, the queries and, per sequence,
+    the mask of its ordinary keys."""
+    kv = synth.paged_kv(lens, Hkv, D, PAGE, seed)
+    kv.k_cache[..., 0] = 0
+    keep = []
+    for b, n in enumerate(lens):
+        j = torch.arange(n)
+        gone = torch.zeros(n, dtype=torch.bool)
+        for s in empty[b]:
+            gone |= j // split == s
+        page = kv.block_table[b, j // PAGE].long()
+        kv.k_cache[page[gone], :, (j % PAGE)[gone], 0] = lowest
+        keep.append(~gone)
+    q = synth.normal_bf16((len(lens), Hq, D), seed + 9)
+    q[..., 0] = 2.0 ** 125
+    return kv, q, keep
+
+
+def definition(q, k_cache, v_cache, block_table, keep):
+    """Softmax attention in 64 bits over each sequence's ordinary keys, zeros
+    where there is none.  Their first channel is 0, so that of q drops out."""
+    q = q.cpu().double().clone()
+    q[..., 0] = 0
+    B, Hq, D = q.shape
+    Hkv = k_cache.shape[1]
+    o = torch.zeros(B, Hq, D, dtype=torch.float64)
+    for b in range(B):
+        j = torch.nonzero(keep[b])[:, 0]
+        if not len(j):
+            continue
+        page = block_table[b].cpu()[j // PAGE].long()
+        k, v = (t.cpu()[page, :, j % PAGE].double() for t in (k_cache, v_cache))
+        qg = q[b].view(Hkv, Hq // Hkv, D)
+        p = torch.softmax(torch.einsum("hgd,khd->hgk", qg, k) / math.sqrt(D), -1)
+        o[b] = torch.einsum("hgk,khd->hgd", p, v).reshape(Hq, D)
+    return o
+
+
+def weight_bound(v):
+    """An output is off by the weights' error times the largest value: below
+    2^-14 for P's two truncated bf16 parts, 2^-21 for ex2, 2^-19 for a score
+    rounded at a magnitude below 2^5, and 2^-24 for each of up to 128 splits
+    folded in; 2^-13 covers their sum."""
+    return 2.0 ** -13 * float(v.abs().max())
+
+
+# splits without a reachable key: none, some, whole chunks of 32 and more at
+# the head of a row, a chunk in the middle, single ones, all of them
+EMPTY = [(), range(3), range(31), range(32), range(33), range(64), range(95), range(32, 64),
+         (0, 33, 64), range(1, 99), range(100)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,copies", [(4, 2, 64, 1), (8, 1, 128, 1), (16, 1, 64, 2),
+                                             (32, 8, 128, 1), (12, 4, 128, 3)])
+def test_splits_without_a_reachable_key(cuda, Hq, Hkv, D, copies):
+    # 100 splits a row; few rows and many take the merge's different forms
+    S = 64
+    empty = [e for e in EMPTY for _ in range(copies)]
+    lens = [100 * S - 7 * (i % 3) for i in range(len(empty))]
+    kv, q, keep = masked_case(lens, empty, Hq, Hkv, D, S, 24100 + Hq)
+    bt, kl, qc = kv.block_table.to(cuda), kv.kv_lens.to(cuda), q.to(cuda)
+    out, out32 = bi.attn_decode(qc, kv.k_cache.to(cuda), kv.v_cache.to(cuda), bt, kl,
+                                max_kv_len=100 * S, split_size=S, want_f32=True)
+    want = definition(q, kv.k_cache, kv.v_cache, kv.block_table, keep)
+    err = (out32.cpu().double() - want).abs().amax((1, 2))
+    assert (err <= weight_bound(kv.v_cache)).all(), err
+    assert (out32[torch.tensor([len(e) == 100 for e in empty])] == 0).all()
+    assert same_bytes(out, out32.to(torch.bfloat16))
+    # each sequence alone: the merge's few-rows form gives the same bytes
+    for b in range(0, len(empty), copies):
+        one = bi.attn_decode(qc[b:b + 1], kv.k_cache.to(cuda), kv.v_cache.to(cuda), bt[b:b + 1],
+                             kl[b:b + 1], max_kv_len=100 * S, split_size=S)
+        assert same_bytes(one, out[b:b + 1].contiguous()), empty[b]
+    assert bi.bi_check_device_errors() == bi.OK
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,copies", [(4, 2, 64, 1), (32, 8, 128, 1), (16, 1, 64, 2)])
+def test_splits_without_a_reachable_key_of_a_quantised_cache(cuda, Hq, Hkv, D, copies):
+    S = 64
+    empty = [e for e in EMPTY for _ in range(copies)]
+    lens = [100 * S - 7 * (i % 3) for i in range(len(empty))]
+    kv, q, keep = masked_case(lens, empty, Hq, Hkv, D, S, 24200 + Hq)
+    rec = records(kv, D, cuda)
+    bt, kl, qc = kv.block_table.to(cuda), kv.kv_lens.to(cuda), q.to(cuda)
+    k, v = bi.kv_read_q8(rec, D, bt, kl, max_kv_len=100 * S)
+    out, out32 = bi.attn_decode_q8(qc, rec, bt, kl, max_kv_len=100 * S, split_size=S,
+                                   want_f32=True)
+    want = definition(q, k, v, kv.block_table, keep)
+    err = (out32.cpu().double() - want).abs().amax((1, 2))
+    assert (err <= weight_bound(v)).all(), err
+    ref, ref32 = bi.attn_decode(qc, k, v, bt, kl, max_kv_len=100 * S, split_size=S, want_f32=True)
+    assert same_bytes(out32, ref32), first_divergence(out32, ref32)
+    assert same_bytes(out, ref)
+    assert bi.bi_check_device_errors() == bi.OK
