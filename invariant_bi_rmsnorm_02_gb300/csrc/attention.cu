@@ -2378,7 +2378,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
   } else {
     // ================================================================ fold
     // Split j's accumulator (m_s, l_s, o_s) into the merged state, in split
-    // order: the decode merge's left fold, one row per thread.  The
+    // order: the decode merge's left fold, one row per thread, which passes
+    // over a split with no key of a score above -inf (m_s = -inf).  The
     // accumulator is released (ofree) as soon as its last columns are read.
     const int r = (warp - kPfFoldWarp0) * 32 + lane;
     const int tk = r / G;
@@ -2394,7 +2395,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
       tc_fence_after();
       const float m_s = xsplit[(j & 1) * 2 * kPfRows + r];
       const float l_s = xsplit[(j & 1) * 2 * kPfRows + kPfRows + r];
-      const bool part = pos >= j * S;  // the split holds keys this row sees
+      // the split holds keys this row sees, and one of them counts
+      const bool part = pos >= j * S && m_s != -CUDART_INF_F;
       float mn = 0.0f, ca = 0.0f, cb = 0.0f;
       if (part && have) lse_coeffs(mg_m, m_s, mn, ca, cb);
       const bool any = __any_sync(kFull, part);
@@ -2438,8 +2440,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(&folded[j & 1]);
     }
-    // the row's 1/l for the output below (the split m, l slots are free now)
-    if (live && pos >= 0) xsplit[r] = inv_l(mg_l);
+    // the row's 1/l for the output below (the split m, l slots are free now);
+    // -1 for a row that no key counts for, whose output is zero as in decode
+    if (live && pos >= 0) xsplit[r] = mg_l != 0.0f ? inv_l(mg_l) : -1.0f;
   }
   tc_fence_before();
   __syncthreads();
@@ -2457,8 +2460,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
     const int c4 = 4 * (u / (kPfRows / 8)) + (lane & 3);
     const int tk = r / oG;
     if (r >= (kPfRows / oG) * oG || tk >= otok) continue;
-    const float rl = xsplit[r];
-    const float4 a = omg[c4 * kPfRows + r];
+    float rl = xsplit[r];
+    float4 a = omg[c4 * kPfRows + r];
+    if (rl < 0.0f) {  // never written
+      a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      rl = 0.0f;
+    }
     const float o0 = normalize(a.x, rl), o1 = normalize(a.y, rl);
     const float o2 = normalize(a.z, rl), o3 = normalize(a.w, rl);
     const int64_t idx = (row0 + (int64_t)tk * p.Hq + r % oG) * D + 4 * c4;

@@ -156,3 +156,45 @@ def test_splits_without_a_reachable_key_of_a_quantised_cache(cuda, Hq, Hkv, D, c
     assert same_bytes(out32, ref32), first_divergence(out32, ref32)
     assert same_bytes(out, ref)
     assert bi.bi_check_device_errors() == bi.OK
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 64), (32, 8, 128), (16, 1, 128), (12, 4, 64)])
+def test_prefill_of_splits_without_a_reachable_key(cuda, Hq, Hkv, D):
+    # the last positions of each sequence, and a whole prompt whose first keys
+    # are out of reach: the bytes of the decode at every position, zeros where
+    # a query reaches no key
+    S = 64
+    lens = [100 * S - 7 * (i % 3) for i in range(len(EMPTY))]
+    kv, _, keep = masked_case(lens, EMPTY, Hq, Hkv, D, S, 24300 + Hq)
+    kc, vc, bt, kl = (t.to(cuda) for t in (kv.k_cache, kv.v_cache, kv.block_table, kv.kv_lens))
+    n = 5
+    q = synth.normal_bf16((n * len(lens), Hq, D), 24301 + Hq)
+    q[..., 0] = 2.0 ** 125
+    qc = q.to(cuda)
+    cu = i32([n * b for b in range(len(lens) + 1)], cuda)
+    pre, pre32 = bi.attn_prefill_chunk(qc, cu, kl - n, kc, vc, bt, kl, max_q_len=n,
+                                       max_kv_len=100 * S, split_size=S, want_f32=True)
+    at = (kl[:, None] - n + 1 + torch.arange(n, device=cuda)[None, :]).to(torch.int32).flatten()
+    rows = bt.repeat_interleave(n, 0).contiguous()
+    each, each32 = bi.attn_decode(qc, kc, vc, rows, at.contiguous(), max_kv_len=100 * S,
+                                  split_size=S, want_f32=True)
+    assert same_bytes(pre32, each32), first_divergence(pre32, each32)
+    assert same_bytes(pre, each)
+    assert (pre32[-n:] == 0).all() and torch.isfinite(pre32).all()
+
+    L = 400                                    # splits 0, 1, 2 and 5 of a prompt out of reach
+    kv, _, keep = masked_case([L], [(0, 1, 2, 5)], Hq, Hkv, D, S, 24400 + Hq)
+    kc, vc, bt, kl = (t.to(cuda) for t in (kv.k_cache, kv.v_cache, kv.block_table, kv.kv_lens))
+    q = synth.normal_bf16((L, Hq, D), 24401 + Hq)
+    q[..., 0] = 2.0 ** 125
+    qc = q.to(cuda)
+    _, pre32 = bi.attn_prefill_chunk(qc, i32([0, L], cuda), i32([0], cuda), kc, vc, bt, kl,
+                                     max_q_len=L, max_kv_len=L, split_size=S, want_f32=True)
+    _, each32 = bi.attn_decode(qc, kc, vc, bt.expand(L, -1).contiguous(),
+                               i32(range(1, L + 1), cuda), max_kv_len=L, split_size=S,
+                               want_f32=True)
+    assert same_bytes(pre32, each32), first_divergence(pre32, each32)
+    assert (pre32[:3 * S] == 0).all()
+    want = definition(q[L - 1:], kv.k_cache, kv.v_cache, kv.block_table, keep)
+    assert (pre32[L - 1:].cpu().double() - want).abs().max() <= weight_bound(kv.v_cache)
+    assert bi.bi_check_device_errors() == bi.OK
