@@ -325,6 +325,12 @@ __device__ __forceinline__ void tile_step(SplitState<D, NQ>& st,
   }
 }
 
+// A split takes part in the merge unless it is empty: no key above -inf, so
+// that its sum is 0.  Scores that are all NaN may leave its reference at -inf
+// too (a maximum passes over NaN), but their sum is NaN and has to be seen.
+__device__ __forceinline__ bool split_counts(float m, float l) {
+  return m != -CUDART_INF_F || l != 0.0f;
+}
 // Log-sum-exp merge of partial (mb, lb, ob) into (m, l, o), in that order.
 __device__ __forceinline__ void lse_coeffs(float m, float mb, float& mn, float& ca, float& cb) {
   mn = fmaxf(m, mb);
@@ -337,7 +343,8 @@ __device__ __forceinline__ float lse_mix(float a, float ca, float b, float cb) {
 // The output's normalisation: o times the correctly rounded reciprocal of l
 // (one reciprocal per row, then one product per element; an IEEE division
 // per element cost the prefill's output phase 2.7 us a block).  Decode, its
-// merge and prefill all normalise with this, so they stay bit-identical.
+// merge and prefill all normalise with this, so they stay bit-identical.  A
+// row that no key counts for (l = 0) is zero; a NaN sum reaches the output.
 __device__ __forceinline__ float inv_l(float l) { return __frcp_rn(l); }
 __device__ __forceinline__ float normalize(float o, float rl) { return __fmul_rn(o, rl); }
 
@@ -908,7 +915,7 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
             const float o_odd = __shfl_xor_sync(kFull, st.o[md][0][2 * hh + 1], 2);
             const float ov = helper ? o_odd : st.o[md][0][2 * hh];
             if (col < G) {
-              const float v = lv > 0.0f ? normalize(ov, inv_l(lv)) : 0.0f;
+              const float v = lv != 0.0f ? normalize(ov, inv_l(lv)) : 0.0f;
               const int64_t idx = orow + 16 * md + g + 8 * hh;
               static_cast<__nv_bfloat16*>(p.out)[idx] = __float2bfloat16_rn(v);
               if (p.out_f32) p.out_f32[idx] = v;
@@ -928,7 +935,7 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
           for (int md = 0; md < D / 16; ++md)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const float v = lv > 0.0f ? normalize(st.o[md][nq][2 * hh + cc], inv_l(lv)) : 0.0f;
+              const float v = lv != 0.0f ? normalize(st.o[md][nq][2 * hh + cc], inv_l(lv)) : 0.0f;
               const int64_t idx = orow + 16 * md + g + 8 * hh;
               static_cast<__nv_bfloat16*>(p.out)[idx] = __float2bfloat16_rn(v);
               if (p.out_f32) p.out_f32[idx] = v;
@@ -1626,9 +1633,9 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
 #pragma unroll
           for (int md = 0; md < D / 16; ++md) {
             const float v0 =
-                lv > 0.0f ? normalize(__fmul_rn(st.o[md][nq][cc], back), rl) : 0.0f;
+                lv != 0.0f ? normalize(__fmul_rn(st.o[md][nq][cc], back), rl) : 0.0f;
             const float v1 =
-                lv > 0.0f ? normalize(__fmul_rn(st.o[md][nq][2 + cc], back), rl) : 0.0f;
+                lv != 0.0f ? normalize(__fmul_rn(st.o[md][nq][2 + cc], back), rl) : 0.0f;
             *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow + 16 * md) =
                 pack_bf16x2(v0, v1);
             if (p.out_f32)
@@ -1720,7 +1727,7 @@ __global__ void __launch_bounds__(32) attn_decode_merge_kernel(const KernelParam
     // coefficients of the chunk's split lane; the next chunk's {m, l} on the way
     const float m = ml.x, lj = ml.y;
     ml = c0 + 32 + lane < ns ? mlrow[c0 + 32 + lane] : none;
-    const bool nonempty = m != -CUDART_INF_F;
+    const bool nonempty = split_counts(m, lj);
     float pm = m;  // inclusive prefix max over the chunk
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
@@ -1799,7 +1806,7 @@ __global__ void __launch_bounds__(32) attn_decode_merge_kernel(const KernelParam
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the block
-  const bool some = ns > 0 && !bad && l > 0.0f;
+  const bool some = ns > 0 && !bad && l != 0.0f;
   const float rl = inv_l(l);
   float r[kCols];
 #pragma unroll
@@ -2379,8 +2386,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
     // ================================================================ fold
     // Split j's accumulator (m_s, l_s, o_s) into the merged state, in split
     // order: the decode merge's left fold, one row per thread, which passes
-    // over a split with no key of a score above -inf (m_s = -inf).  The
-    // accumulator is released (ofree) as soon as its last columns are read.
+    // over an empty split (split_counts).  The accumulator is released
+    // (ofree) as soon as its last columns are read.
     const int r = (warp - kPfFoldWarp0) * 32 + lane;
     const int tk = r / G;
     const int pos = (r < TPB * G && tk < ntok) ? start + tok0 + tk : -1;
@@ -2396,7 +2403,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
       const float m_s = xsplit[(j & 1) * 2 * kPfRows + r];
       const float l_s = xsplit[(j & 1) * 2 * kPfRows + kPfRows + r];
       // the split holds keys this row sees, and one of them counts
-      const bool part = pos >= j * S && m_s != -CUDART_INF_F;
+      const bool part = pos >= j * S && split_counts(m_s, l_s);
       float mn = 0.0f, ca = 0.0f, cb = 0.0f;
       if (part && have) lse_coeffs(mg_m, m_s, mn, ca, cb);
       const bool any = __any_sync(kFull, part);

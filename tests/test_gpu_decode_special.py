@@ -198,3 +198,72 @@ def test_prefill_of_splits_without_a_reachable_key(cuda, Hq, Hkv, D):
     want = definition(q[L - 1:], kv.k_cache, kv.v_cache, kv.block_table, keep)
     assert (pre32[L - 1:].cpu().double() - want).abs().max() <= weight_bound(kv.v_cache)
     assert bi.bi_check_device_errors() == bi.OK
+
+
+def nan_agree(a, b):
+    """The same elements NaN and the same bytes elsewhere."""
+    nan = torch.isnan(a)
+    return torch.equal(nan, torch.isnan(b)) and same_bytes(a[~nan], b[~nan])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 4, 64), (16, 4, 128), (48, 4, 128), (64, 4, 64)])
+@pytest.mark.parametrize("split", [64, 512])
+def test_a_key_that_is_not_finite_is_not_hidden(cuda, Hq, Hkv, D, split):
+    # a NaN or an infinite key (NaN in a quantised cache) makes its head's
+    # whole output NaN in its own sequence, and nothing else: one split or
+    # several, decode and prefill
+    G = Hq // Hkv
+    lens = [100, 300, 200]
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        kv = synth.paged_kv(lens, Hkv, D, PAGE, 24500 + Hq)
+        page = int(kv.block_table[1, 2])
+        kv.k_cache[page, 1, 3, 17] = bad                # key 35 of sequence 1, kv head 1
+        kc, vc, bt, kl = (t.to(cuda) for t in (kv.k_cache, kv.v_cache, kv.block_table,
+                                               kv.kv_lens))
+        rec = records(kv, D, cuda)
+        kb, vb = bi.kv_read_q8(rec, D, bt, kl, max_kv_len=300)
+        assert torch.isnan(kb[page, 1, 3]).all()
+        q = synth.normal_bf16((3, Hq, D), 24501 + Hq, device=cuda)
+        args = dict(max_kv_len=300, split_size=split, want_f32=True)
+        want = torch.zeros(3, Hkv, G, D, dtype=torch.bool, device=cuda)
+        want[1, 1] = True
+        out, out32 = bi.attn_decode_q8(q, rec, bt, kl, **args)
+        assert torch.equal(torch.isnan(out32), want.view(3, Hq, D))
+        assert torch.equal(torch.isnan(out), want.view(3, Hq, D))
+        _, ref32 = bi.attn_decode(q, kb, vb, bt, kl, **args)
+        assert nan_agree(out32, ref32)
+        if math.isnan(bad):                             # an infinite key scores +-inf there
+            _, raw32 = bi.attn_decode(q, kc, vc, bt, kl, **args)
+            assert torch.equal(torch.isnan(raw32), want.view(3, Hq, D))
+        # positions 20 .. 299 of sequence 1: finite up to the key, NaN from it on
+        qp = synth.normal_bf16((280, Hq, D), 24502 + Hq, device=cuda)
+        _, pre32 = bi.attn_prefill_chunk(qp, i32([0, 280], cuda), i32([20], cuda), kb, vb,
+                                         bt[1:2], kl[1:2], max_q_len=280, **args)
+        _, each32 = bi.attn_decode_q8(qp, rec, bt[1:2].expand(280, -1).contiguous(),
+                                      i32(range(21, 301), cuda), **args)
+        nan = torch.isnan(pre32).view(280, Hkv, G, D)
+        assert nan[15:, 1].all() and not nan[:15].any() and not nan[:, [0, 2, 3]].any()
+        assert nan_agree(pre32, each32)
+    assert bi.bi_check_device_errors() == bi.OK
+
+
+def test_a_query_that_is_not_finite_is_not_hidden(cuda):
+    for D, Hq, Hkv in ((64, 4, 2), (128, 32, 8), (128, 16, 1)):
+        lens = [50, 700, 64]
+        kv = synth.paged_kv(lens, Hkv, D, PAGE, 24600 + Hq)
+        rec = records(kv, D, cuda)
+        bt, kl = kv.block_table.to(cuda), kv.kv_lens.to(cuda)
+        kb, vb = bi.kv_read_q8(rec, D, bt, kl, max_kv_len=700)
+        q = synth.normal_bf16((3, Hq, D), 24601 + Hq, device=cuda)
+        q[0, 1, 5] = q[1, 2, 7] = float("nan")
+        want = torch.zeros(3, Hq, D, dtype=torch.bool, device=cuda)
+        want[0, 1] = want[1, 2] = True
+        for split in (64, 256, 1024):
+            args = dict(max_kv_len=700, split_size=split, want_f32=True)
+            _, out32 = bi.attn_decode_q8(q, rec, bt, kl, **args)
+            _, ref32 = bi.attn_decode(q, kb, vb, bt, kl, **args)
+            _, pre32 = bi.attn_prefill_chunk(q, i32([0, 1, 2, 3], cuda), kl - 1, kb, vb, bt, kl,
+                                             max_q_len=1, **args)
+            assert torch.equal(torch.isnan(out32), want)
+            assert nan_agree(out32, ref32) and nan_agree(pre32, ref32)
+    assert bi.bi_check_device_errors() == bi.OK
