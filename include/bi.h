@@ -219,7 +219,8 @@ bi_status bi_gemm_swiglu(const void* A, const void* W, void* out, int64_t M, int
 
 /* Decode: one new query token per sequence.
  *   q [B][Hq][D] bf16, out [B][Hq][D] bf16.
- *   max_kv_len: host-side upper bound on kv_lens (sizes the grid only).
+ *   max_kv_len: host-side upper bound on kv_lens (sizes the grid only); here
+ *   and in the other calls a bound above 2^30 counts as 2^30.
  *   Workspace: bi_attn_decode_workspace_size(...) bytes. */
 bi_status bi_attn_decode(const void* q, const void* k_cache, const void* v_cache,
                          const int32_t* block_table, const int32_t* kv_lens, void* out,

@@ -8,6 +8,7 @@
 
 #include <math.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "bi.h"
@@ -338,6 +339,14 @@ bi_status bi_gemm_swiglu(const void* A, const void* W, void* out, int64_t M, int
 // maximum of the scaled scores only for a positive scale.
 static bool scale_ok(float s) { return s > 0.0f && s <= 3.4e38f; }
 
+// The bound on lengths and the split size as the kernels take them: none above
+// 2^30, so that sums of the two fit an int, and no split size above the bound
+// rounded up to a tile, since a larger one cuts no sequence either.
+static int kernel_max_kv_len(int max_kv_len) { return std::min(max_kv_len, kMaxKvLen); }
+static int kernel_split_size(int split_size, int max_kv_len) {
+  return std::min(split_size, std::max(64, (kernel_max_kv_len(max_kv_len) + 63) / 64 * 64));
+}
+
 static bi_status attn_common_checks(const void* q, const void* k, const void* v,
                                     const int32_t* bt, const int32_t* kl, const void* out,
                                     const float* out_f32, int B, int Hq, int Hkv, int D,
@@ -388,7 +397,8 @@ static bi_status attn_decode(const void* q, const void* k_cache, const void* v_c
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.q8 = q8; a.block_table = block_table;
   a.kv_lens = kv_lens; a.out = out; a.out_f32 = out_f32;
   a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.page_size = page_size; a.num_pages = num_pages;
-  a.max_blocks = max_blocks_per_seq; a.max_kv_len = max_kv_len; a.split_size = split_size;
+  a.max_blocks = max_blocks_per_seq; a.max_kv_len = kernel_max_kv_len(max_kv_len);
+  a.split_size = kernel_split_size(split_size, max_kv_len);
   a.variant = mode == BI_MODE_VARIANT; a.sm_scale = sm_scale;
   a.err = device_error_word();
   if (a.variant) {
@@ -453,8 +463,9 @@ bi_status bi_attn_prefill_chunk(const void* q, const int32_t* cu_q, const int32_
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.block_table = block_table;
   a.kv_lens = kv_lens; a.cu_q = cu_q; a.q_start = q_start_pos; a.out = out; a.out_f32 = out_f32;
   a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.page_size = page_size; a.num_pages = num_pages;
-  a.max_blocks = max_blocks_per_seq; a.max_kv_len = max_kv_len; a.total_q = total_q;
-  a.max_q_len = max_q_len; a.split_size = split_size; a.sm_scale = sm_scale;
+  a.max_blocks = max_blocks_per_seq; a.max_kv_len = kernel_max_kv_len(max_kv_len);
+  a.total_q = total_q; a.max_q_len = max_q_len;
+  a.split_size = kernel_split_size(split_size, max_kv_len); a.sm_scale = sm_scale;
   a.variant = mode == BI_MODE_VARIANT;
   a.err = device_error_word();
   if (a.variant) {
@@ -465,8 +476,8 @@ bi_status bi_attn_prefill_chunk(const void* q, const int32_t* cu_q, const int32_
       c = attn_variant_split_count(B, Hkv, max_kv_len, sms);
     }
     // chunk-derived split size: the boundaries move with the chunk's length
-    const int per = (max_kv_len + c - 1) / c;
-    a.split_size = ((per + 63) / 64) * 64;
+    const int64_t per = (a.max_kv_len + int64_t(c) - 1) / c;
+    a.split_size = static_cast<int>((per + 63) / 64 * 64);
     if (a.split_size <= 0) a.split_size = 64;
     a.split_count = c;
   }
@@ -543,7 +554,8 @@ bi_status bi_kv_read_q8(const void* cache, const int32_t* block_table, const int
       overlap(v_out, pool, cache, records))
     return BI_ERR_INVALID_ARG;
   return launch_kv_read_q8(cache, block_table, kv_lens, B, Hkv, D, num_pages, max_blocks_per_seq,
-                           k_out, v_out, out_table, num_out_pages, max_out_blocks, max_kv_len,
+                           k_out, v_out, out_table, num_out_pages, max_out_blocks,
+                           kernel_max_kv_len(max_kv_len),
                            device_error_word(), static_cast<cudaStream_t>(stream));
 }
 

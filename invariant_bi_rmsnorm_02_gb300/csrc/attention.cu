@@ -426,7 +426,8 @@ struct KernelParams {
 };
 
 __device__ __forceinline__ bool len_ok(int L, const KernelParams& p) {
-  return L >= 0 && L <= p.max_kv_len && L <= p.max_blocks * kPage;
+  // max_kv_len is at most 2^30, so the sum fits; max_blocks * kPage need not
+  return L >= 0 && L <= p.max_kv_len && (L + kPage - 1) / kPage <= p.max_blocks;
 }
 
 // --------------------------------------------------------------- decode plan
@@ -2807,7 +2808,7 @@ int attn_variant_split_count(int B, int Hkv, int max_kv_len, int num_sms) {
 int attn_decode_max_splits(int max_kv_len, int split_size, bool variant, int split_count) {
   if (max_kv_len <= 0) return 0;
   if (variant) return split_count > 0 ? split_count : 1;
-  return (max_kv_len + split_size - 1) / split_size;
+  return static_cast<int>((static_cast<int64_t>(max_kv_len) + split_size - 1) / split_size);
 }
 
 size_t attn_decode_workspace_bytes(int B, int Hq, int D, int max_splits) {

@@ -40,6 +40,10 @@ bool make_tmap_records(CUtensorMap* map, const void* base, uint64_t records, int
 // then 16 scale bytes of K and 16 of V.
 constexpr int kv_q8_record_bytes(int D) { return 32 * D + 32; }
 
+// The longest sequence of the paged cache, in tokens (a larger host bound on
+// the lengths counts as this one).
+constexpr int kMaxKvLen = 1 << 30;
+
 inline bi_status cuda_status(cudaError_t e) { return e == cudaSuccess ? BI_OK : BI_ERR_CUDA; }
 
 // ---- RMSNorm (rmsnorm.cu) ---------------------------------------------------

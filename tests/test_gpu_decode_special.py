@@ -267,3 +267,33 @@ def test_a_query_that_is_not_finite_is_not_hidden(cuda):
             assert torch.equal(torch.isnan(out32), want)
             assert nan_agree(out32, ref32) and nan_agree(pre32, ref32)
     assert bi.bi_check_device_errors() == bi.OK
+
+
+def test_bounds_at_the_ends_of_their_ranges(cuda):
+    # the largest bound on the lengths and the largest split size are those of
+    # a call with no split and the sequence's own length
+    D, Hq, Hkv = 64, 4, 2
+    lens = [300, 1, 0, 129]
+    kv = synth.paged_kv(lens, Hkv, D, PAGE, 24700)
+    rec = records(kv, D, cuda)
+    bt, kl = kv.block_table.to(cuda), kv.kv_lens.to(cuda)
+    q = synth.normal_bf16((4, Hq, D), 24701, device=cuda)
+    top, whole = 2 ** 31 - 1, 2 ** 31 - 64
+    kb, vb = bi.kv_read_q8(rec, D, bt, kl, max_kv_len=300)
+    k2, v2 = bi.kv_read_q8(rec, D, bt, kl, max_kv_len=top)
+    assert same_bytes(kb, k2) and same_bytes(vb, v2)
+    cu, start = i32([0, 1, 1, 1, 2], cuda), i32([299, 0, 0, 128], cuda)
+    qp = q[:2].contiguous()
+    for mode in (bi.INVARIANT, bi.VARIANT):
+        # the variant mode's plan goes by the bound itself, so it keeps it
+        bound = top if mode == bi.INVARIANT else 300
+        args = dict(split_size=320, max_kv_len=300, mode=mode)
+        wide = dict(split_size=whole, max_kv_len=bound, mode=mode)
+        a = bi.attn_decode_q8(q, rec, bt, kl, **args)
+        assert same_bytes(a, bi.attn_decode_q8(q, rec, bt, kl, **wide))
+        b = bi.attn_decode(q, kb, vb, bt, kl, **args)
+        assert same_bytes(b, bi.attn_decode(q, kb, vb, bt, kl, **wide))
+        c = bi.attn_prefill_chunk(qp, cu, start, kb, vb, bt, kl, max_q_len=1, **args)
+        d = bi.attn_prefill_chunk(qp, cu, start, kb, vb, bt, kl, max_q_len=1, **wide)
+        assert same_bytes(c, d)
+    assert bi.bi_check_device_errors() == bi.OK
