@@ -423,6 +423,8 @@ bi_status bi_rope_qkv(const void* qkv, const int32_t* pos, int64_t T, int Hq, in
  *                    p(low_turns)), rot_dim - 1) (b - a at least 0.001),
  *                    p(n) = rot_dim ln(trained_len / (2 pi n)) / (2 ln theta);
  *                    *attn_scale = 0.1 ln(factor) + 1 (1 in the other cases)
+ * The published ramps run from 4 turns (high_turns) to 1 (low_turns) for
+ * LLAMA3 and from 32 to 1 for YARN.
  * theta > 1; factor >= 1 (not read for NONE); trained_len >= 1 and
  * 0 < low_turns < high_turns (read for LLAMA3 and YARN only); rot_dim even,
  * at most 1024 (NTK: above 2).  Touches no device. */

@@ -37,7 +37,7 @@ __all__ = [
     "bi_kv_write_q8", "bi_kv_read_q8", "bi_attn_decode_q8", "bi_rope_frequencies",
     "bi_rope_qkv_scaled", "ROPE_NONE", "ROPE_LINEAR", "ROPE_NTK", "ROPE_LLAMA3", "ROPE_YARN",
     "kv_q8_record_bytes", "kv_cache_q8", "kv_write_q8", "kv_read_q8", "attn_decode_q8",
-    "rope_frequencies", "rope_qkv_scaled",
+    "rope_frequencies", "rope_high_turns", "rope_qkv_scaled",
     "NOALLOC_SCRATCH_BYTES", "rmsnorm", "add_rmsnorm", "gemm", "gemm_swiglu",
     "swiglu_interleave", "attn_decode", "attn_prefill_chunk", "kv_write", "sample",
     "gather_rows", "rope_qkv", "silu_mul", "EXPORTED_SYMBOLS",
@@ -644,11 +644,20 @@ def attn_decode_q8(q, cache, block_table, kv_lens, *, max_kv_len, split_size, sm
     return (out, out32) if want_f32 else out
 
 
+def rope_high_turns(scaling) -> float:
+    """The published upper end of a scaling's ramp, in turns over the trained
+    length: 32 for YaRN, 4 for Llama 3 (the others have no ramp)."""
+    return 32.0 if scaling == ROPE_YARN else 4.0
+
+
 def rope_frequencies(rot_dim, theta=500000.0, scaling=ROPE_NONE, factor=1.0, trained_len=8192,
-                     low_turns=1.0, high_turns=4.0, device=None):
+                     low_turns=1.0, high_turns=None, device=None):
     """(freqs, attn_scale) of rotary positions: a float64 tensor of
     rot_dim / 2 rotation frequencies on ``device`` (the current CUDA device
-    if None) and the factor on cosine and sine, both for rope_qkv_scaled."""
+    if None) and the factor on cosine and sine, both for rope_qkv_scaled.
+    ``high_turns`` None: the scaling's published value (rope_high_turns)."""
+    if high_turns is None:
+        high_turns = rope_high_turns(scaling)
     f = np.empty(int(rot_dim) // 2, np.float64)
     m = bi_rope_frequencies(rot_dim, theta, scaling, factor, trained_len, low_turns, high_turns, f)
     return torch.from_numpy(f).to("cuda" if device is None else device), m

@@ -77,7 +77,7 @@ class DecoderConfig:
     rope_factor: float = 1.0
     rope_trained_len: int = 8192
     rope_low_turns: float = 1.0
-    rope_high_turns: float = 4.0
+    rope_high_turns: float | None = None # None: the scaling's published value (YaRN 32, Llama 3 4)
     kv_cache: str = "bf16"               # "bf16" or "e4m3" (one byte an element)
 
     def __post_init__(self):
@@ -87,6 +87,11 @@ class DecoderConfig:
             raise ValueError('kv_cache must be "bf16" or "e4m3"')
         if self.kv_cache == "e4m3" and (self.page_size != 16 or self.head_dim not in (64, 128)):
             raise ValueError("an e4m3 cache needs pages of 16 tokens and heads of 64 or 128")
+        # settled only where it is read, so that a configuration without a ramp
+        # can be replaced by one with either
+        if self.rope_high_turns is None and self.rope_scaling in ("llama3", "yarn"):
+            object.__setattr__(self, "rope_high_turns",
+                               bi.rope_high_turns(ROPE_SCALINGS[self.rope_scaling]))
 
     @property
     def plain_rope(self) -> bool:
