@@ -2012,7 +2012,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
   if (tok0 >= q_len) return;
   const int start = p.q_start[b];
   const int kvl = p.kv_lens[b];
-  if (!len_ok(kvl, p) || start < 0 || q_len < 0 || start + q_len > kvl) {
+  if (!len_ok(kvl, p) || start < 0 || q_len < 0 || start > kvl - q_len) {
     if (tid == 0) record_error(p.err, BI_ERR_DEVICE_BOUNDS);
     return;
   }

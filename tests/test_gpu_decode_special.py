@@ -297,3 +297,19 @@ def test_bounds_at_the_ends_of_their_ranges(cuda):
         d = bi.attn_prefill_chunk(qp, cu, start, kb, vb, bt, kl, max_q_len=1, **wide)
         assert same_bytes(c, d)
     assert bi.bi_check_device_errors() == bi.OK
+
+
+def test_prefill_refuses_a_start_whose_end_passes_32_bits(cuda):
+    D, Hq, Hkv, n = 64, 4, 2, 200
+    kv = synth.paged_kv([300, 300], Hkv, D, PAGE, 24800)
+    kc, vc, bt, kl = (t.to(cuda) for t in (kv.k_cache, kv.v_cache, kv.block_table, kv.kv_lens))
+    q = synth.normal_bf16((2 * n, Hq, D), 24801, device=cuda)
+    cu = i32([0, n, 2 * n], cuda)
+    want = bi.attn_prefill_chunk(q, cu, i32([100, 100], cuda), kc, vc, bt, kl, max_q_len=n,
+                                 max_kv_len=300, split_size=64)
+    for start in (101, 2 ** 31 - 1, 2 ** 31 - n, 2 ** 31 - 100, -1):
+        out = torch.full_like(q, 7.0)
+        bi.bi_attn_prefill_chunk(q, cu, i32([100, start], cuda), kc, vc, bt, kl, out,
+                                 max_q_len=n, max_kv_len=300, split_size=64, sm_scale=D ** -0.5)
+        assert bi.bi_check_device_errors() == bi.ERR_DEVICE_BOUNDS, start
+        assert same_bytes(out[:n], want[:n]) and (out[n:] == 7.0).all(), start
