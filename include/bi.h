@@ -372,8 +372,18 @@ bi_status bi_kv_read_q8(const void* cache, const int32_t* block_table, const int
  * two (same modes, split plan, workspace size, checks and errors).  The
  * result in BI_MODE_INVARIANT has exactly the bytes of bi_attn_decode on the
  * pages that bi_kv_read_q8 gives, and so those of bi_attn_prefill_chunk on
- * them at every position.  BI_MODE_VARIANT sizes its chunks from this
- * kernel's resident blocks, so its plan may differ from bi_attn_decode's. */
+ * them at every position, wherever
+ *   - no element of q is 2^64 or more in magnitude and no |q . k| 2^127 or more
+ *     (further up, bi_attn_decode's unscaled sum becomes infinite where this
+ *     one need not);
+ *   - every part of an output element, the sum over its row's first keys or one
+ *     key's weight times its value, is zero or above 2^-100 both in magnitude
+ *     and beside the largest value of V in the row's keys (the two kernels hold
+ *     their sums times different powers of two, and smaller ones lose low bits).
+ * Past the second bound an element is off by less than 2^-120 of the largest
+ * value of V beside the usual error.  NaN results are NaN in both.
+ * BI_MODE_VARIANT sizes its chunks from this kernel's resident blocks, so its
+ * plan may differ from bi_attn_decode's. */
 bi_status bi_attn_decode_q8(const void* q, const void* cache, const int32_t* block_table,
                             const int32_t* kv_lens, void* out, float* out_f32, int B, int Hq,
                             int Hkv, int D, int page_size, int64_t num_pages,

@@ -971,13 +971,15 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
 // The same units, arithmetic and outputs over the records of the quantised
 // cache: every e4m3 element stands for the bf16 value that reading the cache
 // back gives, and the sums are those of the bf16 kernel on the pages read
-// back, bit for bit.
+// back, bit for bit (as long as neither kernel's sums leave fp32's normal
+// range: the header states the bounds).
 //
 // What bounds it: half the bytes per tile, but every element has to be
 // unpacked for the MMA, and at the measured HBM rate an SM receives a 64-key
 // tile of D = 128 every ~700 cycles, in which its four schedulers issue
 // ~1,600 instructions at a good rate.  So instructions are what is saved:
-//   * powers of two are moved where they cost least, changing no bit.  K's
+//   * powers of two are moved where they cost least, changing no bit within
+//     those bounds.  K's
 //     elements become fp16 numbers (one conversion a pair) with Q's rows in
 //     fp16 times a power of two each, and the key's scale multiplies the
 //     score.  (A row of Q whose elements do not all survive as fp16, more
@@ -1170,8 +1172,9 @@ __device__ __forceinline__ void q8_scores(float (&s)[4][NQ][4],
 // The factors of P for V's rows of two scale bytes, relative to the largest
 // scale byte `top` so far: 2^(c - top + 110).  V's elements carry 2^-120, so
 // O is held times 2^-(top - 127) - 10; its true scale comes back at the end
-// (q8_unscale).  A row that is not finite has an infinite factor: its
-// elements are 0, and 0 times infinity is NaN.
+// (q8_unscale).  A part of a sum that is below 2^-100 of the largest value may
+// so become subnormal and lose low bits.  A row that is not finite has an
+// infinite factor: its elements are 0, and 0 times infinity is NaN.
 constexpr int kQ8PScale = 110;
 __device__ __forceinline__ uint32_t q8_p_factors(uint32_t c0_c1, int top) {
   const uint32_t c0 = c0_c1 & 0xffu, c1 = c0_c1 >> 8;

@@ -313,3 +313,65 @@ def test_prefill_refuses_a_start_whose_end_passes_32_bits(cuda):
                                  max_q_len=n, max_kv_len=300, split_size=64, sm_scale=D ** -0.5)
         assert bi.bi_check_device_errors() == bi.ERR_DEVICE_BOUNDS, start
         assert same_bytes(out[:n], want[:n]) and (out[n:] == 7.0).all(), start
+
+
+def spread_values(D, Hkv, lens, lo, hi, seed):
+    """A cache whose V rows have magnitudes from 2^lo to 2^hi, row by row in a
+    shuffled order; the upper half of the columns is zero in every row above
+    the middle of that range, so that only small rows reach those columns."""
+    kv = synth.paged_kv(lens, Hkv, D, PAGE, seed)
+    rows = kv.num_pages * PAGE
+    order = torch.randperm(rows, generator=torch.Generator().manual_seed(seed))
+    e = (lo + (hi - lo) * order.double() / (rows - 1)).round().view(-1, 1, PAGE, 1)
+    v = kv.v_cache.double()
+    v = v / v.abs().amax(-1, keepdim=True) * torch.exp2(e)
+    v[..., D // 2:] = torch.where(e > (lo + hi) / 2, 0.0, v[..., D // 2:])
+    kv.v_cache.copy_(v.to(torch.bfloat16))
+    return kv
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (64, 16, 1), (64, 4, 4)])
+def test_values_of_unlike_scales_give_the_bf16_bytes(cuda, D, Hq, Hkv):
+    # scores below 2^3 in magnitude (weights above 2^-8 of the largest) and V
+    # rows 2^72 apart: every part of a sum is above 2^-72 - 8 - 9 (the least
+    # e4m3 number beside the largest of its row) = 2^-89 of the largest value
+    lens = [700, 64, 130]
+    kv = spread_values(D, Hkv, lens, -60, 12, 24900 + D)
+    rec = records(kv, D, cuda)
+    bt, kl = kv.block_table.to(cuda), kv.kv_lens.to(cuda)
+    kb, vb = bi.kv_read_q8(rec, D, bt, kl, max_kv_len=700)
+    q = synth.normal_bf16((3, Hq, D), 24901 + D, std=0.3, device=cuda)
+    for split in (64, 1024):
+        out = bi.attn_decode_q8(q, rec, bt, kl, max_kv_len=700, split_size=split, want_f32=True)
+        ref = bi.attn_decode(q, kb, vb, bt, kl, max_kv_len=700, split_size=split, want_f32=True)
+        assert same_bytes(out[1], ref[1]), first_divergence(out[1], ref[1])
+        assert same_bytes(out[0], ref[0])
+    assert bi.bi_check_device_errors() == bi.OK
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (64, 16, 1)])
+def test_values_over_the_whole_range_of_scales(cuda, D, Hq, Hkv):
+    # from the least scale to the largest: beyond the range of equal bytes, but
+    # off by no more than the weights' error in each column's own values and
+    # 2^-120 of the largest value
+    lens = [700, 64, 130]
+    kv = spread_values(D, Hkv, lens, -115, 15, 25000 + D)
+    rec = records(kv, D, cuda)
+    bt, kl = kv.block_table.to(cuda), kv.kv_lens.to(cuda)
+    kb, vb = bi.kv_read_q8(rec, D, bt, kl, max_kv_len=700)
+    scale = rec[..., 32 * D + PAGE:]
+    assert int(scale.min()) <= 4 and int(scale.max()) == 134
+    q = synth.normal_bf16((3, Hq, D), 25001 + D, std=0.3, device=cuda)
+    keep = [torch.ones(n, dtype=torch.bool) for n in lens]
+    q[..., 0] = 0                                # as the definition takes it
+    want = definition(q, kb, vb, kv.block_table, keep).view(3, Hkv, Hq // Hkv, D)
+    for split in (64, 1024):
+        _, out = bi.attn_decode_q8(q, rec, bt, kl, max_kv_len=700, split_size=split,
+                                   want_f32=True)
+        got = out.cpu().double().view(3, Hkv, Hq // Hkv, D)
+        for b, n in enumerate(lens):
+            page = kv.block_table[b, torch.arange(n) // PAGE].long()
+            v = vb.cpu().double()[page, :, torch.arange(n) % PAGE]          # [n, Hkv, D]
+            bound = 2.0 ** -13 * v.abs().amax(0) + 2.0 ** -120 * v.abs().max()
+            assert ((got[b] - want[b]).abs() <= bound[:, None]).all(), (b, split)
+    assert bi.bi_check_device_errors() == bi.OK
