@@ -458,8 +458,10 @@ bi_status bi_rope_frequencies(int rot_dim, double theta, bi_rope_scaling scaling
  *   interleaved = 1: x0 = x[2i], x1 = x[2i + 1];
  *   y0 = x0 c - x1 s, y1 = x1 c + x0 s in their places.
  * Elements rot_dim .. D-1 and the value heads are copied.  The angle is kept
- * in turns as a 64-bit fraction (an error below 2^-33 turns beside that of
- * freqs at any int32 position, negative ones included); cosine, sine and the
+ * in turns as a 64-bit fraction: beside the error of freqs it is off by less
+ * than |pos| (|freqs[i]| 2^-52 + 2^-62) radians (2^-35 at position 131072 and
+ * 2^-21 at the last int32 position for a frequency of 1; negative positions
+ * alike), and is rounded to fp32 within half a turn of 0.  Cosine, sine and the
  * rotation are fp32, rounded once to bf16.
  * q, k and v must not overlap qkv or one another (BI_ERR_INVALID_ARG).
  * Requirements: D % 16 == 0, D <= 1024, rot_dim even and at most D,

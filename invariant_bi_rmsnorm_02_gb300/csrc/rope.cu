@@ -19,8 +19,10 @@ constexpr int kThreads = 192;
 
 // The fraction of a turn that one position adds, freq / (2 pi) mod 1, in
 // units of 2^-64.  An angle is then a 64-bit product that wraps at whole
-// turns by itself, with an error of pos * 2^-65 turns beside the table's own
-// 53 bits: exact enough at any 32-bit position with no range reduction.
+// turns by itself, with no range reduction.  1 / (2 pi) and the product with
+// it are rounded to 53 bits each and the fraction to 2^-65, so an angle is off
+// by less than pos * (freq * 2^-52 + 2^-62) radians: below half a unit of its
+// rounding to fp32 up to positions of some 2^27, and 2^-21 at the last one.
 __device__ __forceinline__ uint64_t turn_fraction(double freq) {
   double t = freq * 0.15915494309189533576888376337251;  // 1 / (2 pi)
   t -= floor(t);

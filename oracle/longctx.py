@@ -120,8 +120,8 @@ def rope(x, pos, freqs, interleaved, attn_scale):
     n = len(freqs)
     i = np.arange(n)
     a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
-    # whole turns are taken out with exact integer arithmetic, so that far
-    # positions keep every digit of the frequency
+    # whole turns are taken out exactly (fmod); the turns made are fp64, so a far
+    # position is off by 2^-52 of them
     turns = np.array([[math.fmod(float(p) * (f / (2 * math.pi)), 1.0) for f in freqs] for p in pos])
     w = attn_scale * np.exp(2j * math.pi * turns)[:, None, :]
     z = (x[..., a] + 1j * x[..., b]) * w
