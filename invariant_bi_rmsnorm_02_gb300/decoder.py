@@ -87,6 +87,9 @@ class DecoderConfig:
             raise ValueError('kv_cache must be "bf16" or "e4m3"')
         if self.kv_cache == "e4m3" and (self.page_size != 16 or self.head_dim not in (64, 128)):
             raise ValueError("an e4m3 cache needs pages of 16 tokens and heads of 64 or 128")
+        if self.rope_dim is not None and (self.rope_dim % 2 or not 0 < self.rope_dim
+                                          <= self.head_dim):
+            raise ValueError("rope_dim must be an even number of a head's elements")
         # settled only where it is read, so that a configuration without a ramp
         # can be replaced by one with either
         if self.rope_high_turns is None and self.rope_scaling in ("llama3", "yarn"):
@@ -240,7 +243,7 @@ class Decoder:
             self.kv = torch.zeros(c.layers, 2, *pool, dtype=torch.bfloat16, device=device)
         if not c.plain_rope:
             self.rope_freqs, self.rope_attn_scale = bi.rope_frequencies(
-                c.rope_dim or c.head_dim, c.rope_theta, ROPE_SCALINGS[c.rope_scaling],
+                c.head_dim if c.rope_dim is None else c.rope_dim, c.rope_theta, ROPE_SCALINGS[c.rope_scaling],
                 c.rope_factor, c.rope_trained_len, c.rope_low_turns, c.rope_high_turns,
                 device=device)
         self.num_pages = num_pages

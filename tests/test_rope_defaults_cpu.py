@@ -36,3 +36,11 @@ def test_configuration_takes_the_published_ramp(base):
     for kind in ("none", "linear", "ntk"):      # no ramp, nothing to settle
         cfg = dataclasses.replace(base, rope_scaling=kind, rope_factor=8.0)
         assert dataclasses.replace(cfg, rope_scaling="yarn").rope_high_turns == 32.0
+
+
+def test_configuration_refuses_a_width_that_is_no_part_of_a_head():
+    for bad in (0, -2, 7, TINY.head_dim + 2):
+        with pytest.raises(ValueError):
+            dataclasses.replace(TINY, rope_dim=bad)
+    for good in (None, 2, TINY.head_dim):
+        assert dataclasses.replace(TINY, rope_dim=good).rope_dim == good
