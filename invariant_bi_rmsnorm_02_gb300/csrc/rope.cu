@@ -9,13 +9,13 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "bi_internal.h"
 #include "device_common.cuh"
 
 namespace bi {
 namespace {
-
-constexpr int kThreads = 192;
 
 // The fraction of a turn that one position adds, freq / (2 pi) mod 1, in
 // units of 2^-64.  An angle is then a 64-bit product that wraps at whole
@@ -69,17 +69,29 @@ __device__ __forceinline__ int div_by(int n, uint32_t m) {
 // flight through the stores and the next step's table.
 // Bound by memory: 8192 tokens of 32 + 2 * 8 heads of 128 move 201 MB in 35 us
 // (5.7 TB/s, 0.85 of the measured copy rate; 37 us with the loads issued at the
-// head of their own step, three items and 128 threads, 39 with 256 threads, 47 and
-// more with the items staged in shared memory by cp.async).
+// head of their own step and three items, 47 and more with the items staged in
+// shared memory by cp.async).
+// A step takes whole tokens, so what a block's slots (kItems per thread) hold
+// of them goes by the heads and their width; the launch takes the block of 192
+// or 256 threads that they fill better.  8192 tokens, us with 192 and 256
+// threads (and the share of the slots filled):
+//   32 + 2*8 of 128: 35.4, 39.7 (100, 75%)   28 + 2*4 of 128: 31.5, 33.9 (75, 56%)
+//   40 + 2*8 of 128: 45.2, 43.5 (58, 88%)    16 + 2*16 of 256: 65.7, 68.8 (100, 75%)
+//   24 + 2*8 of 80:  24.3, 21.7 (52, 78%)    32 + 2*8 of 80:  27.9, 24.0 (62, 94%)
+// 128 and 384 threads are between the two or behind both in most shapes, and 4%
+// ahead at best (64 + 2 * 8 heads of 128, 128 threads).
+// A width that is no multiple of 16 is bound by its 2-byte loads and the pairs
+// turned twice instead: 24 + 2 * 8 heads of 80, 20 of them rotated, take 45 us
+// (rotate-half) and 37 (interleaved) where 80 rotated take 22.
 constexpr int kItems = 2;  // items in flight per thread
-constexpr int kChunk = kItems * kThreads;
 
 // kAligned: rot_dim % 16 == 0, so that rotated items are whole vectors of
 // either half of the rotated part (rotate-half) or of pairs.  Otherwise the
 // items that hold rotated elements gather their pairs one by one; the head's
 // other items stay vectors.
-template <bool kInterleaved, bool kAligned>
+template <int kThreads, bool kInterleaved, bool kAligned>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+  constexpr int kChunk = kItems * kThreads;
   const int heads = a.Hq + 2 * a.Hkv, half = a.rot / 2;
   extern __shared__ __align__(16) uint8_t smem[];
   float2* table = reinterpret_cast<float2*>(smem);                       // [tokens][rot / 2]
@@ -215,9 +227,17 @@ bi_status launch_rope_qkv_scaled(const void* qkv, const int32_t* pos, int64_t T,
   if (sms <= 0) return BI_ERR_CUDA;
   const int heads = Hq + 2 * Hkv;
   const int per_token = heads * (D / 16), half = rot_dim / 2;
+  // the share of a block's slots that whole tokens fill, out of 2^20
+  auto filled = [&](int threads) {
+    const int64_t slots = kItems * threads;
+    return per_token <= slots ? (slots / per_token * per_token << 20) / slots
+                              : (int64_t(per_token) << 20) /
+                                    ((per_token + slots - 1) / slots * slots);
+  };
+  const int threads = filled(256) > filled(192) ? 256 : 192;
   // enough tokens to give every thread its kItems items, no more than the
   // default 48 KB of shared memory hold, and no fewer blocks than two an SM
-  int tokens = kChunk / per_token;
+  int tokens = kItems * threads / per_token;
   const int room = (49152 - half * 12) / (half * 8);
   if (tokens > room) tokens = room;
   while (tokens > 1 && T / tokens < 2 * sms) --tokens;
@@ -231,9 +251,14 @@ bi_status launch_rope_qkv_scaled(const void* qkv, const int32_t* pos, int64_t T,
   if (blocks > 16 * sms) blocks = 16 * sms;
   const size_t sm = static_cast<size_t>(half) * (8 * tokens + 12);
   const bool aligned = rot_dim % 16 == 0;
-  auto kernel = interleaved ? (aligned ? rope_kernel<true, true> : rope_kernel<true, false>)
-                            : (aligned ? rope_kernel<false, true> : rope_kernel<false, false>);
-  kernel<<<static_cast<unsigned>(blocks), kThreads, sm, s>>>(a);
+  auto form = [&](auto t) {
+    constexpr int n = decltype(t)::value;
+    return interleaved ? (aligned ? rope_kernel<n, true, true> : rope_kernel<n, true, false>)
+                       : (aligned ? rope_kernel<n, false, true> : rope_kernel<n, false, false>);
+  };
+  auto kernel = threads == 256 ? form(std::integral_constant<int, 256>())
+                               : form(std::integral_constant<int, 192>());
+  kernel<<<static_cast<unsigned>(blocks), threads, sm, s>>>(a);
   return cuda_status(cudaGetLastError());
 }
 

@@ -1,13 +1,15 @@
-"""How far off an angle of the scaled rotary positions may be at the last int32
-positions, on the GPU against integer arithmetic of 200 bits."""
+"""Scaled rotary positions on the GPU: how far off an angle may be at the last
+int32 positions, against integer arithmetic of 200 bits, and heads of many
+counts and widths against the fp64 definition."""
 import math
 from decimal import Decimal, localcontext
 
-import numpy as np
 import pytest
 import torch
 
 import invariant_bi_rmsnorm_02_gb300 as bi
+from invariant_bi_rmsnorm_02_gb300 import synth
+from test_gpu_rope_scaled import check
 
 pytestmark = pytest.mark.gpu
 BITS = 200
@@ -53,3 +55,19 @@ def test_angles_of_far_positions_stay_within_their_bound(cuda, f):
         bound = abs(p) * (f * 2.0 ** -52 + 2.0 ** -62) + math.pi * 2.0 ** -24 + \
             2.0 ** -8 * abs(want)
         assert abs(y - want) <= bound, (p, y, want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,rot", [(24, 8, 80, 80), (32, 8, 80, 40), (40, 8, 128, 128),
+                                          (28, 4, 128, 128), (64, 8, 128, 64), (16, 16, 256, 256),
+                                          (1, 1, 16, 16), (7, 1, 128, 6), (100, 7, 112, 112)])
+def test_heads_of_many_counts_and_widths(cuda, Hq, Hkv, D, rot):
+    # blocks of either size, steps of several tokens and tokens of several
+    # chunks, with a last step that is not whole
+    freqs, m = bi.rope_frequencies(rot, 10000.0)
+    for T in (1, 2, 1203):
+        qkv = synth.normal_bf16((T, (Hq + 2 * Hkv) * D), 34000 + T, device=cuda)
+        pos = synth.uniform_int(T, 0, 131072, 34001 + T).to(torch.int32)
+        for inter in (False, True):
+            q, k, v = bi.rope_qkv_scaled(qkv, pos.to(cuda), Hq, Hkv, D, freqs, inter, m)
+            check(q, k, v, qkv, pos.tolist(), Hq, Hkv, D, freqs.cpu().numpy(), inter, m, 131072)
+    assert bi.bi_check_device_errors() == bi.OK
