@@ -206,10 +206,12 @@ bi_status bi_gemm_swiglu(const void* A, const void* W, void* out, int64_t M, int
  *   sequence b is cut at multiples of C into ceil(L_b / C) chunks.  Every
  *   boundary moves with the lengths of the other sequences in the call.
  * A sequence with L == 0 produces zeros, and so does a row whose every score
- *   is -inf.  A NaN score or value makes the rows that attend to it NaN.  (A
- *   prefill chunk takes tiles of 64 keys for up to 128 rows at once: a value
- *   that is not finite up to 190 positions behind a row may make that row NaN
- *   as well.  Decode uses no position behind its row.)
+ *   is -inf.  A NaN score makes its row NaN, and a value of V that is not
+ *   finite the rows that attend to its position, whatever its weight.  (Two
+ *   differences where values are not finite: decode passes over those of a
+ *   split whose scores are all -inf; and a prefill chunk takes tiles of 64 keys
+ *   for up to 128 rows at once, so that one up to 190 positions behind a row
+ *   may make that row NaN as well.)
  * Requirements: D in {64, 128}; Hq % Hkv == 0 and Hq/Hkv <= 16;
  *   page_size == 16; split_size a positive multiple of 64; num_pages >= 1;
  *   max_blocks_per_seq >= 1.

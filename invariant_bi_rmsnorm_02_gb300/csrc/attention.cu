@@ -45,6 +45,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math_constants.h>
 
 #include <algorithm>
@@ -415,7 +416,9 @@ struct KernelParams {
   float* ml;         // decode partials: {m, l} per (b, q-head, split)
   float* o;          // decode partials: o[D] per (b, q-head, split)
   int* err;
-  int B, Hq, Hkv, G, max_blocks, max_kv_len, split_size, split_count, max_splits;
+  int B, Hq, Hkv, G, max_blocks;
+  int max_kv_len;    // the call's bound on a length, the table's if that is less
+  int split_size, split_count, max_splits;
   int ml_stride;     // decode partials: {m, l} pairs per (b, q-head) row, even
   int local_plan;    // decode: the split kernel works out its units itself
   int2* order;       // decode, in-kernel plan: {sequence, split count}, most splits first
@@ -426,8 +429,7 @@ struct KernelParams {
 };
 
 __device__ __forceinline__ bool len_ok(int L, const KernelParams& p) {
-  // max_kv_len is at most 2^30, so the sum fits; max_blocks * kPage need not
-  return L >= 0 && L <= p.max_kv_len && (L + kPage - 1) / kPage <= p.max_blocks;
+  return L >= 0 && L <= p.max_kv_len;
 }
 
 // --------------------------------------------------------------- decode plan
@@ -2380,7 +2382,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
           live = __all_sync(kFull, mbar_wait(&folded[j & 1], ((j - 2) >> 1) & 1, p.err,
                                            &s_abort));
         if (!live) break;
-        xsplit[(j & 1) * 2 * kPfRows + r] = m;
+        // An empty split's reference, -inf, goes as the least finite number:
+        // its l and o are 0, so that its coefficient, 0 beside any counting
+        // split and 1 beside an empty one, changes nothing.  (Skipping it in
+        // the fold as the decode's merge does took 427 us in place of 419 for
+        // a 2048-token chunk of 8192: a few more instructions in that loop.)
+        xsplit[(j & 1) * 2 * kPfRows + r] = fmaxf(m, -FLT_MAX);
         xsplit[(j & 1) * 2 * kPfRows + kPfRows + r] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sdone[j & 1]);
@@ -2389,9 +2396,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
   } else {
     // ================================================================ fold
     // Split j's accumulator (m_s, l_s, o_s) into the merged state, in split
-    // order: the decode merge's left fold, one row per thread, which passes
-    // over an empty split (split_counts).  The accumulator is released
-    // (ofree) as soon as its last columns are read.
+    // order: the decode merge's left fold, one row per thread.  The
+    // accumulator is released (ofree) as soon as its last columns are read.
     const int r = (warp - kPfFoldWarp0) * 32 + lane;
     const int tk = r / G;
     const int pos = (r < TPB * G && tk < ntok) ? start + tok0 + tk : -1;
@@ -2406,8 +2412,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
       tc_fence_after();
       const float m_s = xsplit[(j & 1) * 2 * kPfRows + r];
       const float l_s = xsplit[(j & 1) * 2 * kPfRows + kPfRows + r];
-      // the split holds keys this row sees, and one of them counts
-      const bool part = pos >= j * S && split_counts(m_s, l_s);
+      const bool part = pos >= j * S;  // the split holds keys this row sees
       float mn = 0.0f, ca = 0.0f, cb = 0.0f;
       if (part && have) lse_coeffs(mg_m, m_s, mn, ca, cb);
       const bool any = __any_sync(kFull, part);
@@ -2452,8 +2457,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
       if (lane == 0) mbar_arrive(&folded[j & 1]);
     }
     // the row's 1/l for the output below (the split m, l slots are free now);
-    // -1 for a row that no key counts for, whose output is zero as in decode
-    if (live && pos >= 0) xsplit[r] = mg_l != 0.0f ? inv_l(mg_l) : -1.0f;
+    // a row that no key counts for is zero, as in decode
+    if (live && pos >= 0) xsplit[r] = mg_l != 0.0f ? inv_l(mg_l) : 0.0f;
   }
   tc_fence_before();
   __syncthreads();
@@ -2471,12 +2476,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_kernel(
     const int c4 = 4 * (u / (kPfRows / 8)) + (lane & 3);
     const int tk = r / oG;
     if (r >= (kPfRows / oG) * oG || tk >= otok) continue;
-    float rl = xsplit[r];
-    float4 a = omg[c4 * kPfRows + r];
-    if (rl < 0.0f) {  // never written
-      a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      rl = 0.0f;
-    }
+    const float rl = xsplit[r];
+    const float4 a = omg[c4 * kPfRows + r];
     const float o0 = normalize(a.x, rl), o1 = normalize(a.y, rl);
     const float o2 = normalize(a.z, rl), o3 = normalize(a.w, rl);
     const int64_t idx = (row0 + (int64_t)tk * p.Hq + r % oG) * D + 4 * c4;
@@ -2532,7 +2533,8 @@ KernelParams make_params(const AttnArgs& a) {
   p.Hkv = a.Hkv;
   p.G = a.Hq / a.Hkv;
   p.max_blocks = a.max_blocks;
-  p.max_kv_len = a.max_kv_len;
+  p.max_kv_len = static_cast<int>(
+      std::min<int64_t>(a.max_kv_len, static_cast<int64_t>(a.max_blocks) * kPage));
   p.split_size = a.split_size;
   p.split_count = a.split_count;
   p.max_splits = a.max_splits;

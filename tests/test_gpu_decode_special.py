@@ -375,3 +375,24 @@ def test_values_over_the_whole_range_of_scales(cuda, D, Hq, Hkv):
             bound = 2.0 ** -13 * v.abs().amax(0) + 2.0 ** -120 * v.abs().max()
             assert ((got[b] - want[b]).abs() <= bound[:, None]).all(), (b, split)
     assert bi.bi_check_device_errors() == bi.OK
+
+
+def test_rows_without_a_reachable_key_are_plus_zero(cuda):
+    # every value negative: weights of 0 must not leave -0, one split or many
+    for D, Hq, Hkv in ((64, 4, 2), (128, 32, 8), (128, 16, 1)):
+        lens = [1, 64, 130, 700]
+        kv, q, _ = masked_case(lens, [range(11)] * 4, Hq, Hkv, D, 64, 25100 + Hq)
+        kv.v_cache.copy_(-kv.v_cache.abs())
+        rec = records(kv, D, cuda)
+        kc, vc, bt, kl, qc = (t.to(cuda) for t in (kv.k_cache, kv.v_cache, kv.block_table,
+                                                   kv.kv_lens, q))
+        for split in (64, 128, 704):
+            args = dict(max_kv_len=704, split_size=split, want_f32=True)
+            outs = [bi.attn_decode(qc, kc, vc, bt, kl, **args),
+                    bi.attn_decode_q8(qc, rec, bt, kl, **args),
+                    bi.attn_prefill_chunk(qc, i32(range(5), cuda), kl - 1, kc, vc, bt, kl,
+                                          max_q_len=1, **args)]
+            for out, out32 in outs:
+                assert same_bytes(out, torch.zeros_like(out)), (D, split)
+                assert same_bytes(out32, torch.zeros_like(out32)), (D, split)
+    assert bi.bi_check_device_errors() == bi.OK
