@@ -998,6 +998,11 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
 template <int D, int NQ>
 struct Q8Geom {
   // As many warps as the registers allow, a multiple of the four schedulers.
+  // Above 8 heads a group that is too few to hide a tile's chain: 160 sequences
+  // of 16 heads on one (52 MB, 26-29 us cold) keep 1.4 warps a scheduler, issue
+  // in 22-24% of the cycles and wait 5.7 cycles an instruction (1.5 of fixed
+  // latencies, 1.4 for instructions, 0.9 for memory), so the time is one
+  // unit's four tiles of 1,950 warp instructions each.
   static constexpr int kWarps = NQ == 1 ? (D == 64 ? 16 : 12) : (D == 64 ? 12 : 8);
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRecord = kv_q8_record_bytes(D);
@@ -1681,7 +1686,10 @@ __global__ void __launch_bounds__(Q8Geom<D, NQ>::kThreads, 1) attn_decode_q8_spl
 // shared memory by cp.async, kStages steps of kStep splits ahead.
 // A row of a sequence with a single split was written by the split kernel and
 // is skipped here.
-// Bound by latency: a row's chain (its length, {m, l}, then the fold).  With
+// Bound by latency: a row's chain (its length, {m, l}, then the fold), where a
+// lone warp issues one instruction in 3.2 cycles: 512 splits of one sequence
+// are 7,200 instructions a warp, 15 us, of which the fold's own dependent sums
+// are about 2.  With
 // many rows a warp takes a whole row, so that the coefficients and l cost one
 // warp's instructions; with few, a row's columns are spread over D / 32 warps
 // and more splits are on their way.
