@@ -375,9 +375,8 @@ bi_status bi_kv_read_q8(const void* cache, const int32_t* block_table, const int
  * result in BI_MODE_INVARIANT has exactly the bytes of bi_attn_decode on the
  * pages that bi_kv_read_q8 gives, and so those of bi_attn_prefill_chunk on
  * them at every position, wherever
- *   - no element of q is 2^64 or more in magnitude and no |q . k| 2^127 or more
- *     (further up, bi_attn_decode's unscaled sum becomes infinite where this
- *     one need not);
+ *   - no element of q is 2^64 or more in magnitude (bi_attn_decode's unscaled
+ *     sums q . k become infinite from 2^128 on, where these need not);
  *   - every part of an output element, the sum over its row's first keys or one
  *     key's weight times its value, is zero or above 2^-100 both in magnitude
  *     and beside the largest value of V in the row's keys (the two kernels hold
