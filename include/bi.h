@@ -375,12 +375,14 @@ bi_status bi_kv_read_q8(const void* cache, const int32_t* block_table, const int
  * result in BI_MODE_INVARIANT has exactly the bytes of bi_attn_decode on the
  * pages that bi_kv_read_q8 gives, and so those of bi_attn_prefill_chunk on
  * them at every position, wherever
- *   - no element of q is 2^64 or more in magnitude (bi_attn_decode's unscaled
- *     sums q . k become infinite from 2^128 on, where these need not);
- *   - every part of an output element, the sum over its row's first keys or one
- *     key's weight times its value, is zero or above 2^-100 both in magnitude
- *     and beside the largest value of V in the row's keys (the two kernels hold
- *     their sums times different powers of two, and smaller ones lose low bits).
+ *   - the elements of q and the stored values are zero or at least 2^-126 in
+ *     magnitude (an MMA aligns subnormal numbers apart), and no element of q is
+ *     2^64 or more (bi_attn_decode's unscaled sums q . k become infinite from
+ *     2^128 on, where these need not);
+ *   - every partial sum of an output element, over its row's first keys, is zero
+ *     or above 2^-100 both in magnitude and beside the largest value of V in the
+ *     row's keys (the two kernels hold their sums times different powers of two,
+ *     and smaller ones lose low bits).
  * Past the second bound an element is off by less than 2^-120 of the largest
  * value of V beside the usual error.  NaN results are NaN in both.
  * BI_MODE_VARIANT sizes its chunks from this kernel's resident blocks, so its

@@ -984,9 +984,9 @@ __global__ void __maxnreg__(NQ == 1 ? 192 : 255) attn_decode_split_kernel(
 //     those bounds.  K's
 //     elements become fp16 numbers (one conversion a pair) with Q's rows in
 //     fp16 times a power of two each, and the key's scale multiplies the
-//     score.  (A row of Q whose elements do not all survive as fp16, more
-//     than 2^32 apart or not finite, takes the bf16 form of the same sums.)
-//     V's elements become bf16 bits times 2^-120 (three instructions a pair)
+//     score.  (A row of Q whose elements are not all normal fp16 numbers, more
+//     than 2^29 apart or not finite, takes the bf16 form of the same sums.)
+//     V's elements become bf16 bits times 2^-117 (four instructions a pair)
 //     and the key's scale, relative to the largest of the tiles so far,
 //     multiplies P's two parts instead;
 //   * every warp is on its own: it works units out, has a unit's tiles copied
@@ -1049,9 +1049,10 @@ __device__ __forceinline__ uint32_t q8_off(int n, int c) {
 // the same places of the MMA's k (its sum over a k-step does not depend on the
 // order inside it; the tests compare the bytes with the bf16 kernel).  Rows
 // G .. 8 NQ - 1 are zero.  Returns whether the fragments are fp16: each row
-// times 2^k with its largest element in [2^15, 2^16), exact for elements down
-// to 2^-32 of it; otherwise bf16 times 2^32 (1 from 2^64 on), for K's elements
-// times 2^-120.
+// times 2^k with its largest element in [2^15, 2^16), exact and normal for
+// elements down to 2^-29 of it; otherwise bf16 times 2^32 (1 from 2^64 on), for
+// K's elements times 2^-117.  (A subnormal fp16 element would be exact down to
+// 2^-32, but see e4m3_even_mma.)
 template <int D, int NQ>
 __device__ __forceinline__ bool q8_load_q(uint32_t (&qf)[NQ][D / 16][2], float (&sc)[NQ][2],
                                           const __nv_bfloat16* q, int G, float scale_log2) {
@@ -1089,16 +1090,17 @@ __device__ __forceinline__ bool q8_load_q(uint32_t (&qf)[NQ][D / 16][2], float (
     grow[nq] = __uint_as_float((uint32_t)up << 23);
     shrink[nq] = __uint_as_float((uint32_t)(254 - up) << 23);
     raise[nq] = et < 127 + 64 ? 32 : 0;
-    // every element a finite one at most 2^32 below the largest (its 8 bits
-    // then end at 2^-24 or above)
-    exact = exact && et < 255 && (int)low + 1 >= (et - 32) * 128;
+    // every element a finite one at most 2^29 below the largest (then it is
+    // a normal fp16 number)
+    exact = exact && et < 255 && (int)low + 1 >= (et - 29) * 128;
   }
   exact = __all_sync(kFull, exact);
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) {
     // what takes the powers of two off a score; column 8 nq + 2t + cc is the
     // row that lanes 4 (2t + cc) .. + 3 hold
-    const float off = exact ? shrink[nq] : __uint_as_float((uint32_t)(247 - raise[nq]) << 23);
+    const float off = exact ? shrink[nq]
+                            : __uint_as_float((uint32_t)(127 + kE4m3MmaShift - raise[nq]) << 23);
     sc[nq][0] = __fmul_rn(scale_log2, __shfl_sync(kFull, off, 8 * t));
     sc[nq][1] = __fmul_rn(scale_log2, __shfl_sync(kFull, off, 8 * t + 4));
     const uint32_t up2 = (uint32_t)(127 + raise[nq]) * 0x00800080u;
@@ -1148,7 +1150,8 @@ __device__ __forceinline__ void q8_scores(float (&s)[4][NQ][4],
           for (int nq = 0; nq < NQ; ++nq)
             mma_f16_free(s[mt][nq], a, qf[nq][2 * kp + u][0], qf[nq][2 * kp + u][1]);
         } else {
-          const uint32_t a[4] = {e4m3_even(x0), e4m3_even(x1), e4m3_odd(x0), e4m3_odd(x1)};
+          const uint32_t a[4] = {e4m3_even_mma(x0), e4m3_even_mma(x1), e4m3_odd_mma(x0),
+                                 e4m3_odd_mma(x1)};
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq)
             mma_bf16_free(s[mt][nq], a, qf[nq][2 * kp + u][0], qf[nq][2 * kp + u][1]);
@@ -1177,12 +1180,12 @@ __device__ __forceinline__ void q8_scores(float (&s)[4][NQ][4],
 }
 
 // The factors of P for V's rows of two scale bytes, relative to the largest
-// scale byte `top` so far: 2^(c - top + 110).  V's elements carry 2^-120, so
+// scale byte `top` so far: 2^(c - top + 107).  V's elements carry 2^-117, so
 // O is held times 2^-(top - 127) - 10; its true scale comes back at the end
 // (q8_unscale).  A part of a sum that is below 2^-100 of the largest value may
 // so become subnormal and lose low bits.  A row that is not finite has an
 // infinite factor: its elements are 0, and 0 times infinity is NaN.
-constexpr int kQ8PScale = 110;
+constexpr int kQ8PScale = 107;
 __device__ __forceinline__ uint32_t q8_p_factors(uint32_t c0_c1, int top) {
   const uint32_t c0 = c0_c1 & 0xffu, c1 = c0_c1 >> 8;
   uint32_t f = (__byte_perm(c0_c1, 0, 0x4140) << 7) + (uint32_t)(127 + kQ8PScale - top) * 0x00800080u;
@@ -1193,7 +1196,7 @@ __device__ __forceinline__ uint32_t q8_p_factors(uint32_t c0_c1, int top) {
   return f;
 }
 __device__ __forceinline__ float q8_unscale(int top) {
-  return __uint_as_float((uint32_t)(top - 127 + 120 - kQ8PScale + 127) << 23);
+  return __uint_as_float((uint32_t)(top - 127 + kE4m3MmaShift - kQ8PScale + 127) << 23);
 }
 
 // The softmax of tile_step on those scores: probabilities into s, the running
@@ -1306,10 +1309,10 @@ __device__ __forceinline__ void q8_values(SplitState<D, NQ>& st, const float (&s
       uint32_t a[2][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        a[u][0] = e4m3_even(r[2 * u]);
-        a[u][1] = e4m3_odd(r[2 * u]);
-        a[u][2] = e4m3_even(r[2 * u + 1]);
-        a[u][3] = e4m3_odd(r[2 * u + 1]);
+        a[u][0] = e4m3_even_mma(r[2 * u]);
+        a[u][1] = e4m3_odd_mma(r[2 * u]);
+        a[u][2] = e4m3_even_mma(r[2 * u + 1]);
+        a[u][3] = e4m3_odd_mma(r[2 * u + 1]);
       }
       // P's high part before its low one for every sum; the sums of other
       // chunks and n-tiles are independent

@@ -59,5 +59,16 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// e4m3_even and e4m3_odd times 2^3, so that an e4m3 subnormal is a normal bf16
+// number too: an MMA aligns a product by its operands' exponent fields, and a
+// subnormal operand, aligned above its own magnitude, can cost the sum its last
+// bit (one fp32 element in some 10^8 came out a unit off without the product).
+constexpr int kE4m3MmaShift = 117;  // the value times 2^-117
+__device__ __forceinline__ uint32_t e4m3_even_mma(uint32_t x) {
+  return mul_bf16x2(e4m3_even(x), 0x41004100u);
+}
+__device__ __forceinline__ uint32_t e4m3_odd_mma(uint32_t x) {
+  return mul_bf16x2(e4m3_odd(x), 0x41004100u);
+}
 
 }  // namespace bi

@@ -396,3 +396,47 @@ def test_rows_without_a_reachable_key_are_plus_zero(cuda):
                 assert same_bytes(out, torch.zeros_like(out)), (D, split)
                 assert same_bytes(out32, torch.zeros_like(out32)), (D, split)
     assert bi.bi_check_device_errors() == bi.OK
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (16, 1, 128), (4, 2, 64), (64, 4, 64)])
+@pytest.mark.parametrize("what", ["values", "keys", "queries"])
+def test_small_elements_give_the_bf16_bytes(cuda, what, Hq, Hkv, D):
+    # elements that the stored or converted types hold as subnormal numbers:
+    # their products must be aligned as the bf16 kernel's are.  Columns of V,
+    # or of K under queries too wide for fp16, that are e4m3 subnormals in every
+    # row; queries whose elements are 2^29 to 2^32 below their largest
+    g = torch.Generator().manual_seed(25200 + D)
+    lens = torch.cat([torch.arange(48), torch.randint(48, 700, (80,), generator=g)]).tolist()
+    kv = synth.paged_kv(lens, Hkv, D, PAGE, 25201 + Hq)
+    q = synth.normal_bf16((len(lens), Hq, D), 25202 + Hq)
+    small = torch.arange(D) >= D // 2
+    if what == "values":
+        kv.v_cache[..., small] *= 2.0 ** -15
+    else:
+        # the scores come from the small elements; one large element of q in
+        # each row meets a zero in every key
+        kv.k_cache[..., 1] = 0
+        if what == "keys":
+            kv.k_cache[..., small] *= 2.0 ** -15
+            q[..., ~small] *= 2.0 ** -20
+            q[..., 1] = 2.0 ** 30
+            q[..., small] *= 2.0 ** 9
+        else:
+            q = ((2 + 14 * torch.rand(q.shape, generator=g)) * q.float().sign()).bfloat16()
+            q[..., 1] = 2.0 ** 33
+    rec = records(kv, D, cuda)
+    if what != "queries":
+        rows, _ = longctx.record_views(rec.cpu().numpy(), D)
+        kind = 1 if what == "values" else 0
+        codes = rows[:, :, kind, :, D // 2:] & 0x7f
+        assert (codes < 8).mean() > 0.9 and (codes > 0).mean() > 0.5
+    bt, kl, qc = kv.block_table.to(cuda), kv.kv_lens.to(cuda), q.to(cuda)
+    kb, vb = bi.kv_read_q8(rec, D, bt, kl, max_kv_len=700)
+    for split in (64, 1024):
+        args = dict(max_kv_len=700, split_size=split, want_f32=True)
+        out = bi.attn_decode_q8(qc, rec, bt, kl, **args)
+        ref = bi.attn_decode(qc, kb, vb, bt, kl, **args)
+        assert torch.isfinite(ref[1]).all()
+        assert same_bytes(out[1], ref[1]), int((out[1] != ref[1]).sum())
+        assert same_bytes(out[0], ref[0])
+    assert bi.bi_check_device_errors() == bi.OK
