@@ -999,10 +999,10 @@ template <int D, int NQ>
 struct Q8Geom {
   // As many warps as the registers allow, a multiple of the four schedulers.
   // Above 8 heads a group that is too few to hide a tile's chain: 160 sequences
-  // of 16 heads on one (52 MB, 26-29 us cold) keep 1.4 warps a scheduler, issue
-  // in 22-24% of the cycles and wait 5.7 cycles an instruction (1.5 of fixed
-  // latencies, 1.4 for instructions, 0.9 for memory), so the time is one
-  // unit's four tiles of 1,950 warp instructions each.
+  // of 16 heads on one (52 MB, 32 us cold) keep 1.4 warps a scheduler, issue in
+  // 21% of the cycles and wait 6.5 cycles an instruction (2.5 for instructions,
+  // 1.5 of fixed latencies, 0.9 for memory), so the time is one unit's four
+  // tiles of 2,080 warp instructions each.
   static constexpr int kWarps = NQ == 1 ? (D == 64 ? 16 : 12) : (D == 64 ? 12 : 8);
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRecord = kv_q8_record_bytes(D);
