@@ -105,6 +105,42 @@ bi_status bi_add_rmsnorm(const void* x, void* residual, const void* w, void* y, 
 size_t bi_rmsnorm_workspace_size(int64_t M, int64_t H, bi_mode mode);
 
 /* ------------------------------------------------------------------------ */
+/* Rows held as e4m3                                                        */
+/* ------------------------------------------------------------------------ */
+/* The pages define no 8-bit activations; these calls and bi_gemm_q8 are the
+ * library's addition.  A row v of n values is held as n e4m3 numbers y and one
+ * fp32 scale:
+ *   t = max(max_j |v[j]|, 448 * 2^-126),  scale = t / 448,
+ *   y[j] = e4m3(448 v[j] / t), rounded to nearest even,
+ * so that y[j] * scale stands for v[j] (off by at most 2^-4 of its magnitude or
+ * 2^-10 of the scale, whichever is larger) and the row's largest magnitude is
+ * stored as 448.  The scale and the quotient are fp32, each rounded once.  A
+ * row with an infinity or a NaN is stored as zeros under the scale NaN and
+ * stands for NaN throughout.
+ * Every row depends on its own values only.
+ * Common requirements: y [M,H] bytes and 16-byte aligned, y_scale [M] 4-byte
+ *   aligned; H % 16 == 0, 16 <= H <= 65536, 0 <= M < 2^31 (0 is a no-op).
+ *   Outputs overlap neither the inputs nor one another (BI_ERR_INVALID_ARG),
+ *   but for h below.  Errors: as bi_rmsnorm. */
+
+/* RMSNorm with that output: v is exactly bi_rmsnorm's y_f32 in
+ * BI_MODE_INVARIANT (x [M,H], w [H] bf16). */
+bi_status bi_rmsnorm_q8(const void* x, const void* w, void* y, float* y_scale, int64_t M,
+                        int64_t H, float eps, void* stream);
+
+/* The same after the residual's addition: h = bf16(x + residual) (an fp32 add,
+ * rounded once) is written to h [M,H], v = RMSNorm(h) * w.  h may be residual
+ * (the stream updated in place, as bi_add_rmsnorm does) or x, or overlap
+ * neither. */
+bi_status bi_add_rmsnorm_q8(const void* x, const void* residual, const void* w, void* h, void* y,
+                            float* y_scale, int64_t M, int64_t H, float eps, void* stream);
+
+/* The rows of x [M,K] bf16 (H above is K): a weight once, or activations that
+ * no norm precedes. */
+bi_status bi_quantize_q8(const void* x, void* y, float* y_scale, int64_t M, int64_t K,
+                         void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* GEMM  (P1 §3.3, §5.4; P3 "Where the reductions are")                     */
 /* ------------------------------------------------------------------------ */
 /* C[i,n] = sum_k A[i,k] * W[n,k]
@@ -168,6 +204,58 @@ int bi_gemm_variant_splits(int64_t M, int64_t N, int64_t K, int num_sms);
 bi_status bi_gemm_swiglu(const void* A, const void* W, void* out, int64_t M, int64_t F,
                          int64_t K, bi_mode mode, int variant_splits, void* workspace,
                          size_t workspace_bytes, void* stream);
+
+/* GEMM with bias, activation and residual in its epilogue (P1 §5.4:
+ * element-wise work is batch-invariant by nature).
+ *   z = (A W^T)[i,n] + bias[n];  C[i,j] = bf16( act(z) + residual[i,j] )
+ *   A [M,K] bf16, W [N,K] bf16; bias [N] bf16 or NULL; residual of C's shape,
+ *   bf16, or NULL; C [M,N] bf16 ([M,N/2] with BI_ACT_SWIGLU).
+ * act, in fp32:
+ *   BI_ACT_NONE       z
+ *   BI_ACT_RELU       max(z, 0) (a NaN stays one)
+ *   BI_ACT_GELU       z/2 (1 + erf(z / sqrt(2)))
+ *   BI_ACT_GELU_TANH  z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
+ *   BI_ACT_SILU       z / (1 + exp(-z))
+ *   BI_ACT_SWIGLU     silu(g) u with column j's pair g = z[i, 32 (j/16) + j%16]
+ *                     and u = z[i, 32 (j/16) + 16 + j%16]: W's rows (and the
+ *                     bias) come in blocks of 16 gate rows and then the 16 up
+ *                     rows of the same features (bi_gemm_swiglu's are of 128)
+ * Sums are fp32, one rounding to bf16 at the end (neither z nor g and u are
+ * rounded before).  With BI_ACT_NONE, no bias and no residual C has exactly
+ * the bytes of bi_gemm in BI_MODE_INVARIANT; every row of C depends only on
+ * its rows of A and residual, on W and on bias, whatever M (there is no
+ * batch-variant mode).  Needs no workspace.
+ * residual may be C (the residual stream updated in place); otherwise C
+ *   overlaps no input (BI_ERR_INVALID_ARG).
+ * Requirements: M >= 0, N, K >= 1, N % 8 == 0 (32 with BI_ACT_SWIGLU),
+ *   K % 8 == 0, all below 2^31 - 256 and K below half that; pointers 16-byte
+ *   aligned.  Errors: as bi_gemm. */
+typedef enum bi_activation {
+  BI_ACT_NONE = 0,
+  BI_ACT_RELU = 1,
+  BI_ACT_GELU = 2,
+  BI_ACT_GELU_TANH = 3,
+  BI_ACT_SILU = 4,
+  BI_ACT_SWIGLU = 5
+} bi_activation;
+bi_status bi_gemm_epilogue(const void* A, const void* W, const void* bias, const void* residual,
+                           void* C, int64_t M, int64_t N, int64_t K, bi_activation act,
+                           void* stream);
+
+/* The same on rows held as e4m3 (bi_rmsnorm_q8, bi_quantize_q8):
+ *   z = (sum_k A[i,k] W[n,k]) * a_scale[i] * w_scale[n] + bias[n],
+ *   A [M,K], W [N,K] e4m3 bytes, a_scale [M], w_scale [N] fp32; the rest as
+ *   bi_gemm_epilogue.  The two products are fp32, in this order, each rounded
+ *   once (so scales whose product with the sum leaves fp32's normal range lose
+ *   digits or overflow).  A row whose scale is NaN makes its row (A) or
+ *   column (W) of C NaN, as do the bytes 0x7f and 0xff, which are NaN.
+ * One instruction family (tcgen05.mma kind::f8f6f4, M=128, K=32) and one K
+ *   order for every shape: rows do not depend on M here either.
+ * Requirements: as bi_gemm_epilogue but K % 16 == 0 and K below 2^31 - 256;
+ *   a_scale 4-byte aligned. */
+bi_status bi_gemm_q8(const void* A, const float* a_scale, const void* W, const float* w_scale,
+                     const void* bias, const void* residual, void* C, int64_t M, int64_t N,
+                     int64_t K, bi_activation act, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Attention over a paged KV cache  (P1 §5.5; P3 "The attention detail that */

@@ -22,6 +22,8 @@ LIB_PATH = os.path.join(_HERE, "libbi.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_BOUNDS, ERR_TIMEOUT = range(7)
 INVARIANT, VARIANT = 0, 1
+(ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU,
+ ACT_SWIGLU) = range(6)                                               # bi_activation
 ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_LLAMA3, ROPE_YARN = range(5)   # bi_rope_scaling
 NOALLOC_SCRATCH_BYTES = 32 << 20   # BI_NOALLOC_SCRATCH_BYTES in include/bi.h
 
@@ -36,6 +38,9 @@ __all__ = [
     "bi_sample", "bi_gather_rows", "bi_rope_qkv", "bi_silu_mul", "bi_gemm_swiglu",
     "bi_kv_write_q8", "bi_kv_read_q8", "bi_attn_decode_q8", "bi_rope_frequencies",
     "bi_rope_qkv_scaled", "ROPE_NONE", "ROPE_LINEAR", "ROPE_NTK", "ROPE_LLAMA3", "ROPE_YARN",
+    "bi_rmsnorm_q8", "bi_add_rmsnorm_q8", "bi_quantize_q8", "bi_gemm_epilogue", "bi_gemm_q8",
+    "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "ACT_SWIGLU",
+    "rmsnorm_q8", "add_rmsnorm_q8", "quantize_q8", "gemm_epilogue", "gemm_q8",
     "kv_q8_record_bytes", "kv_cache_q8", "kv_write_q8", "kv_read_q8", "attn_decode_q8",
     "rope_frequencies", "rope_high_turns", "rope_qkv_scaled",
     "NOALLOC_SCRATCH_BYTES", "rmsnorm", "add_rmsnorm", "gemm", "gemm_swiglu",
@@ -51,7 +56,8 @@ EXPORTED_SYMBOLS = (
     "bi_version", "bi_attn_decode_noalloc", "bi_selftest_wait_timeout", "bi_add_rmsnorm",
     "bi_sample", "bi_gather_rows", "bi_rope_qkv", "bi_silu_mul", "bi_gemm_swiglu",
     "bi_kv_write_q8", "bi_kv_read_q8", "bi_attn_decode_q8", "bi_rope_frequencies",
-    "bi_rope_qkv_scaled",
+    "bi_rope_qkv_scaled", "bi_rmsnorm_q8", "bi_add_rmsnorm_q8", "bi_quantize_q8",
+    "bi_gemm_epilogue", "bi_gemm_q8",
 )
 
 
@@ -127,6 +133,12 @@ def load(build_if_missing: bool = True):
                                            ctypes.POINTER(ctypes.c_float)]),
             "bi_rope_qkv_scaled": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _f32,
                                           _vp, _vp, _vp, _vp]),
+            "bi_rmsnorm_q8": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _f32, _vp]),
+            "bi_add_rmsnorm_q8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _vp]),
+            "bi_quantize_q8": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp]),
+            "bi_gemm_epilogue": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp]),
+            "bi_gemm_q8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32,
+                                  _vp]),
             "bi_check_device_errors": (_i32, [_vp]),
             "bi_selftest_wait_timeout": (_i32, [ctypes.c_uint32, _vp]),
             "bi_status_string": (ctypes.c_char_p, [_i32]),
@@ -481,6 +493,85 @@ def bi_silu_mul(gate_up, out, block=None, stream=None):
                               _ptr(out, torch.bfloat16, "out"), _stream(stream)), "bi_silu_mul")
 
 
+def bi_rmsnorm_q8(x, w, y, y_scale, eps, stream=None):
+    """y, y_scale <- RMSNorm(x) * w as e4m3 rows with a scale each (include/bi.h)."""
+    shape = x.shape
+    M, H = shape
+    if y.shape != shape or w.shape != (H,) or y_scale.shape != (M,):
+        raise ValueError("y must have x's shape, w [H] and y_scale [M]")
+    dev = torch.cuda.current_device()
+    _check(load().bi_rmsnorm_q8(
+        _dptr(x, torch.bfloat16, dev, "x"), _dptr(w, torch.bfloat16, dev, "w"),
+        _dptr(y, torch.float8_e4m3fn, dev, "y"), _dptr(y_scale, torch.float32, dev, "y_scale"),
+        M, H, float(eps), _stream(stream)), "bi_rmsnorm_q8")
+
+
+def bi_add_rmsnorm_q8(x, residual, w, h, y, y_scale, eps, stream=None):
+    """h <- bf16(x + residual) (h may be residual or x); y, y_scale <-
+    RMSNorm(h) * w as e4m3 rows with a scale each (include/bi.h)."""
+    shape = x.shape
+    M, H = shape
+    if residual.shape != shape or h.shape != shape or y.shape != shape or w.shape != (H,) \
+            or y_scale.shape != (M,):
+        raise ValueError("residual, h and y must have x's shape, w [H] and y_scale [M]")
+    dev = torch.cuda.current_device()
+    _check(load().bi_add_rmsnorm_q8(
+        _dptr(x, torch.bfloat16, dev, "x"), _dptr(residual, torch.bfloat16, dev, "residual"),
+        _dptr(w, torch.bfloat16, dev, "w"), _dptr(h, torch.bfloat16, dev, "h"),
+        _dptr(y, torch.float8_e4m3fn, dev, "y"), _dptr(y_scale, torch.float32, dev, "y_scale"),
+        M, H, float(eps), _stream(stream)), "bi_add_rmsnorm_q8")
+
+
+def bi_quantize_q8(x, y, y_scale, stream=None):
+    """y, y_scale <- the rows of x as e4m3 with a scale each (include/bi.h)."""
+    shape = x.shape
+    M, K = shape
+    if y.shape != shape or y_scale.shape != (M,):
+        raise ValueError("y must have x's shape and y_scale [M]")
+    dev = torch.cuda.current_device()
+    _check(load().bi_quantize_q8(
+        _dptr(x, torch.bfloat16, dev, "x"), _dptr(y, torch.float8_e4m3fn, dev, "y"),
+        _dptr(y_scale, torch.float32, dev, "y_scale"), M, K, _stream(stream)), "bi_quantize_q8")
+
+
+def _fused_shapes(A, W, C, bias, residual, activation):
+    """(M, N, K) of a GEMM with an epilogue, once the tensors' shapes agree."""
+    M, K = A.shape
+    N, K2 = W.shape
+    out = (M, N // 2 if activation == ACT_SWIGLU else N)
+    if K2 != K or C.shape != out or (bias is not None and bias.shape != (N,)) \
+            or (residual is not None and residual.shape != out):
+        raise ValueError("W must be [N, K], bias [N], C and residual [M, N] ([M, N/2] for SwiGLU)")
+    return M, N, K
+
+
+def bi_gemm_epilogue(A, W, C, bias=None, residual=None, activation=ACT_NONE, stream=None):
+    """C <- act(A W^T + bias) + residual (include/bi.h); residual may be C."""
+    M, N, K = _fused_shapes(A, W, C, bias, residual, activation)
+    dev = torch.cuda.current_device()
+    _check(load().bi_gemm_epilogue(
+        _dptr(A, torch.bfloat16, dev, "A"), _dptr(W, torch.bfloat16, dev, "W"),
+        _dptr(bias, torch.bfloat16, dev, "bias"), _dptr(residual, torch.bfloat16, dev, "residual"),
+        _dptr(C, torch.bfloat16, dev, "C"), M, N, K, int(activation), _stream(stream)),
+        "bi_gemm_epilogue")
+
+
+def bi_gemm_q8(A, a_scale, W, w_scale, C, bias=None, residual=None, activation=ACT_NONE,
+               stream=None):
+    """C <- act((A W^T) a_scale w_scale + bias) + residual of e4m3 rows
+    (include/bi.h); residual may be C."""
+    M, N, K = _fused_shapes(A, W, C, bias, residual, activation)
+    if a_scale.shape != (M,) or w_scale.shape != (N,):
+        raise ValueError("a_scale must be [M] and w_scale [N]")
+    dev = torch.cuda.current_device()
+    _check(load().bi_gemm_q8(
+        _dptr(A, torch.float8_e4m3fn, dev, "A"), _dptr(a_scale, torch.float32, dev, "a_scale"),
+        _dptr(W, torch.float8_e4m3fn, dev, "W"), _dptr(w_scale, torch.float32, dev, "w_scale"),
+        _dptr(bias, torch.bfloat16, dev, "bias"), _dptr(residual, torch.bfloat16, dev, "residual"),
+        _dptr(C, torch.bfloat16, dev, "C"), M, N, K, int(activation), _stream(stream)),
+        "bi_gemm_q8")
+
+
 def bi_check_device_errors(stream=None) -> int:
     return int(load().bi_check_device_errors(_stream(stream)))
 
@@ -671,6 +762,55 @@ def rope_qkv_scaled(qkv, pos, Hq, Hkv, D, freqs, interleaved=False, attn_scale=1
     return q, k, v
 
 
+def _q8_rows(x, stream):
+    """Outputs for rows of x held as e4m3."""
+    return _alloc(stream, lambda: (
+        torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device),
+        torch.empty(x.shape[0], dtype=torch.float32, device=x.device)))
+
+
+def rmsnorm_q8(x, w, eps=1e-6, stream=None):
+    """RMSNorm(x) * w as (e4m3 rows, fp32 scale per row)."""
+    y, scale = _q8_rows(x, stream)
+    bi_rmsnorm_q8(x, w, y, scale, eps, stream)
+    return y, scale
+
+
+def add_rmsnorm_q8(x, residual, w, eps=1e-6, stream=None):
+    """Updates residual in place (residual <- bf16(x + residual)) and returns
+    RMSNorm(residual) * w as (e4m3 rows, fp32 scale per row)."""
+    y, scale = _q8_rows(x, stream)
+    bi_add_rmsnorm_q8(x, residual, w, residual, y, scale, eps, stream)
+    return y, scale
+
+
+def quantize_q8(x, stream=None):
+    """The rows of x as (e4m3 rows, fp32 scale per row)."""
+    y, scale = _q8_rows(x, stream)
+    bi_quantize_q8(x, y, scale, stream)
+    return y, scale
+
+
+def _product(A, W, activation, stream):
+    N = W.shape[0] // 2 if activation == ACT_SWIGLU else W.shape[0]
+    return _alloc(stream, lambda: [torch.empty(A.shape[0], N, dtype=torch.bfloat16,
+                                               device=A.device)])[0]
+
+
+def gemm_epilogue(A, W, bias=None, residual=None, activation=ACT_NONE, stream=None):
+    """act(A W^T + bias) + residual."""
+    C = _product(A, W, activation, stream)
+    bi_gemm_epilogue(A, W, C, bias, residual, activation, stream)
+    return C
+
+
+def gemm_q8(A, a_scale, W, w_scale, bias=None, residual=None, activation=ACT_NONE, stream=None):
+    """act((A W^T) a_scale w_scale + bias) + residual of e4m3 rows."""
+    C = _product(A, W, activation, stream)
+    bi_gemm_q8(A, a_scale, W, w_scale, C, bias, residual, activation, stream)
+    return C
+
+
 def gemm_swiglu(A, W, mode=INVARIANT, variant_splits=0, stream=None):
     out = torch.empty(A.shape[0], W.shape[0] // 2, dtype=torch.bfloat16, device=A.device)
     ws = _workspace(bi_gemm_workspace_size(A.shape[0], W.shape[0], A.shape[1], mode,
@@ -679,15 +819,16 @@ def gemm_swiglu(A, W, mode=INVARIANT, variant_splits=0, stream=None):
     return out
 
 
-def swiglu_interleave(F: int) -> np.ndarray:
-    """Row order of bi_gemm_swiglu's weight: entry r is the row of a [gate;
-    up] stacked weight (gate rows 0..F-1, up rows F..2F-1) that goes to row r
-    (blocks of 128 features, the gate rows of a block before its up rows)."""
-    if F % 128:
-        raise ValueError("F must be a multiple of 128")
+def swiglu_interleave(F: int, block: int = 128) -> np.ndarray:
+    """Row order of bi_gemm_swiglu's weight (and of ACT_SWIGLU's with block =
+    16): entry r is the row of a [gate; up] stacked weight (gate rows 0..F-1,
+    up rows F..2F-1) that goes to row r (blocks of ``block`` features, the gate
+    rows of a block before its up rows)."""
+    if F % block:
+        raise ValueError("F must be a multiple of %d" % block)
     j = np.arange(2 * F)
-    blk, r = j // 256, j % 256
-    return np.where(r < 128, blk * 128 + r, F + blk * 128 + (r - 128)).astype(np.int32)
+    blk, r = j // (2 * block), j % (2 * block)
+    return np.where(r < block, blk * block + r, F + blk * block + (r - block)).astype(np.int32)
 
 
 def silu_mul(gate_up, block=None, stream=None):

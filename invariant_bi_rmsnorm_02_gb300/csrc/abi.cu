@@ -127,6 +127,21 @@ bool make_tmap_records(CUtensorMap* map, const void* base, uint64_t records, int
          CUDA_SUCCESS;
 }
 
+bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
+                    uint32_t box_rows, uint32_t kg) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (!encode) return false;
+  const cuuint64_t flat[2] = {row_bytes, rows}, deep[3] = {128, rows, row_bytes / 128};
+  const cuuint64_t strides[2] = {row_bytes, 128};
+  const cuuint32_t box[3] = {128, box_rows, kg};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (kg > 1 && (row_bytes % 128 != 0 || kg > row_bytes / 128)) return false;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, kg > 1 ? 3 : 2, const_cast<void*>(base),
+                kg > 1 ? deep : flat, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace bi
 
 using namespace bi;
@@ -237,6 +252,62 @@ bi_status bi_add_rmsnorm(const void* x, void* residual, const void* w, void* y, 
   return bi_rmsnorm(residual, w, y, y_f32, M, H, eps, mode, workspace, workspace_bytes, stream);
 }
 
+// -------------------------------------------------------- rows held as e4m3
+// H: elements of a row of the bf16 input, H bytes of the e4m3 output
+static bi_status q8_row_checks(int64_t M, int64_t H) {
+  if (M < 0 || H <= 0) return BI_ERR_INVALID_ARG;
+  if (H % 16 != 0 || H > 65536 || M > 0x7fffffff) return BI_ERR_UNSUPPORTED;
+  return BI_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static bi_status rmsnorm_q8(const void* x, const void* residual, const void* w, void* h, void* y,
+                            float* y_scale, int64_t M, int64_t H, float eps, bool add,
+                            void* stream) {
+  const bi_status st = q8_row_checks(M, H);
+  if (st != BI_OK) return st;
+  if (!(eps >= 0.0f)) return BI_ERR_INVALID_ARG;
+  if (M == 0) return BI_OK;
+  if (!x || !w || !y || !y_scale || (add && (!residual || !h))) return BI_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(w) || !aligned16(h) || !aligned16(y) ||
+      !aligned4(y_scale))
+    return BI_ERR_INVALID_ARG;
+  const int64_t in = 2 * M * H, out = M * H, sc = 4 * M;
+  if (overlap(y, out, x, in) || overlap(y, out, w, 2 * H) || overlap(y, out, y_scale, sc) ||
+      overlap(y_scale, sc, x, in) || overlap(y_scale, sc, w, 2 * H))
+    return BI_ERR_INVALID_ARG;
+  if (add && (overlap(y, out, residual, in) || overlap(y, out, h, in) ||
+              overlap(y_scale, sc, residual, in) || overlap(y_scale, sc, h, in) ||
+              overlap(h, in, w, 2 * H) || (h != x && overlap(h, in, x, in)) ||
+              (h != residual && overlap(h, in, residual, in))))
+    return BI_ERR_INVALID_ARG;
+  return launch_rmsnorm_q8(x, add ? residual : nullptr, w, h, y, y_scale, M, H, eps,
+                           static_cast<cudaStream_t>(stream));
+}
+
+bi_status bi_rmsnorm_q8(const void* x, const void* w, void* y, float* y_scale, int64_t M,
+                        int64_t H, float eps, void* stream) {
+  return rmsnorm_q8(x, nullptr, w, nullptr, y, y_scale, M, H, eps, false, stream);
+}
+
+bi_status bi_add_rmsnorm_q8(const void* x, const void* residual, const void* w, void* h, void* y,
+                            float* y_scale, int64_t M, int64_t H, float eps, void* stream) {
+  return rmsnorm_q8(x, residual, w, h, y, y_scale, M, H, eps, true, stream);
+}
+
+bi_status bi_quantize_q8(const void* x, void* y, float* y_scale, int64_t M, int64_t K,
+                         void* stream) {
+  const bi_status st = q8_row_checks(M, K);
+  if (st != BI_OK || M == 0) return st;
+  if (!x || !y || !y_scale || !aligned16(x) || !aligned16(y) || !aligned4(y_scale))
+    return BI_ERR_INVALID_ARG;
+  if (overlap(y, M * K, x, 2 * M * K) || overlap(y, M * K, y_scale, 4 * M) ||
+      overlap(y_scale, 4 * M, x, 2 * M * K))
+    return BI_ERR_INVALID_ARG;
+  return launch_quantize_q8(x, y, y_scale, M, K, static_cast<cudaStream_t>(stream));
+}
+
 // --------------------------------------------------------------------- GEMM
 // The variant's split count, over the output tiles bi_gemm uses for this
 // shape (gemm_n_tile: 64 columns where the narrow ring runs, else 256).
@@ -331,6 +402,46 @@ bi_status bi_gemm_swiglu(const void* A, const void* W, void* out, int64_t M, int
   }
   return launch_gemm(A, W, out, M, N, K, splits, static_cast<float*>(workspace),
                      device_error_word(), s, /*swiglu=*/true);
+}
+
+// The GEMM with an epilogue, for both operand types (bytes per element: 2 or 1).
+static bi_status gemm_fused(const void* A, const float* a_scale, const void* W,
+                            const float* w_scale, const void* bias, const void* residual, void* C,
+                            int64_t M, int64_t N, int64_t K, bi_activation act, bool q8,
+                            void* stream) {
+  if (M < 0 || N <= 0 || K <= 0) return BI_ERR_INVALID_ARG;
+  if (act < BI_ACT_NONE || act > BI_ACT_SWIGLU) return BI_ERR_INVALID_ARG;
+  const bool swiglu = act == BI_ACT_SWIGLU;
+  const int64_t wide = q8 ? 1 : 2;
+  if (N % (swiglu ? 32 : 8) != 0 || K * wide % 16 != 0) return BI_ERR_UNSUPPORTED;
+  // (the kernels form tile coordinates and byte offsets along K in 32 bits)
+  constexpr int64_t kMost = (int64_t(1) << 31) - 256;
+  if (M > kMost || N > kMost || K > kMost / wide) return BI_ERR_UNSUPPORTED;
+  if (M == 0) return BI_OK;
+  if (!A || !W || !C || (q8 && (!a_scale || !w_scale))) return BI_ERR_INVALID_ARG;
+  if (!aligned16(A) || !aligned16(W) || !aligned16(C) || !aligned16(bias) ||
+      !aligned16(residual) || (q8 && (!aligned4(a_scale) || !aligned16(w_scale))))
+    return BI_ERR_INVALID_ARG;
+  const int64_t c = 2 * M * (swiglu ? N / 2 : N);
+  if (overlap(C, c, A, M * K * wide) || overlap(C, c, W, N * K * wide) ||
+      (bias && overlap(C, c, bias, 2 * N)) ||
+      (residual && residual != C && overlap(C, c, residual, c)) ||
+      (q8 && (overlap(C, c, a_scale, 4 * M) || overlap(C, c, w_scale, 4 * N))))
+    return BI_ERR_INVALID_ARG;
+  return launch_gemm_fused(A, a_scale, W, w_scale, bias, residual, C, M, N, K, act, q8,
+                           device_error_word(), static_cast<cudaStream_t>(stream));
+}
+
+bi_status bi_gemm_epilogue(const void* A, const void* W, const void* bias, const void* residual,
+                           void* C, int64_t M, int64_t N, int64_t K, bi_activation act,
+                           void* stream) {
+  return gemm_fused(A, nullptr, W, nullptr, bias, residual, C, M, N, K, act, false, stream);
+}
+
+bi_status bi_gemm_q8(const void* A, const float* a_scale, const void* W, const float* w_scale,
+                     const void* bias, const void* residual, void* C, int64_t M, int64_t N,
+                     int64_t K, bi_activation act, void* stream) {
+  return gemm_fused(A, a_scale, W, w_scale, bias, residual, C, M, N, K, act, true, stream);
 }
 
 // ---------------------------------------------------------------- attention

@@ -36,6 +36,14 @@ bool make_tmap_groups_bf16(CUtensorMap* map, const void* base, uint64_t rows, ui
 // box of 16 rows, swizzled over the row's width (128 or 64 bytes).
 bool make_tmap_records(CUtensorMap* map, const void* base, uint64_t records, int D);
 
+// Encode a tensor map over a row-major matrix of rows x row_bytes bytes
+// (row_bytes a multiple of 16) whose box is box_rows rows of kg neighbouring
+// k-blocks of 128 bytes, each with the 128-byte swizzle: 2-D with byte
+// coordinate x for kg = 1, else (row_bytes a multiple of 128, at least kg
+// k-blocks) the 3-D view of make_tmap_groups_bf16.
+bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
+                    uint32_t box_rows, uint32_t kg);
+
 // Bytes of one (page, kv head) of the quantised cache: K[16][D], V[16][D],
 // then 16 scale bytes of K and 16 of V.
 constexpr int kv_q8_record_bytes(int D) { return 32 * D + 32; }
@@ -65,6 +73,10 @@ bi_status launch_silu_mul(const void* gu, int64_t T, int64_t F, int64_t block, v
 bi_status launch_sample(const void* logits, int64_t B, int64_t V, const float* temperature,
                         const uint64_t* seed, const uint64_t* step, int32_t* tokens,
                         cudaStream_t s);
+bi_status launch_rmsnorm_q8(const void* x, const void* res, const void* w, void* h, void* y,
+                            float* scale, int64_t M, int64_t H, float eps, cudaStream_t s);
+bi_status launch_quantize_q8(const void* x, void* y, float* scale, int64_t M, int64_t K,
+                             cudaStream_t s);
 int rmsnorm_variant_splits(int64_t M, int64_t H, int num_sms);
 bi_status launch_rmsnorm_variant(const void* x, const void* w, void* y, float* y_f32, int64_t M,
                                  int64_t H, float eps, int splits, float* ws, int* err,
@@ -113,6 +125,12 @@ inline int gemm_n_tile(int64_t M, int64_t N, int64_t K, int num_sms, bool swiglu
 // swiglu: C is [M, N/2], the SwiGLU product of each tile's two column halves
 bi_status launch_gemm(const void* A, const void* W, void* C, int64_t M, int64_t N, int64_t K,
                       int splits, float* ws, int* err, cudaStream_t s, bool swiglu = false);
+
+// act(A W^T + bias) + residual (gemm_epilogue.cu); scales for e4m3 only
+bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
+                            const float* w_scale, const void* bias, const void* residual, void* C,
+                            int64_t M, int64_t N, int64_t K, int act, bool q8, int* err,
+                            cudaStream_t s);
 
 // ---- attention (attention.cu) -------------------------------------------------
 struct AttnArgs {

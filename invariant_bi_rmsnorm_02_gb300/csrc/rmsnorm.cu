@@ -21,43 +21,10 @@
 
 #include "bi_internal.h"
 #include "device_common.cuh"
+#include "rmsnorm_row.cuh"
 
 namespace bi {
 namespace {
-
-constexpr unsigned kFull = 0xffffffffu;
-
-__device__ __forceinline__ float sum_squares8(const uint4& v, float acc) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = bf16_lo(w[i]), b = bf16_hi(w[i]);
-    acc = __fmaf_rn(a, a, acc);
-    acc = __fmaf_rn(b, b, acc);
-  }
-  return acc;
-}
-
-// Fixed xor-butterfly over the 32 lanes; every lane ends with the same sum
-// (fp32 addition is commutative, so lane i and lane i^o add the same pair).
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
-  return v;
-}
-
-// Sum of one value per thread over the block, in a fixed order: warp
-// butterflies, then the same butterfly over the warp sums (missing warps
-// contribute +0, which leaves a sum of squares unchanged).
-__device__ __forceinline__ float block_sum(float v, float* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  v = warp_sum(v);
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  const int nw = (blockDim.x + 31) >> 5;
-  float t = lane < nw ? red[lane] : 0.0f;
-  return warp_sum(t);
-}
 
 // y = (x * r) * w for 8 elements; the bf16 result is returned, the fp32
 // values are also stored to yf (8 floats) when it is not null.
@@ -78,10 +45,6 @@ __device__ __forceinline__ uint4 scale_row8(const uint4& xv, const uint4& wv, fl
     reinterpret_cast<float4*>(yf)[1] = make_float4(f[4], f[5], f[6], f[7]);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
-__device__ __forceinline__ float inv_rms(float sum_sq, float inv_h, float eps) {
-  return rsqrtf(__fadd_rn(__fmul_rn(sum_sq, inv_h), eps));
 }
 
 // ---------------------------------------------------------------- invariant
@@ -116,16 +79,6 @@ __global__ void __launch_bounds__(1024) rmsnorm_row_kernel(const uint4* __restri
 // Residual add fused in front: h = bf16(x + res) (an fp32 add, rounded once)
 // overwrites res, and y = RMSNorm(h) * w with exactly the row reduction of
 // rmsnorm_row_kernel, so the result equals a bf16 add followed by RMSNorm.
-__device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
-  const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[4] = {b.x, b.y, b.z, b.w};
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = pack_bf16x2(__fadd_rn(bf16_lo(as[i]), bf16_lo(bs[i])),
-                       __fadd_rn(bf16_hi(as[i]), bf16_hi(bs[i])));
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 template <int VPT>
 __global__ void __launch_bounds__(1024) add_rmsnorm_row_kernel(
     const uint4* __restrict__ x, uint4* __restrict__ res, const uint4* __restrict__ w,
@@ -165,20 +118,6 @@ __global__ void add_bf16_kernel(const uint4* __restrict__ x, uint4* __restrict__
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < nvec_total;
        i += (int64_t)gridDim.x * blockDim.x)
     res[i] = add_bf16x8(x[i], res[i]);
-}
-
-// Block shape as a function of H only: VPT vectors of 8 elements per thread,
-// T threads (a multiple of 32, at most 1024).
-struct RowShape {
-  int vpt, threads;
-};
-RowShape row_shape(int64_t H) {
-  const int nvec = static_cast<int>(H / 8);
-  int vpt = nvec >= 256 ? 4 : (nvec >= 64 ? 2 : 1);
-  while ((nvec + vpt - 1) / vpt > 1024) vpt *= 2;
-  int t = (nvec + vpt - 1) / vpt;
-  t = (t + 31) / 32 * 32;
-  return {vpt, t};
 }
 
 // ------------------------------------------------------------------ variant

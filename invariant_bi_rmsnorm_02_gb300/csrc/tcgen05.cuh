@@ -20,6 +20,12 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N, bool a_mn_m
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Instruction descriptor of tcgen05.mma.kind::f8f6f4 with e4m3 A and B (format
+// 0 in bits 7-9 and 10-12), both K-major, and an fp32 accumulator.
+__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
 // Shared memory matrix descriptor for a tile in the 128-byte swizzled layout
 // (rows of 128 bytes, 16-byte chunk c of row r stored at chunk c ^ (r % 8),
 // 8-row groups of 1024 bytes): start address, leading and stride byte
