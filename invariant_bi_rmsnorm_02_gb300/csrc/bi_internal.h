@@ -44,6 +44,10 @@ bool make_tmap_records(CUtensorMap* map, const void* base, uint64_t records, int
 bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
                     uint32_t box_rows, uint32_t kg);
 
+// Encode a tensor map over a bf16 matrix of rows x cols (cols a multiple of 8)
+// in boxes of 32 rows x 32 columns, swizzled over their 64-byte rows.
+bool make_tmap_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols);
+
 // Bytes of one (page, kv head) of the quantised cache: K[16][D], V[16][D],
 // then 16 scale bytes of K and 16 of V.
 constexpr int kv_q8_record_bytes(int D) { return 32 * D + 32; }

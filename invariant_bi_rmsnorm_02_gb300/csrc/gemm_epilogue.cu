@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "bi_internal.h"
 #include "device_common.cuh"
@@ -35,14 +36,25 @@
 namespace bi {
 namespace {
 
-constexpr int BM = 128;
-constexpr int kThreads = 192;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int BM = 128;                      // rows of a CTA's tile
+constexpr int kEpiWarps = 8;                 // two per quarter of the accumulator's lanes
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kBlockBytes = 128;             // bytes of a row in one k-block
 constexpr int kMaxStages = 8;
-constexpr int kRingBytes = 208 * 1024;
-constexpr size_t kSmemBytes = 1024 + kRingBytes;
+constexpr int kChunk = 32;                   // columns of C that a warp stores at once
+constexpr int kChunkBytes = 32 * kChunk * 2; // of 32 rows of them
+constexpr int kMaxBufs = 5;                  // buffers of that size a warp may have
+constexpr int kPadBytes = 1024;              // to the ring's alignment
+constexpr int kColumnBytes = 2 * 256 * (4 + 2);  // a tile's w_scale and bias, twice
+// the operand ring and the epilogue's buffers share the rest (less than 1 KB
+// of barriers is static)
+constexpr int kPoolBytes = 227 * 1024 - 1024 - kPadBytes - kColumnBytes;
+static_assert(kPoolBytes % 1024 == 0, "the buffers behind the ring are aligned as it is");
+constexpr size_t kSmemBytes = kPadBytes + kPoolBytes + kColumnBytes;
 constexpr uint32_t kAccCols = 256;           // columns between the two accumulators
 constexpr int kSwigluBlock = 16;             // gate (then up) rows of a block of W
+constexpr int kDirectRows = 64;              // at most this many rows of A: MMAs of 64, plain stores
 
 struct FusedParams {
   __nv_bfloat16* C;
@@ -54,7 +66,9 @@ struct FusedParams {
   int M, N, n_out;                // n_out: columns of C
   int act;
   int bn, a_rows, kg, stages;     // tile width, rows of A and k-blocks per stage
-  int m_tiles, n_tiles, kb_total;
+  int mma_rows;                   // rows of an MMA in this CTA
+  int ring, bufs;                 // the ring's bytes, epilogue buffers per warp
+  int m_tiles, n_tiles, kb_total; // m_tiles: of the pair's 256 rows where kCtas is 2
   int group, m_fast;              // raster, as in the plain GEMM
   uint32_t idesc;
 };
@@ -74,67 +88,232 @@ __device__ __forceinline__ Tile tile_of(int u, const FusedParams& p) {
   return p.m_fast ? Tile{fast, slow} : Tile{slow, fast};
 }
 
-// D (tmem) = A B (+ D if accumulate), one CTA, e4m3 operands.
-__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The activations take the special-function unit's exponential and reciprocal
+// (2^-22 relative) instead of expf and a division: the division's path for
+// special cases kept a warp from interleaving its 32 values (100 cycles a
+// value; 8192 x 14336 x 1024 with SiLU 815 us against 483 without), and the
+// result is rounded to 2^-9.
+constexpr float kLog2e = 1.4426950408889634f;
 
-// silu(z) = z / (1 + exp(-z)), as silu_mul_f32 forms it.
-__device__ __forceinline__ float silu_f32(float z) {
-  return __fdiv_rn(z, __fadd_rn(1.0f, expf(-z)));
+// z / (1 + 2^e)
+__device__ __forceinline__ float z_sigmoid(float z, float e) {
+  return __fmul_rn(z, rcp(__fadd_rn(1.0f, ex2(e))));
+}
+__device__ __forceinline__ float silu(float z) { return z_sigmoid(z, __fmul_rn(z, -kLog2e)); }
+// z/2 (1 + tanh u) = z / (1 + exp(-2 u)), u = sqrt(2/pi) (z + 0.044715 z^3)
+__device__ __forceinline__ float gelu_tanh(float z) {
+  const float c = __fmul_rn(__fmul_rn(z, z), 0.044715f);
+  return z_sigmoid(z, __fmul_rn(__fmaf_rn(z, c, z), -1.5957691216057308f * kLog2e));
+}
+// z/2 (1 + erf(z / sqrt 2)) = max(z, 0) - |z|/2 erfcx(x) exp(-x^2), x = |z| / sqrt 2,
+// with erfcx(x)/2 as t times a polynomial in t = 1 / (1 + x/2): the least
+// largest relative error of degree 6 over 0 <= x <= 11.4, by linear
+// programming; 2^-18.8 in fp32.  Both tails keep their digits.  Past |z| = 16
+// the second term is 0.
+__device__ __forceinline__ float gelu(float z) {
+  const float m = fminf(fabsf(z), 16.0f);
+  const float t = rcp(__fmaf_rn(m, 0.35355339059327376f, 1.0f));
+  float s = 0.0429137014f;
+  s = __fmaf_rn(s, t, -0.174213769f);
+  s = __fmaf_rn(s, t, 0.188846613f);
+  s = __fmaf_rn(s, t, 0.0229806649f);
+  s = __fmaf_rn(s, t, 0.139260697f);
+  s = __fmaf_rn(s, t, 0.139064864f);
+  s = __fmaf_rn(s, t, 0.141146311f);
+  const float e = ex2(__fmul_rn(__fmul_rn(m, m), -0.5f * kLog2e));
+  const float top = z <= 0.0f ? 0.0f : z;  // (a NaN stays one)
+  return __fmaf_rn(__fmul_rn(__fmul_rn(s, t), -m), e, top);
 }
 
 // In 32 values, one activation; the choice is the same for the whole call.
 __device__ __forceinline__ void activate(float (&z)[32], int act) {
   switch (act) {
-    case BI_ACT_RELU:  // a NaN stays one
+    case BI_ACT_RELU:  // (a NaN stays one)
 #pragma unroll
       for (int i = 0; i < 32; ++i) z[i] = z[i] <= 0.0f ? 0.0f : z[i];
       break;
-    case BI_ACT_GELU:  // z/2 (1 + erf(z / sqrt 2)), by erfc so that the left tail keeps its digits
+    case BI_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        z[i] = __fmul_rn(__fmul_rn(0.5f, z[i]), erfcf(__fmul_rn(z[i], -0.70710678118654752f)));
+      for (int i = 0; i < 32; ++i) z[i] = gelu(z[i]);
       break;
-    case BI_ACT_GELU_TANH:  // z/2 (1 + tanh u) = z / (1 + exp(-2u)), u = sqrt(2/pi) (z + 0.044715 z^3)
+    case BI_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float c = __fmul_rn(__fmul_rn(z[i], z[i]), 0.044715f);
-        const float u2 = __fmul_rn(__fmaf_rn(z[i], c, z[i]), -1.5957691216057308f);
-        z[i] = __fdiv_rn(z[i], __fadd_rn(1.0f, expf(u2)));
-      }
+      for (int i = 0; i < 32; ++i) z[i] = gelu_tanh(z[i]);
       break;
     case BI_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = silu_f32(z[i]);
+      for (int i = 0; i < 32; ++i) z[i] = silu(z[i]);
       break;
     default:
       break;
   }
 }
 
+// 32 accumulator columns of this lane's row times the scales and with the
+// bias; ws and bias: those columns' values in shared memory.
 template <bool kQ8>
+__device__ __forceinline__ void load_z(float (&z)[32], uint32_t taddr, const float* ws,
+                                       const __nv_bfloat16* bias, bool add_bias, float a_scale) {
+  uint32_t v[32];
+  __syncwarp();
+  tmem_ld32(taddr, v);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float4 w4;
+    if constexpr (kQ8) w4 = reinterpret_cast<const float4*>(ws)[q];
+    uint2 b2 = make_uint2(0, 0);
+    if (add_bias) b2 = reinterpret_cast<const uint2*>(bias)[q];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x = __uint_as_float(v[4 * q + e]);
+      if constexpr (kQ8)
+        x = __fmul_rn(__fmul_rn(x, a_scale), e == 0 ? w4.x : e == 1 ? w4.y : e == 2 ? w4.z : w4.w);
+      const uint32_t b = e < 2 ? b2.x : b2.y;
+      if (add_bias) x = __fadd_rn(x, e & 1 ? bf16_hi(b) : bf16_lo(b));
+      z[4 * q + e] = x;
+    }
+  }
+}
+
+// z + residual for eight columns, rounded
+__device__ __forceinline__ uint4 add_pack8(const float* z, bool add, const uint4& r) {
+  const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo = z[2 * i], hi = z[2 * i + 1];
+    if (add) {
+      lo = __fadd_rn(lo, bf16_lo(rw[i]));
+      hi = __fadd_rn(hi, bf16_hi(rw[i]));
+    }
+    o[i] = pack_bf16x2(lo, hi);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// An epilogue warp's chunks (32 rows by 32 columns of C) of one tile: the first
+// or the second half of the tile's columns, none where its rows are past M.
+struct Span {
+  int c, end;
+};
+template <int kCtas>
+__device__ __forceinline__ Span span_of(const Tile& t, const FusedParams& p, int bn_out,
+                                        int row_in_unit, int half) {
+  if (t.m * (BM * kCtas) + row_in_unit >= p.M) return Span{0, 0};
+  const int n = (min(bn_out, p.n_out - t.n * bn_out) + kChunk - 1) / kChunk;
+  const int mid = (n + 1) >> 1;
+  return half == 0 ? Span{0, mid} : Span{mid, n};
+}
+
+struct Ring {
+  uint64_t *full, *empty, *tfull, *tempty, *drain;
+  uint32_t a, b;     // the operands' tiles
+  int a_sub, b_sub;  // bytes of one k-block's
+  uint32_t tmem;
+};
+
+// The MMAs of all of a block's tiles, by one thread, kKG k-blocks a stage.
+// The loop's own instructions are what a narrow tile waits for (some 50 cycles
+// an MMA and 150 around a stage; with the k-blocks of a stage counted at run
+// time and the addresses formed anew 100 more: 256 x 4096 x 14336 e4m3 21 us
+// in place of 27), so nothing is recomputed in it, and the next stage's
+// barrier is looked at while the MMAs are on their way.
+template <bool kQ8, bool kPair, int kKG>
+__device__ __forceinline__ void issue_mmas(const FusedParams& p, const Ring& r, int first,
+                                           int units, int step, volatile int* abort_flag) {
+  // K-major tiles, 128-byte swizzle: rows of 128 bytes, 8-row groups 1024
+  // bytes apart; an instruction takes 32 bytes of each row, the next ones
+  // start 32 bytes (two units of a descriptor) further on
+  const uint64_t ad0 = umma_desc_sw128(r.a, 16, 1024), bd0 = umma_desc_sw128(r.b, 16, 1024);
+  const uint32_t a_step = r.a_sub >> 4, b_step = r.b_sub >> 4;
+  const int stages = p.stages, kb_total = p.kb_total;
+  const uint32_t idesc = p.idesc;
+  int* err = p.err;
+  uint64_t ad = ad0, bd = bd0;
+  int stage = 0, acc = 0;
+  uint32_t phase = 0, acc_phase = 0;
+  bool ok = true, there = false;
+  for (int u = first; u < units && ok; u += step) {
+    if (!mbar_wait(&r.tempty[acc], acc_phase ^ 1u, err, abort_flag)) {
+      ok = false;
+      break;
+    }
+    tc_fence_after();
+    const uint32_t d = r.tmem + static_cast<uint32_t>(acc) * kAccCols;
+    uint32_t add = 0;  // 0: the tile's first MMA
+    for (int left = kb_total; left > 0; left -= kKG) {
+      if (!there && !mbar_wait(&r.full[stage], phase, err, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int g = 0; g < kKG; ++g) {
+        if (g > 0 && g >= left) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          tc_mma_any<kQ8, kPair>(d, ad + g * a_step + 2u * k, bd + g * b_step + 2u * k, idesc, add);
+          add = 1;
+        }
+      }
+      uint64_t* done = &r.empty[stage];
+      ad += kKG * a_step;
+      bd += kKG * b_step;
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+        ad = ad0;
+        bd = bd0;
+      }
+      there = mbar_test(&r.full[stage], phase);
+      tc_commit_any<kPair, true>(done);
+    }
+    if (!ok) break;
+    tc_commit_any<kPair, true>(&r.tfull[acc]);
+    acc ^= 1;
+    if (acc == 0) acc_phase ^= 1u;
+  }
+  if (!ok) {  // all issued MMAs done before tensor memory is freed
+    tc_commit_any<kPair, false>(r.drain);
+    mbar_wait(r.drain, 0, nullptr);
+  }
+}
+
+// kCtas = 2: a pair of CTAs computes 256 x bn tiles with one MMA over both
+// SMs; each loads its 128 rows of A and half of the tile's rows of W, which
+// both read.
+template <bool kQ8, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
     const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+    const __grid_constant__ CUtensorMap tc, const __grid_constant__ CUtensorMap tr,
     const FusedParams p) {
+  constexpr bool kPair = kCtas == 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+  __shared__ uint64_t rbar[kEpiWarps][kMaxBufs];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  const int a_sub = p.a_rows * kBlockBytes, b_sub = p.bn * kBlockBytes;  // of one k-block
+  const int b_rows = p.bn / kCtas;
+  const int a_sub = p.a_rows * kBlockBytes, b_sub = b_rows * kBlockBytes;  // of one k-block
   uint8_t* sA = smem;
   uint8_t* sB = smem + p.stages * p.kg * a_sub;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
   const int units = p.m_tiles * p.n_tiles;
+  const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
   if (threadIdx.x == 0) {
     prefetch_tmap(&ta);
@@ -145,41 +324,58 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 4);  // one arrival per epilogue warp
+      mbar_init(&tempty[a], kCtas * kEpiWarps);  // one arrival per epilogue warp of the pair
     }
+    for (int w = 0; w < kEpiWarps; ++w)
+      for (int b = 0; b < p.bufs; ++b) mbar_init(&rbar[w][b], 1);
     mbar_init(&drain, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&tmem_slot, 2 * kAccCols);
+  if (warp == 1) {
+    if constexpr (kPair) tmem_alloc_pair(&tmem_slot, 2 * kAccCols);
+    else tmem_alloc(&tmem_slot, 2 * kAccCols);
+  }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
+  // the next kernel in the stream may begin its own prologue; this one's
+  // inputs are there, and nobody reads its output any more, past the wait
+  launch_dependents();
+  grid_dependency_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ------------------------------------------------------------ producer
+      const int a_stage = p.kg * a_sub, b_stage = p.kg * b_sub;
+      // both CTAs' bytes are counted on the even one's barriers
+      const uint32_t bytes = static_cast<uint32_t>(kCtas * (a_stage + b_stage));
+      const uint32_t full0 = kPair ? cluster_addr(full, 0) : 0u;
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
-      const uint32_t bytes = static_cast<uint32_t>(p.kg * (a_sub + b_sub));
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      for (int u = first; u < units && ok; u += step) {
         const Tile t = tile_of(u, p);
+        const int ra = (t.m * kCtas + rank) * BM, rb = t.n * p.bn + rank * b_rows;
         for (int kb = 0; kb < p.kb_total; kb += p.kg) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, p.err, &abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], bytes);
-          uint8_t* a = sA + stage * p.kg * a_sub;
-          uint8_t* b = sB + stage * p.kg * b_sub;
-          if (p.kg == 1) {
-            tma_load_2d(a, &ta, kb * kBlockBytes, t.m * BM, &full[stage]);
-            tma_load_2d(b, &tb, kb * kBlockBytes, t.n * p.bn, &full[stage]);
+          uint8_t* a = sA + stage * a_stage;
+          uint8_t* b = sB + stage * b_stage;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+          if constexpr (kPair) {
+            tma_load_2d_pair(a, &ta, kb * kBlockBytes, ra, full0 + stage * 8);
+            tma_load_2d_pair(b, &tb, kb * kBlockBytes, rb, full0 + stage * 8);
+          } else if (p.kg == 1) {
+            tma_load_2d(a, &ta, kb * kBlockBytes, ra, &full[stage]);
+            tma_load_2d(b, &tb, kb * kBlockBytes, rb, &full[stage]);
           } else {  // k-blocks past the last read as zero and are not used
-            tma_load_3d(a, &ta, 0, t.m * BM, kb, &full[stage]);
-            tma_load_3d(b, &tb, 0, t.n * p.bn, kb, &full[stage]);
+            tma_load_3d(a, &ta, 0, ra, kb, &full[stage]);
+            tma_load_3d(b, &tb, 0, rb, kb, &full[stage]);
           }
           ++issued;
           if (++stage == p.stages) {
@@ -188,173 +384,327 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
           }
         }
       }
+      const int last = issued > p.stages ? issued - p.stages : 0;
       if (!ok) {
         // let the copies already issued land before the block goes away
-        const int first = issued > p.stages ? issued - p.stages : 0;
-        for (int i = first; i < issued; ++i)
-          mbar_wait(&full[i % p.stages], (i / p.stages) & 1, nullptr);
+        if (rank == 0)
+          for (int i = last; i < issued; ++i)
+            mbar_wait(&full[i % p.stages], (i / p.stages) & 1, nullptr);
+      } else if (kPair) {
+        // the even CTA's MMAs arrive on this CTA's barriers: none is left to
+        for (int i = last; i < issued; ++i)
+          if (!mbar_wait(&empty[i % p.stages], (i / p.stages) & 1, p.err, &abort_flag)) break;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ----------------------------------------------------------- MMA issuer
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, p.err, &abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * kAccCols;
-        for (int kb0 = 0; kb0 < p.kb_total; kb0 += p.kg) {
-          if (!mbar_wait(&full[stage], phase, p.err, &abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const int here = min(p.kg, p.kb_total - kb0);
-          for (int g = 0; g < here; ++g) {
-            // K-major tiles, 128-byte swizzle: rows of 128 bytes, 8-row groups
-            // 1024 bytes apart; an instruction takes 32 bytes of each row
-            const uint64_t ad =
-                umma_desc_sw128(smem_u32(sA + (stage * p.kg + g) * a_sub), 16, 1024);
-            const uint64_t bd =
-                umma_desc_sw128(smem_u32(sB + (stage * p.kg + g) * b_sub), 16, 1024);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t add = (kb0 + g > 0 || k > 0) ? 1u : 0u;
-              if constexpr (kQ8)
-                tc_mma_f8(d, ad + 2u * k, bd + 2u * k, p.idesc, add);
-              else
-                tc_mma(d, ad + 2u * k, bd + 2u * k, p.idesc, add);
-            }
-          }
-          tc_commit(&empty[stage]);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (!ok) break;
-        tc_commit(&tfull[acc]);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
-      }
-      if (!ok) {
-        tc_commit(&drain);  // all issued MMAs done before tensor memory is freed
-        mbar_wait(&drain, 0, nullptr);
-      }
+    if (elect_one() && rank == 0) {
+      const Ring ring{full, empty, tfull, tempty, &drain, smem_u32(sA), smem_u32(sB), a_sub, b_sub,
+                      tmem_base};
+      if (kPair || p.kg == 1) issue_mmas<kQ8, kPair, 1>(p, ring, first, units, step, &abort_flag);
+      else if (p.kg == 2) issue_mmas<kQ8, kPair, 2>(p, ring, first, units, step, &abort_flag);
+      else issue_mmas<kQ8, kPair, 4>(p, ring, first, units, step, &abort_flag);
     }
   } else {
     // ------------------------------------------------------------- epilogue
-    const int wq = warp & 3;  // this warp may access accumulator lanes 32*wq ..
-    const bool swiglu = p.act == BI_ACT_SWIGLU;
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int ew = warp - 2, wq = warp & 3;  // this warp may access accumulator lanes 32*wq ..
+    const int half = ew >> 2;
+    const bool swiglu = p.act == BI_ACT_SWIGLU, add_bias = p.bias != nullptr;
+    const int bn_out = swiglu ? p.bn / 2 : p.bn, acc_chunk = swiglu ? 2 * kChunk : kChunk;
+    // (an MMA of 64 rows leaves rows 16 q .. 16 q + 15 in the first half of the
+    // q-th quarter of the lanes)
+    const int row_in_unit = rank * BM + wq * (p.mma_rows == 64 ? 16 : 32);
+    const bool mine_too = p.mma_rows != 64 || lane < 16;
+    const bool staged = p.bufs > 0, fetch = staged && p.residual != nullptr;
+    uint8_t* buf = smem + p.ring + ew * p.bufs * kChunkBytes;
+    float* columns = reinterpret_cast<float*>(smem + kPoolBytes);  // [2][256] scales, then biases
+    const uint32_t row_off = static_cast<uint32_t>(lane) * 64;
+    const uint32_t swz = (static_cast<uint32_t>(lane) >> 1) & 3;
+
+    // residuals, asked for up to `distance` chunks ahead by lane 0
+    int ahead_u = first, fetch_buf = 0;
+    uint32_t fetched = 0;
+    Tile ahead_t{0, 0};
+    Span ahead{0, 0};
+    bool more = fetch && lane == 0 && first < units;
+    if (more) {
+      ahead_t = tile_of(ahead_u, p);
+      ahead = span_of<kCtas>(ahead_t, p, bn_out, row_in_unit, half);
+    }
+    auto fetch_one = [&]() {
+      while (ahead.c >= ahead.end) {
+        ahead_u += step;
+        if (ahead_u >= units) {
+          more = false;
+          return;
+        }
+        ahead_t = tile_of(ahead_u, p);
+        ahead = span_of<kCtas>(ahead_t, p, bn_out, row_in_unit, half);
+      }
+      uint64_t* bar = &rbar[ew][fetch_buf];
+      mbar_arrive_expect_tx(bar, kChunkBytes);
+      tma_load_2d(buf + fetch_buf * kChunkBytes, &tr, ahead_t.n * bn_out + ahead.c * kChunk,
+                  ahead_t.m * (BM * kCtas) + row_in_unit, bar);
+      ++ahead.c;
+      ++fetched;
+      if (++fetch_buf == p.bufs) fetch_buf = 0;
+    };
+    // a buffer is filled again once the store of the chunk before last has
+    // read it
+    const int distance = p.bufs - 2;
+    for (int i = 0; i < distance && more; ++i) fetch_one();
+
+    int acc = 0, b = 0;
+    uint32_t acc_phase = 0, buf_phase = 0, count = 0;  // count: chunks done
+    bool ok = true;                                    // the same in every lane
+    for (int u = first; u < units && ok; u += step) {
       const Tile t = tile_of(u, p);
-      if (!mbar_wait(&tfull[acc], acc_phase, p.err, &abort_flag)) break;
-      __syncwarp();
+      const int row0 = t.m * (BM * kCtas) + row_in_unit, row = row0 + lane;
+      const Span span = span_of<kCtas>(t, p, bn_out, row_in_unit, half);
+      // this half's scales and biases, four columns a lane (N % 8 == 0)
+      const int col0 = span.c * acc_chunk, col = t.n * p.bn + col0 + 4 * lane;
+      float4 ws = make_float4(0.f, 0.f, 0.f, 0.f);
+      uint2 bs = make_uint2(0, 0);
+      float a_scale = 1.0f;
+      if (span.c < span.end && col < p.N) {
+        if constexpr (kQ8) ws = __ldg(reinterpret_cast<const float4*>(p.w_scale + col));
+        if (add_bias) bs = __ldg(reinterpret_cast<const uint2*>(p.bias + col));
+      }
+      if (kQ8 && row < p.M) a_scale = __ldg(p.a_scale + row);
+      ok = __all_sync(kFull, mbar_wait(&tfull[acc], acc_phase, p.err, &abort_flag));
+      if (!ok) break;
       tc_fence_after();
-      const int row0 = t.m * BM + wq * 32, row = row0 + lane;
-      const int n0 = t.n * p.bn, n_end = min(n0 + p.bn, p.N);
+      // (the four warps of a half write the same values; the accumulator's
+      // last use, whose columns these replace, is over)
+      float* cw = columns + acc * 256;
+      __nv_bfloat16* cb = reinterpret_cast<__nv_bfloat16*>(columns + 512) + acc * 256;
+      if (span.c < span.end && col0 + 4 * lane < 256) {
+        if constexpr (kQ8) *reinterpret_cast<float4*>(cw + col0 + 4 * lane) = ws;
+        if (add_bias) *reinterpret_cast<uint2*>(cb + col0 + 4 * lane) = bs;
+      }
+      const int out0 = t.n * bn_out, cols = min(bn_out, p.n_out - out0);
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) +
                              static_cast<uint32_t>(acc) * kAccCols;
-      float a_scale = 1.0f;
-      if (kQ8 && row < p.M) a_scale = __ldg(p.a_scale + row);
-      // 32 accumulator columns at a time (the last chunk of a tile may have
-      // 16: its other columns are read and not stored)
-      for (int col = n0; row0 < p.M && col < n_end; col += 32) {
-        uint32_t v[32];
-        __syncwarp();
-        tmem_ld32(tbase + static_cast<uint32_t>(col - n0), v);
-        if (row >= p.M) continue;
-        float z[32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {  // eight columns: N % 8 == 0
-          const bool in = col + 8 * q < n_end;
-          float ws[8];
-          if constexpr (kQ8) {
-            const float4* src = reinterpret_cast<const float4*>(p.w_scale + col + 8 * q);
-            const float4 x = in ? __ldg(src) : make_float4(0, 0, 0, 0);
-            const float4 y = in ? __ldg(src + 1) : make_float4(0, 0, 0, 0);
-            ws[0] = x.x; ws[1] = x.y; ws[2] = x.z; ws[3] = x.w;
-            ws[4] = y.x; ws[5] = y.y; ws[6] = y.z; ws[7] = y.w;
-          }
-          uint4 b = make_uint4(0, 0, 0, 0);
-          if (p.bias && in) b = __ldg(reinterpret_cast<const uint4*>(p.bias + col + 8 * q));
-          const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float x = __uint_as_float(v[8 * q + e]);
-            if constexpr (kQ8) x = __fmul_rn(__fmul_rn(x, a_scale), ws[e]);
-            if (p.bias) x = __fadd_rn(x, e & 1 ? bf16_hi(bw[e >> 1]) : bf16_lo(bw[e >> 1]));
-            z[8 * q + e] = x;
-          }
+      for (int c = span.c; c < span.end; ++c) {
+        uint8_t* mine = buf + b * kChunkBytes;
+        if (staged && lane == 0) {
+          bulk_wait_read<1>();
+          if (more) fetch_one();
         }
-        int groups = 4;  // of eight columns
-        int64_t at = static_cast<int64_t>(row) * p.n_out + col;
-        if (swiglu) {  // 16 gate columns, then the 16 up columns of the same features
+        float z[32];
+        if (swiglu) {
+          // two blocks of 16 gate columns and the 16 up columns of the same
+          // features; the second may lie past the tile
 #pragma unroll
-          for (int i = 0; i < kSwigluBlock; ++i) z[i] = silu_mul_f32(z[i], z[kSwigluBlock + i]);
-          groups = 2;
-          at = static_cast<int64_t>(row) * p.n_out + col / 2;
+          for (int h = 0; h < 2; ++h) {
+            if (c * kChunk + h * kSwigluBlock >= cols) {
+#pragma unroll
+              for (int i = 0; i < kSwigluBlock; ++i) z[h * kSwigluBlock + i] = 0.0f;
+              continue;
+            }
+            float g[32];
+            const int ac = c * 2 * kChunk + h * 32;
+            load_z<kQ8>(g, tbase + static_cast<uint32_t>(ac), cw + ac, cb + ac, add_bias, a_scale);
+#pragma unroll
+            for (int i = 0; i < kSwigluBlock; ++i)
+              z[h * kSwigluBlock + i] = __fmul_rn(silu(g[i]), g[kSwigluBlock + i]);
+          }
         } else {
+          const int ac = c * kChunk;
+          load_z<kQ8>(z, tbase + static_cast<uint32_t>(ac), cw + ac, cb + ac, add_bias, a_scale);
           activate(z, p.act);
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (q >= groups || (!swiglu && col + 8 * q >= n_end)) continue;
-          if (p.residual) {  // may be C: read before it is written, by the same thread
-            const uint4 r = *reinterpret_cast<const uint4*>(p.residual + at + 8 * q);
-            const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              z[8 * q + e] = __fadd_rn(z[8 * q + e],
-                                       e & 1 ? bf16_hi(rw[e >> 1]) : bf16_lo(rw[e >> 1]));
+        if (staged) {
+          if (fetch) {
+            ok = __all_sync(kFull, mbar_wait(&rbar[ew][b], buf_phase, p.err, &abort_flag));
+            if (!ok) break;
           }
-          *reinterpret_cast<uint4*>(p.C + at + 8 * q) = make_uint4(
-              pack_bf16x2(z[8 * q], z[8 * q + 1]), pack_bf16x2(z[8 * q + 2], z[8 * q + 3]),
-              pack_bf16x2(z[8 * q + 4], z[8 * q + 5]), pack_bf16x2(z[8 * q + 6], z[8 * q + 7]));
+#pragma unroll
+          for (uint32_t q = 0; q < 4; ++q) {
+            uint4* at = reinterpret_cast<uint4*>(mine + row_off + ((q ^ swz) << 4));
+            uint4 r = make_uint4(0, 0, 0, 0);
+            if (fetch) r = *at;
+            *at = add_pack8(z + 8 * q, fetch, r);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tc, mine, out0 + c * kChunk, row0);
+            bulk_commit();
+          }
+          ++count;
+          if (++b == p.bufs) {
+            b = 0;
+            buf_phase ^= 1u;
+          }
+        } else if (row < p.M && mine_too) {
+          const int64_t at = static_cast<int64_t>(row) * p.n_out + out0 + c * kChunk;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (c * kChunk + 8 * q >= cols) continue;
+            uint4 r = make_uint4(0, 0, 0, 0);
+            // (may be C: read before it is written, by the same thread)
+            if (p.residual) r = *reinterpret_cast<const uint4*>(p.residual + at + 8 * q);
+            *reinterpret_cast<uint4*>(p.C + at + 8 * q) =
+                add_pack8(z + 8 * q, p.residual != nullptr, r);
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[acc]);
+      if (lane == 0) {
+        if constexpr (kPair) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
+        else mbar_arrive(&tempty[acc]);
+      }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
+    if (staged && lane == 0) {
+      // (after a wait that ran out, residuals may still be on their way)
+      for (; count < fetched; ++count) {
+        mbar_wait(&rbar[ew][b], buf_phase, nullptr);
+        if (++b == p.bufs) {
+          b = 0;
+          buf_phase ^= 1u;
+        }
+      }
+      bulk_wait_all();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
-    tmem_dealloc(tmem_base, 2 * kAccCols);
+    if constexpr (kPair) tmem_dealloc_pair(tmem_base, 2 * kAccCols);
+    else tmem_dealloc(tmem_base, 2 * kAccCols);
   }
 }
 
-// The tile width: rounds of #SM tiles times what a tile costs.  A tile's
-// k-block takes the MMA 2 bn cycles, or as long as its operands take to come,
-// in proportion to bn plus the rows of A; widths are multiples of 16 (32 with
-// SwiGLU, whose blocks of 16 gate and 16 up rows stay together).
-int tile_width(int64_t M, int64_t N, int sms, bool swiglu) {
-  const int step = swiglu ? 32 : 16;
-  const int64_t mt = (M + BM - 1) / BM;
-  const int64_t rows = std::min<int64_t>(M, BM);
-  int best = 256;
-  int64_t best_cost = INT64_MAX;
-  for (int bn = 256; bn >= step; bn -= step) {
-    const int64_t tiles = mt * ((N + bn - 1) / bn);
-    const int64_t cost = (tiles + sms - 1) / sms * std::max<int64_t>(2 * bn, bn + rows);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = bn;
+// How a call's work is cut up.
+struct Plan {
+  int ctas, bn;      // CTAs of a tile (1: 128 rows, 2: 256) and its width
+  int a_rows;        // rows of A per stage
+  int kg, stages;    // k-blocks per stage, stages
+  int bufs;          // epilogue buffers per warp, 0: plain stores
+  int ring;          // the operand ring's bytes
+};
+
+// The tile with the least cost: rounds of as many tiles as the device runs at
+// once, each as long as its MMAs or its epilogue, then one epilogue.  In ns,
+// fitted to 1900 timings (both types, M 1 .. 8192, N 1000 .. 28672, K 1024 ..
+// 14336, every width; the tile chosen takes 1.01 times the best one's time on
+// average, 1.11 at most above one row): a k-block takes a pair of CTAs 160 or
+// 0.7 a column, one CTA 180 or 60 + 0.75 a column (it loads twice the rows of
+// W for the same MMAs: 8192 x 28672 x 4096 e4m3 621 us against 526), an
+// epilogue 1200 + 8 a column, starting a pair 1000.  At most 64 rows wait for
+// the instructions of the MMAs and their stages, whatever the width.
+void choose_tile(int64_t M, int64_t N, int64_t kb, int sms, bool swiglu, Plan* q) {
+  const bool few = M <= kDirectRows;
+  const int step = few ? (swiglu ? 32 : 16) : (swiglu ? 64 : 32);
+  double least = 1e300;
+  for (int ctas = 1; ctas <= (M > BM ? 2 : 1); ++ctas)
+    // (with few rows a second round of narrow tiles streams W better than one
+    // of wide tiles: 64 x 28672 x 4096 e4m3 22.3 us in tiles of 96, 23.1 in 192)
+    for (int bn = few ? 128 : 256; bn >= step; bn -= step) {
+      const int64_t tiles = (M + BM * ctas - 1) / (BM * ctas) * ((N + bn - 1) / bn);
+      const int64_t rounds = (tiles + sms / ctas - 1) / (sms / ctas);
+      const double block = few ? 350.0 + 3.0 * bn
+                           : ctas == 2 ? std::max(160.0, 0.7 * bn)
+                                       : std::max(180.0, 60.0 + 0.75 * bn);
+      const double epilogue = 1200.0 + 8.0 * bn;
+      const double cost = (ctas == 2 ? 1000.0 : 0.0) +
+                          static_cast<double>(rounds) * std::max(kb * block, epilogue) + epilogue;
+      if (cost < least) {
+        least = cost;
+        q->ctas = ctas;
+        q->bn = bn;
+      }
     }
+}
+
+Plan fused_plan(int64_t M, int64_t N, uint64_t row_bytes, int sms, bool swiglu, bool residual) {
+  Plan q{};
+  const int64_t kb = static_cast<int64_t>((row_bytes + kBlockBytes - 1) / kBlockBytes);
+  choose_tile(M, N, kb, sms, swiglu, &q);
+  // the MMA always reads a window of 128 rows (64 up to 64 rows), whose rows
+  // past M reach accumulator rows that are never stored
+  q.a_rows = M <= 32 ? 32 : M <= 64 ? 64 : BM;
+  // epilogue buffers: two a warp to store from while the next is made, with a
+  // residual one more for the chunk fetched ahead (8192 x 14336 x 1024: 175 us
+  // with one ahead, 171 with two or three, which take stages from long K)
+  q.bufs = M <= kDirectRows ? 0 : residual ? 3 : 2;
+  q.ring = kPoolBytes - kEpiWarps * q.bufs * kChunkBytes;
+  // k-blocks per stage, where three such stages fit: one copy then reads
+  // kg * 128 contiguous bytes of each row, and the instructions around a stage
+  // are shared (16 x 4096 x 14336 bf16: 23 us with four, 25 with two); four
+  // only where K fills the ring twice (16 x 4096 x 4096 e4m3: 6.4 us with two,
+  // 6.9 with four)
+  const int sub = (q.a_rows + q.bn / q.ctas) * kBlockBytes;
+  q.kg = 1;
+  if (q.ctas == 1 && row_bytes % kBlockBytes == 0)
+    for (int g = kb >= 64 ? 4 : 2; g > 1; g /= 2)
+      if (g <= kb && 3 * g * sub <= q.ring) {
+        q.kg = g;
+        break;
+      }
+  q.stages = std::min(kMaxStages, q.ring / (q.kg * sub));
+  // the last window of A stays inside the ring
+  while (q.stages * q.kg * q.a_rows + BM - q.a_rows > q.ring / kBlockBytes) --q.stages;
+  return q;
+}
+
+// Pairs of CTAs that fit on the device at once (0 on failure); the same for
+// both operand types, asked once per device.
+int resident_pairs() {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
+  int d = -1;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return 0;
+  int n = known[d].load(std::memory_order_relaxed);
+  if (n == 0) {
+    const auto kernel = gemm_fused_kernel<true, 2>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemBytes)) != cudaSuccess)
+      return 0;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) return 0;
+    known[d].store(n, std::memory_order_relaxed);
   }
-  return best;
+  return n;
+}
+
+template <bool kQ8, int kCtas>
+bi_status launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
+                 const CUtensorMap& tr, const FusedParams& p, int grid, cudaStream_t s) {
+  const auto kernel = gemm_fused_kernel<kQ8, kCtas>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kSmemBytes)) != cudaSuccess)
+    return BI_ERR_CUDA;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCtas == 1 ? 1 : 2;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, ta, tb, tc, tr, p));
 }
 
 }  // namespace
@@ -367,6 +717,7 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   if (sms <= 0) return BI_ERR_CUDA;
   const bool swiglu = act == BI_ACT_SWIGLU;
   const uint64_t row_bytes = static_cast<uint64_t>(K) * (q8 ? 1 : 2);
+  const Plan plan = fused_plan(M, N, row_bytes, sms, swiglu, residual != nullptr);
   FusedParams p{};
   p.C = static_cast<__nv_bfloat16*>(C);
   p.bias = static_cast<const __nv_bfloat16*>(bias);
@@ -378,49 +729,50 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   p.N = static_cast<int>(N);
   p.n_out = static_cast<int>(swiglu ? N / 2 : N);
   p.act = act;
-  p.bn = tile_width(M, N, sms, swiglu);
-  // rows of A per stage: the MMA always reads a window of 128 rows, whose
-  // rows past M reach accumulator rows that are never stored
-  p.a_rows = M <= 32 ? 32 : M <= 64 ? 64 : BM;
+  p.bn = plan.bn;
+  p.a_rows = plan.a_rows;
+  p.kg = plan.kg;
+  p.stages = plan.stages;
+  p.bufs = plan.bufs;
+  p.ring = plan.ring;
   p.kb_total = static_cast<int>((row_bytes + kBlockBytes - 1) / kBlockBytes);
-  // k-blocks per stage: one copy then reads kg * 128 contiguous bytes of each
-  // row; at least four stages
-  const int sub = (p.a_rows + p.bn) * kBlockBytes;
-  p.kg = 1;
-  if (row_bytes % kBlockBytes == 0)
-    for (int g = 4; g > 1; g /= 2)
-      if (g <= p.kb_total && 4 * g * sub <= kRingBytes) {
-        p.kg = g;
-        break;
-      }
-  // (the last window of A stays inside the ring: with stages of at most four
-  // k-blocks A takes at most 8 * 4 of its tiles, and W's follow them)
-  p.stages = std::min(kMaxStages, kRingBytes / (p.kg * sub));
-  while (p.stages * p.kg * p.a_rows + BM - p.a_rows > kRingBytes / kBlockBytes) --p.stages;
-  p.m_tiles = static_cast<int>((M + BM - 1) / BM);
+  const int rows = BM * plan.ctas;
+  p.m_tiles = static_cast<int>((M + rows - 1) / rows);
   p.n_tiles = static_cast<int>((N + p.bn - 1) / p.bn);
   // (a block's tile index passes the last one by at most a grid)
   if (static_cast<int64_t>(p.m_tiles) * p.n_tiles > 0x7fffffff - sms) return BI_ERR_UNSUPPORTED;
   // raster: about 40 MB of the smaller operand stay in L2 per group
   p.m_fast = M <= N ? 1 : 0;
-  const int64_t tile_bytes = static_cast<int64_t>(p.m_fast ? BM : p.bn) * row_bytes;
+  const int64_t tile_bytes = static_cast<int64_t>(p.m_fast ? rows : p.bn) * row_bytes;
   const int64_t span = p.m_fast ? p.m_tiles : p.n_tiles;
   p.group = static_cast<int>(
       std::min(span, std::max<int64_t>(1, (int64_t(40) << 20) / std::max<int64_t>(1, tile_bytes))));
-  p.idesc = q8 ? umma_idesc_e4m3(BM, p.bn) : umma_idesc_bf16(BM, p.bn, false, false);
-  CUtensorMap ta, tb;
+  // up to 64 rows the MMA takes 64 (an element's sum is the same): below some
+  // 100 columns its time goes by its rows, not by them
+  p.mma_rows = M <= kDirectRows ? 64 : BM;
+  const int mma = p.mma_rows * plan.ctas;
+  p.idesc = q8 ? umma_idesc_e4m3(mma, p.bn) : umma_idesc_bf16(mma, p.bn, false, false);
+  CUtensorMap ta, tb, tc{}, tr{};
   const uint64_t ra = static_cast<uint64_t>(M), rb = static_cast<uint64_t>(N);
-  if (!make_tmap_rows(&ta, A, ra, row_bytes, p.a_rows, p.kg) ||
-      !make_tmap_rows(&tb, W, rb, row_bytes, p.bn, p.kg))
+  if (!make_tmap_rows(&ta, A, ra, row_bytes, plan.a_rows, plan.kg) ||
+      !make_tmap_rows(&tb, W, rb, row_bytes, p.bn / plan.ctas, plan.kg))
+    return BI_ERR_CUDA;
+  if (plan.bufs > 0 && (!make_tmap_chunks(&tc, C, ra, static_cast<uint64_t>(p.n_out)) ||
+                        (residual && !make_tmap_chunks(&tr, residual, ra,
+                                                       static_cast<uint64_t>(p.n_out)))))
     return BI_ERR_CUDA;
   const int units = p.m_tiles * p.n_tiles;
-  const int grid = std::min(units, sms);
-  const auto kernel = q8 ? gemm_fused_kernel<true> : gemm_fused_kernel<false>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kSmemBytes)) != cudaSuccess)
-    return BI_ERR_CUDA;
-  kernel<<<grid, kThreads, kSmemBytes, s>>>(ta, tb, p);
-  return cuda_status(cudaGetLastError());
+  int blocks = sms;
+  if (plan.ctas == 2) {
+    blocks = resident_pairs();
+    if (blocks <= 0) return BI_ERR_CUDA;
+  }
+  const int grid = std::min(units, blocks) * plan.ctas;
+  if (plan.ctas == 2)
+    return q8 ? launch<true, 2>(ta, tb, tc, tr, p, grid, s)
+              : launch<false, 2>(ta, tb, tc, tr, p, grid, s);
+  return q8 ? launch<true, 1>(ta, tb, tc, tr, p, grid, s)
+            : launch<false, 1>(ta, tb, tc, tr, p, grid, s);
 }
 
 }  // namespace bi

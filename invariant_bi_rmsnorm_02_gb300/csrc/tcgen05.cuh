@@ -65,12 +65,65 @@ __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
       : "memory");
 }
 
+// Whether this is the one thread of the warp, the same one every time, that
+// is elected (all lanes call).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+// D = A B (+ D if accumulate) for e4m3 (kQ8) or bf16 operands, over one CTA or
+// a pair (cta_group::2, issued by the even one: A's and B's rows come half
+// from each CTA's shared memory, the descriptors hold for both, and D's rows
+// stay half in each CTA's tensor memory).
+template <bool kQ8, bool kPair>
+__device__ __forceinline__ void tc_mma_any(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+#define BI_MMA(GROUP, KIND)                                                              \
+  asm volatile(                                                                          \
+      "{\n\t.reg .pred p;\n\t"                                                          \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                        \
+      "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(  \
+          d_tmem),                                                                       \
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)                                \
+      : "memory")
+  if constexpr (kQ8 && kPair) BI_MMA("2", "f8f6f4");
+  else if constexpr (kQ8) BI_MMA("1", "f8f6f4");
+  else if constexpr (kPair) BI_MMA("2", "f16");
+  else BI_MMA("1", "f16");
+#undef BI_MMA
+}
+
 // Arrive on `bar` once every MMA issued so far by this thread has completed.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_u32(bar))
       : "memory");
+}
+
+// The same for MMAs of a pair of CTAs: on the barrier at this offset in both
+// CTAs (kBoth) or in this one alone.
+template <bool kPair, bool kBoth>
+__device__ __forceinline__ void tc_commit_any(uint64_t* bar) {
+  if constexpr (kPair && kBoth)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+        ".multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_u32(bar))
+        : "memory");
+  else
+    tc_commit(bar);
 }
 
 // Allocate `cols` TMEM columns (a power of two >= 32); the base address is
@@ -84,6 +137,19 @@ __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
 }
 __device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
+               : "memory");
+}
+
+// The same for a pair of CTAs, one warp of each; both get as many columns.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(slot)),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t base, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
                : "memory");
 }
 
