@@ -114,9 +114,10 @@ size_t bi_rmsnorm_workspace_size(int64_t M, int64_t H, bi_mode mode);
  *   y[j] = e4m3(448 v[j] / t), rounded to nearest even,
  * so that y[j] * scale stands for v[j] (off by at most 2^-4 of its magnitude or
  * 2^-10 of the scale, whichever is larger) and the row's largest magnitude is
- * stored as 448.  The scale and the quotient are fp32, each rounded once.  A
- * row with an infinity or a NaN is stored as zeros under the scale NaN and
- * stands for NaN throughout.
+ * stored as 448.  The scale is fp32, rounded once; the quotient is fp32 too:
+ * bi_quantize_q8's rounded once (so that the codes are the formula's, ties
+ * included), the norms' v[j] times the rounded 448 / t.  A row with an infinity
+ * or a NaN is stored as zeros under the scale NaN and stands for NaN throughout.
  * Every row depends on its own values only.
  * Common requirements: y [M,H] bytes and 16-byte aligned, y_scale [M] 4-byte
  *   aligned; H % 16 == 0, 16 <= H <= 65536, 0 <= M < 2^31 (0 is a no-op).

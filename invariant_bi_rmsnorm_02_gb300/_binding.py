@@ -363,6 +363,8 @@ def _dptr(t, dtype, dev, name):
         return None
     try:
         on = t.get_device()
+        if on == dev and t.dtype is dtype and t.is_contiguous():
+            return t.data_ptr()
     except AttributeError:
         raise TypeError("%s must be a CUDA tensor" % name) from None
     if on != dev:
@@ -371,9 +373,18 @@ def _dptr(t, dtype, dev, name):
         raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, on, dev))
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
+
+
+_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+def _here(stream):
+    """(current device, the stream's handle), asking for the device once."""
+    dev = torch.cuda.current_device()
+    if stream is None and _raw_stream is not None:
+        return dev, _raw_stream(dev)
+    return dev, _stream(stream)
 
 
 def _cache_q8(cache, Hkv, D) -> int:
@@ -499,11 +510,11 @@ def bi_rmsnorm_q8(x, w, y, y_scale, eps, stream=None):
     M, H = shape
     if y.shape != shape or w.shape != (H,) or y_scale.shape != (M,):
         raise ValueError("y must have x's shape, w [H] and y_scale [M]")
-    dev = torch.cuda.current_device()
+    dev, on = _here(stream)
     _check(load().bi_rmsnorm_q8(
-        _dptr(x, torch.bfloat16, dev, "x"), _dptr(w, torch.bfloat16, dev, "w"),
-        _dptr(y, torch.float8_e4m3fn, dev, "y"), _dptr(y_scale, torch.float32, dev, "y_scale"),
-        M, H, float(eps), _stream(stream)), "bi_rmsnorm_q8")
+        _dptr(x, _BF16, dev, "x"), _dptr(w, _BF16, dev, "w"),
+        _dptr(y, _E4M3, dev, "y"), _dptr(y_scale, _F32, dev, "y_scale"),
+        M, H, float(eps), on), "bi_rmsnorm_q8")
 
 
 def bi_add_rmsnorm_q8(x, residual, w, h, y, y_scale, eps, stream=None):
@@ -514,12 +525,12 @@ def bi_add_rmsnorm_q8(x, residual, w, h, y, y_scale, eps, stream=None):
     if residual.shape != shape or h.shape != shape or y.shape != shape or w.shape != (H,) \
             or y_scale.shape != (M,):
         raise ValueError("residual, h and y must have x's shape, w [H] and y_scale [M]")
-    dev = torch.cuda.current_device()
+    dev, on = _here(stream)
     _check(load().bi_add_rmsnorm_q8(
-        _dptr(x, torch.bfloat16, dev, "x"), _dptr(residual, torch.bfloat16, dev, "residual"),
-        _dptr(w, torch.bfloat16, dev, "w"), _dptr(h, torch.bfloat16, dev, "h"),
-        _dptr(y, torch.float8_e4m3fn, dev, "y"), _dptr(y_scale, torch.float32, dev, "y_scale"),
-        M, H, float(eps), _stream(stream)), "bi_add_rmsnorm_q8")
+        _dptr(x, _BF16, dev, "x"), _dptr(residual, _BF16, dev, "residual"),
+        _dptr(w, _BF16, dev, "w"), _dptr(h, _BF16, dev, "h"),
+        _dptr(y, _E4M3, dev, "y"), _dptr(y_scale, _F32, dev, "y_scale"),
+        M, H, float(eps), on), "bi_add_rmsnorm_q8")
 
 
 def bi_quantize_q8(x, y, y_scale, stream=None):
@@ -528,10 +539,10 @@ def bi_quantize_q8(x, y, y_scale, stream=None):
     M, K = shape
     if y.shape != shape or y_scale.shape != (M,):
         raise ValueError("y must have x's shape and y_scale [M]")
-    dev = torch.cuda.current_device()
+    dev, on = _here(stream)
     _check(load().bi_quantize_q8(
-        _dptr(x, torch.bfloat16, dev, "x"), _dptr(y, torch.float8_e4m3fn, dev, "y"),
-        _dptr(y_scale, torch.float32, dev, "y_scale"), M, K, _stream(stream)), "bi_quantize_q8")
+        _dptr(x, _BF16, dev, "x"), _dptr(y, _E4M3, dev, "y"),
+        _dptr(y_scale, _F32, dev, "y_scale"), M, K, on), "bi_quantize_q8")
 
 
 def _fused_shapes(A, W, C, bias, residual, activation):
@@ -548,11 +559,11 @@ def _fused_shapes(A, W, C, bias, residual, activation):
 def bi_gemm_epilogue(A, W, C, bias=None, residual=None, activation=ACT_NONE, stream=None):
     """C <- act(A W^T + bias) + residual (include/bi.h); residual may be C."""
     M, N, K = _fused_shapes(A, W, C, bias, residual, activation)
-    dev = torch.cuda.current_device()
+    dev, on = _here(stream)
     _check(load().bi_gemm_epilogue(
-        _dptr(A, torch.bfloat16, dev, "A"), _dptr(W, torch.bfloat16, dev, "W"),
-        _dptr(bias, torch.bfloat16, dev, "bias"), _dptr(residual, torch.bfloat16, dev, "residual"),
-        _dptr(C, torch.bfloat16, dev, "C"), M, N, K, int(activation), _stream(stream)),
+        _dptr(A, _BF16, dev, "A"), _dptr(W, _BF16, dev, "W"),
+        _dptr(bias, _BF16, dev, "bias"), _dptr(residual, _BF16, dev, "residual"),
+        _dptr(C, _BF16, dev, "C"), M, N, K, int(activation), on),
         "bi_gemm_epilogue")
 
 
@@ -563,12 +574,12 @@ def bi_gemm_q8(A, a_scale, W, w_scale, C, bias=None, residual=None, activation=A
     M, N, K = _fused_shapes(A, W, C, bias, residual, activation)
     if a_scale.shape != (M,) or w_scale.shape != (N,):
         raise ValueError("a_scale must be [M] and w_scale [N]")
-    dev = torch.cuda.current_device()
+    dev, on = _here(stream)
     _check(load().bi_gemm_q8(
-        _dptr(A, torch.float8_e4m3fn, dev, "A"), _dptr(a_scale, torch.float32, dev, "a_scale"),
-        _dptr(W, torch.float8_e4m3fn, dev, "W"), _dptr(w_scale, torch.float32, dev, "w_scale"),
-        _dptr(bias, torch.bfloat16, dev, "bias"), _dptr(residual, torch.bfloat16, dev, "residual"),
-        _dptr(C, torch.bfloat16, dev, "C"), M, N, K, int(activation), _stream(stream)),
+        _dptr(A, _E4M3, dev, "A"), _dptr(a_scale, _F32, dev, "a_scale"),
+        _dptr(W, _E4M3, dev, "W"), _dptr(w_scale, _F32, dev, "w_scale"),
+        _dptr(bias, _BF16, dev, "bias"), _dptr(residual, _BF16, dev, "residual"),
+        _dptr(C, _BF16, dev, "C"), M, N, K, int(activation), on),
         "bi_gemm_q8")
 
 

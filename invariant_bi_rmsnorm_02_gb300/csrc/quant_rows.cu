@@ -5,19 +5,22 @@
 //   y_j = e4m3(448 v_j / t)
 //
 // so that y * scale stands for v and the largest magnitude is stored as 448,
-// the largest e4m3 number.  The quotient is formed from v and t directly,
-// rounded once to fp32, and not from the rounded scale: for a bf16 row it is
-// exact wherever it lies midway between two e4m3 numbers, so ties go to the
-// even one as the formula says.  A row with an infinity or a NaN gets the
-// scale NaN and zeros.
+// the largest e4m3 number.  A row with an infinity or a NaN gets the scale NaN
+// and zeros.  Rows of a bf16 matrix take the quotient of 448 v and t rounded
+// once to fp32 (exact where it lies midway between two e4m3 numbers, so ties,
+// which such quotients do hit, go to the even one); the norm's fp32 values v,
+// which hit no ties but by chance, take v times the rounded 448 / t.
 //
 // Each row is a function of its own elements only, in an order fixed by its
 // length: the norm's reduction is the batch-invariant RMSNorm's
 // (rmsnorm_row.cuh; v is exactly that kernel's fp32 value), and a maximum does
 // not depend on its order.
 //
-// Bound by memory: a row is read once and kept in registers.  One row per
-// block, or one per warp (eight a block) where the row's shape is one warp.
+// A row is read once and kept in registers; one row per block, or one per warp
+// (eight a block) where the row's shape is one warp.  What bounds it at first
+// is instructions, not memory (33 million elements at 16 instructions each are
+// 15 us of issue slots, against 15 of memory), so products and quotients are
+// formed two at a time (f32x2).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -33,6 +36,38 @@ constexpr float kTop = 448.0f;                    // the largest e4m3 number
 constexpr float kLeastTop = 448.0f * 0x1p-126f;   // a scale is never below 2^-126
 constexpr int kRowsPerBlock = 8;                  // of rows of one warp each
 
+// Two floats for the packed operations, each half rounded as its own.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
+__device__ __forceinline__ float2 halves(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// The bf16 pair w as floats.
+__device__ __forceinline__ uint64_t widen2(uint32_t w) { return pair(bf16_lo(w), bf16_hi(w)); }
+
+// max(a, |b|), a NaN where either is one
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
 // The largest magnitude's bits over the row (fp32 magnitudes order as
 // integers, NaN above infinity above the rest).
 template <bool kWarpRow>
@@ -46,82 +81,22 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   return __reduce_max_sync(kFull, lane < nw ? red[lane] : 0u);
 }
 
-// 448 v / t of a row's values.  A quotient q = RN(u r), r = RN(1 / t),
-// corrected by its exact remainder is the correctly rounded u / t (Markstein,
-// IBM J. Res. Dev. 34, 1990) while no step over- or underflows; so u and t are
-// taken times a power of two that brings t between 2^-53 and 2^64 (quotients
-// whose remainder still underflows are far below the least e4m3 number).
-struct RowDivisor {
-  float c, t, r;
-  __device__ explicit RowDivisor(float top) {
-    const float p = top < 0x1p-40f ? 0x1p64f : top > 0x1p60f ? 0x1p-64f : 1.0f;
-    c = 0.875f * p;  // 448 / 512
-    t = top * p;
-    r = __fdiv_rn(1.0f, t);
-  }
-  __device__ __forceinline__ float operator()(float v) const {
-    const float u = __fmul_rn(v, c);
-    const float q = __fmul_rn(u, r);
-    // (the remainder's sign the way round that keeps a zero's sign)
-    return __fmul_rn(__fmaf_rn(__fmaf_rn(q, t, -u), -r, q), 512.0f);
+// What a row's largest magnitude (bits) gives: whether it is finite, and t.
+// The row's first thread stores the scale.
+struct RowTop {
+  bool fine;
+  float t;
+  __device__ RowTop(uint32_t top, bool first, float* scale) {
+    fine = top < 0x7f800000u;
+    t = fmaxf(__uint_as_float(top), kLeastTop);
+    if (first) *scale = fine ? __fdiv_rn(t, kTop) : __uint_as_float(0x7fffffffu);
   }
 };
 
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t e4m3x4(uint64_t a, uint64_t b) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(halves(a), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(halves(b), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
-}
-
-__device__ __forceinline__ uint32_t magnitude(float v) {
-  return __float_as_uint(v) & 0x7fffffffu;
-}
-
-__device__ __forceinline__ void widen8(const uint4& x, float (&v)[8]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-
-// One row's vectors of 8 values as this thread holds them: vector
-// first + k * stride of the row, k < VPT.  `values(k, i, v)` gives the 8
-// values of vector i (again in the second pass: a few products cost less than
-// the registers that would hold them).
-template <int VPT, bool kWarpRow, typename Values>
-__device__ __forceinline__ void quantise_row(const Values& values, uint32_t* red,
-                                             uint2* __restrict__ y, float* __restrict__ scale,
-                                             int64_t row, int nvec, int first, int stride) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int i = first + k * stride;
-    if (i >= nvec) continue;
-    float v[8];
-    values(k, i, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[e]));
-  }
-  top = row_max<kWarpRow>(top, red);
-  const bool fine = top < 0x7f800000u;
-  const float t = fmaxf(__uint_as_float(top), kLeastTop);
-  if (first == 0) scale[row] = fine ? __fdiv_rn(t, kTop) : __uint_as_float(0x7fffffffu);
-  const RowDivisor part(t);
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int i = first + k * stride;
-    if (i >= nvec) continue;
-    uint2 o = make_uint2(0u, 0u);
-    if (fine) {
-      float v[8];
-      values(k, i, v);
-      o = make_uint2(e4m3x4(part(v[0]), part(v[1]), part(v[2]), part(v[3])),
-                     e4m3x4(part(v[4]), part(v[5]), part(v[6]), part(v[7])));
-    }
-    __stcs(y + row * nvec + i, o);
-  }
 }
 
 // kAdd: h = bf16(x + res) first, written to h (which may be x or res: a
@@ -160,22 +135,44 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
   for (int k = 0; k < VPT; ++k) ss = sum_squares8(hv[k], ss);
   // (a row of one warp: block_sum's second butterfly adds zeros)
   const float r = inv_rms(kWarpRow ? warp_sum(ss) : block_sum(ss, red), inv_h, eps);
-  quantise_row<VPT, kWarpRow>(
-      [&](int k, int i, float (&v)[8]) {
-        float g[8];
-        widen8(__ldg(w + i), g);
-        widen8(hv[k], v);
+  const uint64_t r2 = both(r);
+  uint64_t v[VPT][4];
+  float top = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(__fmul_rn(v[e], r), g[e]);
-      },
-      red_max, y, scale, row, nvec, first, stride);
+  for (int k = 0; k < VPT; ++k) {
+    const int i = first + k * stride;
+    const uint4 wv = i < nvec ? __ldg(w + i) : make_uint4(0, 0, 0, 0);
+    const uint32_t hw[4] = {hv[k].x, hv[k].y, hv[k].z, hv[k].w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[k][e] = mul2(mul2(widen2(hw[e]), r2), widen2(ww[e]));
+    if (i >= nvec) continue;  // (0 times an infinite r is no element's value)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = halves(v[k][e]);
+      top = max_nan(max_nan(top, f.x), f.y);
+    }
+  }
+  const RowTop t(row_max<kWarpRow>(__float_as_uint(top), red_max), first == 0, scale + row);
+  // (t is between 2^-117.2 and 2^128, so 448 / t is a normal number)
+  const uint64_t q = both(__fdiv_rn(kTop, t.t));
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int i = first + k * stride;
+    if (i >= nvec) continue;
+    uint2 o = make_uint2(0u, 0u);
+    if (t.fine) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[k][e] = mul2(v[k][e], q);
+      o = make_uint2(e4m3x4(v[k][0], v[k][1]), e4m3x4(v[k][2], v[k][3]));
+    }
+    __stcs(y + row * nvec + i, o);
+  }
 }
 
 template <int VPT, bool kWarpRow>
-__global__ void __launch_bounds__(1024) quantize_q8_kernel(const uint4* __restrict__ x,
-                                                           uint2* __restrict__ y,
-                                                           float* __restrict__ scale, int64_t M,
-                                                           int nvec) {
+__global__ void __launch_bounds__(1024) quantize_q8_kernel(
+    const uint4* __restrict__ x, uint2* __restrict__ y, float* __restrict__ scale, int64_t M,
+    int nvec) {
   __shared__ uint32_t red_max[32];
   const int first = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
   const int stride = kWarpRow ? 32 : blockDim.x;
@@ -188,8 +185,46 @@ __global__ void __launch_bounds__(1024) quantize_q8_kernel(const uint4* __restri
     const int i = first + k * stride;
     xv[k] = i < nvec ? __ldcs(x + row * nvec + i) : make_uint4(0, 0, 0, 0);
   }
-  quantise_row<VPT, kWarpRow>([&](int k, int, float (&v)[8]) { widen8(xv[k], v); }, red_max, y,
-                              scale, row, nvec, first, stride);
+  // bf16 magnitudes order as integers, two at a time
+  uint32_t top2 = 0;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const uint32_t w[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(w[e] & 0x7fff7fffu));
+  }
+  const uint32_t top = max(top2 & 0xffffu, top2 >> 16) << 16;
+  const RowTop t(row_max<kWarpRow>(top, red_max), first == 0, scale + row);
+  // (448 v) / t: a quotient q = RN(u r), r = RN(1 / t), corrected by its exact
+  // remainder is the correctly rounded u / t (Markstein, IBM J. Res. Dev. 34,
+  // 1990) while no step over- or underflows; so both are taken times a power of
+  // two p that brings t between 2^-53 and 2^64 (quotients whose remainder
+  // underflows all the same are far below the least e4m3 number).  u = 448 v is
+  // exact for a bf16 v.
+  const float p = t.t < 0x1p-40f ? 0x1p64f : t.t > 0x1p60f ? 0x1p-64f : 1.0f;
+  const float d = __fmul_rn(t.t, p), inv = __fdiv_rn(1.0f, d), top_p = __fmul_rn(kTop, p);
+  const uint64_t c = both(top_p), minus_c = both(-top_p), d2 = both(d), r2 = both(inv),
+                 minus_r2 = both(-inv);
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int i = first + k * stride;
+    if (i >= nvec) continue;
+    uint2 o = make_uint2(0u, 0u);
+    if (t.fine) {
+      const uint32_t w[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
+      uint64_t q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t v = widen2(w[e]);
+        q[e] = mul2(mul2(v, c), r2);
+        // (the remainder's sign the way round that keeps a zero's sign)
+        q[e] = fma2(fma2(q[e], d2, mul2(v, minus_c)), minus_r2, q[e]);
+      }
+      o = make_uint2(e4m3x4(q[0], q[1]), e4m3x4(q[2], q[3]));
+    }
+    __stcs(y + row * nvec + i, o);
+  }
 }
 
 template <int VPT, bool kAdd>

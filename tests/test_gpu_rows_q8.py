@@ -79,12 +79,12 @@ def test_rows_with_infinities_or_nan(cuda, K):
 
 
 def as_kernel_rounds(v32):
-    """codes and scale of fp32 rows, the quotient formed from fp32 steps: the
-    product with 448/512 and the quotient each rounded once."""
+    """codes and scale of fp32 rows: v times 448 / t, the quotient and the
+    product each rounded once to fp32."""
     v = v32.cpu().numpy()
     t = np.maximum(np.abs(v).max(1, keepdims=True), np.float32(linear8.LEAST_TOP))
-    q = (v * np.float32(0.875)) / t
-    return longctx.e4m3_codes(q.astype(np.float64) * 512.0), (t[:, 0] / np.float32(448.0))
+    q = v * (np.float32(448.0) / t)
+    return longctx.e4m3_codes(q.astype(np.float64)), (t[:, 0] / np.float32(448.0))
 
 
 @pytest.mark.parametrize("H", WIDTHS)
