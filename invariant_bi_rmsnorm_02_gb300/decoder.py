@@ -22,7 +22,16 @@ configuration may ask for rotary positions scaled for long contexts
 element (``kv_cache="e4m3"``): decode reads that cache as it is, a prompt chunk
 reads its sequences' pages back into one layer's worth of bf16 pages first, and
 the two still give the same bytes for the same position.  Weights are
-random (no trained checkpoint is needed for invariance); the shapes default to
+random (no trained checkpoint is needed for invariance).  With ``linear="e4m3"``
+the layers' four projections run on one byte an element, weights and inputs:
+
+    y8  = RMSNorm(h) * w as e4m3 rows                 bi_rmsnorm_q8
+    qkv = y8 W_qkv^T (+ bias)                         bi_gemm_q8
+    h  += a8 W_o^T, a8 the attention's rows           bi_quantize_q8, bi_gemm_q8
+    f   = silu(y8 W_gate^T) * y8 W_up^T               bi_rmsnorm_q8, bi_gemm_q8
+    h  += f8 W_down^T                                 bi_quantize_q8, bi_gemm_q8
+
+with the residual stream added in the products' epilogues.  The shapes default to
 Llama-3-8B's.  PyTorch only owns memory; every arithmetic step is a libbi call.
 
 A step's tokens are ordered decode rows first (one token per sequence, run by
@@ -79,12 +88,19 @@ class DecoderConfig:
     rope_low_turns: float = 1.0
     rope_high_turns: float | None = None # None: the scaling's published value (YaRN 32, Llama 3 4)
     kv_cache: str = "bf16"               # "bf16" or "e4m3" (one byte an element)
+    linear: str = "bf16"                 # the layers' projections: "bf16" or "e4m3"
+    qkv_bias: bool = False               # a bias on the query, key and value projection
 
     def __post_init__(self):
         if self.rope_scaling not in ROPE_SCALINGS:
             raise ValueError("rope_scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
         if self.kv_cache not in ("bf16", "e4m3"):
             raise ValueError('kv_cache must be "bf16" or "e4m3"')
+        if self.linear not in ("bf16", "e4m3"):
+            raise ValueError('linear must be "bf16" or "e4m3"')
+        if self.linear == "e4m3" and (self.hidden % 16 or self.heads * self.head_dim % 16
+                                      or self.ffn % 128):
+            raise ValueError("e4m3 projections need rows of a multiple of 16 elements")
         if self.kv_cache == "e4m3" and (self.page_size != 16 or self.head_dim not in (64, 128)):
             raise ValueError("an e4m3 cache needs pages of 16 tokens and heads of 64 or 128")
         if self.rope_dim is not None and (self.rope_dim % 2 or not 0 < self.rope_dim
@@ -123,12 +139,23 @@ TINY = DecoderConfig(layers=2, hidden=256, heads=4, kv_heads=2, head_dim=64, ffn
 SWIGLU_FUSE_MIN_ROWS = 128
 
 
+def _rows_in_blocks_of_16(ffn, device):
+    """Rows of a gate/up weight in blocks of 128 features, in the order of
+    blocks of 16 (what ACT_SWIGLU's product reads)."""
+    r = torch.arange(2 * ffn, device=device)
+    feature, up = r // 32 * 16 + r % 16, r % 32 // 16
+    return feature // 128 * 256 + up * 128 + feature % 128
+
+
 class DecoderWeights:
     """Random bf16 weights N(0, init_std^2), norm weights 1.  Linear weights
     are [out, in] (the GEMM's W [N, K]); the q/k/v and gate/up projections are
     stacked into one matrix each, the gate/up one in blocks of 128 features
     (the block's gate rows, then its up rows: the layout bi_gemm_swiglu reads,
-    so the SwiGLU product comes out of the GEMM epilogue).  ``gen_device`` is
+    so the SwiGLU product comes out of the GEMM epilogue).  With e4m3
+    projections on a GPU, wqkv, wo, wgu and wdown hold (e4m3 rows, scales) of
+    the same numbers, wgu in blocks of 16 features (on the CPU they stay bf16, in
+    blocks of 128); with ``qkv_bias``, bqkv holds a bias per layer.  ``gen_device`` is
     where the numbers are drawn (CPU for configurations an oracle also reads,
     the GPU for speed)."""
 
@@ -144,14 +171,20 @@ class DecoderWeights:
         self.final_norm = torch.ones(H, dtype=torch.bfloat16, device=device)
         self.attn_norm, self.mlp_norm, self.wqkv, self.wo, self.wgu, self.wdown = ([] for _ in
                                                                                     range(6))
+        self.bqkv = []
+        q8 = cfg.linear == "e4m3" and torch.device(device).type == "cuda"
+        blocks = _rows_in_blocks_of_16(cfg.ffn, device) if q8 else None
+        held = bi.quantize_q8 if q8 else (lambda w: w)
         for layer in range(cfg.layers):
             k = 16 * (layer + 1)
             self.attn_norm.append(torch.ones(H, dtype=torch.bfloat16, device=device))
             self.mlp_norm.append(torch.ones(H, dtype=torch.bfloat16, device=device))
-            self.wqkv.append(draw((cfg.qkv_dim, H), k + 1))
-            self.wo.append(draw((H, cfg.heads * cfg.head_dim), k + 2))
-            self.wgu.append(draw((2 * cfg.ffn, H), k + 3))
-            self.wdown.append(draw((H, cfg.ffn), k + 4))
+            self.wqkv.append(held(draw((cfg.qkv_dim, H), k + 1)))
+            self.wo.append(held(draw((H, cfg.heads * cfg.head_dim), k + 2)))
+            wgu = draw((2 * cfg.ffn, H), k + 3)
+            self.wgu.append(held(wgu[blocks] if q8 else wgu))
+            self.wdown.append(held(draw((H, cfg.ffn), k + 4)))
+            self.bqkv.append(draw((cfg.qkv_dim,), k + 5) if cfg.qkv_bias else None)
 
 
 @dataclass
@@ -257,8 +290,13 @@ class Decoder:
                                   buf(T, c.kv_heads, c.head_dim))
         self.att, self.o = buf(T, c.heads, c.head_dim), buf(T, H)
         self.act, self.delta = buf(T, c.ffn), buf(T, H)
-        # the gate/up projection of steps below SWIGLU_FUSE_MIN_ROWS tokens
-        self.gu = buf(min(T, SWIGLU_FUSE_MIN_ROWS - 1), 2 * c.ffn)
+        if c.linear == "e4m3":
+            # a projection's input at a time, and its scales
+            self.x8 = buf(T * max(H, c.heads * c.head_dim, c.ffn), dtype=torch.float8_e4m3fn)
+            self.x8_scale = buf(T, dtype=torch.float32)
+        else:
+            # the gate/up projection of steps below SWIGLU_FUSE_MIN_ROWS tokens
+            self.gu = buf(min(T, SWIGLU_FUSE_MIN_ROWS - 1), 2 * c.ffn)
         self.ys, self.logits = buf(max_seqs, H), buf(max_seqs, c.vocab)
         self.tokens_out = buf(max_seqs, dtype=torch.int32)
         self.tokens_host = torch.empty(max_seqs, dtype=torch.int32, pin_memory=True)
@@ -322,6 +360,21 @@ class Decoder:
             ws = self._workspace(bi.bi_gemm_workspace_size(T, W.shape[0], A.shape[1], self.mode))
         bi.bi_gemm_swiglu(A, W, out, self.mode, 0, ws)
 
+    # a projection's input as e4m3 rows, in the one buffer for it (the calls run
+    # in stream order: its last reader is done)
+    def _held_q8(self, T, width):
+        return self.x8[:T * width].view(T, width), self.x8_scale[:T]
+
+    def _norm_q8(self, h, norm):
+        x8, xs = self._held_q8(*h.shape)
+        bi.bi_rmsnorm_q8(h, norm, x8, xs, self.cfg.eps)
+        return x8, xs
+
+    def _rows_q8(self, x):
+        x8, xs = self._held_q8(*x.shape)
+        bi.bi_quantize_q8(x, x8, xs)
+        return x8, xs
+
     def step(self, plan: StepPlan) -> np.ndarray:
         """Run one forward step; returns the chosen tokens of plan.sample_rows
         (host int32)."""
@@ -332,6 +385,8 @@ class Decoder:
             raise ValueError("step outside the decoder's buffers")
         if plan.table.shape[1] != self.max_blocks:
             raise ValueError("page table width differs from max_blocks")
+        if self.mode != bi.INVARIANT and (c.linear != "bf16" or c.qkv_bias):
+            raise ValueError("e4m3 projections and a bias have no batch-variant form")
         p = self.pack
         p.add(plan.tokens.astype(np.int32), torch.int32)
         p.add(plan.pos.astype(np.int32), torch.int32)
@@ -382,16 +437,27 @@ class Decoder:
         keep = self.capture is not None and not torch.cuda.is_current_stream_capturing()
         cap = self._keep if keep else (lambda *a: None)
         h, y = self.h[:T], self.y[:T]
+        l8 = c.linear == "e4m3"
         bi.bi_gather_rows(w.embed, tok, h)
-        bi.bi_rmsnorm(h, w.attn_norm[0], y, c.eps, mode, self._ws_norm(T))
+        if not l8:
+            bi.bi_rmsnorm(h, w.attn_norm[0], y, c.eps, mode, self._ws_norm(T))
         delta = self.delta[:T]
         for layer in range(c.layers):
-            if layer:
+            if layer and not l8:
                 bi.bi_add_rmsnorm(delta, h, w.attn_norm[layer], y, c.eps, mode, self._ws_norm(T))
             cap(layer, "h", h)
-            cap(layer, "y_attn", y)
             qkv = self.qkv[:T]
-            self._gemm(y, w.wqkv[layer], qkv)
+            if l8:
+                x8, xs = self._norm_q8(h, w.attn_norm[layer])
+                cap(layer, "y8_attn", x8)
+                cap(layer, "y8_attn_scale", xs)
+                bi.bi_gemm_q8(x8, xs, *w.wqkv[layer], qkv, bias=w.bqkv[layer])
+            elif c.qkv_bias:
+                cap(layer, "y_attn", y)
+                bi.bi_gemm_epilogue(y, w.wqkv[layer], qkv, bias=w.bqkv[layer])
+            else:
+                cap(layer, "y_attn", y)
+                self._gemm(y, w.wqkv[layer], qkv)
             q, k, v = self.q[:T], self.k[:T], self.v[:T]
             if c.plain_rope:
                 bi.bi_rope_qkv(qkv, pos, c.heads, c.kv_heads, c.head_dim, c.rope_theta, q, k, v)
@@ -430,20 +496,35 @@ class Decoder:
                                          max_kv_len=kv_max, split_size=c.split_size,
                                          sm_scale=self.sm_scale, mode=mode)
             cap(layer, "att", att)
+            act = self.act[:T]
+            if l8:
+                x8, xs = self._rows_q8(att.view(T, c.heads * c.head_dim))
+                bi.bi_gemm_q8(x8, xs, *w.wo[layer], h, residual=h)
+                cap(layer, "h_mid", h)
+                x8, xs = self._norm_q8(h, w.mlp_norm[layer])
+                cap(layer, "y8_mlp", x8)
+                cap(layer, "y8_mlp_scale", xs)
+                bi.bi_gemm_q8(x8, xs, *w.wgu[layer], act, activation=bi.ACT_SWIGLU)
+                cap(layer, "act", act)
+                x8, xs = self._rows_q8(act)
+                bi.bi_gemm_q8(x8, xs, *w.wdown[layer], h, residual=h)
+                continue
             o = self.o[:T]
             self._gemm(att.view(T, c.heads * c.head_dim), w.wo[layer], o)
             cap(layer, "o", o)
             bi.bi_add_rmsnorm(o, h, w.mlp_norm[layer], y, c.eps, mode, self._ws_norm(T))
             cap(layer, "h_mid", h)
             cap(layer, "y_mlp", y)
-            act = self.act[:T]
             self._gemm_swiglu(y, w.wgu[layer], act)
             if T < SWIGLU_FUSE_MIN_ROWS:
                 cap(layer, "gate_up", self.gu[:T])
             cap(layer, "act", act)
             self._gemm(act, w.wdown[layer], delta)
             cap(layer, "delta", delta)
-        bi.bi_add_rmsnorm(delta, h, w.final_norm, y, c.eps, mode, self._ws_norm(T))
+        if l8:
+            bi.bi_rmsnorm(h, w.final_norm, y, c.eps, mode, self._ws_norm(T))
+        else:
+            bi.bi_add_rmsnorm(delta, h, w.final_norm, y, c.eps, mode, self._ws_norm(T))
         cap(-1, "h", h)
         cap(-1, "y_final", y)
         if n_s == 0:

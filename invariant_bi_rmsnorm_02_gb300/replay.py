@@ -9,6 +9,7 @@ request's output does not depend on the batch around it).
     python -m invariant_bi_rmsnorm_02_gb300.replay            # 256 requests
     python -m invariant_bi_rmsnorm_02_gb300.replay --requests 32 --new-tokens 64
     python -m invariant_bi_rmsnorm_02_gb300.replay --kv-cache e4m3 --rope-scaling llama3
+    python -m invariant_bi_rmsnorm_02_gb300.replay --linear e4m3
 
 Mixes: every request at step 0 with all slots open; Poisson arrivals into
 fewer slots and a smaller token budget; and a few requests served alone.
@@ -74,13 +75,17 @@ def main(argv=None) -> int:
     ap.add_argument("--seed", type=int, default=5)
     ap.add_argument("--variant", action="store_true", help="also run the batch-variant kernels")
     ap.add_argument("--kv-cache", choices=("bf16", "e4m3"), default="bf16")
+    ap.add_argument("--linear", choices=("bf16", "e4m3"), default="bf16",
+                    help="the layers' projections")
     ap.add_argument("--rope-scaling", choices=tuple(ROPE_SCALINGS), default="none")
     ap.add_argument("--rope-factor", type=float, default=8.0,
                     help="how far --rope-scaling stretches the positions")
     a = ap.parse_args(argv)
+    if a.variant and a.linear != "bf16":
+        ap.error("e4m3 projections have no batch-variant form")
 
     dev = torch.device("cuda", torch.cuda.current_device())
-    cfg = dataclasses.replace(LLAMA3_8B, layers=a.layers, kv_cache=a.kv_cache,
+    cfg = dataclasses.replace(LLAMA3_8B, layers=a.layers, kv_cache=a.kv_cache, linear=a.linear,
                               rope_scaling=a.rope_scaling, rope_factor=a.rope_factor)
     reqs = synthetic_requests(a.requests, a.prompt_lo, a.prompt_hi, a.new_tokens, cfg.vocab,
                               seed=a.seed, mean_gap=2.0)

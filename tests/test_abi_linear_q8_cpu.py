@@ -170,3 +170,24 @@ def test_product_definition():
             g = a[i] @ w[32 * (j // 16) + j % 16] + b[32 * (j // 16) + j % 16]
             u = a[i] @ w[32 * (j // 16) + 16 + j % 16] + b[32 * (j // 16) + 16 + j % 16]
             assert math.isclose(got[i, j], g / (1 + math.exp(-g)) * u + r[i, j], rel_tol=1e-12)
+
+
+# ------------------------------------------------------- the decoder's options
+def test_the_decoders_configuration():
+    import dataclasses
+
+    from invariant_bi_rmsnorm_02_gb300.decoder import TINY, DecoderWeights, _rows_in_blocks_of_16
+    with pytest.raises(ValueError):
+        dataclasses.replace(TINY, linear="fp8")
+    with pytest.raises(ValueError):
+        dataclasses.replace(TINY, linear="e4m3", ffn=192)
+    with pytest.raises(ValueError):
+        dataclasses.replace(TINY, linear="e4m3", hidden=264)
+    a = DecoderWeights(TINY, 3, "cpu")
+    b = DecoderWeights(dataclasses.replace(TINY, linear="e4m3", qkv_bias=True), 3, "cpu")
+    for k in ("wqkv", "wo", "wgu", "wdown"):   # the same numbers, whatever holds them
+        assert all(torch.equal(x, y) for x, y in zip(getattr(a, k), getattr(b, k)))
+    assert a.bqkv == [None] * TINY.layers and b.bqkv[1].shape == (TINY.qkv_dim,)
+    rows = _rows_in_blocks_of_16(256, "cpu").tolist()
+    perm = bi.swiglu_interleave(256, 128).tolist()      # row -> row of [gate; up]
+    assert [perm[r] for r in rows] == bi.swiglu_interleave(256, 16).tolist()
