@@ -31,6 +31,7 @@
 
 #include "bi_internal.h"
 #include "device_common.cuh"
+#include "f32x2.cuh"
 #include "tcgen05.cuh"
 
 namespace bi {
@@ -44,7 +45,7 @@ constexpr int kBlockBytes = 128;             // bytes of a row in one k-block
 constexpr int kMaxStages = 8;
 constexpr int kChunk = 32;                   // columns of C that a warp stores at once
 constexpr int kChunkBytes = 32 * kChunk * 2; // of 32 rows of them
-constexpr int kMaxBufs = 5;                  // buffers of that size a warp may have
+constexpr int kBufs = 2;                     // buffers of that size a warp has
 constexpr int kPadBytes = 1024;              // to the ring's alignment
 constexpr int kColumnBytes = 2 * 256 * (4 + 2);  // a tile's w_scale and bias, twice
 // the operand ring and the epilogue's buffers share the rest (less than 1 KB
@@ -53,8 +54,28 @@ constexpr int kPoolBytes = 227 * 1024 - 1024 - kPadBytes - kColumnBytes;
 static_assert(kPoolBytes % 1024 == 0, "the buffers behind the ring are aligned as it is");
 constexpr size_t kSmemBytes = kPadBytes + kPoolBytes + kColumnBytes;
 constexpr uint32_t kAccCols = 256;           // columns between the two accumulators
+constexpr int kLongBlocks = 32;              // k-blocks from which a tile's MMAs outlast its epilogue
 constexpr int kSwigluBlock = 16;             // gate (then up) rows of a block of W
 constexpr int kDirectRows = 64;              // at most this many rows of A: MMAs of 64, plain stores
+
+// Division of 0 <= n < 2^31 by d >= 1 as a product: with s = ceil(log2 d) and
+// m = ceil(2^(31 + s) / d), n / d is the high word of n m, s - 1 places down
+// (a divide takes some 150 cycles, and a tile's place three of them).
+struct Divisor {
+  int d;
+  uint32_t m, shift;
+  Divisor() = default;
+  explicit Divisor(int64_t by) : d(static_cast<int>(by)), m(0), shift(0) {
+    int s = 0;
+    while ((int64_t(1) << s) < by) ++s;
+    if (s == 0) return;  // by 1: n itself
+    m = static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + by - 1) / by);
+    shift = s - 1;
+  }
+  __device__ __forceinline__ int of(int n) const {
+    return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), m) >> shift);
+  }
+};
 
 struct FusedParams {
   __nv_bfloat16* C;
@@ -67,11 +88,16 @@ struct FusedParams {
   int act;
   int bn, a_rows, kg, stages;     // tile width, rows of A and k-blocks per stage
   int mma_rows;                   // rows of an MMA in this CTA
-  int ring, bufs;                 // the ring's bytes, epilogue buffers per warp
+  int ring, staged;               // the ring's bytes; whether C goes through shared memory
   int m_tiles, n_tiles, kb_total; // m_tiles: of the pair's 256 rows where kCtas is 2
-  int group, m_fast;              // raster, as in the plain GEMM
+  int m_fast;                     // raster, as in the plain GEMM: 1: M's tiles in groups
+  Divisor by_per, by_group, by_last;  // tiles of a group times the others, a group, the last
   uint32_t idesc;
 };
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 struct Tile {
   int m, n;
@@ -80,79 +106,94 @@ struct Tile {
 // operand is kept resident in L2 in groups of `group` tiles while the other
 // one streams past it once per group.
 __device__ __forceinline__ Tile tile_of(int u, const FusedParams& p) {
-  const int span = p.m_fast ? p.m_tiles : p.n_tiles, other = p.m_fast ? p.n_tiles : p.m_tiles;
-  const int per = p.group * other;
-  const int g = u / per, r = u - g * per;
-  const int gs = min(p.group, span - g * p.group);
-  const int fast = g * p.group + r % gs, slow = r / gs;
+  const int span = p.m_fast ? p.m_tiles : p.n_tiles;
+  const int g = p.by_per.of(u), r = u - g * p.by_per.d;
+  const int first = g * p.by_group.d;
+  const bool whole = span - first >= p.by_group.d;  // the last group may be smaller
+  const int slow = whole ? p.by_group.of(r) : p.by_last.of(r);
+  const int fast = first + r - slow * (whole ? p.by_group.d : p.by_last.d);
   return p.m_fast ? Tile{fast, slow} : Tile{slow, fast};
 }
 
+// The activations take the special-function unit's exponential and reciprocal
+// (2^-22 relative, results below 2^-126 flushed to zero) instead of expf and a
+// division, whose path for special cases kept a warp from interleaving its 32
+// values (100 cycles a value; 8192 x 14336 x 1024 e4m3 with SiLU 815 us against
+// 483 without), and the result is rounded to 2^-9.  Everything else goes two
+// values at a time (f32x2).
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float rcp(float x) {
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The activations take the special-function unit's exponential and reciprocal
-// (2^-22 relative) instead of expf and a division: the division's path for
-// special cases kept a warp from interleaving its 32 values (100 cycles a
-// value; 8192 x 14336 x 1024 with SiLU 815 us against 483 without), and the
-// result is rounded to 2^-9.
+__device__ __forceinline__ f32x2 ex2_2(f32x2 x) {
+  const float2 f = halves(x);
+  return pair(ex2(f.x), ex2(f.y));
+}
+__device__ __forceinline__ f32x2 rcp_2(f32x2 x) {
+  const float2 f = halves(x);
+  return pair(rcp(f.x), rcp(f.y));
+}
 constexpr float kLog2e = 1.4426950408889634f;
 
 // z / (1 + 2^e)
-__device__ __forceinline__ float z_sigmoid(float z, float e) {
-  return __fmul_rn(z, rcp(__fadd_rn(1.0f, ex2(e))));
+__device__ __forceinline__ f32x2 z_sigmoid(f32x2 z, f32x2 e) {
+  return mul2(z, rcp_2(add2(ex2_2(e), both(1.0f))));
 }
-__device__ __forceinline__ float silu(float z) { return z_sigmoid(z, __fmul_rn(z, -kLog2e)); }
+__device__ __forceinline__ f32x2 silu(f32x2 z) { return z_sigmoid(z, mul2(z, both(-kLog2e))); }
 // z/2 (1 + tanh u) = z / (1 + exp(-2 u)), u = sqrt(2/pi) (z + 0.044715 z^3)
-__device__ __forceinline__ float gelu_tanh(float z) {
-  const float c = __fmul_rn(__fmul_rn(z, z), 0.044715f);
-  return z_sigmoid(z, __fmul_rn(__fmaf_rn(z, c, z), -1.5957691216057308f * kLog2e));
+__device__ __forceinline__ f32x2 gelu_tanh(f32x2 z) {
+  const f32x2 c = mul2(mul2(z, z), both(0.044715f));
+  return z_sigmoid(z, mul2(fma2(z, c, z), both(-1.5957691216057308f * kLog2e)));
+}
+// max(z, 0), a NaN where z is one
+__device__ __forceinline__ f32x2 relu(f32x2 z) {
+  const float2 f = halves(z);
+  return pair(f.x <= 0.0f ? 0.0f : f.x, f.y <= 0.0f ? 0.0f : f.y);
 }
 // z/2 (1 + erf(z / sqrt 2)) = max(z, 0) - |z|/2 erfcx(x) exp(-x^2), x = |z| / sqrt 2,
 // with erfcx(x)/2 as t times a polynomial in t = 1 / (1 + x/2): the least
 // largest relative error of degree 6 over 0 <= x <= 11.4, by linear
 // programming; 2^-18.8 in fp32.  Both tails keep their digits.  Past |z| = 16
 // the second term is 0.
-__device__ __forceinline__ float gelu(float z) {
-  const float m = fminf(fabsf(z), 16.0f);
-  const float t = rcp(__fmaf_rn(m, 0.35355339059327376f, 1.0f));
-  float s = 0.0429137014f;
-  s = __fmaf_rn(s, t, -0.174213769f);
-  s = __fmaf_rn(s, t, 0.188846613f);
-  s = __fmaf_rn(s, t, 0.0229806649f);
-  s = __fmaf_rn(s, t, 0.139260697f);
-  s = __fmaf_rn(s, t, 0.139064864f);
-  s = __fmaf_rn(s, t, 0.141146311f);
-  const float e = ex2(__fmul_rn(__fmul_rn(m, m), -0.5f * kLog2e));
-  const float top = z <= 0.0f ? 0.0f : z;  // (a NaN stays one)
-  return __fmaf_rn(__fmul_rn(__fmul_rn(s, t), -m), e, top);
+__device__ __forceinline__ f32x2 gelu(f32x2 z) {
+  const float2 f = halves(z);
+  const f32x2 m = pair(fminf(fabsf(f.x), 16.0f), fminf(fabsf(f.y), 16.0f));
+  const f32x2 t = rcp_2(fma2(m, both(0.35355339059327376f), both(1.0f)));
+  f32x2 s = both(0.0429137014f);
+  s = fma2(s, t, both(-0.174213769f));
+  s = fma2(s, t, both(0.188846613f));
+  s = fma2(s, t, both(0.0229806649f));
+  s = fma2(s, t, both(0.139260697f));
+  s = fma2(s, t, both(0.139064864f));
+  s = fma2(s, t, both(0.141146311f));
+  const f32x2 e = ex2_2(mul2(mul2(m, m), both(-0.5f * kLog2e)));
+  return fma2(mul2(mul2(s, t), mul2(m, both(-1.0f))), e, relu(z));
 }
 
 // In 32 values, one activation; the choice is the same for the whole call.
-__device__ __forceinline__ void activate(float (&z)[32], int act) {
+__device__ __forceinline__ void activate(f32x2 (&z)[16], int act) {
   switch (act) {
-    case BI_ACT_RELU:  // (a NaN stays one)
+    case BI_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = z[i] <= 0.0f ? 0.0f : z[i];
+      for (int i = 0; i < 16; ++i) z[i] = relu(z[i]);
       break;
     case BI_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = gelu(z[i]);
+      for (int i = 0; i < 16; ++i) z[i] = gelu(z[i]);
       break;
     case BI_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = gelu_tanh(z[i]);
+      for (int i = 0; i < 16; ++i) z[i] = gelu_tanh(z[i]);
       break;
     case BI_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = silu(z[i]);
+      for (int i = 0; i < 16; ++i) z[i] = silu(z[i]);
       break;
     default:
       break;
@@ -162,41 +203,38 @@ __device__ __forceinline__ void activate(float (&z)[32], int act) {
 // 32 accumulator columns of this lane's row times the scales and with the
 // bias; ws and bias: those columns' values in shared memory.
 template <bool kQ8>
-__device__ __forceinline__ void load_z(float (&z)[32], uint32_t taddr, const float* ws,
-                                       const __nv_bfloat16* bias, bool add_bias, float a_scale) {
+__device__ __forceinline__ void load_z(f32x2 (&z)[16], uint32_t taddr, const float* ws,
+                                       const __nv_bfloat16* bias, bool add_bias, f32x2 a_scale) {
   uint32_t v[32];
   __syncwarp();
   tmem_ld32(taddr, v);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    float4 w4;
-    if constexpr (kQ8) w4 = reinterpret_cast<const float4*>(ws)[q];
-    uint2 b2 = make_uint2(0, 0);
-    if (add_bias) b2 = reinterpret_cast<const uint2*>(bias)[q];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float x = __uint_as_float(v[4 * q + e]);
-      if constexpr (kQ8)
-        x = __fmul_rn(__fmul_rn(x, a_scale), e == 0 ? w4.x : e == 1 ? w4.y : e == 2 ? w4.z : w4.w);
-      const uint32_t b = e < 2 ? b2.x : b2.y;
-      if (add_bias) x = __fadd_rn(x, e & 1 ? bf16_hi(b) : bf16_lo(b));
-      z[4 * q + e] = x;
+    f32x2 x = pair(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]));
+    f32x2 y = pair(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+    if constexpr (kQ8) {
+      const float4 w4 = reinterpret_cast<const float4*>(ws)[q];
+      x = mul2(mul2(x, a_scale), pair(w4.x, w4.y));
+      y = mul2(mul2(y, a_scale), pair(w4.z, w4.w));
     }
+    if (add_bias) {
+      const uint2 b2 = reinterpret_cast<const uint2*>(bias)[q];
+      x = add2(x, widen2(b2.x));
+      y = add2(y, widen2(b2.y));
+    }
+    z[2 * q] = x;
+    z[2 * q + 1] = y;
   }
 }
 
 // z + residual for eight columns, rounded
-__device__ __forceinline__ uint4 add_pack8(const float* z, bool add, const uint4& r) {
+__device__ __forceinline__ uint4 add_pack8(const f32x2* z, bool add, const uint4& r) {
   const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float lo = z[2 * i], hi = z[2 * i + 1];
-    if (add) {
-      lo = __fadd_rn(lo, bf16_lo(rw[i]));
-      hi = __fadd_rn(hi, bf16_hi(rw[i]));
-    }
-    o[i] = pack_bf16x2(lo, hi);
+    const float2 f = halves(add ? add2(z[i], widen2(rw[i])) : z[i]);
+    o[i] = pack_bf16x2(f.x, f.y);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -295,12 +333,10 @@ __device__ __forceinline__ void issue_mmas(const FusedParams& p, const Ring& r, 
 template <bool kQ8, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
     const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-    const __grid_constant__ CUtensorMap tc, const __grid_constant__ CUtensorMap tr,
-    const FusedParams p) {
+    const __grid_constant__ CUtensorMap tc, const FusedParams p) {
   constexpr bool kPair = kCtas == 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
-  __shared__ uint64_t rbar[kEpiWarps][kMaxBufs];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -326,8 +362,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], kCtas * kEpiWarps);  // one arrival per epilogue warp of the pair
     }
-    for (int w = 0; w < kEpiWarps; ++w)
-      for (int b = 0; b < p.bufs; ++b) mbar_init(&rbar[w][b], 1);
     mbar_init(&drain, 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -414,83 +448,68 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
     // q-th quarter of the lanes)
     const int row_in_unit = rank * BM + wq * (p.mma_rows == 64 ? 16 : 32);
     const bool mine_too = p.mma_rows != 64 || lane < 16;
-    const bool staged = p.bufs > 0, fetch = staged && p.residual != nullptr;
-    uint8_t* buf = smem + p.ring + ew * p.bufs * kChunkBytes;
+    const bool staged = p.staged != 0;
+    uint8_t* buf = smem + p.ring + ew * kBufs * kChunkBytes;
     float* columns = reinterpret_cast<float*>(smem + kPoolBytes);  // [2][256] scales, then biases
     const uint32_t row_off = static_cast<uint32_t>(lane) * 64;
     const uint32_t swz = (static_cast<uint32_t>(lane) >> 1) & 3;
 
-    // residuals, asked for up to `distance` chunks ahead by lane 0
-    int ahead_u = first, fetch_buf = 0;
-    uint32_t fetched = 0;
-    Tile ahead_t{0, 0};
-    Span ahead{0, 0};
-    bool more = fetch && lane == 0 && first < units;
-    if (more) {
-      ahead_t = tile_of(ahead_u, p);
-      ahead = span_of<kCtas>(ahead_t, p, bn_out, row_in_unit, half);
-    }
-    auto fetch_one = [&]() {
-      while (ahead.c >= ahead.end) {
-        ahead_u += step;
-        if (ahead_u >= units) {
-          more = false;
-          return;
-        }
-        ahead_t = tile_of(ahead_u, p);
-        ahead = span_of<kCtas>(ahead_t, p, bn_out, row_in_unit, half);
-      }
-      uint64_t* bar = &rbar[ew][fetch_buf];
-      mbar_arrive_expect_tx(bar, kChunkBytes);
-      tma_load_2d(buf + fetch_buf * kChunkBytes, &tr, ahead_t.n * bn_out + ahead.c * kChunk,
-                  ahead_t.m * (BM * kCtas) + row_in_unit, bar);
-      ++ahead.c;
-      ++fetched;
-      if (++fetch_buf == p.bufs) fetch_buf = 0;
-    };
-    // a buffer is filled again once the store of the chunk before last has
-    // read it
-    const int distance = p.bufs - 2;
-    for (int i = 0; i < distance && more; ++i) fetch_one();
-
     int acc = 0, b = 0;
-    uint32_t acc_phase = 0, buf_phase = 0, count = 0;  // count: chunks done
-    bool ok = true;                                    // the same in every lane
+    uint32_t acc_phase = 0;
+    bool ok = true;  // the same in every lane
     for (int u = first; u < units && ok; u += step) {
       const Tile t = tile_of(u, p);
       const int row0 = t.m * (BM * kCtas) + row_in_unit, row = row0 + lane;
       const Span span = span_of<kCtas>(t, p, bn_out, row_in_unit, half);
       // this half's scales and biases, four columns a lane (N % 8 == 0)
-      const int col0 = span.c * acc_chunk, col = t.n * p.bn + col0 + 4 * lane;
+      const int col0 = span.c * acc_chunk + 4 * lane, col = t.n * p.bn + col0;
       float4 ws = make_float4(0.f, 0.f, 0.f, 0.f);
       uint2 bs = make_uint2(0, 0);
-      float a_scale = 1.0f;
+      float row_scale = 1.0f;
       if (span.c < span.end && col < p.N) {
         if constexpr (kQ8) ws = __ldg(reinterpret_cast<const float4*>(p.w_scale + col));
         if (add_bias) bs = __ldg(reinterpret_cast<const uint2*>(p.bias + col));
       }
-      if (kQ8 && row < p.M) a_scale = __ldg(p.a_scale + row);
+      if (kQ8 && row < p.M && mine_too) row_scale = __ldg(p.a_scale + row);
+      // the residual of the first chunk, while the tile's MMAs run; each further
+      // one as soon as the one before is used, and, unless the epilogue is what
+      // the blocks wait for (fetching twice then costs more than it hides), all
+      // of them into L2 now
+      const int out0 = t.n * bn_out, cols = min(bn_out, p.n_out - out0);
+      const bool adds = p.residual != nullptr && row < p.M && mine_too;
+      const __nv_bfloat16* res = p.residual + static_cast<int64_t>(row) * p.n_out + out0;
+      uint4 r[4];
+      auto load_residual = [&](int c) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          r[q] = make_uint4(0, 0, 0, 0);
+          if (adds && c < span.end && c * kChunk + 8 * q < cols)
+            r[q] = *reinterpret_cast<const uint4*>(res + c * kChunk + 8 * q);
+        }
+      };
+      load_residual(span.c);
+      if (adds && (p.kb_total >= kLongBlocks || units <= step))
+        for (int c = span.c + 1; c < span.end; ++c) prefetch_l2(res + c * kChunk);
       ok = __all_sync(kFull, mbar_wait(&tfull[acc], acc_phase, p.err, &abort_flag));
       if (!ok) break;
       tc_fence_after();
+      const f32x2 a_scale = both(row_scale);
       // (the four warps of a half write the same values; the accumulator's
       // last use, whose columns these replace, is over)
       float* cw = columns + acc * 256;
       __nv_bfloat16* cb = reinterpret_cast<__nv_bfloat16*>(columns + 512) + acc * 256;
-      if (span.c < span.end && col0 + 4 * lane < 256) {
-        if constexpr (kQ8) *reinterpret_cast<float4*>(cw + col0 + 4 * lane) = ws;
-        if (add_bias) *reinterpret_cast<uint2*>(cb + col0 + 4 * lane) = bs;
+      if (span.c < span.end && col0 < 256) {
+        if constexpr (kQ8) *reinterpret_cast<float4*>(cw + col0) = ws;
+        if (add_bias) *reinterpret_cast<uint2*>(cb + col0) = bs;
       }
-      const int out0 = t.n * bn_out, cols = min(bn_out, p.n_out - out0);
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) +
                              static_cast<uint32_t>(acc) * kAccCols;
       for (int c = span.c; c < span.end; ++c) {
         uint8_t* mine = buf + b * kChunkBytes;
-        if (staged && lane == 0) {
-          bulk_wait_read<1>();
-          if (more) fetch_one();
-        }
-        float z[32];
+        // (here, and not between the values and their stores, where a branch on
+        // one lane cost the values 400 cycles a chunk)
+        if (staged && lane == 0) bulk_wait_read<kBufs - 1>();
+        f32x2 z[16];
         if (swiglu) {
           // two blocks of 16 gate columns and the 16 up columns of the same
           // features; the second may lie past the tile
@@ -498,15 +517,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
           for (int h = 0; h < 2; ++h) {
             if (c * kChunk + h * kSwigluBlock >= cols) {
 #pragma unroll
-              for (int i = 0; i < kSwigluBlock; ++i) z[h * kSwigluBlock + i] = 0.0f;
+              for (int i = 0; i < 8; ++i) z[h * 8 + i] = 0;
               continue;
             }
-            float g[32];
+            f32x2 g[16];
             const int ac = c * 2 * kChunk + h * 32;
             load_z<kQ8>(g, tbase + static_cast<uint32_t>(ac), cw + ac, cb + ac, add_bias, a_scale);
 #pragma unroll
-            for (int i = 0; i < kSwigluBlock; ++i)
-              z[h * kSwigluBlock + i] = __fmul_rn(silu(g[i]), g[kSwigluBlock + i]);
+            for (int i = 0; i < 8; ++i) z[h * 8 + i] = mul2(silu(g[i]), g[8 + i]);
           }
         } else {
           const int ac = c * kChunk;
@@ -514,39 +532,27 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
           activate(z, p.act);
         }
         if (staged) {
-          if (fetch) {
-            ok = __all_sync(kFull, mbar_wait(&rbar[ew][b], buf_phase, p.err, &abort_flag));
-            if (!ok) break;
-          }
+          __syncwarp();  // (lane 0's wait for the buffer holds for the warp)
 #pragma unroll
-          for (uint32_t q = 0; q < 4; ++q) {
-            uint4* at = reinterpret_cast<uint4*>(mine + row_off + ((q ^ swz) << 4));
-            uint4 r = make_uint4(0, 0, 0, 0);
-            if (fetch) r = *at;
-            *at = add_pack8(z + 8 * q, fetch, r);
-          }
+          for (uint32_t q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(mine + row_off + ((q ^ swz) << 4)) =
+                add_pack8(z + 4 * q, p.residual != nullptr, r[q]);
+          load_residual(c + 1);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             tma_store_2d(&tc, mine, out0 + c * kChunk, row0);
             bulk_commit();
           }
-          ++count;
-          if (++b == p.bufs) {
-            b = 0;
-            buf_phase ^= 1u;
-          }
-        } else if (row < p.M && mine_too) {
-          const int64_t at = static_cast<int64_t>(row) * p.n_out + out0 + c * kChunk;
+          b ^= 1;
+        } else {
+          __nv_bfloat16* out = p.C + static_cast<int64_t>(row) * p.n_out + out0 + c * kChunk;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (c * kChunk + 8 * q >= cols) continue;
-            uint4 r = make_uint4(0, 0, 0, 0);
-            // (may be C: read before it is written, by the same thread)
-            if (p.residual) r = *reinterpret_cast<const uint4*>(p.residual + at + 8 * q);
-            *reinterpret_cast<uint4*>(p.C + at + 8 * q) =
-                add_pack8(z + 8 * q, p.residual != nullptr, r);
-          }
+          for (int q = 0; q < 4; ++q)
+            if (row < p.M && mine_too && c * kChunk + 8 * q < cols)
+              *reinterpret_cast<uint4*>(out + 8 * q) =
+                  add_pack8(z + 4 * q, p.residual != nullptr, r[q]);
+          load_residual(c + 1);
         }
       }
       tc_fence_before();
@@ -558,17 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
-    if (staged && lane == 0) {
-      // (after a wait that ran out, residuals may still be on their way)
-      for (; count < fetched; ++count) {
-        mbar_wait(&rbar[ew][b], buf_phase, nullptr);
-        if (++b == p.bufs) {
-          b = 0;
-          buf_phase ^= 1u;
-        }
-      }
-      bulk_wait_all();
-    }
+    if (staged && lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   if constexpr (kPair) cluster_sync();
@@ -586,7 +582,7 @@ struct Plan {
   int ctas, bn;      // CTAs of a tile (1: 128 rows, 2: 256) and its width
   int a_rows;        // rows of A per stage
   int kg, stages;    // k-blocks per stage, stages
-  int bufs;          // epilogue buffers per warp, 0: plain stores
+  bool staged;       // C goes through shared memory and TMA stores, not plain ones
   int ring;          // the operand ring's bytes
 };
 
@@ -623,18 +619,15 @@ void choose_tile(int64_t M, int64_t N, int64_t kb, int sms, bool swiglu, Plan* q
     }
 }
 
-Plan fused_plan(int64_t M, int64_t N, uint64_t row_bytes, int sms, bool swiglu, bool residual) {
+Plan fused_plan(int64_t M, int64_t N, uint64_t row_bytes, int sms, bool swiglu) {
   Plan q{};
   const int64_t kb = static_cast<int64_t>((row_bytes + kBlockBytes - 1) / kBlockBytes);
   choose_tile(M, N, kb, sms, swiglu, &q);
   // the MMA always reads a window of 128 rows (64 up to 64 rows), whose rows
   // past M reach accumulator rows that are never stored
   q.a_rows = M <= 32 ? 32 : M <= 64 ? 64 : BM;
-  // epilogue buffers: two a warp to store from while the next is made, with a
-  // residual one more for the chunk fetched ahead (8192 x 14336 x 1024: 175 us
-  // with one ahead, 171 with two or three, which take stages from long K)
-  q.bufs = M <= kDirectRows ? 0 : residual ? 3 : 2;
-  q.ring = kPoolBytes - kEpiWarps * q.bufs * kChunkBytes;
+  q.staged = M > kDirectRows;
+  q.ring = kPoolBytes - (q.staged ? kEpiWarps * kBufs * kChunkBytes : 0);
   // k-blocks per stage, where three such stages fit: one copy then reads
   // kg * 128 contiguous bytes of each row, and the instructions around a stage
   // are shared (16 x 4096 x 14336 bf16: 23 us with four, 25 with two); four
@@ -685,7 +678,7 @@ int resident_pairs() {
 
 template <bool kQ8, int kCtas>
 bi_status launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
-                 const CUtensorMap& tr, const FusedParams& p, int grid, cudaStream_t s) {
+                 const FusedParams& p, int grid, cudaStream_t s) {
   const auto kernel = gemm_fused_kernel<kQ8, kCtas>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kSmemBytes)) != cudaSuccess)
@@ -704,7 +697,7 @@ bi_status launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = kCtas == 1 ? 1 : 2;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, ta, tb, tc, tr, p));
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, ta, tb, tc, p));
 }
 
 }  // namespace
@@ -717,7 +710,7 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   if (sms <= 0) return BI_ERR_CUDA;
   const bool swiglu = act == BI_ACT_SWIGLU;
   const uint64_t row_bytes = static_cast<uint64_t>(K) * (q8 ? 1 : 2);
-  const Plan plan = fused_plan(M, N, row_bytes, sms, swiglu, residual != nullptr);
+  const Plan plan = fused_plan(M, N, row_bytes, sms, swiglu);
   FusedParams p{};
   p.C = static_cast<__nv_bfloat16*>(C);
   p.bias = static_cast<const __nv_bfloat16*>(bias);
@@ -733,7 +726,7 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   p.a_rows = plan.a_rows;
   p.kg = plan.kg;
   p.stages = plan.stages;
-  p.bufs = plan.bufs;
+  p.staged = plan.staged;
   p.ring = plan.ring;
   p.kb_total = static_cast<int>((row_bytes + kBlockBytes - 1) / kBlockBytes);
   const int rows = BM * plan.ctas;
@@ -745,21 +738,22 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   p.m_fast = M <= N ? 1 : 0;
   const int64_t tile_bytes = static_cast<int64_t>(p.m_fast ? rows : p.bn) * row_bytes;
   const int64_t span = p.m_fast ? p.m_tiles : p.n_tiles;
-  p.group = static_cast<int>(
-      std::min(span, std::max<int64_t>(1, (int64_t(40) << 20) / std::max<int64_t>(1, tile_bytes))));
+  const int64_t group =
+      std::min(span, std::max<int64_t>(1, (int64_t(40) << 20) / std::max<int64_t>(1, tile_bytes)));
+  p.by_per = Divisor(group * (p.m_fast ? p.n_tiles : p.m_tiles));
+  p.by_group = Divisor(group);
+  p.by_last = Divisor(span % group ? span % group : group);
   // up to 64 rows the MMA takes 64 (an element's sum is the same): below some
   // 100 columns its time goes by its rows, not by them
   p.mma_rows = M <= kDirectRows ? 64 : BM;
   const int mma = p.mma_rows * plan.ctas;
   p.idesc = q8 ? umma_idesc_e4m3(mma, p.bn) : umma_idesc_bf16(mma, p.bn, false, false);
-  CUtensorMap ta, tb, tc{}, tr{};
+  CUtensorMap ta, tb, tc{};
   const uint64_t ra = static_cast<uint64_t>(M), rb = static_cast<uint64_t>(N);
   if (!make_tmap_rows(&ta, A, ra, row_bytes, plan.a_rows, plan.kg) ||
       !make_tmap_rows(&tb, W, rb, row_bytes, p.bn / plan.ctas, plan.kg))
     return BI_ERR_CUDA;
-  if (plan.bufs > 0 && (!make_tmap_chunks(&tc, C, ra, static_cast<uint64_t>(p.n_out)) ||
-                        (residual && !make_tmap_chunks(&tr, residual, ra,
-                                                       static_cast<uint64_t>(p.n_out)))))
+  if (plan.staged && !make_tmap_chunks(&tc, C, ra, static_cast<uint64_t>(p.n_out)))
     return BI_ERR_CUDA;
   const int units = p.m_tiles * p.n_tiles;
   int blocks = sms;
@@ -769,10 +763,10 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   }
   const int grid = std::min(units, blocks) * plan.ctas;
   if (plan.ctas == 2)
-    return q8 ? launch<true, 2>(ta, tb, tc, tr, p, grid, s)
-              : launch<false, 2>(ta, tb, tc, tr, p, grid, s);
-  return q8 ? launch<true, 1>(ta, tb, tc, tr, p, grid, s)
-            : launch<false, 1>(ta, tb, tc, tr, p, grid, s);
+    return q8 ? launch<true, 2>(ta, tb, tc, p, grid, s)
+              : launch<false, 2>(ta, tb, tc, p, grid, s);
+  return q8 ? launch<true, 1>(ta, tb, tc, p, grid, s)
+            : launch<false, 1>(ta, tb, tc, p, grid, s);
 }
 
 }  // namespace bi

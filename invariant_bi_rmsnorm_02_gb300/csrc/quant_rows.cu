@@ -27,6 +27,7 @@
 
 #include "bi_internal.h"
 #include "device_common.cuh"
+#include "f32x2.cuh"
 #include "rmsnorm_row.cuh"
 
 namespace bi {
@@ -35,31 +36,6 @@ namespace {
 constexpr float kTop = 448.0f;                    // the largest e4m3 number
 constexpr float kLeastTop = 448.0f * 0x1p-126f;   // a scale is never below 2^-126
 constexpr int kRowsPerBlock = 8;                  // of rows of one warp each
-
-// Two floats for the packed operations, each half rounded as its own.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
-__device__ __forceinline__ float2 halves(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-// The bf16 pair w as floats.
-__device__ __forceinline__ uint64_t widen2(uint32_t w) { return pair(bf16_lo(w), bf16_hi(w)); }
 
 // max(a, |b|), a NaN where either is one
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -93,7 +69,7 @@ struct RowTop {
   }
 };
 
-__device__ __forceinline__ uint32_t e4m3x4(uint64_t a, uint64_t b) {
+__device__ __forceinline__ uint32_t e4m3x4(f32x2 a, f32x2 b) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(halves(a), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(halves(b), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
@@ -135,8 +111,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
   for (int k = 0; k < VPT; ++k) ss = sum_squares8(hv[k], ss);
   // (a row of one warp: block_sum's second butterfly adds zeros)
   const float r = inv_rms(kWarpRow ? warp_sum(ss) : block_sum(ss, red), inv_h, eps);
-  const uint64_t r2 = both(r);
-  uint64_t v[VPT][4];
+  const f32x2 r2 = both(r);
+  f32x2 v[VPT][4];
   float top = 0.0f;
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
@@ -154,7 +130,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
   }
   const RowTop t(row_max<kWarpRow>(__float_as_uint(top), red_max), first == 0, scale + row);
   // (t is between 2^-117.2 and 2^128, so 448 / t is a normal number)
-  const uint64_t q = both(__fdiv_rn(kTop, t.t));
+  const f32x2 q = both(__fdiv_rn(kTop, t.t));
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int i = first + k * stride;
@@ -204,7 +180,7 @@ __global__ void __launch_bounds__(1024) quantize_q8_kernel(
   // exact for a bf16 v.
   const float p = t.t < 0x1p-40f ? 0x1p64f : t.t > 0x1p60f ? 0x1p-64f : 1.0f;
   const float d = __fmul_rn(t.t, p), inv = __fdiv_rn(1.0f, d), top_p = __fmul_rn(kTop, p);
-  const uint64_t c = both(top_p), minus_c = both(-top_p), d2 = both(d), r2 = both(inv),
+  const f32x2 c = both(top_p), minus_c = both(-top_p), d2 = both(d), r2 = both(inv),
                  minus_r2 = both(-inv);
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
@@ -213,10 +189,10 @@ __global__ void __launch_bounds__(1024) quantize_q8_kernel(
     uint2 o = make_uint2(0u, 0u);
     if (t.fine) {
       const uint32_t w[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
-      uint64_t q[4];
+      f32x2 q[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint64_t v = widen2(w[e]);
+        const f32x2 v = widen2(w[e]);
         q[e] = mul2(mul2(v, c), r2);
         // (the remainder's sign the way round that keeps a zero's sign)
         q[e] = fma2(fma2(q[e], d2, mul2(v, minus_c)), minus_r2, q[e]);

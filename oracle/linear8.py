@@ -81,7 +81,8 @@ def product_bound(a, w, bias=None, residual=None, act="none"):
     - Its evaluation: erfc, exp and a quotient of a few units each, and an
       argument off by 2 units, which moves erfc(x) by 2 x^2 and exp(x) by x
       units: below 2^-14 relative for |x| <= 88 and erfc's x <= 9.3, past
-      which the result is below 2^-120.
+      which the result is below 2^-120.  A factor below 2^-126 counts as zero,
+      at most 88 * 2^-126 < 2^-119 of a result (times |u| with SwiGLU).
     - The residual's addition, half a unit; then one rounding to bf16 (2^-8).
     """
     K = a.shape[1]
@@ -94,11 +95,12 @@ def product_bound(a, w, bias=None, residual=None, act="none"):
         (g, u), (eg, eu) = gate_up(z), gate_up(ez)
         s = activation(g, "silu")
         r = s * u
-        e = 1.13 * eg * (np.abs(u) + eu) + np.abs(s) * eu + 2.0 ** -14 * np.abs(r)
+        e = 1.13 * eg * (np.abs(u) + eu) + np.abs(s) * eu + 2.0 ** -14 * np.abs(r) \
+            + 2.0 ** -119 * np.abs(u)
     else:
         r = activation(z, act)
         e = 1.13 * ez + (2.0 ** -14 * np.abs(r) if act not in ("none", "relu") else 0.0)
     if residual is not None:
         r = r + residual
         e = e + 2.0 ** -23 * np.abs(r)
-    return e + 2.0 ** -8 * (np.abs(r) + e) + 2.0 ** -120
+    return e + 2.0 ** -8 * (np.abs(r) + e) + 2.0 ** -118
