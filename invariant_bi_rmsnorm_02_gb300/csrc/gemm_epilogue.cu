@@ -42,7 +42,7 @@ constexpr int BM = 128;                      // rows of a CTA's tile
 constexpr int kEpiWarps = 8;                 // two per quarter of the accumulator's lanes
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kBlockBytes = 128;             // bytes of a row in one k-block
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 24;
 constexpr int kChunk = 32;                   // columns of C that a warp stores at once
 constexpr int kChunkBytes = 32 * kChunk * 2; // of 32 rows of them
 constexpr int kBufs = 2;                     // buffers of that size a warp has
@@ -87,6 +87,7 @@ struct FusedParams {
   int M, N, n_out;                // n_out: columns of C
   int act;
   int bn, a_rows, kg, stages;     // tile width, rows of A and k-blocks per stage
+  int deep;                       // a stage's k-blocks come by one copy
   int mma_rows;                   // rows of an MMA in this CTA
   int ring, staged;               // the ring's bytes; whether C goes through shared memory
   int m_tiles, n_tiles, kb_total; // m_tiles: of the pair's 256 rows where kCtas is 2
@@ -401,15 +402,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
           uint8_t* a = sA + stage * a_stage;
           uint8_t* b = sB + stage * b_stage;
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
-          if constexpr (kPair) {
-            tma_load_2d_pair(a, &ta, kb * kBlockBytes, ra, full0 + stage * 8);
-            tma_load_2d_pair(b, &tb, kb * kBlockBytes, rb, full0 + stage * 8);
-          } else if (p.kg == 1) {
-            tma_load_2d(a, &ta, kb * kBlockBytes, ra, &full[stage]);
-            tma_load_2d(b, &tb, kb * kBlockBytes, rb, &full[stage]);
-          } else {  // k-blocks past the last read as zero and are not used
+          if (!kPair && p.deep) {  // k-blocks past the last read as zero and are not used
             tma_load_3d(a, &ta, 0, ra, kb, &full[stage]);
             tma_load_3d(b, &tb, 0, rb, kb, &full[stage]);
+          } else {
+            for (int g = 0; g < p.kg; ++g) {
+              const int x = (kb + g) * kBlockBytes;
+              if constexpr (kPair) {
+                tma_load_2d_pair(a + g * a_sub, &ta, x, ra, full0 + stage * 8);
+                tma_load_2d_pair(b + g * b_sub, &tb, x, rb, full0 + stage * 8);
+              } else {
+                tma_load_2d(a + g * a_sub, &ta, x, ra, &full[stage]);
+                tma_load_2d(b + g * b_sub, &tb, x, rb, &full[stage]);
+              }
+            }
           }
           ++issued;
           if (++stage == p.stages) {
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
     if (elect_one() && rank == 0) {
       const Ring ring{full, empty, tfull, tempty, &drain, smem_u32(sA), smem_u32(sB), a_sub, b_sub,
                       tmem_base};
-      if (kPair || p.kg == 1) issue_mmas<kQ8, kPair, 1>(p, ring, first, units, step, &abort_flag);
+      if (p.kg == 1) issue_mmas<kQ8, kPair, 1>(p, ring, first, units, step, &abort_flag);
       else if (p.kg == 2) issue_mmas<kQ8, kPair, 2>(p, ring, first, units, step, &abort_flag);
       else issue_mmas<kQ8, kPair, 4>(p, ring, first, units, step, &abort_flag);
     }
@@ -582,69 +588,79 @@ struct Plan {
   int ctas, bn;      // CTAs of a tile (1: 128 rows, 2: 256) and its width
   int a_rows;        // rows of A per stage
   int kg, stages;    // k-blocks per stage, stages
+  bool deep;         // one copy per operand and stage
   bool staged;       // C goes through shared memory and TMA stores, not plain ones
   int ring;          // the operand ring's bytes
 };
 
+// k-blocks per stage: the more, the fewer instructions around them (a narrow
+// tile waits for those: 4 x 1088 x 12824 bf16 38 us with one, 18 with four;
+// 256 x 4096 x 4096 13.6 and 12.5 with one and two), as long as enough stages
+// are in flight.  Rows that are whole k-blocks come by one copy of kg * 128
+// contiguous bytes of each row; other rows, and pairs, take a copy per k-block
+// and more stages (128-row tiles of 64 columns: 99 x 8296 x 10176 bf16 41 us
+// with one, 44 with two).
+bool whole_blocks(uint64_t row_bytes, int ctas) {
+  return ctas == 1 && row_bytes % kBlockBytes == 0;
+}
+int stage_blocks(const Plan& q, bool few, int64_t kb, uint64_t row_bytes) {
+  const int sub = (q.a_rows + q.bn / q.ctas) * kBlockBytes;
+  const int stages = whole_blocks(row_bytes, q.ctas) ? 3 : q.ctas == 2 ? 4 : 5;
+  for (int g = few ? 4 : 2; g > 1; g /= 2)
+    if (g <= kb && stages * g * sub <= q.ring) return g;
+  return 1;
+}
+
 // The tile with the least cost: rounds of as many tiles as the device runs at
 // once, each as long as its MMAs or its epilogue, then one epilogue.  In ns,
-// fitted to 1900 timings (both types, M 1 .. 8192, N 1000 .. 28672, K 1024 ..
-// 14336, every width; the tile chosen takes 1.01 times the best one's time on
-// average, 1.11 at most above one row): a k-block takes a pair of CTAs 160 or
-// 0.7 a column, one CTA 180 or 60 + 0.75 a column (it loads twice the rows of
-// W for the same MMAs: 8192 x 28672 x 4096 e4m3 621 us against 526), an
-// epilogue 1200 + 8 a column, starting a pair 1000.  At most 64 rows wait for
-// the instructions of the MMAs and their stages, whatever the width.
-void choose_tile(int64_t M, int64_t N, int64_t kb, int sms, bool swiglu, Plan* q) {
+// fitted to 3400 timings (both types, every width; M, N and K from 1, 32 and 72
+// to 8192, 28672 and 14336; the tile chosen takes 1.01 times the best one's time
+// on average): a k-block takes one CTA 30 + 85 / kg or 55 + 0.85 a column, a
+// pair 65 + 75 / kg or 0.6 a column (it loads half the rows of W for the same
+// MMAs: 8192 x 28672 x 4096 e4m3 526 us against 621), an epilogue 500 + 7 a
+// column, starting a pair 200.  Up to 64 rows a k-block's time hardly goes by
+// the width.
+Plan fused_plan(int64_t M, int64_t N, uint64_t row_bytes, int sms, bool swiglu) {
+  const int64_t kb = static_cast<int64_t>((row_bytes + kBlockBytes - 1) / kBlockBytes);
   const bool few = M <= kDirectRows;
+  Plan q{};
+  // The MMA always reads a window of 128 rows (64 up to 64 rows), whose rows
+  // past A's tile reach accumulator rows that are never stored.  Only the rows
+  // that there are get loaded, in eights (the swizzle's groups): rows that a copy
+  // fills with zeros cost more than rows of data, as if all of them came from one
+  // place (1 x 6144 x 4096 e4m3 8.7 us with 31 such rows, 6.0 with 7).
+  q.a_rows = M >= BM ? BM : static_cast<int>((M + 7) / 8 * 8);
+  q.staged = !few;
+  q.ring = kPoolBytes - (q.staged ? kEpiWarps * kBufs * kChunkBytes : 0);
   const int step = few ? (swiglu ? 32 : 16) : (swiglu ? 64 : 32);
+  Plan best{};
   double least = 1e300;
-  for (int ctas = 1; ctas <= (M > BM ? 2 : 1); ++ctas)
-    // (with few rows a second round of narrow tiles streams W better than one
-    // of wide tiles: 64 x 28672 x 4096 e4m3 22.3 us in tiles of 96, 23.1 in 192)
-    for (int bn = few ? 128 : 256; bn >= step; bn -= step) {
-      const int64_t tiles = (M + BM * ctas - 1) / (BM * ctas) * ((N + bn - 1) / bn);
-      const int64_t rounds = (tiles + sms / ctas - 1) / (sms / ctas);
-      const double block = few ? 350.0 + 3.0 * bn
-                           : ctas == 2 ? std::max(160.0, 0.7 * bn)
-                                       : std::max(180.0, 60.0 + 0.75 * bn);
-      const double epilogue = 1200.0 + 8.0 * bn;
-      const double cost = (ctas == 2 ? 1000.0 : 0.0) +
+  for (q.ctas = 1; q.ctas <= (M >= BM ? 2 : 1); ++q.ctas)
+    // (with few rows a second round of narrow tiles streams a long K better than
+    // one of wide tiles: 64 x 28672 x 4096 e4m3 22.3 us in tiles of 96, 23.1 in
+    // 192; 7 x 19848 x 1136 11.9 in 128, 9.7 in 144)
+    for (q.bn = few && kb >= 24 ? 128 : 256; q.bn >= step; q.bn -= step) {
+      q.kg = stage_blocks(q, few, kb, row_bytes);
+      const int64_t tiles = (M + BM * q.ctas - 1) / (BM * q.ctas) * ((N + q.bn - 1) / q.bn);
+      const int64_t rounds = (tiles + sms / q.ctas - 1) / (sms / q.ctas);
+      const double block = few ? 700.0 + 0.25 * q.bn
+                           : q.ctas == 2 ? std::max(65.0 + 75.0 / q.kg, 0.6 * q.bn)
+                                         : std::max(30.0 + 85.0 / q.kg, 55.0 + 0.85 * q.bn);
+      const double epilogue = 500.0 + 7.0 * q.bn;
+      const double cost = (q.ctas == 2 ? 200.0 : 0.0) +
                           static_cast<double>(rounds) * std::max(kb * block, epilogue) + epilogue;
       if (cost < least) {
         least = cost;
-        q->ctas = ctas;
-        q->bn = bn;
+        best = q;
       }
     }
-}
-
-Plan fused_plan(int64_t M, int64_t N, uint64_t row_bytes, int sms, bool swiglu) {
-  Plan q{};
-  const int64_t kb = static_cast<int64_t>((row_bytes + kBlockBytes - 1) / kBlockBytes);
-  choose_tile(M, N, kb, sms, swiglu, &q);
-  // the MMA always reads a window of 128 rows (64 up to 64 rows), whose rows
-  // past M reach accumulator rows that are never stored
-  q.a_rows = M <= 32 ? 32 : M <= 64 ? 64 : BM;
-  q.staged = M > kDirectRows;
-  q.ring = kPoolBytes - (q.staged ? kEpiWarps * kBufs * kChunkBytes : 0);
-  // k-blocks per stage, where three such stages fit: one copy then reads
-  // kg * 128 contiguous bytes of each row, and the instructions around a stage
-  // are shared (16 x 4096 x 14336 bf16: 23 us with four, 25 with two); four
-  // only where K fills the ring twice (16 x 4096 x 4096 e4m3: 6.4 us with two,
-  // 6.9 with four)
-  const int sub = (q.a_rows + q.bn / q.ctas) * kBlockBytes;
-  q.kg = 1;
-  if (q.ctas == 1 && row_bytes % kBlockBytes == 0)
-    for (int g = kb >= 64 ? 4 : 2; g > 1; g /= 2)
-      if (g <= kb && 3 * g * sub <= q.ring) {
-        q.kg = g;
-        break;
-      }
-  q.stages = std::min(kMaxStages, q.ring / (q.kg * sub));
+  best.deep = best.kg > 1 && whole_blocks(row_bytes, best.ctas);
+  const int sub = (best.a_rows + best.bn / best.ctas) * kBlockBytes;
+  best.stages = std::min(kMaxStages, best.ring / (best.kg * sub));
   // the last window of A stays inside the ring
-  while (q.stages * q.kg * q.a_rows + BM - q.a_rows > q.ring / kBlockBytes) --q.stages;
-  return q;
+  while (best.stages * best.kg * best.a_rows + BM - best.a_rows > best.ring / kBlockBytes)
+    --best.stages;
+  return best;
 }
 
 // Pairs of CTAs that fit on the device at once (0 on failure); the same for
@@ -725,6 +741,7 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   p.bn = plan.bn;
   p.a_rows = plan.a_rows;
   p.kg = plan.kg;
+  p.deep = plan.deep;
   p.stages = plan.stages;
   p.staged = plan.staged;
   p.ring = plan.ring;
@@ -750,8 +767,8 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   p.idesc = q8 ? umma_idesc_e4m3(mma, p.bn) : umma_idesc_bf16(mma, p.bn, false, false);
   CUtensorMap ta, tb, tc{};
   const uint64_t ra = static_cast<uint64_t>(M), rb = static_cast<uint64_t>(N);
-  if (!make_tmap_rows(&ta, A, ra, row_bytes, plan.a_rows, plan.kg) ||
-      !make_tmap_rows(&tb, W, rb, row_bytes, p.bn / plan.ctas, plan.kg))
+  if (!make_tmap_rows(&ta, A, ra, row_bytes, plan.a_rows, plan.deep ? plan.kg : 1) ||
+      !make_tmap_rows(&tb, W, rb, row_bytes, p.bn / plan.ctas, plan.deep ? plan.kg : 1))
     return BI_ERR_CUDA;
   if (plan.staged && !make_tmap_chunks(&tc, C, ra, static_cast<uint64_t>(p.n_out)))
     return BI_ERR_CUDA;
