@@ -145,61 +145,75 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
   }
 }
 
-template <int VPT, bool kWarpRow>
-__global__ void __launch_bounds__(1024) quantize_q8_kernel(
+// kAhead: a block takes every gridDim.x-th row, the next one on its way while
+// this one is quantised and stored.  For rows that leave two or three blocks to
+// an SM, which load and store in step (8192 rows of 14336 66 -> 58 us in a loop);
+// with eight blocks an SM they cover for one another and the copies of a row
+// ahead cost more (28672 rows of 4096 53 -> 57).
+template <int VPT, bool kWarpRow, bool kAhead>
+__global__ void __launch_bounds__(kAhead ? 512 : 1024) quantize_q8_kernel(
     const uint4* __restrict__ x, uint2* __restrict__ y, float* __restrict__ scale, int64_t M,
     int nvec) {
-  __shared__ uint32_t red_max[32];
+  __shared__ uint32_t red_max[2][32];  // of rows in turn: a warp may be a row ahead
   const int first = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
   const int stride = kWarpRow ? 32 : blockDim.x;
-  const int64_t row =
+  int64_t row =
       kWarpRow ? blockIdx.x * (int64_t)kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
-  if (kWarpRow && row >= M) return;
   uint4 xv[VPT];
+  auto load = [&](int64_t r) {
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int i = first + k * stride;
-    xv[k] = i < nvec ? __ldcs(x + row * nvec + i) : make_uint4(0, 0, 0, 0);
-  }
-  // bf16 magnitudes order as integers, two at a time
-  uint32_t top2 = 0;
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const uint32_t w[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(w[e] & 0x7fff7fffu));
-  }
-  const uint32_t top = max(top2 & 0xffffu, top2 >> 16) << 16;
-  const RowTop t(row_max<kWarpRow>(top, red_max), first == 0, scale + row);
-  // (448 v) / t: a quotient q = RN(u r), r = RN(1 / t), corrected by its exact
-  // remainder is the correctly rounded u / t (Markstein, IBM J. Res. Dev. 34,
-  // 1990) while no step over- or underflows; so both are taken times a power of
-  // two p that brings t between 2^-53 and 2^64 (quotients whose remainder
-  // underflows all the same are far below the least e4m3 number).  u = 448 v is
-  // exact for a bf16 v.
-  const float p = t.t < 0x1p-40f ? 0x1p64f : t.t > 0x1p60f ? 0x1p-64f : 1.0f;
-  const float d = __fmul_rn(t.t, p), inv = __fdiv_rn(1.0f, d), top_p = __fmul_rn(kTop, p);
-  const f32x2 c = both(top_p), minus_c = both(-top_p), d2 = both(d), r2 = both(inv),
-                 minus_r2 = both(-inv);
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int i = first + k * stride;
-    if (i >= nvec) continue;
-    uint2 o = make_uint2(0u, 0u);
-    if (t.fine) {
-      const uint32_t w[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
-      f32x2 q[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f32x2 v = widen2(w[e]);
-        q[e] = mul2(mul2(v, c), r2);
-        // (the remainder's sign the way round that keeps a zero's sign)
-        q[e] = fma2(fma2(q[e], d2, mul2(v, minus_c)), minus_r2, q[e]);
-      }
-      o = make_uint2(e4m3x4(q[0], q[1]), e4m3x4(q[2], q[3]));
+    for (int k = 0; k < VPT; ++k) {
+      const int i = first + k * stride;
+      xv[k] = i < nvec && r < M ? __ldcs(x + r * nvec + i) : make_uint4(0, 0, 0, 0);
     }
-    __stcs(y + row * nvec + i, o);
+  };
+  load(row);
+  for (int turn = 0; row < M; row += gridDim.x, turn ^= 1) {
+    uint4 cur[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) cur[k] = xv[k];
+    if (kAhead) load(row + gridDim.x);
+    // bf16 magnitudes order as integers, two at a time
+    uint32_t top2 = 0;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const uint32_t w[4] = {cur[k].x, cur[k].y, cur[k].z, cur[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(w[e] & 0x7fff7fffu));
+    }
+    const uint32_t top = max(top2 & 0xffffu, top2 >> 16) << 16;
+    const RowTop t(row_max<kWarpRow>(top, red_max[turn]), first == 0, scale + row);
+    // (448 v) / t: a quotient q = RN(u r), r = RN(1 / t), corrected by its exact
+    // remainder is the correctly rounded u / t (Markstein, IBM J. Res. Dev. 34,
+    // 1990) while no step over- or underflows; so both are taken times a power of
+    // two p that brings t between 2^-53 and 2^64 (quotients whose remainder
+    // underflows all the same are far below the least e4m3 number).  u = 448 v is
+    // exact for a bf16 v.
+    const float p = t.t < 0x1p-40f ? 0x1p64f : t.t > 0x1p60f ? 0x1p-64f : 1.0f;
+    const float d = __fmul_rn(t.t, p), inv = __fdiv_rn(1.0f, d), top_p = __fmul_rn(kTop, p);
+    const f32x2 c = both(top_p), minus_c = both(-top_p), d2 = both(d), r2 = both(inv),
+                minus_r2 = both(-inv);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int i = first + k * stride;
+      if (i >= nvec) continue;
+      uint2 o = make_uint2(0u, 0u);
+      if (t.fine) {
+        const uint32_t w[4] = {cur[k].x, cur[k].y, cur[k].z, cur[k].w};
+        f32x2 q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f32x2 v = widen2(w[e]);
+          q[e] = mul2(mul2(v, c), r2);
+          // (the remainder's sign the way round that keeps a zero's sign)
+          q[e] = fma2(fma2(q[e], d2, mul2(v, minus_c)), minus_r2, q[e]);
+        }
+        o = make_uint2(e4m3x4(q[0], q[1]), e4m3x4(q[2], q[3]));
+      }
+      __stcs(y + row * nvec + i, o);
+    }
+    if (!kAhead) break;
   }
 }
 
@@ -226,21 +240,32 @@ void launch_norm(const void* x, const void* res, const void* w, void* h, void* y
 }
 
 template <int VPT>
-void launch_rows(const void* x, void* y, float* scale, int64_t M, int64_t K, int threads,
-                 cudaStream_t s) {
+bi_status launch_rows(const void* x, void* y, float* scale, int64_t M, int64_t K, int threads,
+                      cudaStream_t s) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return BI_ERR_CUDA;
   const int nvec = static_cast<int>(K / 8);
   const auto* xp = static_cast<const uint4*>(x);
   auto* yp = static_cast<uint2*>(y);
   if constexpr (VPT <= 2) {
     if (threads == 32) {
-      quantize_q8_kernel<VPT, true>
+      quantize_q8_kernel<VPT, true, false>
           <<<static_cast<unsigned>((M + kRowsPerBlock - 1) / kRowsPerBlock), 32 * kRowsPerBlock, 0,
              s>>>(xp, yp, scale, M, nvec);
-      return;
+      return cuda_status(cudaGetLastError());
     }
   }
-  quantize_q8_kernel<VPT, false>
+  if constexpr (VPT == 4) {
+    const int64_t most = static_cast<int64_t>(sms) * (1024 / threads);
+    if (threads > 256 && threads <= 512 && M > most) {
+      quantize_q8_kernel<VPT, false, true>
+          <<<static_cast<unsigned>(most), threads, 0, s>>>(xp, yp, scale, M, nvec);
+      return cuda_status(cudaGetLastError());
+    }
+  }
+  quantize_q8_kernel<VPT, false, false>
       <<<static_cast<unsigned>(M), threads, 0, s>>>(xp, yp, scale, M, nvec);
+  return cuda_status(cudaGetLastError());
 }
 
 }  // namespace
@@ -265,13 +290,12 @@ bi_status launch_quantize_q8(const void* x, void* y, float* scale, int64_t M, in
                              cudaStream_t s) {
   const RowShape sh = row_shape(K);
   switch (sh.vpt) {
-    case 1: launch_rows<1>(x, y, scale, M, K, sh.threads, s); break;
-    case 2: launch_rows<2>(x, y, scale, M, K, sh.threads, s); break;
-    case 4: launch_rows<4>(x, y, scale, M, K, sh.threads, s); break;
-    case 8: launch_rows<8>(x, y, scale, M, K, sh.threads, s); break;
+    case 1: return launch_rows<1>(x, y, scale, M, K, sh.threads, s);
+    case 2: return launch_rows<2>(x, y, scale, M, K, sh.threads, s);
+    case 4: return launch_rows<4>(x, y, scale, M, K, sh.threads, s);
+    case 8: return launch_rows<8>(x, y, scale, M, K, sh.threads, s);
     default: return BI_ERR_UNSUPPORTED;
   }
-  return cuda_status(cudaGetLastError());
 }
 
 }  // namespace bi

@@ -146,6 +146,21 @@ def test_a_row_does_not_depend_on_its_batch(cuda, H):
             assert same_bytes(ys, y[sel]) and same_bytes(ss, s[sel])
 
 
+def test_blocks_that_take_several_rows(cuda):
+    """More rows of more than 8192 elements than blocks: the same bytes as few."""
+    M, K = 700, 12304
+    x = stream_rows(M, K, 61, cuda)
+    x[311, 5] = float("nan")
+    y, s = bi.quantize_q8(x)
+    for at in range(0, M, 100):
+        ys, ss = bi.quantize_q8(x[at:at + 100].contiguous())
+        assert same_bytes(ys, y[at:at + 100])
+        assert same_bytes(ss, s[at:at + 100])
+    want, scale = linear8.quantise(f64(x[300:320]))
+    assert np.array_equal(codes(y[300:320]), want)
+    assert np.array_equal(s[300:320].cpu().numpy(), scale, equal_nan=True)
+
+
 def test_in_place_streams_and_what_lies_behind_the_last_row(cuda):
     M, H, more = 13, 1040, 3
     x, r = stream_rows(M, H, 41, cuda), stream_rows(M, H, 42, cuda)
