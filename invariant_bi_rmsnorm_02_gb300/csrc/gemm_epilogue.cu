@@ -376,9 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
-  // the next kernel in the stream may begin its own prologue; this one's
-  // inputs are there, and nobody reads its output any more, past the wait
-  launch_dependents();
+  // past the wait this kernel's inputs are there and nobody reads its output any
+  // more (it may have started while the one before it in the stream drains)
   grid_dependency_wait();
 
   if (warp == 0) {

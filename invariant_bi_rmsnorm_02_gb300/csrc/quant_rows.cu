@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
   const int stride = kWarpRow ? 32 : blockDim.x;
   const int64_t row =
       kWarpRow ? blockIdx.x * (int64_t)kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
+  grid_dependency_wait();  // (these kernels may start while the one before drains)
   if (kWarpRow && row >= M) return;
   uint4 hv[VPT];
 #pragma unroll
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(kAhead ? 512 : 1024) quantize_q8_kernel(
   const int stride = kWarpRow ? 32 : blockDim.x;
   int64_t row =
       kWarpRow ? blockIdx.x * (int64_t)kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
+  grid_dependency_wait();
   uint4 xv[VPT];
   auto load = [&](int64_t r) {
 #pragma unroll
@@ -217,9 +219,27 @@ __global__ void __launch_bounds__(kAhead ? 512 : 1024) quantize_q8_kernel(
   }
 }
 
+// Launch with programmatic stream serialisation: the blocks may be set up while
+// the previous kernel in the stream drains, and wait for it in the kernel.
+template <typename... KArgs, typename... Args>
+bi_status launch(void (*kernel)(KArgs...), int64_t grid, int threads, cudaStream_t s,
+                 Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...));
+}
+
 template <int VPT, bool kAdd>
-void launch_norm(const void* x, const void* res, const void* w, void* h, void* y, float* scale,
-                 int64_t M, int64_t H, int threads, float eps, cudaStream_t s) {
+bi_status launch_norm(const void* x, const void* res, const void* w, void* h, void* y,
+                      float* scale, int64_t M, int64_t H, int threads, float eps,
+                      cudaStream_t s) {
   const int nvec = static_cast<int>(H / 8);
   const float inv_h = 1.0f / static_cast<float>(H);
   const auto* xp = static_cast<const uint4*>(x);
@@ -228,44 +248,34 @@ void launch_norm(const void* x, const void* res, const void* w, void* h, void* y
   auto* hp = static_cast<uint4*>(h);
   auto* yp = static_cast<uint2*>(y);
   if constexpr (VPT <= 2) {  // a row of one warp has at most 64 vectors
-    if (threads == 32) {
-      rmsnorm_q8_kernel<VPT, kAdd, true>
-          <<<static_cast<unsigned>((M + kRowsPerBlock - 1) / kRowsPerBlock), 32 * kRowsPerBlock, 0,
-             s>>>(xp, rp, wp, hp, yp, scale, M, nvec, inv_h, eps);
-      return;
-    }
+    if (threads == 32)
+      return launch(rmsnorm_q8_kernel<VPT, kAdd, true>, (M + kRowsPerBlock - 1) / kRowsPerBlock,
+                    32 * kRowsPerBlock, s, xp, rp, wp, hp, yp, scale, M, nvec, inv_h, eps);
   }
-  rmsnorm_q8_kernel<VPT, kAdd, false><<<static_cast<unsigned>(M), threads, 0, s>>>(
-      xp, rp, wp, hp, yp, scale, M, nvec, inv_h, eps);
+  return launch(rmsnorm_q8_kernel<VPT, kAdd, false>, M, threads, s, xp, rp, wp, hp, yp, scale, M,
+                nvec, inv_h, eps);
 }
 
 template <int VPT>
 bi_status launch_rows(const void* x, void* y, float* scale, int64_t M, int64_t K, int threads,
                       cudaStream_t s) {
-  const int sms = device_sm_count();
-  if (sms <= 0) return BI_ERR_CUDA;
   const int nvec = static_cast<int>(K / 8);
   const auto* xp = static_cast<const uint4*>(x);
   auto* yp = static_cast<uint2*>(y);
   if constexpr (VPT <= 2) {
-    if (threads == 32) {
-      quantize_q8_kernel<VPT, true, false>
-          <<<static_cast<unsigned>((M + kRowsPerBlock - 1) / kRowsPerBlock), 32 * kRowsPerBlock, 0,
-             s>>>(xp, yp, scale, M, nvec);
-      return cuda_status(cudaGetLastError());
-    }
+    if (threads == 32)
+      return launch(quantize_q8_kernel<VPT, true, false>, (M + kRowsPerBlock - 1) / kRowsPerBlock,
+                    32 * kRowsPerBlock, s, xp, yp, scale, M, nvec);
   }
   if constexpr (VPT == 4) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return BI_ERR_CUDA;
     const int64_t most = static_cast<int64_t>(sms) * (1024 / threads);
-    if (threads > 256 && threads <= 512 && M > most) {
-      quantize_q8_kernel<VPT, false, true>
-          <<<static_cast<unsigned>(most), threads, 0, s>>>(xp, yp, scale, M, nvec);
-      return cuda_status(cudaGetLastError());
-    }
+    if (threads > 256 && threads <= 512 && M > most)
+      return launch(quantize_q8_kernel<VPT, false, true>, most, threads, s, xp, yp, scale, M,
+                    nvec);
   }
-  quantize_q8_kernel<VPT, false, false>
-      <<<static_cast<unsigned>(M), threads, 0, s>>>(xp, yp, scale, M, nvec);
-  return cuda_status(cudaGetLastError());
+  return launch(quantize_q8_kernel<VPT, false, false>, M, threads, s, xp, yp, scale, M, nvec);
 }
 
 }  // namespace
@@ -274,16 +284,14 @@ bi_status launch_rmsnorm_q8(const void* x, const void* res, const void* w, void*
                             float* scale, int64_t M, int64_t H, float eps, cudaStream_t s) {
   const RowShape sh = row_shape(H);
   switch (sh.vpt) {
-#define BI_NORM(V)                                                                    \
-  case V:                                                                             \
-    if (res) launch_norm<V, true>(x, res, w, h, y, scale, M, H, sh.threads, eps, s);  \
-    else launch_norm<V, false>(x, res, w, h, y, scale, M, H, sh.threads, eps, s);     \
-    break;
+#define BI_NORM(V)                                                                             \
+  case V:                                                                                      \
+    return res ? launch_norm<V, true>(x, res, w, h, y, scale, M, H, sh.threads, eps, s)        \
+               : launch_norm<V, false>(x, res, w, h, y, scale, M, H, sh.threads, eps, s);
     BI_NORM(1) BI_NORM(2) BI_NORM(4) BI_NORM(8)
 #undef BI_NORM
     default: return BI_ERR_UNSUPPORTED;
   }
-  return cuda_status(cudaGetLastError());
 }
 
 bi_status launch_quantize_q8(const void* x, void* y, float* scale, int64_t M, int64_t K,
