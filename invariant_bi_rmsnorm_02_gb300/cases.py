@@ -16,13 +16,18 @@ flush between runs -- the unit a profiler capture or a quick timing needs.
     python -m invariant_bi_rmsnorm_02_gb300.cases kv_write_q8 --M 8192
     python -m invariant_bi_rmsnorm_02_gb300.cases kv_read_q8 --B 64
     python -m invariant_bi_rmsnorm_02_gb300.cases decode_q8 --B 64
+    python -m invariant_bi_rmsnorm_02_gb300.cases norm_q8 --M 8192 --H 4096
+    python -m invariant_bi_rmsnorm_02_gb300.cases quantize_q8 --M 8192 --H 14336
+    python -m invariant_bi_rmsnorm_02_gb300.cases gemm_q8 --M 8192 --N 28672 --act swiglu
+    python -m invariant_bi_rmsnorm_02_gb300.cases gemm_epilogue --M 2048 --K 14336 --N 4096 --residual
 
 Prints one line per run with the CUDA-event time of the call (the device is
 kept busy while the call is queued, so host launch latency is not in the
 time) and, for the element-wise, cache and sampling ops, the algorithmic bytes moved
 per second; for the GEMMs, the flops per second.  gemm_swiglu is the gate/up
 projection with SwiGLU in the GEMM epilogue, gemm_silu the same work as two
-calls (the GEMM into [M, 2F], then the SwiGLU kernel).
+calls (the GEMM into [M, 2F], then the SwiGLU kernel).  norm_q8 adds the
+residual first.
 """
 from __future__ import annotations
 
@@ -39,7 +44,8 @@ def main(argv=None):
     ap.add_argument("op", choices=["rmsnorm", "gemm", "decode", "prefill", "add_rmsnorm",
                                    "sample", "rope", "silu", "gather", "gemm_swiglu",
                                    "gemm_silu", "rope_scaled", "kv_write_q8", "kv_read_q8",
-                                   "decode_q8"])
+                                   "decode_q8", "norm_q8", "quantize_q8", "gemm_q8",
+                                   "gemm_epilogue"])
     ap.add_argument("--mode", type=int, default=bi.INVARIANT)
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--M", type=int, default=8192)
@@ -60,6 +66,10 @@ def main(argv=None):
     ap.add_argument("--min-len", type=int, default=1)
     ap.add_argument("--rot", type=int, default=128)
     ap.add_argument("--interleaved", action="store_true")
+    ap.add_argument("--act", choices=["none", "relu", "gelu", "gelu_tanh", "silu", "swiglu"],
+                    default="none")
+    ap.add_argument("--bias", action="store_true")
+    ap.add_argument("--residual", action="store_true")
     a = ap.parse_args(argv)
     nbytes = 0  # algorithmic bytes of one call (element-wise and sampling ops)
     flops = 0   # algorithmic flops of one call (GEMMs)
@@ -135,6 +145,28 @@ def main(argv=None):
         w = synth.normal_bf16((a.H,), 2, device=dev)
         fn = lambda: bi.add_rmsnorm(x, r, w, 1e-6, a.mode)
         nbytes = 4 * a.M * a.H * 2 + a.H * 2       # read x, r; write h, y; w once
+    elif a.op == "norm_q8":
+        x, r = (synth.normal_bf16((a.M, a.H), i, device=dev) for i in (1, 3))
+        w = synth.normal_bf16((a.H,), 2, device=dev)
+        fn = lambda: bi.add_rmsnorm_q8(x, r, w, 1e-6)
+        nbytes = a.M * (7 * a.H + 4) + a.H * 2     # read x, r; write h, y, scale; w once
+    elif a.op == "quantize_q8":
+        x = synth.normal_bf16((a.M, a.H), 1, device=dev)
+        fn = lambda: bi.quantize_q8(x)
+        nbytes = a.M * (3 * a.H + 4)
+    elif a.op in ("gemm_q8", "gemm_epilogue"):
+        act = getattr(bi, "ACT_" + a.act.upper())
+        n = a.N // 2 if act == bi.ACT_SWIGLU else a.N
+        A = synth.normal_bf16((a.M, a.K), 1, device=dev)
+        W = synth.normal_bf16((a.N, a.K), 2, std=0.02, device=dev)
+        b = synth.normal_bf16((a.N,), 3, device=dev) if a.bias else None
+        r = synth.normal_bf16((a.M, n), 4, device=dev) if a.residual else None
+        if a.op == "gemm_q8":
+            (A, sa), (W, sw) = bi.quantize_q8(A), bi.quantize_q8(W)
+            fn = lambda: bi.gemm_q8(A, sa, W, sw, b, r, act)
+        else:
+            fn = lambda: bi.gemm_epilogue(A, W, b, r, act)
+        flops = 2 * a.M * a.N * a.K
     elif a.op == "sample":
         z = synth.normal_bf16((a.B, a.V), 1, std=2.0, device=dev)
         T = torch.full((a.B,), a.temp, device=dev)
