@@ -222,15 +222,17 @@ bi_status bi_gemm_swiglu(const void* A, const void* W, void* out, int64_t M, int
  *                     bias) come in blocks of 16 gate rows and then the 16 up
  *                     rows of the same features (bi_gemm_swiglu's are of 128)
  * Sums are fp32, one rounding to bf16 at the end (neither z nor g and u are
- * rounded before).  With BI_ACT_NONE, no bias and no residual C has exactly
- * the bytes of bi_gemm in BI_MODE_INVARIANT; every row of C depends only on
- * its rows of A and residual, on W and on bias, whatever M (there is no
- * batch-variant mode).  Needs no workspace.
+ * rounded before); the activations are evaluated to 2^-14 of their value and
+ * 2^-119, or better.  At z = -inf RELU and GELU give 0, the others but NONE NaN.
+ * With BI_ACT_NONE, no bias and no residual C has exactly the bytes of bi_gemm
+ * in BI_MODE_INVARIANT; every row of C depends only on its rows of A and
+ * residual, on W and on bias, whatever M (there is no batch-variant mode).
+ * Needs no workspace.
  * residual may be C (the residual stream updated in place); otherwise C
  *   overlaps no input (BI_ERR_INVALID_ARG).
  * Requirements: M >= 0, N, K >= 1, N % 8 == 0 (32 with BI_ACT_SWIGLU),
- *   K % 8 == 0, all below 2^31 - 256 and K below half that; pointers 16-byte
- *   aligned.  Errors: as bi_gemm. */
+ *   K % 8 == 0, M and N at most 2^31 - 1024, K at most half that; pointers
+ *   16-byte aligned.  Errors: as bi_gemm. */
 typedef enum bi_activation {
   BI_ACT_NONE = 0,
   BI_ACT_RELU = 1,
@@ -250,9 +252,9 @@ bi_status bi_gemm_epilogue(const void* A, const void* W, const void* bias, const
  *   once (so scales whose product with the sum leaves fp32's normal range lose
  *   digits or overflow).  A row whose scale is NaN makes its row (A) or
  *   column (W) of C NaN, as do the bytes 0x7f and 0xff, which are NaN.
- * One instruction family (tcgen05.mma kind::f8f6f4, M=128, K=32) and one K
- *   order for every shape: rows do not depend on M here either.
- * Requirements: as bi_gemm_epilogue but K % 16 == 0 and K below 2^31 - 256;
+ * One instruction family (tcgen05.mma kind::f8f6f4, K=32) and one K order for
+ *   every shape: rows do not depend on M here either.
+ * Requirements: as bi_gemm_epilogue but K % 16 == 0 and at most 2^31 - 1024;
  *   a_scale 4-byte aligned. */
 bi_status bi_gemm_q8(const void* A, const float* a_scale, const void* W, const float* w_scale,
                      const void* bias, const void* residual, void* C, int64_t M, int64_t N,

@@ -427,8 +427,9 @@ static bi_status gemm_fused(const void* A, const float* a_scale, const void* W,
   const bool swiglu = act == BI_ACT_SWIGLU;
   const int64_t wide = q8 ? 1 : 2;
   if (N % (swiglu ? 32 : 8) != 0 || K * wide % 16 != 0) return BI_ERR_UNSUPPORTED;
-  // (the kernels form tile coordinates and byte offsets along K in 32 bits)
-  constexpr int64_t kMost = (int64_t(1) << 31) - 256;
+  // (the kernels form tile coordinates and byte offsets along K in 32 bits, up
+  // to a stage past the end)
+  constexpr int64_t kMost = (int64_t(1) << 31) - 1024;
   if (M > kMost || N > kMost || K > kMost / wide) return BI_ERR_UNSUPPORTED;
   if (M == 0) return BI_OK;
   if (!A || !W || !C || (q8 && (!a_scale || !w_scale))) return BI_ERR_INVALID_ARG;

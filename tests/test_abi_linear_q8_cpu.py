@@ -75,8 +75,8 @@ def _q8(lib, **kw):
 
 @pytest.mark.parametrize("call", [_bf16, _q8])
 def test_products_refuse_shapes_and_pointers(lib, call):
-    for bad in (dict(N=12), dict(K=12), dict(N=48, act=bi.ACT_SWIGLU), dict(M=(1 << 31) - 255),
-                dict(N=(1 << 31) - 248), dict(K=(1 << 31) - 240)):
+    for bad in (dict(N=12), dict(K=12), dict(N=48, act=bi.ACT_SWIGLU), dict(M=(1 << 31) - 1023),
+                dict(N=(1 << 31) - 992), dict(K=(1 << 31) - 1008)):
         assert call(lib, **bad) == bi.ERR_UNSUPPORTED, bad
     for bad in (dict(M=-1), dict(N=0), dict(K=0), dict(act=6), dict(act=-1), dict(A=None),
                 dict(W=None), dict(C=None), dict(A=P + 8), dict(W=2 * P + 8), dict(b=3 * P + 8),

@@ -153,6 +153,92 @@ def test_values_that_are_not_finite_stay_in_their_row(cuda, kind):
     assert same_bytes(got[:, cols].contiguous(), want[:, cols].contiguous())
 
 
+def test_e4m3_nan_bytes(cuda):
+    for M in (5, 200):
+        c = Case("q8", M, 96, 144, cuda, 7100 + M, "silu", residual=False)
+        want = c.run()
+        c.a.view(torch.uint8)[3, 100] = 0x7f
+        c.w.view(torch.uint8)[50, 7] = 0xff
+        got = c.run()
+        assert torch.isnan(got[3]).all() and torch.isnan(got[:, 50]).all()
+        rows = [i for i in range(M) if i != 3]
+        cols = [j for j in range(96) if j != 50]
+        assert same_bytes(got[rows][:, cols].contiguous(), want[rows][:, cols].contiguous())
+
+
+def test_activations_at_their_ends(cuda):
+    """z far into both tails, both infinities and NaN, through a product with an
+    identity."""
+    z = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 2.0 ** -120, 0.5, -0.5, 5.0, -5.0, -12.0, -30.0, -87.0,
+                      -88.5, -100.0, -1e4, -3e38, 12.0, 30.0, 1e4, 3e38, float("inf"),
+                      -float("inf"), float("nan")])
+    A = torch.zeros(len(z), 32)
+    A[:, 0] = z
+    W = torch.zeros(32, 32)
+    W[0, 0] = 1.0        # column 0 is z, the others 0 (0 times inf or NaN: NaN)
+    A, W = A.to(torch.bfloat16).to(cuda), W.to(torch.bfloat16).to(cuda)
+    zb = A[:, 0].double().cpu().numpy()
+    inf = np.inf
+    ends = {"none": (inf, -inf), "relu": (inf, 0.0), "gelu": (inf, 0.0), "gelu_tanh": (inf, None),
+            "silu": (inf, None)}
+    for act, (hi, lo) in ends.items():
+        got = bi.gemm_epilogue(A, W, activation=ACTS[act])[:, 0].double().cpu().numpy()
+        fin = np.isfinite(zb)
+        want = linear8.activation(zb[fin], act)
+        bound = 2.0 ** -14 * np.abs(want) + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -10) + 2.0 ** -118
+        assert (np.abs(got[fin] - want) <= bound).all(), (act, got, want)
+        assert got[20] == hi and (np.isnan(got[21]) if lo is None else got[21] == lo), act
+        assert np.isnan(got[22]), act
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+def test_operands_on_16_byte_boundaries(cuda, kind):
+    """Every pointer 16 bytes past a 256-byte boundary, rows of no whole k-block."""
+    def off(t):
+        n = t.numel() * t.element_size()
+        b = torch.zeros(n + 272, dtype=torch.uint8, device=cuda)
+        at = (-b.data_ptr()) % 256 + 16
+        v = b[at:at + n].view(t.dtype).view(t.shape)
+        v.copy_(t)
+        assert v.data_ptr() % 32 == 16
+        return v
+    for M in (3, 65, 300):
+        c = Case(kind, M, 328, 208, cuda, 9000 + M, "gelu")
+        want = c.run()
+        out = off(torch.zeros_like(want))
+        b, r = off(c.b), off(c.r)
+        if kind == "q8":
+            bi.bi_gemm_q8(off(c.a), off(c.sa), off(c.w), off(c.sw), out, b, r, c.act)
+        else:
+            bi.bi_gemm_epilogue(off(c.a), off(c.w), out, b, r, c.act)
+        assert same_bytes(out, want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+def test_outputs_past_32_bits(cuda, kind):
+    """C of 2.3e9 elements with a residual: rows at both ends as a small call
+    gives them."""
+    M, N, K = 70016, 32768, 64
+    A = synth.normal_bf16((M, K), 41, device=cuda)
+    W = synth.normal_bf16((N, K), 42, std=0.1, device=cuda)
+    b = synth.normal_bf16((N,), 43, device=cuda)
+    h = torch.full((M, N), 0.5, dtype=torch.bfloat16, device=cuda)
+    if kind == "q8":
+        (a, sa), (w, sw) = bi.quantize_q8(A), bi.quantize_q8(W)
+        bi.bi_gemm_q8(a, sa, w, sw, h, b, h, bi.ACT_SILU)
+        few = lambda i: bi.gemm_q8(a[i].contiguous(), sa[i].contiguous(), w, sw, b,
+                                   torch.full((i.stop - i.start, N), 0.5, dtype=torch.bfloat16,
+                                              device=cuda), bi.ACT_SILU)
+    else:
+        bi.bi_gemm_epilogue(A, W, h, b, h, bi.ACT_SILU)
+        few = lambda i: bi.gemm_epilogue(A[i].contiguous(), W, b,
+                                         torch.full((i.stop - i.start, N), 0.5,
+                                                    dtype=torch.bfloat16, device=cuda), bi.ACT_SILU)
+    for i in (slice(0, 5), slice(M // 2 - 3, M // 2 + 3), slice(65530, 65540), slice(M - 130, M)):
+        assert same_bytes(h[i], few(i))
+    assert bi.bi_check_device_errors() == bi.OK
+
+
 def test_e4m3_sums_are_exact_where_fp32_holds_them(cuda):
     """Operands whose products and partial sums are integers below 2^24: every
     output is the integer sum rounded once."""

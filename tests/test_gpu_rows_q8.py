@@ -161,6 +161,23 @@ def test_blocks_that_take_several_rows(cuda):
     assert np.array_equal(s[300:320].cpu().numpy(), scale, equal_nan=True)
 
 
+def test_rows_past_32_bits(cuda):
+    """2.3e9 elements: rows at both ends as a small call gives them."""
+    M, H = 140000, 16400
+    x = torch.empty(M, H, dtype=torch.bfloat16, device=cuda)
+    part = stream_rows(7, H, 71, cuda)
+    x[:] = part[0]
+    x[M - 7:] = part
+    x[M // 2:M // 2 + 7] = part.flip(0)
+    w = synth.normal_bf16((H,), 72, device=cuda)
+    for call in (bi.quantize_q8, lambda t: bi.rmsnorm_q8(t, w),
+                 lambda t: bi.add_rmsnorm_q8(t, t.clone(), w)):
+        y, s = call(x)
+        for at in (0, M // 2, M - 7):
+            ys, ss = call(x[at:at + 7].contiguous())
+            assert same_bytes(ys, y[at:at + 7]) and same_bytes(ss, s[at:at + 7])
+
+
 def test_in_place_streams_and_what_lies_behind_the_last_row(cuda):
     M, H, more = 13, 1040, 3
     x, r = stream_rows(M, H, 41, cuda), stream_rows(M, H, 42, cuda)
