@@ -17,9 +17,11 @@
 // not depend on its order.
 //
 // A row is read once and kept in registers; one row per block, or one per warp
-// (eight a block) where the row's shape is one warp.  What bounds it at first
-// is instructions, not memory (33 million elements at 16 instructions each are
-// 15 us of issue slots, against 15 of memory), so products and quotients are
+// (eight a block) where the row's shape is one warp.  Bound by memory for many
+// rows (8192 of 14336 quantised 56 us = 6.3 TB/s, 0.93 of the measured rate), by
+// the launch for few (64 of 4096: 1.5 us among others).  With one value an
+// instruction it was instructions that bounded it (33 million elements at 16 each
+// are 15 us of issue slots, against 15 of memory); products and quotients are
 // formed two at a time (f32x2).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -76,9 +78,12 @@ __device__ __forceinline__ uint32_t e4m3x4(f32x2 a, f32x2 b) {
 }
 
 // kAdd: h = bf16(x + res) first, written to h (which may be x or res: a
-// thread reads its elements of both before it writes any).
-template <int VPT, bool kAdd, bool kWarpRow>
-__global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
+// thread reads its elements of both before it writes any).  kShort: blocks of at
+// most 256 threads, of which 48 registers let five (of 256) share an SM and cover
+// for one another (8192 rows of 4096 without a residual 18.9 us, 17.1 in a loop,
+// 0.87 of the measured rate; with one 41.4 and 40.9, 0.85).
+template <int VPT, bool kAdd, bool kWarpRow, bool kShort>
+__global__ void __launch_bounds__(kShort ? 256 : 1024, kShort ? 5 : 1) rmsnorm_q8_kernel(
     const uint4* x, const uint4* res, const uint4* __restrict__ w, uint4* h,
     uint2* __restrict__ y, float* __restrict__ scale, int64_t M, int nvec, float inv_h,
     float eps) {
@@ -249,11 +254,16 @@ bi_status launch_norm(const void* x, const void* res, const void* w, void* h, vo
   auto* yp = static_cast<uint2*>(y);
   if constexpr (VPT <= 2) {  // a row of one warp has at most 64 vectors
     if (threads == 32)
-      return launch(rmsnorm_q8_kernel<VPT, kAdd, true>, (M + kRowsPerBlock - 1) / kRowsPerBlock,
+      return launch(rmsnorm_q8_kernel<VPT, kAdd, true, false>, (M + kRowsPerBlock - 1) / kRowsPerBlock,
                     32 * kRowsPerBlock, s, xp, rp, wp, hp, yp, scale, M, nvec, inv_h, eps);
   }
-  return launch(rmsnorm_q8_kernel<VPT, kAdd, false>, M, threads, s, xp, rp, wp, hp, yp, scale, M,
-                nvec, inv_h, eps);
+  if constexpr (VPT == 4) {
+    if (threads <= 256)
+      return launch(rmsnorm_q8_kernel<VPT, kAdd, false, true>, M, threads, s, xp, rp, wp, hp, yp,
+                    scale, M, nvec, inv_h, eps);
+  }
+  return launch(rmsnorm_q8_kernel<VPT, kAdd, false, false>, M, threads, s, xp, rp, wp, hp, yp,
+                scale, M, nvec, inv_h, eps);
 }
 
 template <int VPT>
