@@ -507,7 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
       load_residual(span.c);
       if (adds && (p.kb_total >= kLongBlocks || units <= step))
         for (int c = span.c + 1; c < span.end; ++c) prefetch_l2(res + c * kChunk);
-      ok = __all_sync(kFull, mbar_wait(&tfull[acc], acc_phase, p.err, &abort_flag));
+      // (the one wait that lasts for a whole tile: a microsecond more for each
+      // k-block, which takes 0.06 to 0.2)
+      ok = __all_sync(kFull, mbar_wait(&tfull[acc], acc_phase, p.err, &abort_flag,
+                                       kWaitNs + static_cast<uint64_t>(p.kb_total) * 1000));
       if (!ok) break;
       tc_fence_after();
       const f32x2 a_scale = both(row_scale);

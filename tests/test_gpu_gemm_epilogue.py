@@ -342,3 +342,83 @@ def test_an_8_bit_feed_forward_layer(cuda):
         graph.replay()
     assert same_bytes(hg, h)
     assert bi.bi_check_device_errors() == bi.OK
+
+
+def test_the_longest_rows(cuda):
+    """The largest K there is: a tile's sum lasts more than a second."""
+    M, N, K = 1, 8, 2 ** 31 - 1024
+    a = torch.zeros(M, K, dtype=torch.float8_e4m3fn, device=cuda)
+    w = torch.zeros(N, K, dtype=torch.float8_e4m3fn, device=cuda)
+    at = torch.tensor([0, 127, 2 ** 30, 2 ** 31 - 2048, K - 1], device=cuda)
+    one = 0x38  # e4m3
+    a.view(torch.uint8)[0, at] = one
+    for n in range(N):
+        w.view(torch.uint8)[n, at[:n % 6]] = one
+    scale = torch.ones(N, dtype=torch.float32, device=cuda)
+    got = bi.gemm_q8(a, scale[:1], w, scale)
+    assert bi.bi_check_device_errors() == bi.OK
+    assert got[0].tolist() == [float(n % 6) for n in range(N)]
+
+
+def chain(x8, sx, w, sw, act, a8, sa, wd, sd, h):
+    """Four calls, each of which reads what the one before it wrote."""
+    bi.bi_quantize_q8(h, x8, sx)
+    bi.bi_gemm_q8(x8, sx, w, sw, act, activation=bi.ACT_GELU_TANH)
+    bi.bi_quantize_q8(act, a8, sa)
+    bi.bi_gemm_q8(a8, sa, wd, sd, h, residual=h)
+
+
+@pytest.mark.parametrize("M", [3, 100, 300, 2048])
+def test_calls_that_follow_one_another(cuda, M):
+    """The feed-forward calls thirty times over the same buffers, with nothing
+    between them: queued at once, from a graph, and from two graphs on two
+    streams they give what they give with the device idle between them."""
+    H, F = 512, 1104
+    f8 = dict(dtype=torch.float8_e4m3fn, device=cuda)
+    w, sw = bi.quantize_q8(synth.normal_bf16((F, H), 61, std=H ** -0.5, device=cuda))
+    wd, sd = bi.quantize_q8(synth.normal_bf16((H, F), 62, std=F ** -0.5, device=cuda))
+    starts = [synth.normal_bf16((M, H), 63 + i, device=cuda) for i in range(2)]
+
+    def buffers():
+        return (torch.empty(M, H, **f8), torch.empty(M, dtype=torch.float32, device=cuda), w, sw,
+                torch.empty(M, F, dtype=torch.bfloat16, device=cuda), torch.empty(M, F, **f8),
+                torch.empty(M, dtype=torch.float32, device=cuda), wd, sd)
+
+    want = []
+    for h0 in starts:
+        h, b = h0.clone(), buffers()
+        for _ in range(30):
+            bi.bi_quantize_q8(h, b[0], b[1])
+            torch.cuda.synchronize()
+            bi.bi_gemm_q8(*b[:5], activation=bi.ACT_GELU_TANH)
+            torch.cuda.synchronize()
+            bi.bi_quantize_q8(b[4], b[5], b[6])
+            torch.cuda.synchronize()
+            bi.bi_gemm_q8(*b[5:], h, residual=h)
+            torch.cuda.synchronize()
+        want.append(h)
+    assert torch.isfinite(want[0]).all() and not same_bytes(want[0], starts[0])
+    h, b = starts[0].clone(), buffers()
+    for _ in range(30):
+        chain(*b, h)
+    assert same_bytes(h, want[0])
+    hs, graphs = [torch.empty_like(h) for h in starts], []
+    for i in range(2):
+        b = buffers()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(30):
+                chain(*b, hs[i])
+        graphs.append((g, b))
+    streams = [torch.cuda.Stream() for _ in starts]
+    for _ in range(2):
+        for i in range(2):
+            hs[i].copy_(starts[i])
+        torch.cuda.synchronize()
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert same_bytes(hs[i], want[i]), first_divergence(hs[i], want[i])
+    assert bi.bi_check_device_errors() == bi.OK
