@@ -29,11 +29,11 @@
 // What bounds it (one GB300, calls in a loop; rates are of the measured 1957
 // TFLOP/s bf16, twice that for e4m3, and 6777 GB/s): with many rows the tensor
 // cores and the power they draw (8192 x 28672 x 4096 e4m3 with SwiGLU 492 us =
-// 3.9 PFLOP/s, 1.00; bf16 2048 x 4096 x 14336 with the residual 137 us, 0.90);
-// with few the weight's bytes (64 x 28672 x 4096 e4m3 22 us, 0.80) and for short
+// 3.9 PFLOP/s, 1.00; bf16 2048 x 4096 x 14336 with the residual 131 us, 0.94);
+// with few the weight's bytes (64 x 28672 x 4096 e4m3 21 us, 0.83) and for short
 // ones start and end, some 3 us, and the chain of one accumulator's MMAs, some
 // 50 cycles each (16 x 6144 x 4096 e4m3 5.9 us, 0.64); short K the epilogue
-// (8192 x 14336 x 1024 e4m3 107 us, with GELU and a residual 197).
+// (8192 x 14336 x 1024 e4m3 101 us, with GELU 155, with a residual too 194).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -131,8 +131,8 @@ __device__ __forceinline__ Tile tile_of(int u, const FusedParams& p) {
 // The activations take the special-function unit's exponential and reciprocal
 // (2^-22 relative, results below 2^-126 flushed to zero) instead of expf and a
 // division, whose path for special cases kept a warp from interleaving its 32
-// values (100 cycles a value; 8192 x 14336 x 1024 e4m3 with SiLU 815 us against
-// 483 without), and the result is rounded to 2^-9.  Everything else goes two
+// values (100 cycles a value: 330 us at 8192 x 14336 x 1024 e4m3 with SiLU, where
+// this takes 20), and the result is rounded to 2^-9.  Everything else goes two
 // values at a time (f32x2).
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -166,27 +166,31 @@ __device__ __forceinline__ f32x2 gelu_tanh(f32x2 z) {
 }
 // max(z, 0), a NaN where z is one
 __device__ __forceinline__ f32x2 relu(f32x2 z) {
-  const float2 f = halves(z);
-  return pair(f.x <= 0.0f ? 0.0f : f.x, f.y <= 0.0f ? 0.0f : f.y);
+  float2 f = halves(z);
+  asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(f.x));
+  asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(f.y));
+  return pair(f.x, f.y);
 }
 // z/2 (1 + erf(z / sqrt 2)) = max(z, 0) - |z|/2 erfcx(x) exp(-x^2), x = |z| / sqrt 2,
-// with erfcx(x)/2 as t times a polynomial in t = 1 / (1 + x/2): the least
+// with -erfcx(x)/2 as t times a polynomial in t = 1 / (1 + x/2): the least
 // largest relative error of degree 6 over 0 <= x <= 11.4, by linear
 // programming; 2^-18.8 in fp32.  Both tails keep their digits.  Past |z| = 16
-// the second term is 0.
+// the second term is 0.  One reciprocal, of the product of both denominators
+// (1 .. 6.7), serves the two values.
 __device__ __forceinline__ f32x2 gelu(f32x2 z) {
   const float2 f = halves(z);
   const f32x2 m = pair(fminf(fabsf(f.x), 16.0f), fminf(fabsf(f.y), 16.0f));
-  const f32x2 t = rcp_2(fma2(m, both(0.35355339059327376f), both(1.0f)));
-  f32x2 s = both(0.0429137014f);
-  s = fma2(s, t, both(-0.174213769f));
-  s = fma2(s, t, both(0.188846613f));
-  s = fma2(s, t, both(0.0229806649f));
-  s = fma2(s, t, both(0.139260697f));
-  s = fma2(s, t, both(0.139064864f));
-  s = fma2(s, t, both(0.141146311f));
+  const float2 d = halves(fma2(m, both(0.35355339059327376f), both(1.0f)));
+  const f32x2 t = mul2(both(rcp(d.x * d.y)), pair(d.y, d.x));
+  f32x2 s = both(-0.0429137014f);
+  s = fma2(s, t, both(0.174213769f));
+  s = fma2(s, t, both(-0.188846613f));
+  s = fma2(s, t, both(-0.0229806649f));
+  s = fma2(s, t, both(-0.139260697f));
+  s = fma2(s, t, both(-0.139064864f));
+  s = fma2(s, t, both(-0.141146311f));
   const f32x2 e = ex2_2(mul2(mul2(m, m), both(-0.5f * kLog2e)));
-  return fma2(mul2(mul2(s, t), mul2(m, both(-1.0f))), e, relu(z));
+  return fma2(mul2(s, mul2(t, m)), e, relu(z));
 }
 
 // In 32 values, one activation; the choice is the same for the whole call.
