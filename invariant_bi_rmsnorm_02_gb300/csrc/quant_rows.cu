@@ -18,7 +18,8 @@
 //
 // A row is read once and kept in registers; one row per block, or one per warp
 // (eight a block) where the row's shape is one warp.  Bound by memory for many
-// rows (8192 of 14336 quantised 56 us = 6.3 TB/s, 0.93 of the measured rate), by
+// rows (8192 of 14336 quantised 56 us = 6.3 TB/s, 0.93 of the measured rate; the norm
+// of 8192 of 4096 with a residual 37 us, 0.93), by
 // the launch for few (64 of 4096: 1.5 us among others).  With one value an
 // instruction it was instructions that bounded it (33 million elements at 16 each
 // are 15 us of issue slots, against 15 of memory); products and quotients are
@@ -81,7 +82,7 @@ __device__ __forceinline__ uint32_t e4m3x4(f32x2 a, f32x2 b) {
 // thread reads its elements of both before it writes any).  kShort: blocks of at
 // most 256 threads, of which 48 registers let five (of 256) share an SM and cover
 // for one another (8192 rows of 4096 without a residual 18.9 us, 17.1 in a loop,
-// 0.87 of the measured rate; with one 41.4 and 40.9, 0.85).
+// 0.87 of the measured rate; with one 37.4, 0.93).
 template <int VPT, bool kAdd, bool kWarpRow, bool kShort>
 __global__ void __launch_bounds__(kShort ? 256 : 1024, kShort ? 5 : 1) rmsnorm_q8_kernel(
     const uint4* x, const uint4* res, const uint4* __restrict__ w, uint4* h,
@@ -95,20 +96,21 @@ __global__ void __launch_bounds__(kShort ? 256 : 1024, kShort ? 5 : 1) rmsnorm_q
       kWarpRow ? blockIdx.x * (int64_t)kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
   grid_dependency_wait();  // (these kernels may start while the one before drains)
   if (kWarpRow && row >= M) return;
-  uint4 hv[VPT];
+  uint4 hv[VPT], rv[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int i = first + k * stride;
-    hv[k] = make_uint4(0, 0, 0, 0);
+    hv[k] = rv[k] = make_uint4(0, 0, 0, 0);
     if (i < nvec) {
       hv[k] = __ldcs(x + row * nvec + i);
-      if (kAdd) hv[k] = add_bf16x8(hv[k], __ldcs(res + row * nvec + i));
+      if (kAdd) rv[k] = __ldcs(res + row * nvec + i);
     }
   }
-  if (kAdd) {
+  if (kAdd) {  // (in a loop of its own: a sum between the loads waits for those before it)
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int i = first + k * stride;
+      hv[k] = add_bf16x8(hv[k], rv[k]);
       if (i < nvec) __stcs(h + row * nvec + i, hv[k]);
     }
   }
