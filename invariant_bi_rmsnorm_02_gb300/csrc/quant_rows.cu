@@ -18,9 +18,9 @@
 //
 // A row is read once and kept in registers; one row per block, or one per warp
 // (eight a block) where the row's shape is one warp.  Bound by memory for many
-// rows (8192 of 14336 quantised 56 us = 6.3 TB/s, 0.93 of the measured rate; the norm
-// of 8192 of 4096 with a residual 37 us, 0.93), by
-// the launch for few (64 of 4096: 1.5 us among others).  With one value an
+// rows (8192 of 14336 quantised 56 us = 6.3 TB/s, 0.93 of the measured rate; the
+// norm of 8192 of 4096 with a residual 36 us, 0.96), by the launch for few (64 of
+// 4096: 1.5 and 2.0 us among others).  With one value an
 // instruction it was instructions that bounded it (33 million elements at 16 each
 // are 15 us of issue slots, against 15 of memory); products and quotients are
 // formed two at a time (f32x2).
@@ -79,12 +79,11 @@ __device__ __forceinline__ uint32_t e4m3x4(f32x2 a, f32x2 b) {
 }
 
 // kAdd: h = bf16(x + res) first, written to h (which may be x or res: a
-// thread reads its elements of both before it writes any).  kShort: blocks of at
-// most 256 threads, of which 48 registers let five (of 256) share an SM and cover
-// for one another (8192 rows of 4096 without a residual 18.9 us, 17.1 in a loop,
-// 0.87 of the measured rate; with one 37.4, 0.93).
-template <int VPT, bool kAdd, bool kWarpRow, bool kShort>
-__global__ void __launch_bounds__(kShort ? 256 : 1024, kShort ? 5 : 1) rmsnorm_q8_kernel(
+// thread reads its elements of both before it writes any).  64 registers a
+// thread; with 48, of which one more block of 256 threads fits an SM, values
+// were spilled (64 rows of 4096 1.8 us, 2.4; 8192 16.9, 17.3).
+template <int VPT, bool kAdd, bool kWarpRow>
+__global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
     const uint4* x, const uint4* res, const uint4* __restrict__ w, uint4* h,
     uint2* __restrict__ y, float* __restrict__ scale, int64_t M, int nvec, float inv_h,
     float eps) {
@@ -96,22 +95,28 @@ __global__ void __launch_bounds__(kShort ? 256 : 1024, kShort ? 5 : 1) rmsnorm_q
       kWarpRow ? blockIdx.x * (int64_t)kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
   grid_dependency_wait();  // (these kernels may start while the one before drains)
   if (kWarpRow && row >= M) return;
-  uint4 hv[VPT], rv[VPT];
+  // (the sums in a loop of their own: one between the loads waits for those before it)
+  constexpr int kGroup = VPT < 4 ? VPT : 4;
+  uint4 hv[VPT];
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int i = first + k * stride;
-    hv[k] = rv[k] = make_uint4(0, 0, 0, 0);
-    if (i < nvec) {
-      hv[k] = __ldcs(x + row * nvec + i);
-      if (kAdd) rv[k] = __ldcs(res + row * nvec + i);
+  for (int k0 = 0; k0 < VPT; k0 += kGroup) {
+    uint4 rv[kGroup];
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      const int i = first + (k0 + g) * stride;
+      hv[k0 + g] = rv[g] = make_uint4(0, 0, 0, 0);
+      if (i < nvec) {
+        hv[k0 + g] = __ldcs(x + row * nvec + i);
+        if (kAdd) rv[g] = __ldcs(res + row * nvec + i);
+      }
     }
-  }
-  if (kAdd) {  // (in a loop of its own: a sum between the loads waits for those before it)
+    if (kAdd) {
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int i = first + k * stride;
-      hv[k] = add_bf16x8(hv[k], rv[k]);
-      if (i < nvec) __stcs(h + row * nvec + i, hv[k]);
+      for (int g = 0; g < kGroup; ++g) {
+        const int i = first + (k0 + g) * stride;
+        hv[k0 + g] = add_bf16x8(hv[k0 + g], rv[g]);
+        if (i < nvec) __stcs(h + row * nvec + i, hv[k0 + g]);
+      }
     }
   }
   float ss = 0.0f;
@@ -120,19 +125,26 @@ __global__ void __launch_bounds__(kShort ? 256 : 1024, kShort ? 5 : 1) rmsnorm_q
   // (a row of one warp: block_sum's second butterfly adds zeros)
   const float r = inv_rms(kWarpRow ? warp_sum(ss) : block_sum(ss, red), inv_h, eps);
   const f32x2 r2 = both(r);
-  f32x2 v[VPT][4];
-  float top = 0.0f;
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) {
+  auto values = [&](int k, f32x2 (&v)[4]) {
     const int i = first + k * stride;
     const uint4 wv = i < nvec ? __ldg(w + i) : make_uint4(0, 0, 0, 0);
     const uint32_t hw[4] = {hv[k].x, hv[k].y, hv[k].z, hv[k].w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[k][e] = mul2(mul2(widen2(hw[e]), r2), widen2(ww[e]));
-    if (i >= nvec) continue;  // (0 times an infinite r is no element's value)
+    for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(widen2(hw[e]), r2), widen2(ww[e]));
+  };
+  // blocks of 1024 threads have registers for the row, not for its values too:
+  // they form them twice (1024 x 65536 with a residual 95 us when kept, 86 when not)
+  constexpr bool kKeep = VPT <= 4;
+  f32x2 v[kKeep ? VPT : 1][4];
+  float top = 0.0f;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    f32x2(&vk)[4] = v[kKeep ? k : 0];
+    values(k, vk);
+    if (first + k * stride >= nvec) continue;  // (0 times an infinite r is no element's value)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 f = halves(v[k][e]);
+      const float2 f = halves(vk[e]);
       top = max_nan(max_nan(top, f.x), f.y);
     }
   }
@@ -145,9 +157,14 @@ __global__ void __launch_bounds__(kShort ? 256 : 1024, kShort ? 5 : 1) rmsnorm_q
     if (i >= nvec) continue;
     uint2 o = make_uint2(0u, 0u);
     if (t.fine) {
+      f32x2(&vk)[4] = v[kKeep ? k : 0];
+      if (!kKeep) {
+        asm volatile("" : "+r"(hv[k].x), "+r"(hv[k].y), "+r"(hv[k].z), "+r"(hv[k].w));
+        values(k, vk);
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[k][e] = mul2(v[k][e], q);
-      o = make_uint2(e4m3x4(v[k][0], v[k][1]), e4m3x4(v[k][2], v[k][3]));
+      for (int e = 0; e < 4; ++e) vk[e] = mul2(vk[e], q);
+      o = make_uint2(e4m3x4(vk[0], vk[1]), e4m3x4(vk[2], vk[3]));
     }
     __stcs(y + row * nvec + i, o);
   }
@@ -256,15 +273,10 @@ bi_status launch_norm(const void* x, const void* res, const void* w, void* h, vo
   auto* yp = static_cast<uint2*>(y);
   if constexpr (VPT <= 2) {  // a row of one warp has at most 64 vectors
     if (threads == 32)
-      return launch(rmsnorm_q8_kernel<VPT, kAdd, true, false>, (M + kRowsPerBlock - 1) / kRowsPerBlock,
+      return launch(rmsnorm_q8_kernel<VPT, kAdd, true>, (M + kRowsPerBlock - 1) / kRowsPerBlock,
                     32 * kRowsPerBlock, s, xp, rp, wp, hp, yp, scale, M, nvec, inv_h, eps);
   }
-  if constexpr (VPT == 4) {
-    if (threads <= 256)
-      return launch(rmsnorm_q8_kernel<VPT, kAdd, false, true>, M, threads, s, xp, rp, wp, hp, yp,
-                    scale, M, nvec, inv_h, eps);
-  }
-  return launch(rmsnorm_q8_kernel<VPT, kAdd, false, false>, M, threads, s, xp, rp, wp, hp, yp,
+  return launch(rmsnorm_q8_kernel<VPT, kAdd, false>, M, threads, s, xp, rp, wp, hp, yp,
                 scale, M, nvec, inv_h, eps);
 }
 
