@@ -6,7 +6,7 @@
 // family (tcgen05.mma kind::f16 with K = 16 or kind::f8f6f4 with K = 32) and
 // accumulates the k-blocks of 128 bytes in increasing k into one fp32
 // accumulator.  What an element's sum is does not depend on how many rows (64,
-// 128, or 256 over two SMs) and columns (16 .. 256) the instruction takes: every
+// 128, or 128 and 256 over two SMs) and columns (16 .. 256) the instruction takes: every
 // shape that a batch size leads to gives a row the same bytes (tests compare
 // them, and those of the plain GEMM), and the epilogue is element-wise.  So a
 // row of C depends only on its rows of A and of the residual, W and the bias,
@@ -18,9 +18,9 @@
 //
 // Structure: persistent blocks, one per SM, 10 warps: a TMA producer, one thread
 // that issues the MMAs into one of two accumulators in tensor memory, eight
-// epilogue warps of 32 accumulator rows and half the tile's columns each.  Three
+// epilogue warps of 32 accumulator rows and half the tile's columns each.  Four
 // forms: up to 64 rows of A (MMAs of 64 rows, narrow tiles, plain stores; a
-// weight is streamed), one CTA with 128 rows, and pairs of CTAs with 256 rows,
+// weight is streamed), one CTA with 128 rows, and pairs of CTAs with 256 or 128 rows,
 // whose one MMA reads half of W's rows from each SM.  Tile width, k-blocks per
 // stage and stages are run-time values.  Every wait is bounded; a wait that runs
 // out records BI_ERR_TIMEOUT, tells the other roles to stop, waits (bounded) for
@@ -261,11 +261,15 @@ __device__ __forceinline__ uint4 add_pack8(const f32x2* z, bool add, const uint4
 struct Span {
   int c, end;
 };
-template <int kCtas>
+template <int kUnit, bool kSides>
 __device__ __forceinline__ Span span_of(const Tile& t, const FusedParams& p, int bn_out,
-                                        int row_in_unit, int half) {
-  if (t.m * (BM * kCtas) + row_in_unit >= p.M) return Span{0, 0};
+                                        int row_in_unit, int half, int side) {
+  if (t.m * kUnit + row_in_unit >= p.M) return Span{0, 0};
   const int n = (min(bn_out, p.n_out - t.n * bn_out) + kChunk - 1) / kChunk;
+  if constexpr (kSides) {  // a lane has its row's columns of one side
+    const int per = bn_out / (2 * kChunk), first = side * per, mid = first + ((per + 1) >> 1);
+    return half == 0 ? Span{min(first, n), min(mid, n)} : Span{min(mid, n), min(first + per, n)};
+  }
   const int mid = (n + 1) >> 1;
   return half == 0 ? Span{0, mid} : Span{mid, n};
 }
@@ -346,12 +350,15 @@ __device__ __forceinline__ void issue_mmas(const FusedParams& p, const Ring& r, 
 
 // kCtas = 2: a pair of CTAs computes 256 x bn tiles with one MMA over both
 // SMs; each loads its 128 rows of A and half of the tile's rows of W, which
-// both read.
-template <bool kQ8, int kCtas>
+// both read.  kSides: the pair's MMA has 128 rows instead of 256, each CTA 64 of
+// them, their first half of the columns in the first half of the accumulator's
+// lanes and the second in the second.
+template <bool kQ8, int kCtas, bool kSides>
 __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
     const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
     const __grid_constant__ CUtensorMap tc, const FusedParams p) {
   constexpr bool kPair = kCtas == 2;
+  constexpr int kCtaRows = kSides ? 64 : BM;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
   __shared__ uint32_t tmem_slot;
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
       bool ok = true;
       for (int u = first; u < units && ok; u += step) {
         const Tile t = tile_of(u, p);
-        const int ra = (t.m * kCtas + rank) * BM, rb = t.n * p.bn + rank * b_rows;
+        const int ra = (t.m * kCtas + rank) * kCtaRows, rb = t.n * p.bn + rank * b_rows;
         for (int kb = 0; kb < p.kb_total; kb += p.kg) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, p.err, &abort_flag)) {
             ok = false;
@@ -467,7 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
     const int bn_out = swiglu ? p.bn / 2 : p.bn, acc_chunk = swiglu ? 2 * kChunk : kChunk;
     // (an MMA of 64 rows leaves rows 16 q .. 16 q + 15 in the first half of the
     // q-th quarter of the lanes)
-    const int row_in_unit = rank * BM + wq * (p.mma_rows == 64 ? 16 : 32);
+    const int side = wq >> 1;  // (kSides)
+    const int row_in_unit = kSides ? rank * kCtaRows + (wq & 1) * 32
+                                   : rank * BM + wq * (p.mma_rows == 64 ? 16 : 32);
     const bool mine_too = p.mma_rows != 64 || lane < 16;
     const bool staged = p.staged != 0;
     uint8_t* buf = smem + p.ring + ew * kBufs * kChunkBytes;
@@ -480,8 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
     bool ok = true;  // the same in every lane
     for (int u = first; u < units && ok; u += step) {
       const Tile t = tile_of(u, p);
-      const int row0 = t.m * (BM * kCtas) + row_in_unit, row = row0 + lane;
-      const Span span = span_of<kCtas>(t, p, bn_out, row_in_unit, half);
+      const int row0 = t.m * (kCtaRows * kCtas) + row_in_unit, row = row0 + lane;
+      const Span span = span_of<kCtaRows * kCtas, kSides>(t, p, bn_out, row_in_unit, half, side);
       // this half's scales and biases, four columns a lane (N % 8 == 0)
       const int col0 = span.c * acc_chunk + 4 * lane, col = t.n * p.bn + col0;
       float4 ws = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -527,7 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
         if (add_bias) *reinterpret_cast<uint2*>(cb + col0) = bs;
       }
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) +
-                             static_cast<uint32_t>(acc) * kAccCols;
+                             static_cast<uint32_t>(acc) * kAccCols -
+                             (kSides ? static_cast<uint32_t>(side * (p.bn / 2)) : 0u);
       for (int c = span.c; c < span.end; ++c) {
         uint8_t* mine = buf + b * kChunkBytes;
         // (here, and not between the values and their stores, where a branch on
@@ -604,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
 // How a call's work is cut up.
 struct Plan {
   int ctas, bn;      // CTAs of a tile (1: 128 rows, 2: 256) and its width
+  int cta_rows;      // rows of a CTA's tile: 128, or 64 of a pair whose MMA has 128
   int a_rows;        // rows of A per stage
   int kg, stages;    // k-blocks per stage, stages
   bool deep;         // one copy per operand and stage
@@ -630,59 +641,76 @@ int stage_blocks(const Plan& q, bool few, int64_t kb, uint64_t row_bytes) {
 }
 
 // The tile with the least cost: rounds of as many tiles as the device runs at
-// once, each as long as its MMAs or its epilogue, then one epilogue.  In ns,
-// fitted to 3400 timings (both types, every width; M, N and K from 1, 32 and 72
-// to 8192, 28672 and 14336; the tile chosen takes 1.01 times the best one's time
-// on average): a k-block takes one CTA 30 + 85 / kg or 55 + 0.85 a column, a
-// pair 65 + 75 / kg or 0.6 a column (it loads half the rows of W for the same
-// MMAs: 8192 x 28672 x 4096 e4m3 526 us against 621), an epilogue 500 + 7 a
-// column, starting a pair 200.  Up to 64 rows a k-block's time hardly goes by
-// the width.
+// once, each as long as its k-blocks or its epilogue, then one epilogue.  In ns,
+// fitted to 19000 timings of 447 shapes (both types, every form and width; M, N and K
+// from 72, 80 and 256 to 8192, 28672 and 14336; the tile chosen takes 1.011 times the
+// best one's time on average).  A k-block takes the MMA thread 40 to 55 and 100 a
+// stage, the copies into the SM 6 and 0.6 a row, a pair's MMAs 0.65 a column that a
+// warp's lanes have; an epilogue 900 and 6 such a column; starting a pair 2200, or
+// 700 with the smaller tile.  Pairs load half the rows of W for the same MMAs (8192 x
+// 28672 x 4096 e4m3 526 us against 621), and with 64 rows a CTA half the rows of A (128
+// x 4096 x 14336 bf16 31 us, 40 with one CTA, 43 with 128; 384 of them 44, 56, 53;
+// 1024 100, 87, 67); short K's epilogues wait for one another in a pair (8192 x
+// 14336 x 1024 e4m3 117 us, 100 with one CTA).  Up to 64 rows of A a k-block's time
+// hardly goes by the width.
 Plan fused_plan(int64_t M, int64_t N, uint64_t row_bytes, int sms, bool swiglu) {
   const int64_t kb = static_cast<int64_t>((row_bytes + kBlockBytes - 1) / kBlockBytes);
   const bool few = M <= kDirectRows;
   Plan q{};
-  // The MMA always reads a window of 128 rows (64 up to 64 rows), whose rows
-  // past A's tile reach accumulator rows that are never stored.  Only the rows
-  // that there are get loaded, in eights (the swizzle's groups): rows that a copy
-  // fills with zeros cost more than rows of data, as if all of them came from one
-  // place (1 x 6144 x 4096 e4m3 8.7 us with 31 such rows, 6.0 with 7).
-  q.a_rows = M >= BM ? BM : static_cast<int>((M + 7) / 8 * 8);
+  // The MMA always reads a window of 128 rows (64 up to 64 rows and in the smaller
+  // pair), whose rows past A's tile reach accumulator rows that are never stored.
+  // Only the rows that there are get loaded, in eights (the swizzle's groups): rows
+  // that a copy fills with zeros cost more than rows of data, as if all of them came
+  // from one place (1 x 6144 x 4096 e4m3 8.7 us with 31 such rows, 6.0 with 7).
+  const int rows_there = M >= BM ? BM : static_cast<int>((M + 7) / 8 * 8);
   q.staged = !few;
   q.ring = kPoolBytes - (q.staged ? kEpiWarps * kBufs * kChunkBytes : 0);
-  const int step = few ? (swiglu ? 32 : 16) : (swiglu ? 64 : 32);
+  struct Form {
+    int ctas, cta_rows;
+    double mma, start;
+  };
+  const Form forms[3] = {{1, BM, 55.0, 0.0}, {2, BM, 40.0, 2200.0}, {2, 64, 50.0, 700.0}};
   Plan best{};
   double least = 1e300;
-  for (q.ctas = 1; q.ctas <= (M >= BM ? 2 : 1); ++q.ctas)
+  for (int f = 0; f < (M >= BM ? 3 : 1); ++f) {
+    q.ctas = forms[f].ctas;
+    q.cta_rows = forms[f].cta_rows;
+    q.a_rows = std::min(rows_there, q.cta_rows);
+    const int sides = BM / q.cta_rows;  // into which a tile's columns are cut
+    const int step = (few ? 16 : 32) * (swiglu ? 2 : 1) * sides;
     // (with few rows a second round of narrow tiles streams a long K better than
     // one of wide tiles: 64 x 28672 x 4096 e4m3 22.3 us in tiles of 96, 23.1 in
     // 192; 7 x 19848 x 1136 11.9 in 128, 9.7 in 144)
     for (q.bn = few && kb >= 24 ? 128 : 256; q.bn >= step; q.bn -= step) {
       q.kg = stage_blocks(q, few, kb, row_bytes);
-      const int64_t tiles = (M + BM * q.ctas - 1) / (BM * q.ctas) * ((N + q.bn - 1) / q.bn);
+      const int64_t rows = q.cta_rows * q.ctas;
+      const int64_t tiles = (M + rows - 1) / rows * ((N + q.bn - 1) / q.bn);
       const int64_t rounds = (tiles + sms / q.ctas - 1) / (sms / q.ctas);
-      const double block = few ? 700.0 + 0.25 * q.bn
-                           : q.ctas == 2 ? std::max(65.0 + 75.0 / q.kg, 0.6 * q.bn)
-                                         : std::max(30.0 + 85.0 / q.kg, 55.0 + 0.85 * q.bn);
-      const double epilogue = 500.0 + 7.0 * q.bn;
-      const double cost = (q.ctas == 2 ? 200.0 : 0.0) +
+      const double block =
+          few ? 700.0 + 0.25 * q.bn
+              : std::max({forms[f].mma + 100.0 / q.kg, 6.0 + 0.6 * (q.a_rows + q.bn / q.ctas),
+                          q.ctas == 2 ? 0.65 * q.bn / sides : 0.0});
+      const double epilogue = few ? 500.0 + 7.0 * q.bn : 900.0 + 6.0 * q.bn / sides;
+      const double cost = forms[f].start +
                           static_cast<double>(rounds) * std::max(kb * block, epilogue) + epilogue;
       if (cost < least) {
         least = cost;
         best = q;
       }
     }
+  }
   best.deep = best.kg > 1 && whole_blocks(row_bytes, best.ctas);
   const int sub = (best.a_rows + best.bn / best.ctas) * kBlockBytes;
   best.stages = std::min(kMaxStages, best.ring / (best.kg * sub));
   // the last window of A stays inside the ring
-  while (best.stages * best.kg * best.a_rows + BM - best.a_rows > best.ring / kBlockBytes)
+  while (best.stages * best.kg * best.a_rows + best.cta_rows - best.a_rows >
+         best.ring / kBlockBytes)
     --best.stages;
   return best;
 }
 
 // Pairs of CTAs that fit on the device at once (0 on failure); the same for
-// both operand types, asked once per device.
+// all of the kernel's pairs, asked once per device.
 int resident_pairs() {
   constexpr int kMaxDevices = 64;
   static std::atomic<int> known[kMaxDevices];
@@ -690,7 +718,7 @@ int resident_pairs() {
   if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return 0;
   int n = known[d].load(std::memory_order_relaxed);
   if (n == 0) {
-    const auto kernel = gemm_fused_kernel<true, 2>;
+    const auto kernel = gemm_fused_kernel<true, 2, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemBytes)) != cudaSuccess)
       return 0;
@@ -710,10 +738,10 @@ int resident_pairs() {
   return n;
 }
 
-template <bool kQ8, int kCtas>
+template <bool kQ8, int kCtas, bool kSides>
 bi_status launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                  const FusedParams& p, int grid, cudaStream_t s) {
-  const auto kernel = gemm_fused_kernel<kQ8, kCtas>;
+  const auto kernel = gemm_fused_kernel<kQ8, kCtas, kSides>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kSmemBytes)) != cudaSuccess)
     return BI_ERR_CUDA;
@@ -732,6 +760,14 @@ bi_status launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap
   cfg.attrs = attr;
   cfg.numAttrs = kCtas == 1 ? 1 : 2;
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, ta, tb, tc, p));
+}
+
+template <bool kQ8>
+bi_status launch(const Plan& plan, const CUtensorMap& ta, const CUtensorMap& tb,
+                 const CUtensorMap& tc, const FusedParams& p, int grid, cudaStream_t s) {
+  if (plan.ctas == 1) return launch<kQ8, 1, false>(ta, tb, tc, p, grid, s);
+  return plan.cta_rows == BM ? launch<kQ8, 2, false>(ta, tb, tc, p, grid, s)
+                             : launch<kQ8, 2, true>(ta, tb, tc, p, grid, s);
 }
 
 }  // namespace
@@ -764,7 +800,7 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   p.staged = plan.staged;
   p.ring = plan.ring;
   p.kb_total = static_cast<int>((row_bytes + kBlockBytes - 1) / kBlockBytes);
-  const int rows = BM * plan.ctas;
+  const int rows = plan.cta_rows * plan.ctas;
   p.m_tiles = static_cast<int>((M + rows - 1) / rows);
   p.n_tiles = static_cast<int>((N + p.bn - 1) / p.bn);
   // (a block's tile index passes the last one by at most a grid)
@@ -784,7 +820,7 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   // up to 64 rows the MMA takes 64 (an element's sum is the same): below some
   // 100 columns its time goes by its rows, not by them
   p.mma_rows = M <= kDirectRows ? 64 : BM;
-  const int mma = p.mma_rows * plan.ctas;
+  const int mma = plan.ctas == 2 ? rows : p.mma_rows;
   p.idesc = q8 ? umma_idesc_e4m3(mma, p.bn) : umma_idesc_bf16(mma, p.bn, false, false);
   CUtensorMap ta, tb, tc{};
   const uint64_t ra = static_cast<uint64_t>(M), rb = static_cast<uint64_t>(N);
@@ -800,11 +836,8 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
     if (blocks <= 0) return BI_ERR_CUDA;
   }
   const int grid = std::min(units, blocks) * plan.ctas;
-  if (plan.ctas == 2)
-    return q8 ? launch<true, 2>(ta, tb, tc, p, grid, s)
-              : launch<false, 2>(ta, tb, tc, p, grid, s);
-  return q8 ? launch<true, 1>(ta, tb, tc, p, grid, s)
-            : launch<false, 1>(ta, tb, tc, p, grid, s);
+  return q8 ? launch<true>(plan, ta, tb, tc, p, grid, s)
+            : launch<false>(plan, ta, tb, tc, p, grid, s);
 }
 
 }  // namespace bi

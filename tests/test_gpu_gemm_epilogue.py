@@ -422,3 +422,22 @@ def test_calls_that_follow_one_another(cuda, M):
         for i in range(2):
             assert same_bytes(hs[i], want[i]), first_divergence(hs[i], want[i])
     assert bi.bi_check_device_errors() == bi.OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("N,K,act", [(6144, 4096, "none"), (4104, 8192, "gelu"),
+                                     (6176, 4096, "swiglu")])
+def test_rows_of_a_few_hundred_and_a_long_k(cuda, kind, N, K, act):
+    """Batches that pairs of 64 rows a CTA take, their columns in two halves of
+    the accumulator's lanes: the bytes of small and of large batches, and the
+    64-bit definition."""
+    c = Case(kind, 1100, N, K, cuda, 7000 + N, act)
+    full = c.run()
+    for M in (40, 64, 128, 130, 200, 256, 300, 384, 520, 777):
+        got = c.run(slice(0, M))
+        assert same_bytes(got, full[:M]), (M, first_divergence(got, full[:M]))
+    rows = slice(120, 320)
+    args = (c.va[rows], c.vw, c.vb, c.vr[rows], c.name)
+    check_close(f64(c.run(rows)), linear8.product(*args), linear8.product_bound(*args),
+                "%s %s" % (kind, act))
+    assert bi.bi_check_device_errors() == bi.OK
