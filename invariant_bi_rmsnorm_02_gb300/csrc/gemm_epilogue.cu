@@ -805,15 +805,15 @@ bi_status launch_gemm_fused(const void* A, const float* a_scale, const void* W,
   p.n_tiles = static_cast<int>((N + p.bn - 1) / p.bn);
   // (a block's tile index passes the last one by at most a grid)
   if (static_cast<int64_t>(p.m_tiles) * p.n_tiles > 0x7fffffff - sms) return BI_ERR_UNSUPPORTED;
-  // raster: the smaller operand whole where it takes half of L2 (2048 x 4096 x
-  // 14336 bf16, A 59 MB: 137 us in two groups, 133 in one), else groups of about
-  // 40 MB of it (8192 x 28672 x 4096 bf16, A 67 MB: 947 us, 996 in groups of 64)
+  // raster: the smaller operand whole where it leaves half of L2 (2048 x 4096 x 14336
+  // bf16, A 56 MiB: 137 us in two groups, 133 in one), else in even groups of up to
+  // 40 MiB of it (8192 x 28672 x 4096 bf16, A 64 MiB, in a run of a second: 1100 us in
+  // two groups, 1167 whole)
   p.m_fast = M <= N ? 1 : 0;
   const int64_t tile_bytes = static_cast<int64_t>(p.m_fast ? rows : p.bn) * row_bytes;
-  const int64_t span = p.m_fast ? p.m_tiles : p.n_tiles;
-  const int64_t group = span * tile_bytes <= int64_t(64) << 20
-                            ? span
-                            : std::max<int64_t>(1, (int64_t(40) << 20) / tile_bytes);
+  const int64_t span = p.m_fast ? p.m_tiles : p.n_tiles, all = span * tile_bytes;
+  const int64_t groups = all <= int64_t(60) << 20 ? 1 : (all - 1) / (int64_t(40) << 20) + 1;
+  const int64_t group = (span + groups - 1) / groups;
   p.by_per = Divisor(group * (p.m_fast ? p.n_tiles : p.m_tiles));
   p.by_group = Divisor(group);
   p.by_last = Divisor(span % group ? span % group : group);
