@@ -200,7 +200,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 // Every thread of the cluster has come here, and sees what the others wrote.
+// (.aligned wants a warp's threads at the barrier together, and single lanes may
+// come from work of their own: the warp meets first)
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
