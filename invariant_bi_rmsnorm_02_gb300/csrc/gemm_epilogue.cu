@@ -496,11 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fused_kernel(
       float4 ws = make_float4(0.f, 0.f, 0.f, 0.f);
       uint2 bs = make_uint2(0, 0);
       float row_scale = 1.0f;
+      // (plain loads: the kernel before, which may write them, can still run when
+      // this one starts, and read-only loads are for what no one writes meanwhile)
       if (span.c < span.end && col < p.N) {
-        if constexpr (kQ8) ws = __ldg(reinterpret_cast<const float4*>(p.w_scale + col));
-        if (add_bias) bs = __ldg(reinterpret_cast<const uint2*>(p.bias + col));
+        if constexpr (kQ8) ws = *reinterpret_cast<const float4*>(p.w_scale + col);
+        if (add_bias) bs = *reinterpret_cast<const uint2*>(p.bias + col);
       }
-      if (kQ8 && row < p.M && mine_too) row_scale = __ldg(p.a_scale + row);
+      if (kQ8 && row < p.M && mine_too) row_scale = p.a_scale[row];
       // the residual of the first chunk, while the tile's MMAs run; each further
       // one as soon as the one before is used, and, unless the epilogue is what
       // the blocks wait for (fetching twice then costs more than it hides), all

@@ -84,9 +84,8 @@ __device__ __forceinline__ uint32_t e4m3x4(f32x2 a, f32x2 b) {
 // were spilled (64 rows of 4096 1.8 us, 2.4; 8192 16.9, 17.3).
 template <int VPT, bool kAdd, bool kWarpRow>
 __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
-    const uint4* x, const uint4* res, const uint4* __restrict__ w, uint4* h,
-    uint2* __restrict__ y, float* __restrict__ scale, int64_t M, int nvec, float inv_h,
-    float eps) {
+    const uint4* x, const uint4* res, const uint4* w, uint4* h, uint2* __restrict__ y,
+    float* __restrict__ scale, int64_t M, int nvec, float inv_h, float eps) {
   __shared__ float red[32];
   __shared__ uint32_t red_max[32];
   const int first = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
@@ -119,6 +118,21 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
       }
     }
   }
+  // blocks of 1024 threads have registers for the row, not for its values too:
+  // they form them twice (1024 x 65536 with a residual 95 us when kept, 86 when not)
+  constexpr bool kKeep = VPT <= 4;
+  // The weight by ordinary loads (read-only ones are for what no one writes while
+  // the kernel lives, and the kernel before may write w while this one starts),
+  // which have to go out before the sum's barrier: 8192 x 4096 16.5 us, 17.8 behind it.
+  auto weight = [&](int k) {
+    const int i = first + k * stride;
+    return i < nvec ? w[i] : make_uint4(0, 0, 0, 0);
+  };
+  uint4 wk[kKeep ? VPT : 1];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) wk[k] = weight(k);
+  }
   float ss = 0.0f;
 #pragma unroll
   for (int k = 0; k < VPT; ++k) ss = sum_squares8(hv[k], ss);
@@ -126,15 +140,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
   const float r = inv_rms(kWarpRow ? warp_sum(ss) : block_sum(ss, red), inv_h, eps);
   const f32x2 r2 = both(r);
   auto values = [&](int k, f32x2 (&v)[4]) {
-    const int i = first + k * stride;
-    const uint4 wv = i < nvec ? __ldg(w + i) : make_uint4(0, 0, 0, 0);
+    uint4 wv;
+    if constexpr (kKeep) wv = wk[k];
+    else wv = weight(k);
     const uint32_t hw[4] = {hv[k].x, hv[k].y, hv[k].z, hv[k].w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(widen2(hw[e]), r2), widen2(ww[e]));
   };
-  // blocks of 1024 threads have registers for the row, not for its values too:
-  // they form them twice (1024 x 65536 with a residual 95 us when kept, 86 when not)
-  constexpr bool kKeep = VPT <= 4;
   f32x2 v[kKeep ? VPT : 1][4];
   float top = 0.0f;
 #pragma unroll

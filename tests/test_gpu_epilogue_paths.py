@@ -1,5 +1,6 @@
-"""Paths of the products with an epilogue that few shapes reach: pairs of CTAs
-whose warps come to their common barriers from work of single lanes."""
+"""Paths of the products with an epilogue that few shapes or calls reach: pairs of CTAs
+whose warps come to their common barriers from work of single lanes, and small
+inputs that the call before writes."""
 import numpy as np
 import pytest
 import torch
@@ -57,3 +58,52 @@ def test_pairs_meet_at_their_start_and_end(cuda, kind, M, N, K):
     assert bi.bi_check_device_errors() == bi.OK
     for g in got:
         assert same_bytes(g, want), first_divergence(g, want)
+
+
+def test_small_inputs_written_by_the_call_before(cuda):
+    """The norm's weight, both scales and the bias, each written anew by the call
+    right before the one that reads it: queued without a pause they give what they
+    give with the device idle between them."""
+    M, N, H = 200, 2048, 512
+    bf = dict(dtype=torch.bfloat16, device=cuda)
+    f8 = dict(dtype=torch.float8_e4m3fn, device=cuda)
+    f32 = dict(dtype=torch.float32, device=cuda)
+    x = synth.normal_bf16((M, H), 11, device=cuda)
+    ws = [synth.normal_bf16((N, H), 12 + i, std=(i + 1) * H ** -0.5, device=cuda) for i in range(3)]
+    ones = [synth.normal_bf16((1, 64), 20 + i, device=cuda) for i in range(3)]
+    to_h = synth.normal_bf16((H, 64), 30, std=0.125, device=cuda)
+    to_n = synth.normal_bf16((N, 64), 31, std=0.125, device=cuda)
+
+    def rounds(pause):
+        g, b = torch.empty(1, H, **bf), torch.empty(1, N, **bf)
+        y8, ys = torch.empty(M, H, **f8), torch.empty(M, **f32)
+        w8, sw = torch.empty(N, H, **f8), torch.empty(N, **f32)
+        outs = [torch.empty(M, N, **bf) for _ in range(30)]
+        torch.cuda.synchronize()
+        for i, out in enumerate(outs):
+            bi.bi_gemm_epilogue(ones[i % 3], to_h, g)                # the norm's weight
+            pause()
+            bi.bi_rmsnorm_q8(x, g.view(H), y8, ys, 1e-6)
+            pause()
+            bi.bi_gemm_epilogue(ones[(i + 1) % 3], to_n, b)          # the bias
+            pause()
+            bi.bi_quantize_q8(ws[(i // 2) % 3], w8, sw)              # the weight's scales
+            pause()
+            bi.bi_gemm_q8(y8, ys, w8, sw, out, bias=b.view(N))
+            pause()
+            bi.bi_gemm_epilogue(ones[i % 3], to_n, b)                # the bias right before
+            pause()
+            bi.bi_gemm_q8(y8, ys, w8, sw, out, bias=b.view(N), residual=out)
+            pause()
+            bi.bi_quantize_q8(x, y8, ys)                             # the rows' scales
+            pause()
+            bi.bi_gemm_q8(y8, ys, w8, sw, out, residual=out)
+            pause()
+        torch.cuda.synchronize()
+        return outs
+
+    want, got = rounds(torch.cuda.synchronize), rounds(lambda: None)
+    assert not same_bytes(want[0], want[1])
+    for a, b in zip(got, want):
+        assert same_bytes(a, b), first_divergence(a, b)
+    assert bi.bi_check_device_errors() == bi.OK
