@@ -223,7 +223,9 @@ bi_status bi_gemm_swiglu(const void* A, const void* W, void* out, int64_t M, int
  *                     rows of the same features (bi_gemm_swiglu's are of 128)
  * Sums are fp32, one rounding to bf16 at the end (neither z nor g and u are
  * rounded before); the activations are evaluated to 2^-14 of their value and
- * 2^-119, or better.  At z = -inf RELU and GELU give 0, the others but NONE NaN.
+ * 2^-119, or better, SWIGLU to 2^-14 of its value and 2^-119 max(|u|, 1) (silu(g)
+ * below 2^-119 counts as 0, and is then multiplied by u).  At z = -inf RELU and
+ * GELU give 0, the others but NONE NaN.
  * With BI_ACT_NONE, no bias and no residual C has exactly the bytes of bi_gemm
  * in BI_MODE_INVARIANT; every row of C depends only on its rows of A and
  * residual, on W and on bias, whatever M (there is no batch-variant mode).

@@ -107,3 +107,32 @@ def test_small_inputs_written_by_the_call_before(cuda):
     for a, b in zip(got, want):
         assert same_bytes(a, b), first_divergence(a, b)
     assert bi.bi_check_device_errors() == bi.OK
+
+
+def test_swiglu_of_far_gates_under_large_ups(cuda):
+    """silu(g) u to 2^-14 of its value and 2^-119 max(|u|, 1): gates where exp(-g)
+    leaves fp32's range, under ups of every size.  (Without the factor |u| the
+    second term does not hold: a gate of -88.5 under 1e30 gives 0 for -3e-7.)"""
+    g = [-60.0, -80.0, -86.0, -87.0, -87.5, -88.5, -90.0, -95.0, -100.0, -200.0, -1e30, 0.0, 3.0, 88.0]
+    u = [1e38, -1e30, 1e12, 1.0, -3.0, 1e-6, 1e-30, 0.0]
+    A = torch.zeros(len(g) * len(u), 32)
+    A[:, 0] = torch.tensor(g).repeat_interleave(len(u))
+    A[:, 1] = torch.tensor(u).repeat(len(g))
+    W = torch.zeros(32, 32)
+    W[0, 0] = W[16, 1] = 1.0       # column 0's gate and up; each sum has one term
+    A = A.to(torch.bfloat16)
+    gv, uv = f64(A[:, 0]), f64(A[:, 1])
+    got = f64(bi.gemm_epilogue(A.to(cuda), W.to(torch.bfloat16).to(cuda),
+                               activation=bi.ACT_SWIGLU)[:, 0])
+    assert bi.bi_check_device_errors() == bi.OK
+    want = linear8.activation(gv, "silu") * uv
+    over = np.abs(want) > 3.389e38            # (88 times 1e38: past bf16)
+    assert np.isinf(got[over]).all()
+    got, want, uv = got[~over], want[~over], uv[~over]
+
+    def bound(least):                         # then one rounding to bf16
+        e = 2.0 ** -14 * np.abs(want) + least
+        return e + 2.0 ** -8 * (np.abs(want) + e) + 2.0 ** -134
+
+    check_close(got, want, bound(2.0 ** -119 * np.maximum(np.abs(uv), 1.0)), "swiglu")
+    assert (np.abs(got - want) > bound(2.0 ** -119)).any()
