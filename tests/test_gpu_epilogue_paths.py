@@ -136,3 +136,29 @@ def test_swiglu_of_far_gates_under_large_ups(cuda):
 
     check_close(got, want, bound(2.0 ** -119 * np.maximum(np.abs(uv), 1.0)), "swiglu")
     assert (np.abs(got - want) > bound(2.0 ** -119)).any()
+
+
+def test_infinite_scales(cuda):
+    """A scale of infinity gives its row (A) or column (W) the sum's sign: relu
+    leaves +inf, 0 and, where the sum is 0, NaN; the rest keeps its bytes."""
+    M, N, K = 40, 96, 128
+    c = Operands("q8", M, N, K, cuda, 7000)
+    (a, sa), (w, sw) = c.a, c.w
+    a.view(torch.uint8)[9, 1:] = 0            # row 9: one element, so that some
+    w.view(torch.uint8)[40:44, 0] = 0         # sums are exactly 0
+    a.view(torch.uint8)[12] = 0               # and, in column 17, a row of zeros
+    want = bi.gemm_q8(a, sa, w, sw, activation=bi.ACT_RELU)
+    sums = torch.from_numpy(linear8.numbers(a.cpu().view(torch.uint8).numpy())
+                            @ linear8.numbers(w.cpu().view(torch.uint8).numpy()).T)
+    sa[9], sw[17] = float("inf"), float("inf")
+    got = bi.gemm_q8(a, sa, w, sw, activation=bi.ACT_RELU).cpu()
+    assert bi.bi_check_device_errors() == bi.OK
+    for rows, cols in ((9, slice(None)), (slice(None), 17)):
+        s, g = sums[rows, cols], got[rows, cols]
+        assert ((s > 0).sum() > 5 and (s < 0).sum() > 5 and (s == 0).any())
+        assert (g[s > 0] == float("inf")).all()
+        assert (g[s < 0] == 0).all()
+        assert torch.isnan(g[s == 0]).all()
+    rows = [i for i in range(M) if i != 9]
+    cols = [j for j in range(N) if j != 17]
+    assert same_bytes(got[rows][:, cols], want.cpu()[rows][:, cols])
