@@ -1,6 +1,7 @@
-"""Paths of the products with an epilogue that few shapes or calls reach: pairs of CTAs
-whose warps come to their common barriers from work of single lanes, and small
-inputs that the call before writes."""
+"""Paths of the products with an epilogue that few shapes or calls reach: pairs of
+CTAs whose warps come to their common barriers from work of single lanes, small
+inputs that the call before writes, gates and scales past fp32's range, stages that
+K does not fill, and operands whose tiles are walked in groups."""
 import numpy as np
 import pytest
 import torch
@@ -162,3 +163,58 @@ def test_infinite_scales(cuda):
     rows = [i for i in range(M) if i != 9]
     cols = [j for j in range(N) if j != 17]
     assert same_bytes(got[rows][:, cols], want.cpu()[rows][:, cols])
+
+
+def check_rows(c, got, rows):
+    """Rows of A W^T + bias against 64-bit sums (on the device: long rows of many
+    columns), within linear8.product_bound's terms for no activation."""
+    def held(side, pick):
+        v = side[0][pick].to(torch.float32).double()
+        return v * side[1][pick].double()[:, None] if len(side) == 2 else v
+    a, w, b = held(c.a, rows), held(c.w, slice(None)), c.b.double()
+    want, mag = a @ w.T + b, a.abs() @ w.abs().T + b.abs()
+    e = (a.shape[1] + 3) * 2.0 ** -23 * mag
+    check_close(f64(got[rows]), f64(want), f64(e + 2.0 ** -8 * (want.abs() + e) + 2.0 ** -118),
+                "%s %s" % (c.kind, tuple(got.shape)))
+
+
+@pytest.mark.parametrize("kind,M,N,K", [
+    # one copy for several k-blocks of rows that are whole k-blocks, some left over
+    # at the end: five in fours and in twos, seven in fours
+    ("q8", 16, 6144, 640), ("q8", 100, 1000, 640), ("q8", 16, 4096, 896),
+    ("bf16", 16, 6144, 320), ("bf16", 100, 1000, 320), ("bf16", 16, 4096, 448),
+    # pairs of 64 rows a CTA: two k-blocks a stage, an odd number of them; one a stage
+    ("q8", 146, 5752, 10320), ("bf16", 146, 5752, 5160),
+    ("q8", 159, 7808, 13296), ("bf16", 159, 7808, 6648),
+    # pairs of 128 rows a CTA, two k-blocks a stage, an odd number of them
+    ("bf16", 275, 392, 12864), ("q8", 275, 392, 25728)])
+def test_stages_that_k_does_not_fill(cuda, kind, M, N, K):
+    c = Operands(kind, M, N, K, cuda, 200 + M)
+    got = c.run()
+    check_rows(c, got, torch.tensor([0, 1, 7, M // 2, M - 1], device=cuda))
+    for at in range(0, M, 50):                   # up to 64 rows: another form
+        part = c.run(slice(at, min(at + 50, M)))
+        assert same_bytes(got[at:at + 50], part), (at, first_divergence(got[at:at + 50], part))
+    one = c.run(slice(M - 1, M))
+    assert same_bytes(got[M - 1:], one)
+    assert bi.bi_check_device_errors() == bi.OK
+
+
+@pytest.mark.parametrize("kind,M,N,K", [("q8", 5400, 5600, 16384), ("q8", 5600, 5400, 16384),
+                                        ("bf16", 5400, 6000, 8192), ("bf16", 6000, 5400, 8192),
+                                        ("q8", 4400, 4600, 16000), ("q8", 4600, 4400, 16000)])
+def test_operands_larger_than_the_cache_share(cuda, kind, M, N, K):
+    """Both operands above 60 MiB: the smaller one's tiles are walked in two even
+    groups, or in three, the last smaller.  Every row as calls of 1000 rows, in one
+    group, give it."""
+    c = Operands(kind, M, N, K, cuda, 300)
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=cuda)
+    if kind == "q8":
+        bi.bi_gemm_q8(*c.a, *c.w, out, c.b)
+    else:
+        bi.bi_gemm_epilogue(*c.a, *c.w, out, c.b)
+    assert bi.bi_check_device_errors() == bi.OK
+    check_rows(c, out, torch.tensor([0, M // 2, M - 1], device=cuda))
+    for at in range(0, M, 1000):
+        part = c.run(slice(at, min(at + 1000, M)))
+        assert same_bytes(out[at:at + 1000], part), (at, first_divergence(out[at:at + 1000], part))
