@@ -26,14 +26,18 @@
 // out records BI_ERR_TIMEOUT, tells the other roles to stop, waits (bounded) for
 // its copies and MMAs in flight, frees tensor memory and returns.
 //
-// What bounds it (one GB300, calls in a loop; rates are of the measured 1957
+// What bounds it (one GB300, a few calls in a loop; rates are of the measured 1957
 // TFLOP/s bf16, twice that for e4m3, and 6777 GB/s): with many rows the tensor
-// cores and the power they draw (8192 x 28672 x 4096 e4m3 with SwiGLU 492 us =
-// 3.9 PFLOP/s, 1.00; bf16 2048 x 4096 x 14336 with the residual 131 us, 0.94);
-// with few the weight's bytes (64 x 28672 x 4096 e4m3 21 us, 0.83) and for short
-// ones start and end, some 3 us, and the chain of one accumulator's MMAs, some
-// 50 cycles each (16 x 6144 x 4096 e4m3 5.9 us, 0.64); short K the epilogue
-// (8192 x 14336 x 1024 e4m3 101 us, with GELU 155, with a residual too 194).
+// cores and the power they draw (8192 x 28672 x 4096 e4m3 with SwiGLU 493 us =
+// 3.9 PFLOP/s, 1.00; bf16 2048 x 4096 x 14336 with the residual 131 us, 0.94; in a
+// run of seconds, which draws the power limit, 572 to 594 us, 0.83 to 0.86, and 154 to
+// 160, 0.77 to 0.80); with few the weight's bytes (64 x 28672 x 4096 e4m3 21.5 us,
+// 0.82) and for short ones start and end, some 3 us, and some 50 cycles an MMA,
+// whatever its width (16 x 6144 x 4096 e4m3 5.9 us with the weight in L2, 8.0 from
+// memory, 0.47).  Those 50 cycles are the same with two accumulators taking turns,
+// so they are not one accumulator's chain, but the issuing thread's instructions or
+// the MMA's own least time.  Short K: C's way out through the epilogue (8192 x 14336 x
+// 256 e4m3 89 us, 2.6 TB/s; x 1024 99, with GELU 152, with a residual too 193).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -282,8 +286,8 @@ struct Ring {
 };
 
 // The MMAs of all of a block's tiles, by one thread, kKG k-blocks a stage.
-// The loop's own instructions are what a narrow tile waits for (some 50 cycles
-// an MMA and 150 around a stage; with the k-blocks of a stage counted at run
+// This loop is what a narrow tile waits for (some 50 cycles an MMA, the loop's
+// instructions or the MMA's own least time, and 150 around a stage; with the k-blocks of a stage counted at run
 // time and the addresses formed anew 100 more: 256 x 4096 x 14336 e4m3 21 us
 // in place of 27), so nothing is recomputed in it, and the next stage's
 // barrier is looked at while the MMAs are on their way.
@@ -643,18 +647,26 @@ int stage_blocks(const Plan& q, bool few, int64_t kb, uint64_t row_bytes) {
 }
 
 // The tile with the least cost: rounds of as many tiles as the device runs at
-// once, each as long as its k-blocks or its epilogue, then one epilogue.  In ns,
-// fitted to 19000 timings of 447 shapes (both types, every form and width; M, N and K
-// from 72, 80 and 256 to 8192, 28672 and 14336; the tile chosen takes 1.011 times the
-// best one's time on average).  A k-block takes the MMA thread 40 to 55 and 100 a
-// stage, the copies into the SM 6 and 0.6 a row, a pair's MMAs 0.65 a column that a
-// warp's lanes have; an epilogue 900 and 6 such a column; starting a pair 2200, or
-// 700 with the smaller tile.  Pairs load half the rows of W for the same MMAs (8192 x
+// once, each as long as its k-blocks or its epilogue, then one epilogue.  The cost is a
+// ranking of one shape's tiles, not a time: its numbers were fitted so that the tile
+// with the least cost is a fast one, over 19000 timings of 447 shapes (both types, every
+// form and width; M, N and K from 72, 80 and 256 to 8192, 28672 and 14336; the tile
+// chosen takes 1.011 times the best one's time on average), and e4m3 8192 x 28672 x
+// 4096 comes out at 260000 and takes 493 us, 16 x 6144 x 4096 at 23600 and takes 6.  A
+// k-block counts 40 to 55 for the MMA thread and 100 a stage, 6 and 0.6 a row for the
+// copies into the SM, 0.65 a column that a warp's lanes have for a pair's MMAs; an
+// epilogue 900 and 6 such a column; starting a pair 2200, or 700 with the smaller
+// tile.  Pairs load half the rows of W for the same MMAs (8192 x
 // 28672 x 4096 e4m3 526 us against 621), and with 64 rows a CTA half the rows of A (128
 // x 4096 x 14336 bf16 31 us, 40 with one CTA, 43 with 128; 384 of them 44, 56, 53;
 // 1024 100, 87, 67); short K's epilogues wait for one another in a pair (8192 x
 // 14336 x 1024 e4m3 117 us, 100 with one CTA).  Up to 64 rows of A a k-block's time
-// hardly goes by the width.
+// hardly goes by the width.  Below 128 rows one CTA loads only the rows there are, where a
+// pair would fill its second half up with zeros: 4096 x 14336 bf16 65 rows 27.6 us, 32.1
+// in a pair of 64 each, 80 29.9 and 32.2, 96 33.4 and 32.2, 112 33.7 and 32.3; e4m3 15.5
+// and 18.7, 16.5 and 18.8, 18.2 and 18.8, 18.3 and 18.8; 28672 x 4096 bf16 41.4 to 42.2
+// and 43.1 to 43.7.  The last rows before 128 would gain by a pair (127 rows 39.8 us,
+// 32.3), and do not get one.
 Plan fused_plan(int64_t M, int64_t N, uint64_t row_bytes, int sms, bool swiglu) {
   const int64_t kb = static_cast<int64_t>((row_bytes + kBlockBytes - 1) / kBlockBytes);
   const bool few = M <= kDirectRows;
@@ -681,8 +693,10 @@ Plan fused_plan(int64_t M, int64_t N, uint64_t row_bytes, int sms, bool swiglu) 
     const int sides = BM / q.cta_rows;  // into which a tile's columns are cut
     const int step = (few ? 16 : 32) * (swiglu ? 2 : 1) * sides;
     // (with few rows a second round of narrow tiles streams a long K better than
-    // one of wide tiles: 64 x 28672 x 4096 e4m3 22.3 us in tiles of 96, 23.1 in
-    // 192; 7 x 19848 x 1136 11.9 in 128, 9.7 in 144)
+    // one of wide tiles: with widths up to 128 and up to 256 e4m3 64 x 28672 x 4096 22.2
+    // and 23.8 us, 1 x 28672 x 4096 21.1, 22.3, bf16 1 x 28672 x 1536 16.9, 17.8, 64 x
+    // 28672 x 2048 22.3, 23.7, but 32 x 20000 x 4096 30.3, 28.9; short K e4m3 7 x 19848 x
+    // 1136 10.3, 9.1, 64 rows 11.4, 9.7, but 64 x 28672 x 2048 12.7, 13.8)
     for (q.bn = few && kb >= 24 ? 128 : 256; q.bn >= step; q.bn -= step) {
       q.kg = stage_blocks(q, few, kb, row_bytes);
       const int64_t rows = q.cta_rows * q.ctas;

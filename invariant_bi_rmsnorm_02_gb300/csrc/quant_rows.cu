@@ -19,8 +19,8 @@
 // A row is read once and kept in registers; one row per block, or one per warp
 // (eight a block) where the row's shape is one warp.  Bound by memory for many
 // rows (8192 of 14336 quantised 56 us = 6.3 TB/s, 0.93 of the measured rate; the
-// norm of 8192 of 4096 with a residual 36 us, 0.96), by the launch for few (64 of
-// 4096: 1.5 and 2.0 us among others).  With one value an
+// norm of 8192 of 4096 with a residual 36 us, 0.96, without one 16.5), by the launch for
+// few (64 of 4096: 1.5 and 1.9 us among others).  With one value an
 // instruction it was instructions that bounded it (33 million elements at 16 each
 // are 15 us of issue slots, against 15 of memory); products and quotients are
 // formed two at a time (f32x2).
@@ -81,7 +81,8 @@ __device__ __forceinline__ uint32_t e4m3x4(f32x2 a, f32x2 b) {
 // kAdd: h = bf16(x + res) first, written to h (which may be x or res: a
 // thread reads its elements of both before it writes any).  64 registers a
 // thread; with 48, of which one more block of 256 threads fits an SM, values
-// were spilled (64 rows of 4096 1.8 us, 2.4; 8192 16.9, 17.3).
+// were spilled (64 rows of 4096 2.4 us where 64 registers took 1.8, 8192 17.3 and
+// 16.9, before the weight's loads went ahead of the sum's barrier).
 template <int VPT, bool kAdd, bool kWarpRow>
 __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
     const uint4* x, const uint4* res, const uint4* w, uint4* h, uint2* __restrict__ y,
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_q8_kernel(
     }
   }
   // blocks of 1024 threads have registers for the row, not for its values too:
-  // they form them twice (1024 x 65536 with a residual 95 us when kept, 86 when not)
+  // they form them twice (1024 x 65536 with a residual 95 us when kept, 87 when not)
   constexpr bool kKeep = VPT <= 4;
   // The weight by ordinary loads (read-only ones are for what no one writes while
   // the kernel lives, and the kernel before may write w while this one starts),
