@@ -287,10 +287,10 @@ struct Ring {
 
 // The MMAs of all of a block's tiles, by one thread, kKG k-blocks a stage.
 // This loop is what a narrow tile waits for (some 50 cycles an MMA, the loop's
-// instructions or the MMA's own least time, and 150 around a stage; with the k-blocks of a stage counted at run
-// time and the addresses formed anew 100 more: 256 x 4096 x 14336 e4m3 21 us
-// in place of 27), so nothing is recomputed in it, and the next stage's
-// barrier is looked at while the MMAs are on their way.
+// instructions or the MMA's own least time, and 150 around a stage; with the
+// k-blocks of a stage counted at run time and the addresses formed anew 100 more:
+// 256 x 4096 x 14336 e4m3 21 us in place of 27), so nothing is recomputed in it, and
+// the next stage's barrier is looked at while the MMAs are on their way.
 template <bool kQ8, bool kPair, int kKG>
 __device__ __forceinline__ void issue_mmas(const FusedParams& p, const Ring& r, int first,
                                            int units, int step, volatile int* abort_flag) {
